@@ -480,6 +480,117 @@ int q4k_mmq(const void *plane, const uint16_t *wq, int M, int K, const int8_t *X
             void *workspace, size_t workspace_bytes, int32_t *partials, int *path_out,
             q6_stream_t s);
 
+/* ------------------------------------------------------------------------
+ * Projections whose weights each token chooses: expert routing and grouping,
+ * the grouped products of K-quant experts, their combination, and low-rank
+ * adapters beside a shared projection. No counterpart in the pages; the
+ * q6_K and q4_K blocks are the ones above.
+ *
+ * Unlike the GEMMs above these take 16-bit activations as they are (nothing
+ * is quantised to int8): products are summed in f32 and rounded once to the
+ * activations' type. The conventions at the top of this file hold. Nothing is
+ * allocated; the grouping lives in caller buffers and stays on the device, so
+ * no call waits for its sizes.
+ *
+ * Types of activations, logits and adapters: */
+#define Q6_TYPE_F32 0
+#define Q6_TYPE_BF16 1
+#define Q6_TYPE_F16 2
+/* Weight formats of the expert plane: */
+#define Q6_FMT_Q4K 4
+#define Q6_FMT_Q6K 6
+
+#define Q6_MAX_GROUPS 1024 /* experts, or adapters, of one grouping */
+#define Q6_MAX_TOPK 32     /* items (chosen experts) of one token */
+#define Q6_LORA_MAX_RANK 256
+
+#define Q6_PATH_EXPERTS_FEW 13 /* grouped product, warp-level MMAs, weights streamed per token tile */
+
+/* A grouping sorts N * per_row items by group, in item order within one; item
+ * i = n * per_row + j is slot j of token n. All device, int32, caller-owned:
+ *   offsets [groups + 2] : group g holds sorted items offsets[g] ..
+ *       offsets[g + 1] - 1; items of no group come last, from offsets[groups]
+ *       to offsets[groups + 1] = N * per_row.
+ *   rows [N * per_row]   : the token n of each sorted item.
+ *   pos  [N][per_row]    : the place of each item among the sorted ones, -1
+ *       for an item of no group.
+ * Size in bytes of the workspace the two calls below need (0: none).
+ * Q6_EINVAL unless N >= 0, 1 <= per_row <= Q6_MAX_TOPK, 1 <= groups <=
+ * Q6_MAX_GROUPS and N * per_row < 2^31. */
+int q6_group_workspace_bytes(int N, int per_row, int groups, size_t *bytes);
+
+/* Groups items by ids [N][per_row] (device int32); an id outside 0 ..
+ * groups - 1 belongs to no group. workspace: device, 4-byte aligned, at least
+ * q6_group_workspace_bytes() (may be NULL when that is 0). */
+int q6_group_rows(const int32_t *ids, int N, int per_row, int groups, int32_t *offsets,
+                  int32_t *rows, int32_t *pos, void *workspace, size_t workspace_bytes,
+                  q6_stream_t s);
+
+/* Routes N tokens to topk of E experts each and groups them:
+ *   ids [N][topk]     : the experts of the topk largest logits, largest first,
+ *       ties to the lowest index. A logit of -inf or NaN is never chosen: the
+ *       slots left over get id -1 and weight 0 (no group).
+ *   weights [N][topk] : f32, exp(l - max) / sum, the sum over the chosen
+ *       experts (renormalize != 0) or over all E. A NaN logit makes its
+ *       token's weights NaN.
+ *   offsets, rows, pos: the grouping of ids by expert (above).
+ *   logits : device [N][ldl] of `type` (f32, bf16, f16), ldl >= E, aligned to
+ *       its element.
+ * 1 <= topk <= min(E, Q6_MAX_TOPK), E <= Q6_MAX_GROUPS. */
+int q6_moe_route(const void *logits, int type, int N, int E, int64_t ldl, int topk,
+                 int renormalize, int32_t *ids, float *weights, int32_t *offsets, int32_t *rows,
+                 int32_t *pos, void *workspace, size_t workspace_bytes, q6_stream_t s);
+
+/* Expert weights: E matrices of M x K in GGUF q4_K or q6_K bytes, one after
+ * another (raw as for q6k_pack_weights: device memory, or host memory the
+ * device reads). With swiglu != 0 the M = 2 H rows are H gate rows, then H up
+ * rows. plane: device, 256-byte aligned; one tile per 128 rows and super-block
+ * (144 or 210 bytes a super-block and row, rows padded to 128), and a power of
+ * two per row. K % 256 == 0, E <= Q6_MAX_GROUPS, M even with swiglu. */
+int q6_expert_plane_bytes(int fmt, int E, int M, int K, int swiglu, size_t *bytes);
+int q6_pack_experts(int fmt, const uint8_t *raw, int E, int M, int K, int swiglu, void *plane,
+                    q6_stream_t s);
+
+/* The grouped product over a grouping by expert:
+ *   Y[i] = W[e(i)] x,  x = X[rows[i]] (gather != 0) or X[i],
+ * for every sorted item i; with swiglu weights Y[i] = silu(gate) * up. Items
+ * of no group get zeros.
+ *   X : device [nx][ldx] of `type` (bf16 or f16), 16-byte aligned, ldx % 8 ==
+ *       0, ldx >= K; nx rows (every rows[i] < nx; without gather nx >= items).
+ *   Y : device [items][ldy] of the same type, ldy >= M (M / 2 with swiglu);
+ *       must not overlap X.
+ *   items : the grouping's number of items (offsets[E + 1]).
+ *   path_out : NULL or receives the Q6_PATH_EXPERTS_* that ran. */
+int q6_experts_mmq(int fmt, const void *plane, int E, int M, int K, int swiglu, const void *X,
+                   int type, int64_t nx, int64_t ldx, int gather, const int32_t *offsets,
+                   const int32_t *rows, int64_t items, void *Y, int64_t ldy, int *path_out,
+                   q6_stream_t s);
+
+/* out[n] = shared[n] + sum over j of weights[n][j] * Y[pos[n][j]], in f32,
+ * rounded once to Y's type (bf16 or f16); a slot with pos < 0 adds nothing.
+ *   Y [items][ldy], out [N][ldo] of `type`; shared f32 [N][lds] or NULL; all
+ *   leading dimensions >= M. out must not overlap Y or shared. */
+int q6_moe_combine(const void *Y, int type, int64_t ldy, const int32_t *pos, const float *weights,
+                   int N, int topk, int M, const float *shared, int64_t lds, void *out,
+                   int64_t ldo, q6_stream_t s);
+
+/* Low-rank adapters beside a shared projection's output Y:
+ *   out[n] = Y[n] + scale[a] * B[a] (A[a] x[n]),  a the adapter of token n;
+ * a token of no adapter keeps Y[n].
+ *   A [L][r][K], B [L][M][r] of `type` (bf16 or f16), 16-byte aligned; scale
+ *       f32 [L]. K % 32 == 0, r % 8 == 0, r <= Q6_LORA_MAX_RANK.
+ *   X : device [.][ldx] of `xtype` (f32, bf16, f16), 16-byte aligned rows,
+ *       ldx >= K.
+ *   offsets, rows : the grouping of the tokens by adapter (per_row 1, groups
+ *       L, N = items).
+ *   Y, out : device f32, ldy, ldo >= M; out may be Y (in place).
+ *   workspace : device, 16-byte aligned, at least q6_lora_workspace_bytes(). */
+int q6_lora_workspace_bytes(int64_t items, int L, int r, int K, size_t *bytes);
+int q6_lora_add(const void *A, const void *B, const float *scale, int type, int L, int r, int M,
+                int K, const void *X, int xtype, int64_t ldx, const int32_t *offsets,
+                const int32_t *rows, int64_t items, const float *Y, int64_t ldy, float *out,
+                int64_t ldo, void *workspace, size_t workspace_bytes, q6_stream_t s);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,13 +20,13 @@ LIB_PATH = os.path.join(_HERE, "_build", "libq6mmq.so")
 Q6_OK, Q6_EINVAL, Q6_EALIGN, Q6_ESIZE, Q6_EARCH, Q6_ECUDA, Q6_ETIMEOUT = range(7)
 (PATH_NONE, PATH_TC_RAW, PATH_TC_WEXP, PATH_SKINNY, PATH_TC_WH, PATH_SYNC_WEXP,
  PATH_SKINNY_FUSED, PATH_Q4K_TC_RAW, PATH_Q4K_TC_WQ, PATH_TC_FUSED_RAW,
- PATH_TC_FUSED_WH, PATH_Q4K_SKINNY, PATH_Q4K_SKINNY_FUSED) = range(13)
+ PATH_TC_FUSED_WH, PATH_Q4K_SKINNY, PATH_Q4K_SKINNY_FUSED, PATH_EXPERTS_FEW) = range(14)
 PATH_NAMES = {PATH_NONE: "none", PATH_TC_RAW: "tc_raw", PATH_TC_WEXP: "tc_wexp",
               PATH_SKINNY: "skinny", PATH_TC_WH: "tc_wh", PATH_SYNC_WEXP: "sync_wexp",
               PATH_SKINNY_FUSED: "skinny_fused", PATH_Q4K_TC_RAW: "q4k_tc_raw",
               PATH_Q4K_TC_WQ: "q4k_tc_wq", PATH_TC_FUSED_RAW: "tc_fused_raw",
               PATH_TC_FUSED_WH: "tc_fused_wh", PATH_Q4K_SKINNY: "q4k_skinny",
-              PATH_Q4K_SKINNY_FUSED: "q4k_skinny_fused"}
+              PATH_Q4K_SKINNY_FUSED: "q4k_skinny_fused", PATH_EXPERTS_FEW: "experts_few"}
 SKINNY_MAX_N = 16
 SKINNY_GROUPS_MAX_N = 96
 SKINNY_GROUP_N = 32
@@ -39,6 +39,7 @@ FUSED_MAX_N = 2
 # Every function include/q6mmq.h declares: (name, restype, argtypes).
 _P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)
 _IP = ctypes.POINTER(ctypes.c_int)
+_L = ctypes.c_int64
 SIGNATURES = [
     ("q6_last_error", ctypes.c_char_p, []),
     ("q6_device_check", _I, []),
@@ -67,6 +68,17 @@ SIGNATURES = [
     ("q4k_unpack_weights", _I, [_P, _I, _I, _P, _P]),
     ("q4k_mmq", _I, [_P, _P, _I, _I, _P, _P, _P, _P, _I, _P, _I, _P, ctypes.c_size_t, _P, _IP,
                      _P]),
+    ("q6_group_workspace_bytes", _I, [_I, _I, _I, _SZ]),
+    ("q6_group_rows", _I, [_P, _I, _I, _I, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("q6_moe_route", _I, [_P, _I, _I, _I, _L, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("q6_expert_plane_bytes", _I, [_I, _I, _I, _I, _I, _SZ]),
+    ("q6_pack_experts", _I, [_I, _P, _I, _I, _I, _I, _P, _P]),
+    ("q6_experts_mmq", _I, [_I, _P, _I, _I, _I, _I, _P, _I, _L, _L, _I, _P, _P, _L, _P, _L, _IP,
+                            _P]),
+    ("q6_moe_combine", _I, [_P, _I, _L, _P, _P, _I, _I, _I, _P, _L, _P, _L, _P]),
+    ("q6_lora_workspace_bytes", _I, [_L, _I, _I, _I, _SZ]),
+    ("q6_lora_add", _I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _L, _P, _P, _L, _P, _L, _P, _L,
+                         _P, ctypes.c_size_t, _P]),
 ]
 
 
@@ -643,3 +655,9 @@ def q4k_mmq(w: Q4Weights, act: Activations, Y=None, source: str = "auto",
                           _ptr(act.da), _ptr(act.us), N, _ptr(Y), _row_stride(Y), _ptr(ws),
                           ws_bytes, _ptr(P), ctypes.byref(path), _stream(stream)))
     return Y, PATH_NAMES.get(path.value, str(path.value)), P
+
+
+from .moe import (ExpertWeights, Groups, LoraAdapters, Route, alloc_groups,  # noqa: E402,F401
+                  alloc_route, expert_plane_bytes, experts_mmq, group_rows,
+                  group_workspace_bytes, lora_add, lora_workspace_bytes, moe_combine, moe_route,
+                  pack_experts)

@@ -7,6 +7,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "moe_internal.cuh"
 #include "q6_internal.cuh"
 
 namespace {
@@ -73,7 +74,7 @@ int device_state(DevState** out) {
     if ((e = cudaMemset(st.status, 0, 256))) return cuda_fail(e, "cudaMemset(status)");
     if ((e = q6::mmq_tc_prepare()) || (e = q6::mmq_skinny_prepare()) ||
         (e = q6::mmq_sync_prepare()) || (e = q6::q4k_skinny_mma_prepare()) ||
-        (e = q6::q4k_skinny_prepare()))
+        (e = q6::q4k_skinny_prepare()) || (e = q6::experts_few_prepare()))
       return cuda_fail(e, "cudaFuncSetAttribute");
     if (!encoder()) return fail(Q6_ECUDA, "cuTensorMapEncodeTiled entry point not found");
     st.arch_ok = 1;
@@ -187,6 +188,13 @@ int encode_tc_maps_q4k(TcMaps* maps, const uint8_t* q4plane, const void* wq, con
 }  // namespace q6
 
 namespace q6 {
+int require_device(unsigned int** status) {
+  DevState* st;
+  const int rc = device_state(&st);
+  if (!rc && status) *status = st->status;
+  return rc;
+}
+int readable_raw(const uint8_t* raw, const uint8_t** src) { return device_readable(raw, src); }
 // Records `code` and its text as the calling thread's last error (for the
 // entry points defined in other translation units).
 int record_error(int code, const char* fmt, va_list ap) {

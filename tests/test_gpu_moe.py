@@ -1,0 +1,379 @@
+"""Expert routing, grouping, grouped K-quant products, combination and low-rank adapters against
+64-bit references (GPU)."""
+import numpy as np
+import pytest
+
+import q6_int8_mmq_gb300 as q6
+from q6_int8_mmq_gb300 import synth
+
+import moe_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+TYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+@pytest.fixture
+def rng(request):
+    return np.random.default_rng(list(request.node.name.encode()))
+
+
+def cuda(a, type=None):
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t if type is None else t.to(TYPE[type])
+
+
+def f64(t):
+    return t.detach().cpu().to(torch.float64).numpy()
+
+
+def check(got, want, bound):
+    got = f64(got)
+    assert got.shape == want.shape
+    off = np.abs(got - want) > bound
+    assert not off.any(), (f"{off.sum()} of {off.size} values off, first at {np.argwhere(off)[0]}: "
+                           f"{got[off][0]} for {want[off][0]}, bound {bound[off][0]}")
+
+
+def raw_experts(seed, fmt, E, M, K):
+    make = synth.q4k_raw_weights if fmt == "q4_K" else synth.q6k_raw_weights
+    return np.stack([make(seed + e, M, K) for e in range(E)])
+
+
+# ------------------------------------------------------------------- route ---
+
+def logits_with_cases(rng, N, E):
+    x = rng.standard_normal((N, E)).astype(np.float32)
+    x = np.round(x * 4) / 4                                   # many ties, and +0 and -0
+    x[rng.random((N, E)) < 0.2] = -np.inf
+    if N > 4:
+        x[1] = -np.inf                                        # nothing left
+        x[2] = np.finfo(np.float32).min                       # the lowest value is a choice
+        x[3, rng.integers(E)] = np.nan
+        x[4, 0] = np.inf
+    return x
+
+
+@pytest.mark.parametrize("N,E,topk", [(1, 64, 8), (1, 1, 1), (7, 3, 3), (33, 31, 4), (64, 8, 8),
+                                      (65, 256, 8), (300, 100, 5), (1000, 1024, 32), (2049, 128, 6)])
+@pytest.mark.parametrize("type,renorm", [("f32", True), ("bf16", False), ("f16", True)])
+def test_route(rng, N, E, topk, type, renorm):
+    x = cuda(logits_with_cases(rng, N, E), type)
+    r = q6.moe_route(x, topk, renormalize=renorm)
+    ids, weights = ref.route(f64(x), topk, renorm)
+    assert np.array_equal(r.ids.cpu().numpy(), ids)
+    got = f64(r.weights)
+    assert np.array_equal(np.isnan(got), np.isnan(weights))
+    # f32: an exponential (2 ulp), a sum of E terms, a division
+    fine = ~np.isnan(weights)
+    assert np.all(np.abs(got - weights)[fine] <= weights[fine] * (8 + E / 32) * 2.0 ** -23)
+    offsets, rows, pos = ref.group(ids, E)
+    assert np.array_equal(r.groups.offsets.cpu().numpy(), offsets)
+    assert np.array_equal(r.groups.rows.cpu().numpy(), rows)
+    assert np.array_equal(r.groups.pos.cpu().numpy(), pos)
+
+
+def test_route_of_no_tokens():
+    r = q6.moe_route(torch.empty((0, 5), device="cuda"), 2)
+    assert r.groups.offsets.tolist() == [0] * 7
+
+
+def test_route_reads_rows_of_a_wider_tensor(rng):
+    wide = cuda(rng.standard_normal((40, 50)), "f32")
+    r = q6.moe_route(wide[:, 3:23], 4)
+    ids, _ = ref.route(f64(wide[:, 3:23]), 4, True)
+    assert np.array_equal(r.ids.cpu().numpy(), ids)
+
+
+@pytest.mark.parametrize("N,per_row,groups", [(1, 1, 1), (0, 2, 4), (500, 1, 7), (513, 1, 1024),
+                                              (129, 4, 33), (5000, 3, 5)])
+def test_group_rows(rng, N, per_row, groups):
+    ids = rng.integers(-2, groups + 2, (N, per_row)).astype(np.int32)
+    if N == 5000:
+        ids[:] = 3                                            # all in one group
+    g = q6.group_rows(cuda(ids), groups)
+    offsets, rows, pos = ref.group(ids, groups)
+    assert np.array_equal(g.offsets.cpu().numpy(), offsets)
+    assert np.array_equal(g.rows.cpu().numpy(), rows)
+    assert np.array_equal(g.pos.cpu().numpy(), pos)
+
+
+# ----------------------------------------------------------------- experts ---
+
+def run_experts(rng, fmt, type, ids, E, M, K, swiglu, gather, seed=5, pad=0):
+    raw = raw_experts(seed, fmt, E, M, K)
+    rows = ids.shape[0] if gather else ids.size
+    X = cuda(rng.standard_normal((rows, K + pad)), type)[:, :K]
+    w = q6.pack_experts(cuda(raw), fmt, E, M, K, swiglu=swiglu)
+    g = q6.group_rows(cuda(ids.astype(np.int32)), E)
+    Y, path = q6.experts_mmq(w, X, g, gather=gather)
+    q6.sync_status()
+    want, bound = ref.experts(raw, fmt, f64(X), ids, E, swiglu, gather, type)
+    check(Y, want, bound)
+    # random roundings: the whole result is far closer than the bound of each value
+    size = np.linalg.norm(want)
+    assert np.linalg.norm(f64(Y) - want) <= 4 * ref.ROUND[type] * size
+    return path
+
+
+@pytest.mark.parametrize("fmt", ["q4_K", "q6_K"])
+@pytest.mark.parametrize("type", ["bf16", "f16"])
+@pytest.mark.parametrize("N,topk,E,M,K,swiglu,gather", [
+    (1, 1, 1, 1, 256, False, True), (1, 2, 4, 34, 512, True, True), (5, 3, 3, 129, 768, False, False),
+    (40, 2, 6, 130, 1024, True, True), (17, 4, 7, 200, 2560, False, True),
+    (150, 2, 3, 258, 512, True, False), (300, 1, 2, 127, 256, False, True),
+])
+def test_experts(rng, fmt, type, N, topk, E, M, K, swiglu, gather):
+    ids = np.stack([rng.permutation(E)[:topk] for _ in range(N)])
+    run_experts(rng, fmt, type, ids, E, M, K, swiglu, gather)
+
+
+@pytest.mark.parametrize("fmt", ["q4_K", "q6_K"])
+@pytest.mark.parametrize("counts", [[8], [9, 0, 16], [0, 0, 33, 1], [15, 17, 31, 32], [257, 0, 1],
+                                    [64, 65, 255, 256]])
+def test_experts_group_sizes(rng, fmt, counts):
+    ids = np.concatenate([np.full(c, e) for e, c in enumerate(counts)])
+    run_experts(rng, fmt, "bf16", rng.permutation(ids)[:, None], len(counts), 144, 512, False, True)
+
+
+@pytest.mark.parametrize("fmt,K", [("q4_K", 18944), ("q6_K", 11008)])
+def test_experts_long_k(rng, fmt, K):
+    run_experts(rng, fmt, "bf16", rng.integers(0, 2, (21, 1)), 2, 48, K, False, True)
+
+
+@pytest.mark.parametrize("N", [6, 400])
+def test_experts_without_an_expert(rng, N):
+    """Items of no expert get zeros, rows behind them included."""
+    ids = rng.integers(-1, 3, (N, 2))
+    ids[-1] = -1
+    run_experts(rng, "q6_K", "bf16", ids, 3, 72, 512, False, True)
+
+
+@pytest.mark.parametrize("N", [3, 600])
+def test_experts_strided_rows(rng, N):
+    run_experts(rng, "q4_K", "bf16", rng.integers(0, 4, (N, 1)), 4, 64, 512, True, True, pad=24)
+
+
+@pytest.mark.parametrize("N", [4, 500])
+@pytest.mark.parametrize("fmt,type", [("q4_K", "bf16"), ("q6_K", "f16")])
+def test_experts_wide_range(rng, N, fmt, type):
+    """Tokens and rows whose sizes lie far apart keep their own precision."""
+    E, M, K = 2, 96, 512
+    raw = raw_experts(9, fmt, E, M, K)
+    at = 0 if fmt == "q4_K" else 208
+    blocks = raw.reshape(E, M, -1, ref.BLOCK[fmt])
+    d = np.array([2.0 ** (e % 20 - 18) for e in range(M)], np.float16)   # row by row
+    blocks[..., at:at + 2] = d.view(np.uint8).reshape(M, 1, 2)
+    if fmt == "q4_K":
+        blocks[..., 2:4] = (d / 2).view(np.uint8).reshape(M, 1, 2)
+    ids = rng.integers(0, E, (N, 1))
+    sizes = 2.0 ** (rng.integers(-40, 40, (N, 1)) if type == "bf16" else rng.integers(-4, 3, (N, 1)))
+    X = cuda(rng.standard_normal((N, K)) * sizes, type)
+    w = q6.pack_experts(cuda(raw), fmt, E, M, K)
+    Y, _ = q6.experts_mmq(w, X, q6.group_rows(cuda(ids.astype(np.int32)), E))
+    want, bound = ref.experts(raw, fmt, f64(X), ids, E, False, True, type)
+    keep = np.abs(want) < 60000 if type == "f16" else np.full(want.shape, True)
+    check(torch.where(cuda(keep), Y.double(), 0.0), np.where(keep, want, 0), bound)
+
+
+def test_experts_nonfinite_token_stays_alone(rng):
+    """A token with an infinity or a NaN leaves the others as they are."""
+    raw = raw_experts(4, "q4_K", 2, 40, 512)
+    w = q6.pack_experts(cuda(raw), "q4_K", 2, 40, 512)
+    for N in (4, 300):
+        g = q6.group_rows(cuda(np.zeros((N, 1), np.int32)), 2)
+        X = cuda(rng.standard_normal((N, 512)), "bf16")
+        good = q6.experts_mmq(w, X, g)[0].clone()
+        X[1, 7], X[2, 300] = float("inf"), float("nan")
+        Y, _ = q6.experts_mmq(w, X, g)
+        assert not torch.isfinite(Y[1]).any() and torch.isnan(Y[2]).all()
+        rest = [n for n in range(N) if n not in (1, 2)]
+        assert torch.equal(Y[rest], good[rest])
+
+
+def test_experts_many_groups(rng):
+    run_experts(rng, "q4_K", "bf16", rng.integers(0, 700, (50, 2)), 700, 16, 256, False, True)
+
+
+def test_experts_repeats(rng):
+    """The same call gives the same bits."""
+    w = q6.pack_experts(cuda(raw_experts(3, "q6_K", 4, 300, 1024)), "q6_K", 4, 300, 1024)
+    for N in (9, 700):
+        X = cuda(rng.standard_normal((N, 1024)), "bf16")
+        g = q6.group_rows(cuda(rng.integers(0, 4, (N, 1)).astype(np.int32)), 4)
+        a = q6.experts_mmq(w, X, g)[0]
+        for _ in range(3):
+            assert torch.equal(a, q6.experts_mmq(w, X, g)[0])
+
+
+# ------------------------------------------------------------------ combine ---
+
+@pytest.mark.parametrize("N,topk,M", [(1, 1, 1), (3, 8, 64), (33, 2, 2056), (100, 5, 999),
+                                      (257, 32, 40), (20, 9, 1032)])
+@pytest.mark.parametrize("type", ["bf16", "f16"])
+@pytest.mark.parametrize("shared", [False, True])
+def test_combine(rng, N, topk, M, type, shared):
+    items = N * topk
+    Y = cuda(rng.standard_normal((items, M)), type)
+    pos = rng.permutation(items).reshape(N, topk).astype(np.int32)
+    pos[rng.random((N, topk)) < 0.2] = -1
+    weights = cuda(rng.random((N, topk)), "f32")
+    weights[cuda(pos < 0)] = float("nan")                     # not looked at
+    sh = cuda(rng.standard_normal((N, M)), "f32") if shared else None
+    out = q6.moe_combine(Y, cuda(pos), weights, shared=sh)
+    wt, y = np.where(pos < 0, 0, f64(weights)), f64(Y)[np.maximum(pos, 0)]
+    terms = np.where((pos < 0)[..., None], 0, wt[..., None] * y)
+    want, size = terms.sum(1), np.abs(terms).sum(1)
+    if shared:
+        want, size = want + f64(sh), size + np.abs(f64(sh))
+    u = ref.ROUND[type]
+    check(out, want, u * np.abs(want) + (1 + u) * (topk + 2) * 2.0 ** -24 * size + 2.0 ** -25)
+
+
+def test_combine_strided(rng):
+    Y = cuda(rng.standard_normal((6, 80)), "bf16")[:, :72]
+    pos = cuda(np.arange(6, dtype=np.int32).reshape(3, 2))
+    weights = cuda(np.ones((3, 2)), "f32")
+    out = torch.zeros((3, 75), dtype=torch.bfloat16, device="cuda")
+    q6.moe_combine(Y, pos, weights, out=out[:, :72])
+    assert torch.equal(out[:, :72], (Y[0::2].float() + Y[1::2].float()).bfloat16())
+    assert not out[:, 72:].any()
+
+
+# --------------------------------------------------------------------- lora ---
+
+def run_lora(rng, N, L, r, K, M, xtype="f32", type="bf16", ids=None, in_place=False, pad=0):
+    ids = rng.integers(-1, L, N) if ids is None else ids
+    X = cuda(rng.standard_normal((N, K + pad)), xtype)[:, :K]
+    A = cuda(rng.standard_normal((L, r, K)) / np.sqrt(K), type)
+    B = cuda(rng.standard_normal((L, M, r)) / np.sqrt(r), type)
+    scale = cuda(rng.standard_normal(L), "f32")
+    Y = cuda(rng.standard_normal((N, M + pad)), "f32")[:, :M]
+    want, bound = ref.lora(f64(Y), f64(X), f64(A), f64(B), f64(scale), ids)
+    g = q6.group_rows(cuda(ids.astype(np.int32)), L)
+    keep = Y.clone()
+    ad = q6.LoraAdapters(A, B, scale)
+    out = q6.lora_add(ad, X, g, Y, out=None if in_place else torch.empty_like(keep))
+    assert (out is Y) == in_place
+    check(out, want, bound)
+    none = cuda(ids < 0)
+    assert torch.equal(out[none], keep[none])
+
+
+@pytest.mark.parametrize("N,L,r,K,M", [(1, 1, 8, 32, 1), (1, 4, 16, 4096, 512), (2, 3, 24, 96, 33),
+                                       (47, 24, 32, 1024, 200), (100, 2, 64, 512, 130),
+                                       (333, 5, 128, 1056, 97), (70, 70, 8, 256, 1001),
+                                       (40, 1, 256, 288, 64), (65, 1, 72, 64, 300)])
+@pytest.mark.parametrize("xtype,type", [("f32", "bf16"), ("f32", "f16"), ("bf16", "bf16"),
+                                        ("f16", "bf16")])
+def test_lora(rng, N, L, r, K, M, xtype, type):
+    run_lora(rng, N, L, r, K, M, xtype, type)
+
+
+@pytest.mark.parametrize("counts", [[16], [17, 0, 1], [0, 32, 33], [15, 16, 31, 100]])
+def test_lora_group_sizes(rng, counts):
+    ids = rng.permutation(np.concatenate([np.full(c, a) for a, c in enumerate(counts)]))
+    run_lora(rng, len(ids), len(counts), 16, 256, 96, ids=ids)
+
+
+def test_lora_in_place_and_strided(rng):
+    run_lora(rng, 37, 3, 16, 512, 100, in_place=True)
+    run_lora(rng, 37, 3, 16, 512, 100, pad=8)
+    run_lora(rng, 120, 3, 16, 512, 101, in_place=True, pad=8)
+
+
+def test_lora_no_token_has_one(rng):
+    run_lora(rng, 9, 2, 8, 64, 40, ids=np.full(9, -1))
+
+
+def test_lora_without_tokens():
+    ad = q6.LoraAdapters(torch.zeros((2, 8, 64), device="cuda", dtype=torch.float16),
+                         torch.zeros((2, 16, 8), device="cuda", dtype=torch.float16),
+                         torch.ones(2, device="cuda"))
+    g = q6.group_rows(torch.empty((0,), dtype=torch.int32, device="cuda"), 2)
+    out = q6.lora_add(ad, torch.empty((0, 64), device="cuda"), g, torch.empty((0, 16), device="cuda"))
+    assert out.shape == (0, 16)
+
+
+# --------------------------------------------------- streams, graphs, errors ---
+
+def moe_step(w_up, w_down, logits, X, topk):
+    r = q6.moe_route(logits, topk)
+    h, _ = q6.experts_mmq(w_up, X, r.groups)
+    y, _ = q6.experts_mmq(w_down, h, r.groups, gather=False)
+    return q6.moe_combine(y, r.groups.pos, r.weights)
+
+
+@pytest.mark.parametrize("N", [3, 200])
+def test_moe_step_on_a_side_stream_and_in_a_graph(rng, N):
+    E, H, D, topk = 6, 64, 512, 2
+    w_up = q6.pack_experts(cuda(raw_experts(1, "q4_K", E, 2 * 256, D)), "q4_K", E, 2 * 256, D,
+                           swiglu=True)
+    w_down = q6.pack_experts(cuda(raw_experts(2, "q6_K", E, D, 256)), "q6_K", E, D, 256)
+    X = cuda(rng.standard_normal((N, D)) / 64, "bf16")
+    logits = cuda(rng.standard_normal((N, E)), "f32")
+    want = moe_step(w_up, w_down, logits, X, topk)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = moe_step(w_up, w_down, logits, X, topk)
+    side.synchronize()
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    x2, l2 = torch.zeros_like(X), torch.zeros_like(logits)
+    with torch.cuda.graph(graph):
+        out = moe_step(w_up, w_down, l2, x2, topk)
+    x2.copy_(X)
+    l2.copy_(logits)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_stream_argument(rng):
+    """The stream argument, scratch memory included."""
+    side = torch.cuda.Stream()
+    ids = cuda(rng.integers(0, 3, 50).astype(np.int32))
+    A = cuda(rng.standard_normal((3, 16, 256)), "f16")
+    B = cuda(rng.standard_normal((3, 64, 16)), "f16")
+    ad = q6.LoraAdapters(A, B, torch.ones(3, device="cuda"))
+    X, Y = cuda(rng.standard_normal((50, 256)), "f32"), cuda(rng.standard_normal((50, 64)), "f32")
+    want = q6.lora_add(ad, X, q6.group_rows(ids, 3), Y, out=torch.empty_like(Y))
+    torch.cuda.synchronize()
+    g = q6.group_rows(ids, 3, stream=side)
+    got = q6.lora_add(ad, X, g, Y, out=torch.empty_like(Y), stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_refusals(rng):
+    X = cuda(rng.standard_normal((4, 512)), "bf16")
+    w = q6.pack_experts(cuda(raw_experts(1, "q4_K", 2, 32, 512)), "q4_K", 2, 32, 512)
+    g = q6.group_rows(cuda(np.zeros((4, 2), np.int32)), 2)
+    bad = [lambda: q6.experts_mmq(w, X.float(), g), lambda: q6.experts_mmq(w, X[:, :256], g),
+           lambda: q6.experts_mmq(w, X[:3], g), lambda: q6.experts_mmq(w, X, g, gather=False),
+           lambda: q6.experts_mmq(w, X.cpu(), g),
+           lambda: q6.experts_mmq(w, X, q6.group_rows(cuda(np.zeros((4, 2), np.int32)), 3)),
+           lambda: q6.experts_mmq(w, X, g, out=torch.empty((8, 31), dtype=torch.bfloat16, device="cuda")),
+           lambda: q6.experts_mmq(w, torch.zeros(4 * 513 + 1, dtype=torch.bfloat16,
+                                                 device="cuda")[1:].view(4, 513)[:, :512], g),
+           lambda: q6.moe_route(X.double(), 2), lambda: q6.moe_route(X, 33),
+           lambda: q6.moe_route(X[:, :4], 5), lambda: q6.moe_route(X.t(), 2),
+           lambda: q6.moe_route(X, 2, out=q6.alloc_route(4, 512, 3)),
+           lambda: q6.group_rows(g.pos.long(), 2), lambda: q6.group_rows(g.pos, 1025),
+           lambda: q6.pack_experts(torch.zeros(100, dtype=torch.uint8, device="cuda"), "q4_K", 1, 1, 256),
+           lambda: q6.moe_combine(X, g.pos, torch.ones((4, 1), device="cuda")),
+           lambda: q6.LoraAdapters(X.view(1, 4, 512), X.view(1, 512, 4), torch.ones(1, device="cuda")),
+           lambda: q6.LoraAdapters(X.view(1, 4, 512).half(), X.view(1, 512, 4), torch.ones(1, device="cuda"))]
+    for i, call in enumerate(bad):
+        with pytest.raises(q6.Q6Error):
+            call()
+            pytest.fail(f"call {i} was accepted")
