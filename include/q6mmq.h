@@ -505,6 +505,7 @@ int q4k_mmq(const void *plane, const uint16_t *wq, int M, int K, const int8_t *X
 #define Q6_LORA_MAX_RANK 256
 
 #define Q6_PATH_EXPERTS_FEW 13 /* grouped product, warp-level MMAs, weights streamed per token tile */
+#define Q6_PATH_EXPERTS_TC 14  /* grouped product on the tensor cores, weights dequantised per tile */
 
 /* A grouping sorts N * per_row items by group, in item order within one; item
  * i = n * per_row + j is slot j of token n. All device, int32, caller-owned:

@@ -20,13 +20,15 @@ LIB_PATH = os.path.join(_HERE, "_build", "libq6mmq.so")
 Q6_OK, Q6_EINVAL, Q6_EALIGN, Q6_ESIZE, Q6_EARCH, Q6_ECUDA, Q6_ETIMEOUT = range(7)
 (PATH_NONE, PATH_TC_RAW, PATH_TC_WEXP, PATH_SKINNY, PATH_TC_WH, PATH_SYNC_WEXP,
  PATH_SKINNY_FUSED, PATH_Q4K_TC_RAW, PATH_Q4K_TC_WQ, PATH_TC_FUSED_RAW,
- PATH_TC_FUSED_WH, PATH_Q4K_SKINNY, PATH_Q4K_SKINNY_FUSED, PATH_EXPERTS_FEW) = range(14)
+ PATH_TC_FUSED_WH, PATH_Q4K_SKINNY, PATH_Q4K_SKINNY_FUSED, PATH_EXPERTS_FEW,
+ PATH_EXPERTS_TC) = range(15)
 PATH_NAMES = {PATH_NONE: "none", PATH_TC_RAW: "tc_raw", PATH_TC_WEXP: "tc_wexp",
               PATH_SKINNY: "skinny", PATH_TC_WH: "tc_wh", PATH_SYNC_WEXP: "sync_wexp",
               PATH_SKINNY_FUSED: "skinny_fused", PATH_Q4K_TC_RAW: "q4k_tc_raw",
               PATH_Q4K_TC_WQ: "q4k_tc_wq", PATH_TC_FUSED_RAW: "tc_fused_raw",
               PATH_TC_FUSED_WH: "tc_fused_wh", PATH_Q4K_SKINNY: "q4k_skinny",
-              PATH_Q4K_SKINNY_FUSED: "q4k_skinny_fused", PATH_EXPERTS_FEW: "experts_few"}
+              PATH_Q4K_SKINNY_FUSED: "q4k_skinny_fused", PATH_EXPERTS_FEW: "experts_few",
+              PATH_EXPERTS_TC: "experts_tc"}
 SKINNY_MAX_N = 16
 SKINNY_GROUPS_MAX_N = 96
 SKINNY_GROUP_N = 32

@@ -14,7 +14,7 @@ LIB = os.path.join(BUILD, "libq6mmq.so")
 SOURCES = ["api.cu", "quantize.cu", "pack.cu", "expand.cu", "mmq_skinny.cu", "mmq_skinny_mma.cu",
            "mmq_tc.cu", "mmq_sync.cu", "diag.cu", "noalloc.cu", "q4k.cu", "q4k_skinny.cu",
            "q4k_skinny_mma.cu", "moe_api.cu", "moe_route.cu", "moe_combine.cu", "experts_pack.cu",
-           "experts_few.cu", "lora.cu"]
+           "experts_few.cu", "experts_tc.cu", "lora.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr"]
 

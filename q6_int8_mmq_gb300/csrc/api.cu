@@ -74,7 +74,8 @@ int device_state(DevState** out) {
     if ((e = cudaMemset(st.status, 0, 256))) return cuda_fail(e, "cudaMemset(status)");
     if ((e = q6::mmq_tc_prepare()) || (e = q6::mmq_skinny_prepare()) ||
         (e = q6::mmq_sync_prepare()) || (e = q6::q4k_skinny_mma_prepare()) ||
-        (e = q6::q4k_skinny_prepare()) || (e = q6::experts_few_prepare()))
+        (e = q6::q4k_skinny_prepare()) || (e = q6::experts_few_prepare()) ||
+        (e = q6::experts_tc_prepare()))
       return cuda_fail(e, "cudaFuncSetAttribute");
     if (!encoder()) return fail(Q6_ECUDA, "cuTensorMapEncodeTiled entry point not found");
     st.arch_ok = 1;
@@ -195,6 +196,14 @@ int require_device(unsigned int** status) {
   return rc;
 }
 int readable_raw(const uint8_t* raw, const uint8_t** src) { return device_readable(raw, src); }
+int encode_gather_map(CUtensorMap* map, int type, const void* X, long long nx, int K,
+                      long long ldx) {
+  return encode_2d(map,
+                   type == Q6_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                   X, (uint64_t)K, (uint64_t)nx, (uint64_t)ldx * 2, 64, 1,
+                   CU_TENSOR_MAP_SWIZZLE_128B, "X");
+}
 // Records `code` and its text as the calling thread's last error (for the
 // entry points defined in other translation units).
 int record_error(int code, const char* fmt, va_list ap) {

@@ -1,0 +1,591 @@
+// Grouped K-quant expert products on the 5th-generation tensor cores, for
+// experts with many tokens.
+//
+//   Y[i][m] = sum_k W[e(i)][m][k] x[t(i)][k]
+//
+// A tile is 128 plane rows of one expert (MMA M, TMEM lanes) by up to 256 of
+// its items (MMA N). The weights are dequantised inside the kernel, once per
+// tile: thread = weight row, f32 arithmetic (w = d * sc * q - dmin * m times a
+// power of two of the row), one rounding to the activations' 16-bit type, the
+// result stored straight into TMEM, where the MMA takes its A operand from.
+// Packed weights are all that memory and shared memory ever see. x rows are
+// gathered by TMA from the caller's tensor (no sorted copy), 4 rows a
+// request, into 128-byte-swizzled K-major tiles.
+//
+// Tiles with few items have short MMAs; the loads' depth in K grows instead:
+// an x stage holds 64, 128 or 256 of K for up to 256, 128 or 64 items.
+//
+// Warp roles (16 warps, persistent CTA, one per SM):
+//   0      gathers x (every lane issues requests)
+//   1      issues the MMAs
+//   2      TMEM allocation
+//   3      streams the packed weights, one super-block a stage
+//   4-11   dequantise: warps 4-7 the even, 8-11 the odd halves (128 of K) of
+//          the super-blocks
+//   12-15  epilogue
+// TMEM: columns 0-255 two accumulators of 128 items (or one of 256), 256-511
+// four A slots of 128 of K.
+// Every wait is bounded (see q6_internal.cuh).
+#include "moe_internal.cuh"
+
+namespace q6 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kTileN = 256;
+constexpr int kXStages = 4, kXStage = 32 * 1024;
+constexpr int kWStages = 3;
+constexpr int kASlots = 4, kACols = 64, kACol0 = 256;
+constexpr int kTmemCols = 512;
+
+enum : uint32_t { kSiteXEmpty = 32, kSiteXFull, kSiteWEmpty, kSiteWFull, kSiteAEmpty, kSiteAFull,
+                  kSiteDEmpty, kSiteDFull, kSiteDrain };
+
+struct Bars {
+  uint64_t x_full[kXStages], x_empty[kXStages];
+  uint64_t w_full[kWStages], w_empty[kWStages];
+  uint64_t a_full[kASlots], a_empty[kASlots];
+  uint64_t d_full[2], d_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+struct Args {
+  const uint8_t* plane;
+  const float* scale;  // 2^e per plane row
+  int gather;
+  const int32_t* offsets;
+  const int32_t* rows;
+  void* Y;
+  long long ldy;
+  int E, bands, sbs, out, vec;
+};
+
+template <int kFmt>
+constexpr int kWTile = kFmt == Q6_FMT_Q4K ? kQ4Tile : kQ6Tile;
+template <int kFmt>
+constexpr int kSmemBytes = 1024 + kXStages * kXStage + kWStages * kWTile<kFmt> +
+                           (kMaxGroups + 1) * 4 + 12 + (int)sizeof(Bars);
+
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                            const int (&r)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(r[0]), "r"(r[1]),
+      "r"(r[2]), "r"(r[3])
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T, kind::f16.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 bd;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 bd, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kSw128DescHi)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld1(uint32_t (&a)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]), "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]), "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]), "+r"(a[22]), "+r"(a[23]), "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27]), "+r"(a[28]), "+r"(a[29]), "+r"(a[30]), "+r"(a[31])
+               :
+               : "memory");
+}
+
+// Instruction descriptor: f16 or bf16 operands, f32 accumulation, M = 128.
+template <typename T>
+__device__ __forceinline__ uint32_t idesc_of(int n) {
+  const uint32_t type = sizeof(T) == 2 && __is_same(T, __nv_bfloat16) ? 1u : 0u;
+  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+
+// ------------------------------------------------------------ dequantising ---
+// q + offset as a float from a code in bits p.. of x: the exponent of
+// 2^(23 - p) makes the code's lowest bit a 1.
+__device__ __forceinline__ float code_f32(uint32_t x, uint32_t mask, uint32_t magic) {
+  return __uint_as_float((x & mask) | magic);
+}
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t round2(uint64_t v) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+  return pack2<T>(a, b);
+}
+__device__ __forceinline__ uint32_t word4(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ float byte_f32(uint32_t w, int i) {
+  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | i)) - 8388608.0f;
+}
+
+// One row's half (128 of K) of a super-block.
+template <int kFmt>
+struct Half;
+template <>
+struct Half<Q6_FMT_Q4K> {
+  uint4 q[4];
+  uint32_t sc, mn;
+  float d, dm;
+  __device__ __forceinline__ void load(const uint8_t* tile, int row, int h, float inv) {
+    const uint4* p = reinterpret_cast<const uint4*>(tile) + row;
+    const uint4 head = p[0];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) q[t] = p[(1 + 2 * t + h) * kBand];
+    const float2 dd = unpack2<__half>(head.x);
+    d = dd.x * inv, dm = dd.y * inv;
+    sc = h ? (head.w & 0x0F0F0F0Fu) | ((head.y >> 2) & 0x30303030u) : head.y & 0x3F3F3F3Fu;
+    mn = h ? ((head.w >> 4) & 0x0F0F0F0Fu) | ((head.z >> 2) & 0x30303030u) : head.z & 0x3F3F3F3Fu;
+  }
+  // 64 of K (chunks 2 * part and 2 * part + 1 of the half) as 32 words. A code
+  // at bit p becomes 2^(23-p) + q; the offset goes with the min (its rounding
+  // is at most 2^-12 of the scale).
+  template <typename T>
+  __device__ __forceinline__ void expand(int part, uint32_t (&out)[32]) const {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int cc = 2 * part + c;
+      const float s = d * byte_f32(sc, cc), m = -dm * byte_f32(mn, cc);
+      const float c11 = fmaf(-4096.0f, s, m), c15 = fmaf(-256.0f, s, m), c19 = fmaf(-16.0f, s, m),
+                  c12 = fmaf(-2048.0f, s, m);
+      const uint64_t ss = f2(s, s), k11 = f2(c11, c11), k15 = f2(c15, c15), k19 = f2(c19, c19),
+                     k12 = f2(c12, c12);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t w = word4(q[t], cc), a = w << 11, b = w >> 5, e = w >> 16;
+        uint32_t* o = out + 16 * c + 4 * t;
+        o[0] = round2<T>(fma_f2(f2(code_f32(a, 0x7800u, 0x45800000u), code_f32(b, 0x7800u, 0x45800000u)), ss, k11));
+        o[1] = round2<T>(fma_f2(f2(code_f32(a, 0x78000u, 0x43800000u), code_f32(b, 0x78000u, 0x43800000u)), ss, k15));
+        o[2] = round2<T>(fma_f2(f2(code_f32(a, 0x780000u, 0x41800000u), code_f32(b, 0x780000u, 0x41800000u)), ss, k19));
+        o[3] = round2<T>(fma_f2(f2(code_f32(w, 0xF000u, 0x45000000u), code_f32(e, 0xF000u, 0x45000000u)), ss, k12));
+      }
+    }
+  }
+};
+template <>
+struct Half<Q6_FMT_Q6K> {
+  uint4 q[4];
+  uint2 high[4];
+  uint32_t sc[2];
+  float d;
+  __device__ __forceinline__ void load(const uint8_t* tile, int row, int h, float inv) {
+    const uint4* p = reinterpret_cast<const uint4*>(tile) + row;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      q[t] = p[(2 * t + h) * kBand];
+      high[t] = reinterpret_cast<const uint2*>(p + (8 + t) * kBand)[h];
+    }
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(p + 12 * kBand);
+    sc[0] = s[h], sc[1] = s[2 + h];
+    d = __half2float(reinterpret_cast<const __half*>(tile + 13 * 2048)[row]) * inv;
+  }
+  template <typename T>
+  __device__ __forceinline__ void expand(int part, uint32_t (&out)[32]) const {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int cc = 2 * part + c;
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {  // runs 0, 1 and 2, 3 of the chunk
+        const float s = d * (byte_f32(sc[sub], cc) - 128.0f);
+        // codes at bits 12 and 16: 2048 + q and 128 + q, and q - 32
+        const uint64_t ss = f2(s, s), k = f2(-2080.0f * s, -160.0f * s);
+#pragma unroll
+        for (int t = 2 * sub; t < 2 * sub + 2; ++t) {
+          const uint32_t w = word4(q[t], cc), hw = cc < 2 ? high[t].x : high[t].y;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const int at = 2 * ((cc % 2) * 4 + m);
+            const uint32_t hi = at < 4 ? hw << (4 - at) : hw >> (at - 4);
+            const uint32_t v = ((w >> (4 * m)) & 0x000F000Fu) | (hi & 0x00300030u);
+            out[16 * c + 4 * t + m] =
+                round2<T>(fma_f2(f2(code_f32(v << 12, 0x3F000u, 0x45000000u),
+                                    code_f32(v, 0x3F0000u, 0x43000000u)), ss, k));
+          }
+        }
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------- schedule ---
+struct Tile {
+  int expert, band, n;  // n: MMA N, a multiple of 16
+  long long first;      // first item
+  int count;            // items
+};
+__device__ __forceinline__ int tiles_of(int count) { return (count + kTileN - 1) / kTileN; }
+
+// Tile t of the list ordered by (expert, item tile, band); start[e] is the
+// number of (expert, item tile) pairs before expert e.
+__device__ __forceinline__ Tile tile_at(const Args& a, const int* start, int t) {
+  const int pair = t / a.bands;
+  int lo = 0, hi = a.E;  // start[lo] <= pair < start[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (start[mid] <= pair) lo = mid;
+    else hi = mid;
+  }
+  Tile r;
+  r.expert = lo, r.band = t % a.bands;
+  const int begin = a.offsets[lo], count = a.offsets[lo + 1] - begin;
+  const int parts = tiles_of(count), j = pair - start[lo];
+  // equal parts, in steps of 16
+  r.n = ((count + parts - 1) / parts + 15) / 16 * 16;
+  r.first = (long long)begin + (long long)j * r.n;
+  r.count = min(r.n, count - j * r.n);
+  return r;
+}
+// 64-of-K blocks an x stage holds.
+__device__ __forceinline__ int blocks_per_stage(int n) { return n > 128 ? 1 : n > 64 ? 2 : 4; }
+
+template <typename T, int kFmt, bool kGlu>
+__global__ void __launch_bounds__(kThreads, 1)
+experts_tc_kernel(const __grid_constant__ CUtensorMap tmX, const Args a, unsigned int* status) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* xring = smem;
+  uint8_t* wring = smem + kXStages * kXStage;
+  int* start = reinterpret_cast<int*>(wring + kWStages * kWTile<kFmt>);
+  Bars* bars = reinterpret_cast<Bars*>(
+      (reinterpret_cast<uintptr_t>(start + kMaxGroups + 1) + 7) & ~static_cast<uintptr_t>(7));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bars->abort;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kXStages; ++i) {
+      mbar_init(&bars->x_full[i], 1);
+      mbar_init(&bars->x_empty[i], 1);
+    }
+    for (int i = 0; i < kWStages; ++i) {
+      mbar_init(&bars->w_full[i], 1);
+      mbar_init(&bars->w_empty[i], 8);
+    }
+    for (int i = 0; i < kASlots; ++i) {
+      mbar_init(&bars->a_full[i], 4);
+      mbar_init(&bars->a_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->d_full[i], 1);
+      mbar_init(&bars->d_empty[i], 4);
+    }
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&tmX);
+  }
+  if (warp == 2) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  if (warp == 3) {  // start[]: the running number of (expert, item tile) pairs
+    int run = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int v = e < a.E ? tiles_of(a.offsets[e + 1] - a.offsets[e]) : 0;
+      int x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (e < a.E) start[e] = run + x - v;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) start[a.E] = run;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const int total = start[a.E] * a.bands;
+  bool ok = true;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- gather x --
+    int g = 0;  // stages issued
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const Tile w = tile_at(a, start, t);
+      int r[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // slots past the items repeat the first one
+          const int n = 4 * (lane + 32 * i) + j;
+          const long long item = w.first + (n < w.count ? n : 0);
+          r[i][j] = a.gather ? a.rows[item] : (int)item;
+        }
+      const int kb = blocks_per_stage(w.n);
+      for (int k = 0; k < 4 * a.sbs; k += kb) {
+        const int slot = g % kXStages;
+        if (!(ok = mbar_wait_warp(&bars->x_empty[slot], ((g / kXStages) & 1) ^ 1, abort_flag, status,
+                                  kSiteXEmpty)))
+          break;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->x_full[slot], (uint32_t)(kb * w.n * 128));
+        __syncwarp();
+        for (int b = 0; b < kb; ++b) {
+          uint8_t* dst = xring + slot * kXStage + b * w.n * 128 + lane * 512;
+          if (4 * lane < w.n) tma_gather4(dst, &tmX, &bars->x_full[slot], (k + b) * 64, r[0]);
+          if (4 * lane + 128 < w.n)
+            tma_gather4(dst + 32 * 512, &tmX, &bars->x_full[slot], (k + b) * 64, r[1]);
+        }
+        ++g;
+      }
+    }
+    if (!ok && lane == 0) {  // copies in flight land before the CTA exits
+      volatile int no_abort = 0;
+      for (int k = g > kXStages ? g - kXStages : 0; k < g; ++k)
+        mbar_wait_bounded(&bars->x_full[k % kXStages], (k / kXStages) & 1, &no_abort, status,
+                          kSiteXFull);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------- packed weights --
+    if (lane == 0) {
+      int g = 0;
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const Tile w = tile_at(a, start, t);
+        const uint8_t* src =
+            a.plane + ((size_t)w.expert * a.bands + w.band) * (size_t)a.sbs * kWTile<kFmt>;
+        for (int sb = 0; sb < a.sbs; ++sb) {
+          const int slot = g % kWStages;
+          if (!(ok = mbar_wait_bounded(&bars->w_empty[slot], ((g / kWStages) & 1) ^ 1, abort_flag,
+                                       status, kSiteWEmpty)))
+            break;
+          mbar_arrive_expect_tx(&bars->w_full[slot], kWTile<kFmt>);
+          bulk_load(wring + slot * kWTile<kFmt>, src + (size_t)sb * kWTile<kFmt>, kWTile<kFmt>,
+                    &bars->w_full[slot]);
+          ++g;
+        }
+      }
+      if (!ok) {
+        volatile int no_abort = 0;
+        for (int k = g > kWStages ? g - kWStages : 0; k < g; ++k)
+          mbar_wait_bounded(&bars->w_full[k % kWStages], (k / kWStages) & 1, &no_abort, status,
+                            kSiteWFull);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA --
+    if (lane == 0) {
+      int gx = 0, ga = 0, next = 0, uses[2] = {0, 0};
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const Tile w = tile_at(a, start, t);
+        const int kb = blocks_per_stage(w.n);
+        const uint32_t idesc = idesc_of<T>(w.n);
+        const bool both = w.n > 128;
+        const int d0 = both ? 0 : next;
+        for (int d = d0; d <= (both ? 1 : d0) && ok; ++d)
+          ok = mbar_wait_bounded(&bars->d_empty[d], (uses[d] & 1) ^ 1, abort_flag, status,
+                                 kSiteDEmpty);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem + (uint32_t)(d0 * 128);
+        for (int k = 0; k < 4 * a.sbs; ++k) {
+          const int xs = gx % kXStages, as = ga % kASlots;
+          if (k % kb == 0 && !(ok = mbar_wait_bounded(&bars->x_full[xs], (gx / kXStages) & 1,
+                                                      abort_flag, status, kSiteXFull)))
+            break;
+          if (k % 2 == 0) {
+            if (!(ok = mbar_wait_bounded(&bars->a_full[as], (ga / kASlots) & 1, abort_flag, status,
+                                         kSiteAFull)))
+              break;
+            tc_fence_after();
+          }
+          const uint32_t b = sw128_desc_lo(smem_u32(xring + xs * kXStage + (k % kb) * w.n * 128));
+          const uint32_t at = tmem + (uint32_t)(kACol0 + as * kACols + (k % 2) * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            umma_f16_ts(d_tmem, at + 8 * i, b + 2 * i, idesc, (uint32_t)(k > 0 || i > 0));
+          if (k % kb == kb - 1) {
+            umma_commit(&bars->x_empty[xs]);
+            ++gx;
+          }
+          if (k % 2) {
+            umma_commit(&bars->a_empty[as]);
+            ++ga;
+          }
+        }
+        if (!ok) break;
+        for (int d = d0; d <= (both ? 1 : d0); ++d) {
+          umma_commit(&bars->d_full[d]);
+          ++uses[d];
+        }
+        next = both ? 0 : next ^ 1;
+      }
+      umma_commit(&bars->drain);
+      volatile int no_abort = 0;
+      mbar_wait_bounded(&bars->drain, 0, &no_abort, status, kSiteDrain);
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // ----------------------------------------------------------- dequantise --
+    const int h = (warp - 4) / 4, row = 32 * (warp % 4) + lane;
+    const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
+    int gw = 0;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const Tile w = tile_at(a, start, t);
+      const float inv = 1.0f / a.scale[((size_t)w.expert * a.bands + w.band) * kBand + row];
+      for (int sb = 0; sb < a.sbs; ++sb, ++gw) {
+        const int ws = gw % kWStages, ga = 2 * gw + h, as = ga % kASlots;
+        if (!(ok = mbar_wait_warp(&bars->w_full[ws], (gw / kWStages) & 1, abort_flag, status,
+                                  kSiteWFull)))
+          break;
+        Half<kFmt> half;
+        half.load(wring + ws * kWTile<kFmt>, row, h, inv);
+        if (!(ok = mbar_wait_warp(&bars->a_empty[as], ((ga / kASlots) & 1) ^ 1, abort_flag, status,
+                                  kSiteAEmpty)))
+          break;
+        tc_fence_after();
+        const uint32_t dst = tmem + lanes + (uint32_t)(kACol0 + as * kACols);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          uint32_t v[32];
+          half.template expand<T>(part, v);
+          tmem_st32(dst + 32 * part, v);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->w_empty[ws]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->a_full[as]);
+      }
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------- epilogue --
+    const int q = warp % 4;
+    T* Y = static_cast<T*>(a.Y);
+    // items of no expert: zeros
+    for (long long i = a.offsets[a.E] + (long long)blockIdx.x; i < a.offsets[a.E + 1];
+         i += gridDim.x)
+      for (int m = 32 * q + lane; m < a.out; m += 128) Y[i * a.ldy + m] = from_f32<T>(0.0f);
+    int next = 0, uses[2] = {0, 0};
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const Tile w = tile_at(a, start, t);
+      const float scale =
+          a.scale[((size_t)w.expert * a.bands + w.band) * kBand + 32 * q + lane];
+      const bool both = w.n > 128;
+      const int d0 = both ? 0 : next;
+      const int m = kGlu ? w.band * 64 + 16 * q + (lane >> 4) * 8 + (lane & 7)
+                         : w.band * 128 + 32 * q + lane;
+      const bool mine = m < a.out && (!kGlu || (lane & 8) == 0);
+      for (int d = d0; d <= (both ? 1 : d0); ++d) {
+        if (!(ok = mbar_wait_warp(&bars->d_full[d], uses[d] & 1, abort_flag, status, kSiteDFull)))
+          break;
+        ++uses[d];
+        tc_fence_after();
+        const int c1 = both ? (d ? w.n : 128) : w.n;
+        for (int c0 = both ? 128 * d : 0; c0 < c1; c0 += 32) {
+          uint32_t v[32];
+          tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(both ? c0 : 128 * d0 + c0), v);
+          tmem_wait_ld1(v);
+          T* y = Y + (w.first + c0) * a.ldy + m;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float f = __uint_as_float(v[j]) * scale;
+            if (kGlu) {
+              const float up = __shfl_down_sync(0xffffffffu, f, 8);
+              f = f / (1.0f + __expf(-f)) * up;
+            }
+            if (mine && c0 + j < w.count) y[(long long)j * a.ldy] = from_f32<T>(f);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->d_empty[d]);
+      }
+      next = both ? 0 : next ^ 1;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+typedef void (*Kernel)(const CUtensorMap, const Args, unsigned int*);
+template <typename T>
+Kernel pick_t(int fmt, int swiglu) {
+  if (fmt == Q6_FMT_Q4K)
+    return swiglu ? experts_tc_kernel<T, Q6_FMT_Q4K, true> : experts_tc_kernel<T, Q6_FMT_Q4K, false>;
+  return swiglu ? experts_tc_kernel<T, Q6_FMT_Q6K, true> : experts_tc_kernel<T, Q6_FMT_Q6K, false>;
+}
+Kernel pick(int type, int fmt, int swiglu) {
+  return type == Q6_TYPE_BF16 ? pick_t<__nv_bfloat16>(fmt, swiglu) : pick_t<__half>(fmt, swiglu);
+}
+int smem_bytes(int fmt) {
+  return fmt == Q6_FMT_Q4K ? kSmemBytes<Q6_FMT_Q4K> : kSmemBytes<Q6_FMT_Q6K>;
+}
+static_assert(kSmemBytes<Q6_FMT_Q6K> <= 227 * 1024, "shared memory");
+
+}  // namespace
+
+cudaError_t experts_tc_prepare() {
+  for (int type : {Q6_TYPE_BF16, Q6_TYPE_F16})
+    for (int fmt : {Q6_FMT_Q4K, Q6_FMT_Q6K})
+      for (int glu : {0, 1}) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            pick(type, fmt, glu), cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(fmt));
+        if (e != cudaSuccess) return e;
+      }
+  return cudaSuccess;
+}
+
+cudaError_t launch_experts_tc(const ExpertCall& c, const CUtensorMap& x, int sms,
+                              unsigned int* status, cudaStream_t s) {
+  Args a;
+  a.plane = c.plane;
+  a.scale = reinterpret_cast<const float*>(c.plane + c.g.scale_off);
+  a.gather = c.gather;
+  a.offsets = c.offsets, a.rows = c.rows;
+  a.Y = c.Y, a.ldy = c.ldy;
+  a.E = c.E, a.bands = c.g.bands, a.sbs = c.g.sbs, a.out = c.g.out;
+  a.vec = 0;
+  // at most this many tiles
+  const long long tiles =
+      (c.items / kTileN + (c.items < c.E ? c.items : c.E)) * (long long)c.g.bands;
+  const unsigned grid = (unsigned)(tiles < sms ? (tiles > 0 ? tiles : 1) : sms);
+  return launch_pdl(pick(c.type, c.fmt, c.swiglu), dim3(grid), dim3(kThreads),
+                    (size_t)smem_bytes(c.fmt), s, x, a, status);
+}
+
+}  // namespace q6

@@ -57,6 +57,9 @@ int check_experts(int fmt, int E, int M, int K, int swiglu) {
   return Q6_OK;
 }
 
+// Items an expert, on average, up to which the few-token kernel runs.
+constexpr int kFewItems = 12;
+
 bool half_type(int type) { return type == Q6_TYPE_BF16 || type == Q6_TYPE_F16; }
 bool any_type(int type) { return half_type(type) || type == Q6_TYPE_F32; }
 
@@ -148,12 +151,23 @@ int q6_experts_mmq(int fmt, const void* plane, int E, int M, int K, int swiglu, 
   if (!aligned(plane, 256) || !aligned(X, 16) || ldx % 8 || !aligned(Y, 2) || !aligned(offsets, 4) ||
       !aligned(rows, 4))
     return fail(Q6_EALIGN, "plane must be 256-byte, X and its rows 16-byte aligned");
-  if ((rc = q6::require_device(nullptr))) return rc;
+  unsigned int* status;
+  if ((rc = q6::require_device(&status))) return rc;
   c.fmt = fmt, c.swiglu = swiglu, c.E = E;
   c.plane = static_cast<const uint8_t*>(plane);
   c.X = X, c.type = type, c.ldx = ldx, c.nx = nx, c.gather = gather;
   c.offsets = offsets, c.rows = rows, c.items = items;
   c.Y = Y, c.ldy = ldy;
+  if (items > kFewItems * (int64_t)E) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return fail(Q6_ECUDA, "SM count: %s", cudaGetErrorString(e));
+    CUtensorMap map;
+    if ((rc = q6::encode_gather_map(&map, type, X, nx, K, ldx))) return rc;
+    if (path_out) *path_out = Q6_PATH_EXPERTS_TC;
+    return launched(q6::launch_experts_tc(c, map, sms, status, (cudaStream_t)s), "grouped product");
+  }
   if (path_out) *path_out = Q6_PATH_EXPERTS_FEW;
   return launched(q6::launch_experts_few(c, (cudaStream_t)s), "grouped product");
 }

@@ -148,6 +148,13 @@ struct ExpertCall {
 };
 cudaError_t experts_few_prepare();
 cudaError_t launch_experts_few(const ExpertCall& c, cudaStream_t s);
+cudaError_t experts_tc_prepare();
+// x: the tensor map of X (encode_gather_map).
+cudaError_t launch_experts_tc(const ExpertCall& c, const CUtensorMap& x, int sms,
+                              unsigned int* status, cudaStream_t s);
+// The tensor map for gathering 64-element pieces of X rows (api.cu).
+int encode_gather_map(CUtensorMap* map, int type, const void* X, long long nx, int K,
+                      long long ldx);
 
 }  // namespace q6
 
