@@ -8,15 +8,18 @@
 // tile: thread = weight row, f32 arithmetic (w = d * sc * q - dmin * m times a
 // power of two of the row), one rounding to the activations' 16-bit type, the
 // result stored straight into TMEM, where the MMA takes its A operand from.
-// Packed weights are all that memory and shared memory ever see. x rows are
-// gathered by TMA from the caller's tensor (no sorted copy), 4 rows a
-// request, into 128-byte-swizzled K-major tiles.
+// Packed weights are all that memory and shared memory ever see. x comes in
+// item order (a gathering call copies the rows into its workspace first) by
+// TMA, as 128-byte-swizzled K-major tiles. TMA's own row gather (4 rows a
+// request) was measured at about 60 cycles a request, 4000 for the 256 rows of
+// a stage whose MMAs take 512: 2.77 against 0.79 ms for 8192 items of 11008 x
+// 4096.
 //
 // Tiles with few items have short MMAs; the loads' depth in K grows instead:
 // an x stage holds 64, 128 or 256 of K for up to 256, 128 or 64 items.
 //
 // Warp roles (16 warps, persistent CTA, one per SM):
-//   0      gathers x (every lane issues requests)
+//   0      loads x
 //   1      issues the MMAs
 //   2      TMEM allocation
 //   3      streams the packed weights, one super-block a stage
@@ -54,29 +57,20 @@ struct Bars {
 struct Args {
   const uint8_t* plane;
   const float* scale;  // 2^e per plane row
-  int gather;
   const int32_t* offsets;
-  const int32_t* rows;
   void* Y;
   long long ldy;
-  int E, bands, sbs, out, vec;
+  int E, bands, sbs, out;
+  int vec;  // Y and its rows are 16-byte aligned
 };
 
 template <int kFmt>
 constexpr int kWTile = kFmt == Q6_FMT_Q4K ? kQ4Tile : kQ6Tile;
+constexpr int kOutWarp = 2048;  // epilogue staging of a warp: 32 items of 64 bytes
 template <int kFmt>
-constexpr int kSmemBytes = 1024 + kXStages * kXStage + kWStages * kWTile<kFmt> +
+constexpr int kSmemBytes = 1024 + kXStages * kXStage + kWStages * kWTile<kFmt> + 4 * kOutWarp +
                            (kMaxGroups + 1) * 4 + 12 + (int)sizeof(Bars);
 
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
-                                            const int (&r)[4]) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(r[0]), "r"(r[1]),
-      "r"(r[2]), "r"(r[3])
-      : "memory");
-}
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
   asm volatile(
@@ -111,10 +105,27 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld1(uint32_t (&a)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]), "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]), "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]), "+r"(a[22]), "+r"(a[23]), "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27]), "+r"(a[28]), "+r"(a[29]), "+r"(a[30]), "+r"(a[31])
+// 16 TMEM lanes x 32 columns as four MMA accumulator fragments: r[4 j + e] is
+// row lane / 4 (+ 8 for e >= 2), column 8 j + 2 (lane % 4) + e % 2.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_frag(uint32_t (&a)[16], uint32_t (&b)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]), "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]),
+                 "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7]), "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15])
                :
+               : "memory");
+}
+// Four transposed 8 x 8 tiles of 16-bit values: lane l gives the address of
+// row l % 8 of tile l / 8.
+__device__ __forceinline__ void store_tiles_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                              uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
 }
 
@@ -242,6 +253,11 @@ struct Half<Q6_FMT_Q6K> {
   }
 };
 
+// x / (1 + exp(-x)), within 2^-20 (exp(-x) past f32 gives 0, as in the limit).
+__device__ __forceinline__ float silu(float x) {
+  return x * __frcp_rn(1.0f + __expf(-x));
+}
+
 // ---------------------------------------------------------------- schedule ---
 struct Tile {
   int expert, band, n;  // n: MMA N, a multiple of 16
@@ -270,18 +286,20 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* start, int t) 
   r.count = min(r.n, count - j * r.n);
   return r;
 }
-// 64-of-K blocks an x stage holds.
-__device__ __forceinline__ int blocks_per_stage(int n) { return n > 128 ? 1 : n > 64 ? 2 : 4; }
+// log2 of the 64-of-K blocks an x stage holds.
+__device__ __forceinline__ int stage_shift(int n) { return n > 128 ? 0 : n > 64 ? 1 : 2; }
 
 template <typename T, int kFmt, bool kGlu>
 __global__ void __launch_bounds__(kThreads, 1)
-experts_tc_kernel(const __grid_constant__ CUtensorMap tmX, const Args a, unsigned int* status) {
+experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
+                  const __grid_constant__ CUtensorMap tmX16, const Args a, unsigned int* status) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* xring = smem;
   uint8_t* wring = smem + kXStages * kXStage;
-  int* start = reinterpret_cast<int*>(wring + kWStages * kWTile<kFmt>);
+  uint8_t* out_stage = wring + kWStages * kWTile<kFmt>;
+  int* start = reinterpret_cast<int*>(out_stage + 4 * kOutWarp);
   Bars* bars = reinterpret_cast<Bars*>(
       (reinterpret_cast<uintptr_t>(start + kMaxGroups + 1) + 7) & ~static_cast<uintptr_t>(7));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -307,7 +325,8 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX, const Args a, unsigne
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     mbar_fence_init();
-    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmX64);
+    tma_prefetch_desc(&tmX16);
   }
   if (warp == 2) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
@@ -339,34 +358,27 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX, const Args a, unsigne
   bool ok = true;
 
   if (warp == 0) {
-    // ------------------------------------------------------------- gather x --
+    // --------------------------------------------------------------- load x --
     int g = 0;  // stages issued
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       const Tile w = tile_at(a, start, t);
-      int r[2][4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // slots past the items repeat the first one
-          const int n = 4 * (lane + 32 * i) + j;
-          const long long item = w.first + (n < w.count ? n : 0);
-          r[i][j] = a.gather ? a.rows[item] : (int)item;
-        }
-      const int kb = blocks_per_stage(w.n);
-      for (int k = 0; k < 4 * a.sbs; k += kb) {
+      // lane l < loads: one request, of 64 rows or of 16 past the last whole 64
+      const int whole = w.n / 64, loads = whole + w.n % 64 / 16;
+      const int row = lane < whole ? 64 * lane : 64 * whole + 16 * (lane - whole);
+      const int shift = stage_shift(w.n);
+      for (int k = 0; k < 4 * a.sbs; k += 1 << shift) {
         const int slot = g % kXStages;
         if (!(ok = mbar_wait_warp(&bars->x_empty[slot], ((g / kXStages) & 1) ^ 1, abort_flag, status,
                                   kSiteXEmpty)))
           break;
-        if (lane == 0) mbar_arrive_expect_tx(&bars->x_full[slot], (uint32_t)(kb * w.n * 128));
+        if (lane == 0) mbar_arrive_expect_tx(&bars->x_full[slot], (uint32_t)(w.n * 128) << shift);
         __syncwarp();
-        for (int b = 0; b < kb; ++b) {
-          uint8_t* dst = xring + slot * kXStage + b * w.n * 128 + lane * 512;
-          if (4 * lane < w.n) tma_gather4(dst, &tmX, &bars->x_full[slot], (k + b) * 64, r[0]);
-          if (4 * lane + 128 < w.n)
-            tma_gather4(dst + 32 * 512, &tmX, &bars->x_full[slot], (k + b) * 64, r[1]);
-        }
+        if (lane < loads)
+          for (int b = 0; b < 1 << shift; ++b)
+            tma_load_2d(xring + slot * kXStage + (b * w.n + row) * 128,
+                        lane < whole ? &tmX64 : &tmX16, &bars->x_full[slot], (k + b) * 64,
+                        (int)w.first + row);
+        __syncwarp();
         ++g;
       }
     }
@@ -408,7 +420,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX, const Args a, unsigne
       int gx = 0, ga = 0, next = 0, uses[2] = {0, 0};
       for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
         const Tile w = tile_at(a, start, t);
-        const int kb = blocks_per_stage(w.n);
+        const int mask = (1 << stage_shift(w.n)) - 1;
         const uint32_t idesc = idesc_of<T>(w.n);
         const bool both = w.n > 128;
         const int d0 = both ? 0 : next;
@@ -420,7 +432,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX, const Args a, unsigne
         const uint32_t d_tmem = tmem + (uint32_t)(d0 * 128);
         for (int k = 0; k < 4 * a.sbs; ++k) {
           const int xs = gx % kXStages, as = ga % kASlots;
-          if (k % kb == 0 && !(ok = mbar_wait_bounded(&bars->x_full[xs], (gx / kXStages) & 1,
+          if ((k & mask) == 0 && !(ok = mbar_wait_bounded(&bars->x_full[xs], (gx / kXStages) & 1,
                                                       abort_flag, status, kSiteXFull)))
             break;
           if (k % 2 == 0) {
@@ -429,12 +441,12 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX, const Args a, unsigne
               break;
             tc_fence_after();
           }
-          const uint32_t b = sw128_desc_lo(smem_u32(xring + xs * kXStage + (k % kb) * w.n * 128));
+          const uint32_t b = sw128_desc_lo(smem_u32(xring + xs * kXStage + (k & mask) * w.n * 128));
           const uint32_t at = tmem + (uint32_t)(kACol0 + as * kACols + (k % 2) * 32);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             umma_f16_ts(d_tmem, at + 8 * i, b + 2 * i, idesc, (uint32_t)(k > 0 || i > 0));
-          if (k % kb == kb - 1) {
+          if ((k & mask) == mask) {
             umma_commit(&bars->x_empty[xs]);
             ++gx;
           }
@@ -490,8 +502,14 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX, const Args a, unsigne
     }
   } else if (warp >= 12) {
     // ------------------------------------------------------------- epilogue --
+    // Thread (r, c) of a warp, r = lane / 4, holds rows 16 h + r and 16 h + 8 +
+    // r of its 32 and items 8 j + 2 c, + 1: pairs of items go to shared memory
+    // transposed, [item][row], and from there to Y in 16-byte pieces.
     const int q = warp % 4;
     T* Y = static_cast<T*>(a.Y);
+    constexpr int kCols = kGlu ? 16 : 32;          // output features of a warp
+    constexpr int kUnits = kCols / 8;              // 16-byte units of an item
+    uint8_t* stage = out_stage + q * kOutWarp;
     // items of no expert: zeros
     for (long long i = a.offsets[a.E] + (long long)blockIdx.x; i < a.offsets[a.E + 1];
          i += gridDim.x)
@@ -499,13 +517,11 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX, const Args a, unsigne
     int next = 0, uses[2] = {0, 0};
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       const Tile w = tile_at(a, start, t);
-      const float scale =
-          a.scale[((size_t)w.expert * a.bands + w.band) * kBand + 32 * q + lane];
+      const float* sc = a.scale + ((size_t)w.expert * a.bands + w.band) * kBand + 32 * q + (lane >> 2);
+      const float scale[4] = {sc[0], sc[8], sc[16], sc[24]};
       const bool both = w.n > 128;
       const int d0 = both ? 0 : next;
-      const int m = kGlu ? w.band * 64 + 16 * q + (lane >> 4) * 8 + (lane & 7)
-                         : w.band * 128 + 32 * q + lane;
-      const bool mine = m < a.out && (!kGlu || (lane & 8) == 0);
+      const int m0 = (w.band * 4 + q) * kCols;     // this warp's first output feature
       for (int d = d0; d <= (both ? 1 : d0); ++d) {
         if (!(ok = mbar_wait_warp(&bars->d_full[d], uses[d] & 1, abort_flag, status, kSiteDFull)))
           break;
@@ -513,23 +529,67 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX, const Args a, unsigne
         tc_fence_after();
         const int c1 = both ? (d ? w.n : 128) : w.n;
         for (int c0 = both ? 128 * d : 0; c0 < c1; c0 += 32) {
-          uint32_t v[32];
-          tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(both ? c0 : 128 * d0 + c0), v);
-          tmem_wait_ld1(v);
-          T* y = Y + (w.first + c0) * a.ldy + m;
+          uint32_t v[2][16];
+          const uint32_t src =
+              tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(both ? c0 : 128 * d0 + c0);
+          tmem_ld_frag(src, v[0]);
+          tmem_ld_frag(src + (16u << 16), v[1]);
+          tmem_wait_frag(v[0], v[1]);
+          if (c0 + 32 >= c1) {  // the accumulator is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->d_empty[d]);
+          }
+          __syncwarp();  // the last piece has left the staging
+          uint32_t p[4][4];  // [j][unit]: item pairs of 8-row blocks
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float f = __uint_as_float(v[j]) * scale;
-            if (kGlu) {
-              const float up = __shfl_down_sync(0xffffffffu, f, 8);
-              f = f / (1.0f + __expf(-f)) * up;
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float f[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                f[e] = __uint_as_float(v[h][4 * j + e]) * scale[2 * h + e / 2];
+              if constexpr (kGlu) {
+                p[j][h] = pack2<T>(silu(f[0]) * f[2], silu(f[1]) * f[3]);
+              } else {
+                p[j][2 * h] = pack2<T>(f[0], f[1]);
+                p[j][2 * h + 1] = pack2<T>(f[2], f[3]);
+              }
             }
-            if (mine && c0 + j < w.count) y[(long long)j * a.ldy] = from_f32<T>(f);
+          if constexpr (kGlu) {
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              const int item = 8 * (j + (lane >> 4)) + (lane & 7), unit = (lane >> 3) & 1;
+              store_tiles_t(smem_u32(stage + item * 32 + (unit ^ ((item >> 2) & 1)) * 16), p[j][0],
+                            p[j][1], p[j + 1][0], p[j + 1][1]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int item = 8 * j + (lane & 7), unit = lane >> 3;
+              store_tiles_t(smem_u32(stage + item * 64 + (unit ^ ((item >> 1) & 3)) * 16), p[j][0],
+                            p[j][1], p[j][2], p[j][3]);
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = lane; i < 32 * kUnits; i += 32) {
+            const int item = i / kUnits, unit = i % kUnits, m = m0 + 8 * unit;
+            const int at = kGlu ? unit ^ ((item >> 2) & 1) : unit ^ ((item >> 1) & 3);
+            const uint4 u = *reinterpret_cast<const uint4*>(stage + (item * kUnits + at) * 16);
+            if (c0 + item >= w.count || m >= a.out) continue;
+            T* y = Y + (w.first + c0 + item) * a.ldy + m;
+            if (a.vec && m + 8 <= a.out) {
+              *reinterpret_cast<uint4*>(y) = u;
+            } else {
+              const T* one = reinterpret_cast<const T*>(&u);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (m + e < a.out) y[e] = one[e];
+            }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->d_empty[d]);
       }
       next = both ? 0 : next ^ 1;
     }
@@ -542,7 +602,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX, const Args a, unsigne
   }
 }
 
-typedef void (*Kernel)(const CUtensorMap, const Args, unsigned int*);
+typedef void (*Kernel)(const CUtensorMap, const CUtensorMap, const Args, unsigned int*);
 template <typename T>
 Kernel pick_t(int fmt, int swiglu) {
   if (fmt == Q6_FMT_Q4K)
@@ -570,22 +630,48 @@ cudaError_t experts_tc_prepare() {
   return cudaSuccess;
 }
 
-cudaError_t launch_experts_tc(const ExpertCall& c, const CUtensorMap& x, int sms,
-                              unsigned int* status, cudaStream_t s) {
+cudaError_t launch_experts_tc(const ExpertCall& c, const CUtensorMap& x64, const CUtensorMap& x16,
+                              int sms, unsigned int* status, cudaStream_t s) {
   Args a;
   a.plane = c.plane;
   a.scale = reinterpret_cast<const float*>(c.plane + c.g.scale_off);
-  a.gather = c.gather;
-  a.offsets = c.offsets, a.rows = c.rows;
+  a.offsets = c.offsets;
   a.Y = c.Y, a.ldy = c.ldy;
   a.E = c.E, a.bands = c.g.bands, a.sbs = c.g.sbs, a.out = c.g.out;
-  a.vec = 0;
+  a.vec = (reinterpret_cast<uintptr_t>(c.Y) | (uintptr_t)(c.ldy * 2)) % 16 == 0;
   // at most this many tiles
   const long long tiles =
       (c.items / kTileN + (c.items < c.E ? c.items : c.E)) * (long long)c.g.bands;
   const unsigned grid = (unsigned)(tiles < sms ? (tiles > 0 ? tiles : 1) : sms);
   return launch_pdl(pick(c.type, c.fmt, c.swiglu), dim3(grid), dim3(kThreads),
-                    (size_t)smem_bytes(c.fmt), s, x, a, status);
+                    (size_t)smem_bytes(c.fmt), s, x64, x16, a, status);
+}
+
+// ------------------------------------------------------- x in item order ---
+namespace {
+constexpr int kSortThreads = 256;
+// out[i] = X[rows[i]], rows of `units` 16-byte units; `per` threads a row.
+__global__ void __launch_bounds__(kSortThreads)
+sort_rows_kernel(const uint4* X, long long ldx, const int32_t* rows, long long items, int units,
+                 int per, uint4* out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const long long i = (long long)blockIdx.x * (kSortThreads / per) + threadIdx.x / per;
+  if (i >= items) return;
+  const uint4* src = X + rows[i] * ldx;
+  uint4* dst = out + i * units;
+#pragma unroll 4
+  for (int u = threadIdx.x % per; u < units; u += per) dst[u] = src[u];
+}
+}  // namespace
+
+cudaError_t launch_sort_rows(const ExpertCall& c, int K, void* out, cudaStream_t s) {
+  const int units = K / 8;
+  const int per = units >= 128 ? 64 : 32;
+  const long long rows = kSortThreads / per;
+  return launch_pdl(sort_rows_kernel, dim3((unsigned)((c.items + rows - 1) / rows)),
+                    dim3(kSortThreads), 0, s, static_cast<const uint4*>(c.X), c.ldx / 8, c.rows,
+                    c.items, units, per, static_cast<uint4*>(out));
 }
 
 }  // namespace q6

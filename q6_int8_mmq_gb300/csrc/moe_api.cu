@@ -59,6 +59,11 @@ int check_experts(int fmt, int E, int M, int K, int swiglu) {
 
 // Items an expert, on average, up to which the few-token kernel runs.
 constexpr int kFewItems = 12;
+bool on_tensor_cores(int64_t items, int E) { return items > kFewItems * (int64_t)E; }
+// Bytes of the X rows in item order that the tensor-core path reads.
+size_t sorted_bytes(int64_t items, int E, int K, int gather) {
+  return gather && on_tensor_cores(items, E) ? (size_t)items * (size_t)K * 2 : 0;
+}
 
 bool half_type(int type) { return type == Q6_TYPE_BF16 || type == Q6_TYPE_F16; }
 bool any_type(int type) { return half_type(type) || type == Q6_TYPE_F32; }
@@ -132,10 +137,17 @@ int q6_pack_experts(int fmt, const uint8_t* raw, int E, int M, int K, int swiglu
                   "expert pack");
 }
 
+int q6_experts_workspace_bytes(int E, int K, int64_t items, int gather, size_t* bytes) {
+  if (E < 1 || K < 1 || K % 256 || items < 0 || !bytes)
+    return fail(Q6_EINVAL, "E >= 1, K a multiple of 256, items >= 0, bytes not NULL");
+  *bytes = sorted_bytes(items, E, K, gather);
+  return Q6_OK;
+}
+
 int q6_experts_mmq(int fmt, const void* plane, int E, int M, int K, int swiglu, const void* X,
                    int type, int64_t nx, int64_t ldx, int gather, const int32_t* offsets,
-                   const int32_t* rows, int64_t items, void* Y, int64_t ldy, int* path_out,
-                   q6_stream_t s) {
+                   const int32_t* rows, int64_t items, void* Y, int64_t ldy, void* workspace,
+                   size_t workspace_bytes, int* path_out, q6_stream_t s) {
   int rc = check_experts(fmt, E, M, K, swiglu);
   if (rc) return rc;
   if (path_out) *path_out = Q6_PATH_NONE;
@@ -158,15 +170,26 @@ int q6_experts_mmq(int fmt, const void* plane, int E, int M, int K, int swiglu, 
   c.X = X, c.type = type, c.ldx = ldx, c.nx = nx, c.gather = gather;
   c.offsets = offsets, c.rows = rows, c.items = items;
   c.Y = Y, c.ldy = ldy;
-  if (items > kFewItems * (int64_t)E) {
+  if (on_tensor_cores(items, E)) {
+    const size_t need = sorted_bytes(items, E, K, gather);
+    if (need && (!workspace || workspace_bytes < need))
+      return fail(Q6_ESIZE, "the product needs a workspace of %zu bytes", need);
+    if (need && !aligned(workspace, 256)) return fail(Q6_EALIGN, "workspace must be 256-byte aligned");
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return fail(Q6_ECUDA, "SM count: %s", cudaGetErrorString(e));
-    CUtensorMap map;
-    if ((rc = q6::encode_gather_map(&map, type, X, nx, K, ldx))) return rc;
+    const void* x = need ? workspace : X;
+    const int64_t n = need ? items : nx, ld = need ? K : ldx;
+    CUtensorMap x64, x16;
+    if ((rc = q6::encode_rows_map(&x64, type, x, n, K, ld, 64)) ||
+        (rc = q6::encode_rows_map(&x16, type, x, n, K, ld, 16)))
+      return rc;
+    if (need && (rc = launched(q6::launch_sort_rows(c, K, workspace, (cudaStream_t)s), "row sort")))
+      return rc;
     if (path_out) *path_out = Q6_PATH_EXPERTS_TC;
-    return launched(q6::launch_experts_tc(c, map, sms, status, (cudaStream_t)s), "grouped product");
+    return launched(q6::launch_experts_tc(c, x64, x16, sms, status, (cudaStream_t)s),
+                    "grouped product");
   }
   if (path_out) *path_out = Q6_PATH_EXPERTS_FEW;
   return launched(q6::launch_experts_few(c, (cudaStream_t)s), "grouped product");

@@ -248,6 +248,13 @@ def pack_experts(raw, fmt: str, E: int, M: int, K: int, swiglu: bool = False, st
     return ExpertWeights(fmt, E, M, K, swiglu, plane)
 
 
+@functools.lru_cache(maxsize=256)
+def experts_workspace_bytes(E: int, K: int, items: int, gather: bool) -> int:
+    b = ctypes.c_size_t()
+    _check(load().q6_experts_workspace_bytes(E, K, items, int(gather), ctypes.byref(b)))
+    return b.value
+
+
 def experts_mmq(w: ExpertWeights, X, groups: Groups, gather: bool = True, out=None, stream=None):
     """The grouped product: row i of the result is W[e] x for the sorted item
     i of `groups` (one group per expert), x the item's token's row of X
@@ -272,12 +279,16 @@ def experts_mmq(w: ExpertWeights, X, groups: Groups, gather: bool = True, out=No
             out = torch.empty(shape, dtype=X.dtype, device=dev)
     else:
         _tensor(out, "out", X.dtype, shape, dev, rows=True)
+    need, ws = experts_workspace_bytes(w.E, w.K, items, bool(gather)), None
+    if need:
+        with _on(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
     path = ctypes.c_int(-1)
     _check(load().q6_experts_mmq(FORMATS[w.fmt], w.plane.data_ptr(), w.E, w.M, w.K, int(w.swiglu),
                                  X.data_ptr(), code, nx, _row_stride(X), int(bool(gather)),
                                  groups.offsets.data_ptr(), groups.rows.data_ptr(), items,
-                                 out.data_ptr(), _row_stride(out), ctypes.byref(path),
-                                 _stream(stream)))
+                                 out.data_ptr(), _row_stride(out), _ptr(ws), need,
+                                 ctypes.byref(path), _stream(stream)))
     return out, PATH_NAMES.get(path.value, str(path.value))
 
 
