@@ -129,6 +129,15 @@ __device__ __forceinline__ void store_tiles_t(uint32_t addr, uint32_t a, uint32_
                : "memory");
 }
 
+// True in one lane of the converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Instruction descriptor: f16 or bf16 operands, f32 accumulation, M = 128.
 template <typename T>
 __device__ __forceinline__ uint32_t idesc_of(int n) {
@@ -416,56 +425,65 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA --
-    if (lane == 0) {
-      int gx = 0, ga = 0, next = 0, uses[2] = {0, 0};
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        const Tile w = tile_at(a, start, t);
-        const int mask = (1 << stage_shift(w.n)) - 1;
-        const uint32_t idesc = idesc_of<T>(w.n);
-        const bool both = w.n > 128;
-        const int d0 = both ? 0 : next;
-        for (int d = d0; d <= (both ? 1 : d0) && ok; ++d)
-          ok = mbar_wait_bounded(&bars->d_empty[d], (uses[d] & 1) ^ 1, abort_flag, status,
-                                 kSiteDEmpty);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem + (uint32_t)(d0 * 128);
-        for (int k = 0; k < 4 * a.sbs; ++k) {
-          const int xs = gx % kXStages, as = ga % kASlots;
-          if ((k & mask) == 0 && !(ok = mbar_wait_bounded(&bars->x_full[xs], (gx / kXStages) & 1,
-                                                      abort_flag, status, kSiteXFull)))
-            break;
-          if (k % 2 == 0) {
-            if (!(ok = mbar_wait_bounded(&bars->a_full[as], (ga / kASlots) & 1, abort_flag, status,
-                                         kSiteAFull)))
-              break;
-            tc_fence_after();
-          }
-          const uint32_t b = sw128_desc_lo(smem_u32(xring + xs * kXStage + (k & mask) * w.n * 128));
-          const uint32_t at = tmem + (uint32_t)(kACol0 + as * kACols + (k % 2) * 32);
+    // The whole warp walks the stages on values that are the same in all
+    // lanes, one elected lane issues: the MMA takes its addresses from uniform
+    // registers, and values of a single lane's own branch have to be moved
+    // there one by one (measured: 700 cycles for the issue of 64 of K).
+    int gx = 0, ga = 0, next = 0, uses0 = 0, uses1 = 0;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const int n = __shfl_sync(0xffffffffu, tile_at(a, start, t).n, 0);
+      const int mask = (1 << stage_shift(n)) - 1;
+      const uint32_t idesc = idesc_of<T>(n);
+      const bool both = n > 128, first = both || next == 0, second = both || next == 1;
+      if (first)
+        ok = mbar_wait_warp(&bars->d_empty[0], (uses0 & 1) ^ 1, abort_flag, status, kSiteDEmpty);
+      if (second && ok)
+        ok = mbar_wait_warp(&bars->d_empty[1], (uses1 & 1) ^ 1, abort_flag, status, kSiteDEmpty);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem + (first ? 0u : 128u);
+      for (int u = 0; u < 2 * a.sbs; ++u) {  // A slots: 128 of K
+        const int as = ga % kASlots;
+        if (!(ok = mbar_wait_warp(&bars->a_full[as], (ga / kASlots) & 1, abort_flag, status,
+                                  kSiteAFull)))
+          break;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            umma_f16_ts(d_tmem, at + 8 * i, b + 2 * i, idesc, (uint32_t)(k > 0 || i > 0));
-          if ((k & mask) == mask) {
-            umma_commit(&bars->x_empty[xs]);
-            ++gx;
+        for (int half = 0; half < 2; ++half) {
+          const int block = (2 * u + half) & mask, xs = gx % kXStages;
+          if (block == 0 && !(ok = mbar_wait_warp(&bars->x_full[xs], (gx / kXStages) & 1, abort_flag,
+                                                  status, kSiteXFull)))
+            break;
+          tc_fence_after();
+          const uint32_t b = sw128_desc_lo(smem_u32(xring) + xs * kXStage + block * n * 128);
+          const uint32_t at = tmem + (uint32_t)(kACol0 + as * kACols + half * 32);
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              umma_f16_ts(d_tmem, at + 8 * i, b + 2 * i, idesc, (uint32_t)(u > 0 || half > 0 || i > 0));
+            if (block == mask) umma_commit(&bars->x_empty[xs]);
+            if (half) umma_commit(&bars->a_empty[as]);
           }
-          if (k % 2) {
-            umma_commit(&bars->a_empty[as]);
-            ++ga;
-          }
+          __syncwarp();
+          if (block == mask) ++gx;
         }
         if (!ok) break;
-        for (int d = d0; d <= (both ? 1 : d0); ++d) {
-          umma_commit(&bars->d_full[d]);
-          ++uses[d];
-        }
-        next = both ? 0 : next ^ 1;
+        ++ga;
       }
+      if (!ok) break;
+      if (elect_one()) {
+        if (first) umma_commit(&bars->d_full[0]);
+        if (second) umma_commit(&bars->d_full[1]);
+      }
+      __syncwarp();
+      uses0 += first, uses1 += second;
+      next = both ? 0 : next ^ 1;
+    }
+    if (elect_one()) {
       umma_commit(&bars->drain);
       volatile int no_abort = 0;
       mbar_wait_bounded(&bars->drain, 0, &no_abort, status, kSiteDrain);
     }
+    __syncwarp();
   } else if (warp >= 4 && warp < 12) {
     // ----------------------------------------------------------- dequantise --
     const int h = (warp - 4) / 4, row = 32 * (warp % 4) + lane;
