@@ -3,24 +3,27 @@
 //
 //   Y[i][m] = sum_k W[e(i)][m][k] x[t(i)][k]
 //
-// A tile is 128 plane rows of one expert (MMA M, TMEM lanes) by up to 256 of
-// its items (MMA N). The weights are dequantised inside the kernel, once per
-// tile: thread = weight row, f32 arithmetic (w = d * sc * q - dmin * m times a
-// power of two of the row), one rounding to the activations' 16-bit type, the
-// result stored straight into TMEM, where the MMA takes its A operand from.
-// Packed weights are all that memory and shared memory ever see. x comes in
-// item order (a gathering call copies the rows into its workspace first) by
-// TMA, as 128-byte-swizzled K-major tiles. TMA's own row gather (4 rows a
-// request) was measured at about 60 cycles a request, 4000 for the 256 rows of
-// a stage whose MMAs take 512: 2.77 against 0.79 ms for 8192 items of 11008 x
-// 4096.
+// A pair of CTAs (cluster of two, cta_group::2) computes a tile of 256 plane
+// rows of one expert (MMA M; 128 rows, one TMEM lane each, a CTA) by up to 256
+// of its items (MMA N; each CTA loads half of their x). Sharing x halves what
+// shared memory has to take in and hand out: one CTA alone on 128 x 256 moves
+// 64 KB in and out of it for 512 cycles of MMA, which is all it can
+// (measured, 8192 items of 11008 x 4096: 621 us alone).
 //
-// Tiles with few items have short MMAs; the loads' depth in K grows instead:
-// an x stage holds 64, 128 or 256 of K for up to 256, 128 or 64 items.
+// The weights are dequantised inside the kernel, once per tile: thread =
+// weight row, f32 arithmetic (w = d * sc * q - dmin * m times a power of two
+// of the row), one rounding to the activations' 16-bit type, the result
+// stored straight into TMEM, where the MMA takes its A operand from. Packed
+// weights are all that memory and shared memory ever see. x comes in item
+// order (a gathering call copies the rows into its workspace first) by TMA,
+// as 128-byte-swizzled K-major tiles. TMA's own row gather (4 rows a request)
+// was measured at about 60 cycles a request, 4000 for the 256 rows of a stage
+// whose MMAs take 512.
 //
-// Warp roles (16 warps, persistent CTA, one per SM):
+// Warp roles (16 warps, persistent CTAs, one per SM):
 //   0      loads x
-//   1      issues the MMAs
+//   1      CTA 0: issues the pair's MMAs; CTA 1: tells CTA 0 which x stages
+//          have arrived
 //   2      TMEM allocation
 //   3      streams the packed weights, one super-block a stage
 //   4-11   dequantise: warps 4-7 the even, 8-11 the odd halves (128 of K) of
@@ -28,10 +31,31 @@
 //   12-15  epilogue
 // TMEM: columns 0-255 two accumulators of 128 items (or one of 256), 256-511
 // four A slots of 128 of K.
-// Every wait is bounded (see q6_internal.cuh).
+// Every wait is bounded (see q6_internal.cuh), and the pair meets once more
+// before either CTA leaves.
+#include <stdint.h>
+
+// Barriers of a pair are waited on with cluster scope.
+namespace q6 {
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity);
+}
+#define MBAR_POLL mbar_try_wait_cluster
 #include "moe_internal.cuh"
 
 namespace q6 {
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 namespace {
 
 constexpr int kThreads = 512;
@@ -79,16 +103,71 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem]^T, kind::f16.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
-                                            uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem]^T over the CTA pair, kind::f16.
+__device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                              uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 bd;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "mov.b64 bd, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], bd, %3, p;\n\t}\n" ::"r"(d_tmem),
       "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kSw128DescHi)
       : "memory");
+}
+// Arrives once on `bar` of both CTAs when every MMA issued so far by this
+// thread has completed.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// The same on this CTA's `bar` alone.
+__device__ __forceinline__ void commit_own(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+// Arrives once on `bar` of CTA 0 of the pair after this thread's tcgen05 loads
+// or stores, which the tcgen05 waits and fences around the barrier order;
+// nothing else is published, so the arrival needs no release (one of cluster
+// scope was measured at 1300 cycles behind the packed-weight reads).
+__device__ __forceinline__ void arrive_leader_tmem(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\t"
+      "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [ra];\n\t}\n" ::"r"(smem_u32(bar))
+      : "memory");
+}
+// Arrives once on `bar` of CTA 0 of the pair.
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\t"
+      "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n\t}\n" ::"r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(dst_smem)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -138,11 +217,11 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Instruction descriptor: f16 or bf16 operands, f32 accumulation, M = 128.
+// Instruction descriptor: f16 or bf16 operands, f32 accumulation, M = 256.
 template <typename T>
 __device__ __forceinline__ uint32_t idesc_of(int n) {
   const uint32_t type = sizeof(T) == 2 && __is_same(T, __nv_bfloat16) ? 1u : 0u;
-  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(n >> 3) << 17) | (16u << 24);
 }
 
 // ------------------------------------------------------------ dequantising ---
@@ -269,34 +348,40 @@ __device__ __forceinline__ float silu(float x) {
 
 // ---------------------------------------------------------------- schedule ---
 struct Tile {
-  int expert, band, n;  // n: MMA N, a multiple of 16
+  int expert, pair, n;  // pair of bands; n: MMA N, a multiple of 32
   long long first;      // first item
   int count;            // items
 };
 __device__ __forceinline__ int tiles_of(int count) { return (count + kTileN - 1) / kTileN; }
 
-// Tile t of the list ordered by (expert, item tile, band); start[e] is the
-// number of (expert, item tile) pairs before expert e.
+// Tile t of the list ordered by (expert, item tile, band pair); start[e] is
+// the number of (expert, item tile)s before expert e.
 __device__ __forceinline__ Tile tile_at(const Args& a, const int* start, int t) {
-  const int pair = t / a.bands;
-  int lo = 0, hi = a.E;  // start[lo] <= pair < start[hi]
+  const int pairs = (a.bands + 1) / 2;
+  const int item_tile = t / pairs;
+  int lo = 0, hi = a.E;  // start[lo] <= item_tile < start[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
-    if (start[mid] <= pair) lo = mid;
+    if (start[mid] <= item_tile) lo = mid;
     else hi = mid;
   }
   Tile r;
-  r.expert = lo, r.band = t % a.bands;
+  r.expert = lo, r.pair = t % pairs;
   const int begin = a.offsets[lo], count = a.offsets[lo + 1] - begin;
-  const int parts = tiles_of(count), j = pair - start[lo];
-  // equal parts, in steps of 16
-  r.n = ((count + parts - 1) / parts + 15) / 16 * 16;
+  const int parts = tiles_of(count), j = item_tile - start[lo];
+  // equal parts, in steps of 32 (their last may hold less, but never nothing)
+  r.n = ((count + parts - 1) / parts + 31) / 32 * 32;
   r.first = (long long)begin + (long long)j * r.n;
   r.count = min(r.n, count - j * r.n);
   return r;
 }
-// log2 of the 64-of-K blocks an x stage holds.
-__device__ __forceinline__ int stage_shift(int n) { return n > 128 ? 0 : n > 64 ? 1 : 2; }
+// This CTA's band of the pair; past an odd number of bands the last one again,
+// whose result is not stored.
+__device__ __forceinline__ int band_of(const Args& a, int pair, int rank) {
+  return min(2 * pair + rank, a.bands - 1);
+}
+// log2 of the 64-of-K blocks an x stage holds (n / 2 rows of 128 bytes each).
+__device__ __forceinline__ int stage_shift(int n) { return n > 128 ? 1 : 2; }
 
 template <typename T, int kFmt, bool kGlu>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -312,11 +397,12 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
   Bars* bars = reinterpret_cast<Bars*>(
       (reinterpret_cast<uintptr_t>(start + kMaxGroups + 1) + 7) & ~static_cast<uintptr_t>(7));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank(), cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
   volatile int* abort_flag = &bars->abort;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kXStages; ++i) {
-      mbar_init(&bars->x_full[i], 1);
+      mbar_init(&bars->x_full[i], rank ? 1 : 2);  // CTA 0: its own copies and CTA 1's word
       mbar_init(&bars->x_empty[i], 1);
     }
     for (int i = 0; i < kWStages; ++i) {
@@ -324,12 +410,12 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
       mbar_init(&bars->w_empty[i], 8);
     }
     for (int i = 0; i < kASlots; ++i) {
-      mbar_init(&bars->a_full[i], 4);
+      mbar_init(&bars->a_full[i], 8);  // both CTAs' warps, in CTA 0
       mbar_init(&bars->a_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->d_full[i], 1);
-      mbar_init(&bars->d_empty[i], 4);
+      mbar_init(&bars->d_empty[i], 8);
     }
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
@@ -338,8 +424,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
     tma_prefetch_desc(&tmX16);
   }
   if (warp == 2) {
-    tmem_alloc(&bars->tmem_base, kTmemCols);
-    tmem_relinquish();
+    tmem_alloc_pair(&bars->tmem_base, kTmemCols);
   }
   griddep_wait();
   griddep_launch_dependents();
@@ -361,18 +446,20 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // the pair's barriers are initialised
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const int total = start[a.E] * a.bands;
+  const int total = start[a.E] * ((a.bands + 1) / 2);
   bool ok = true;
 
   if (warp == 0) {
     // --------------------------------------------------------------- load x --
     int g = 0;  // stages issued
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    for (int t = cluster; t < total && ok; t += clusters) {
       const Tile w = tile_at(a, start, t);
       // lane l < loads: one request, of 64 rows or of 16 past the last whole 64
-      const int whole = w.n / 64, loads = whole + w.n % 64 / 16;
+      const int rows = w.n / 2;  // this CTA's
+      const int whole = rows / 64, loads = whole + rows % 64 / 16;
       const int row = lane < whole ? 64 * lane : 64 * whole + 16 * (lane - whole);
       const int shift = stage_shift(w.n);
       for (int k = 0; k < 4 * a.sbs; k += 1 << shift) {
@@ -380,17 +467,21 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
         if (!(ok = mbar_wait_warp(&bars->x_empty[slot], ((g / kXStages) & 1) ^ 1, abort_flag, status,
                                   kSiteXEmpty)))
           break;
-        if (lane == 0) mbar_arrive_expect_tx(&bars->x_full[slot], (uint32_t)(w.n * 128) << shift);
+        if (lane == 0) mbar_arrive_expect_tx(&bars->x_full[slot], (uint32_t)(rows * 128) << shift);
         __syncwarp();
         if (lane < loads)
           for (int b = 0; b < 1 << shift; ++b)
-            tma_load_2d(xring + slot * kXStage + (b * w.n + row) * 128,
+            tma_load_2d(xring + slot * kXStage + (b * rows + row) * 128,
                         lane < whole ? &tmX64 : &tmX16, &bars->x_full[slot], (k + b) * 64,
-                        (int)w.first + row);
+                        (int)w.first + rank * rows + row);
         __syncwarp();
         ++g;
       }
     }
+    // the last stages' releases reach this CTA before it leaves
+    for (int k = g > kXStages ? g - kXStages : 0; k < g && ok; ++k)
+      ok = mbar_wait_warp(&bars->x_empty[k % kXStages], (k / kXStages) & 1, abort_flag, status,
+                          kSiteXEmpty);
     if (!ok && lane == 0) {  // copies in flight land before the CTA exits
       volatile int no_abort = 0;
       for (int k = g > kXStages ? g - kXStages : 0; k < g; ++k)
@@ -401,10 +492,11 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
     // ------------------------------------------------------- packed weights --
     if (lane == 0) {
       int g = 0;
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      for (int t = cluster; t < total && ok; t += clusters) {
         const Tile w = tile_at(a, start, t);
         const uint8_t* src =
-            a.plane + ((size_t)w.expert * a.bands + w.band) * (size_t)a.sbs * kWTile<kFmt>;
+            a.plane + ((size_t)w.expert * a.bands + band_of(a, w.pair, rank)) *
+                          (size_t)a.sbs * kWTile<kFmt>;
         for (int sb = 0; sb < a.sbs; ++sb) {
           const int slot = g % kWStages;
           if (!(ok = mbar_wait_bounded(&bars->w_empty[slot], ((g / kWStages) & 1) ^ 1, abort_flag,
@@ -423,6 +515,21 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
                             kSiteWFull);
       }
     }
+  } else if (warp == 1 && rank == 1) {
+    // ------------------------------------------- CTA 1: its x has arrived --
+    if (lane == 0) {
+      int g = 0;
+      for (int t = cluster; t < total && ok; t += clusters) {
+        const int stages = 4 * a.sbs >> stage_shift(tile_at(a, start, t).n);
+        for (int k = 0; k < stages; ++k, ++g) {
+          const int slot = g % kXStages;
+          if (!(ok = mbar_wait_bounded(&bars->x_full[slot], (g / kXStages) & 1, abort_flag, status,
+                                       kSiteXFull)))
+            break;
+          arrive_leader(&bars->x_full[slot]);
+        }
+      }
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA --
     // The whole warp walks the stages on values that are the same in all
@@ -430,7 +537,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
     // registers, and values of a single lane's own branch have to be moved
     // there one by one (measured: 700 cycles for the issue of 64 of K).
     int gx = 0, ga = 0, next = 0, uses0 = 0, uses1 = 0;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    for (int t = cluster; t < total && ok; t += clusters) {
       const int n = __shfl_sync(0xffffffffu, tile_at(a, start, t).n, 0);
       const int mask = (1 << stage_shift(n)) - 1;
       const uint32_t idesc = idesc_of<T>(n);
@@ -454,14 +561,14 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
                                                   status, kSiteXFull)))
             break;
           tc_fence_after();
-          const uint32_t b = sw128_desc_lo(smem_u32(xring) + xs * kXStage + block * n * 128);
+          const uint32_t b = sw128_desc_lo(smem_u32(xring) + xs * kXStage + block * n * 64);
           const uint32_t at = tmem + (uint32_t)(kACol0 + as * kACols + half * 32);
           if (elect_one()) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              umma_f16_ts(d_tmem, at + 8 * i, b + 2 * i, idesc, (uint32_t)(u > 0 || half > 0 || i > 0));
-            if (block == mask) umma_commit(&bars->x_empty[xs]);
-            if (half) umma_commit(&bars->a_empty[as]);
+              umma_f16_pair(d_tmem, at + 8 * i, b + 2 * i, idesc, (uint32_t)(u > 0 || half > 0 || i > 0));
+            if (block == mask) commit_pair(&bars->x_empty[xs]);
+            if (half) commit_pair(&bars->a_empty[as]);
           }
           __syncwarp();
           if (block == mask) ++gx;
@@ -471,15 +578,15 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
       }
       if (!ok) break;
       if (elect_one()) {
-        if (first) umma_commit(&bars->d_full[0]);
-        if (second) umma_commit(&bars->d_full[1]);
+        if (first) commit_pair(&bars->d_full[0]);
+        if (second) commit_pair(&bars->d_full[1]);
       }
       __syncwarp();
       uses0 += first, uses1 += second;
       next = both ? 0 : next ^ 1;
     }
     if (elect_one()) {
-      umma_commit(&bars->drain);
+      commit_own(&bars->drain);
       volatile int no_abort = 0;
       mbar_wait_bounded(&bars->drain, 0, &no_abort, status, kSiteDrain);
     }
@@ -489,9 +596,9 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
     const int h = (warp - 4) / 4, row = 32 * (warp % 4) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
     int gw = 0;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    for (int t = cluster; t < total && ok; t += clusters) {
       const Tile w = tile_at(a, start, t);
-      const float inv = 1.0f / a.scale[((size_t)w.expert * a.bands + w.band) * kBand + row];
+      const float inv = 1.0f / a.scale[((size_t)w.expert * a.bands + band_of(a, w.pair, rank)) * kBand + row];
       for (int sb = 0; sb < a.sbs; ++sb, ++gw) {
         const int ws = gw % kWStages, ga = 2 * gw + h, as = ga % kASlots;
         if (!(ok = mbar_wait_warp(&bars->w_full[ws], (gw / kWStages) & 1, abort_flag, status,
@@ -515,9 +622,13 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->a_full[as]);
+        if (lane == 0) arrive_leader_tmem(&bars->a_full[as]);
       }
     }
+    // the last A slots' releases reach this CTA before it leaves
+    for (int k = gw > 2 ? gw - 2 : 0; k < gw && ok; ++k)
+      ok = mbar_wait_warp(&bars->a_empty[(2 * k + h) % kASlots], ((2 * k + h) / kASlots) & 1,
+                          abort_flag, status, kSiteAEmpty);
   } else if (warp >= 12) {
     // ------------------------------------------------------------- epilogue --
     // Thread (r, c) of a warp, r = lane / 4, holds rows 16 h + r and 16 h + 8 +
@@ -533,13 +644,15 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
          i += gridDim.x)
       for (int m = 32 * q + lane; m < a.out; m += 128) Y[i * a.ldy + m] = from_f32<T>(0.0f);
     int next = 0, uses[2] = {0, 0};
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    for (int t = cluster; t < total && ok; t += clusters) {
       const Tile w = tile_at(a, start, t);
-      const float* sc = a.scale + ((size_t)w.expert * a.bands + w.band) * kBand + 32 * q + (lane >> 2);
+      const int band = band_of(a, w.pair, rank);
+      const bool mine = 2 * w.pair + rank < a.bands;
+      const float* sc = a.scale + ((size_t)w.expert * a.bands + band) * kBand + 32 * q + (lane >> 2);
       const float scale[4] = {sc[0], sc[8], sc[16], sc[24]};
       const bool both = w.n > 128;
       const int d0 = both ? 0 : next;
-      const int m0 = (w.band * 4 + q) * kCols;     // this warp's first output feature
+      const int m0 = (band * 4 + q) * kCols;     // this warp's first output feature
       for (int d = d0; d <= (both ? 1 : d0); ++d) {
         if (!(ok = mbar_wait_warp(&bars->d_full[d], uses[d] & 1, abort_flag, status, kSiteDFull)))
           break;
@@ -556,7 +669,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
           if (c0 + 32 >= c1) {  // the accumulator is in registers
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->d_empty[d]);
+            if (lane == 0) arrive_leader_tmem(&bars->d_empty[d]);
           }
           __syncwarp();  // the last piece has left the staging
           uint32_t p[4][4];  // [j][unit]: item pairs of 8-row blocks
@@ -596,7 +709,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
             const int item = i / kUnits, unit = i % kUnits, m = m0 + 8 * unit;
             const int at = kGlu ? unit ^ ((item >> 2) & 1) : unit ^ ((item >> 1) & 3);
             const uint4 u = *reinterpret_cast<const uint4*>(stage + (item * kUnits + at) * 16);
-            if (c0 + item >= w.count || m >= a.out) continue;
+            if (c0 + item >= w.count || m >= a.out || !mine) continue;
             T* y = Y + (w.first + c0 + item) * a.ldy + m;
             if (a.vec && m + 8 <= a.out) {
               *reinterpret_cast<uint4*>(y) = u;
@@ -614,9 +727,10 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may still signal it
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc_pair(tmem, kTmemCols);
   }
 }
 
@@ -635,21 +749,55 @@ int smem_bytes(int fmt) {
 }
 static_assert(kSmemBytes<Q6_FMT_Q6K> <= 227 * 1024, "shared memory");
 
+// Fills a launch of `pairs` CTA pairs; attr holds two attributes.
+void pair_launch(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int fmt, unsigned pairs,
+                 cudaStream_t s) {
+  *cfg = cudaLaunchConfig_t{};
+  cfg->gridDim = dim3(2 * pairs);
+  cfg->blockDim = dim3(kThreads);
+  cfg->dynamicSmemBytes = (size_t)smem_bytes(fmt);
+  cfg->stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 2;
+}
+
+// CTA pairs each device runs at a time (a device's SMs need not all pair up).
+int g_pairs[64];
+
 }  // namespace
 
 cudaError_t experts_tc_prepare() {
+  int dev = 0, least = 1 << 30;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
   for (int type : {Q6_TYPE_BF16, Q6_TYPE_F16})
     for (int fmt : {Q6_FMT_Q4K, Q6_FMT_Q6K})
       for (int glu : {0, 1}) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            pick(type, fmt, glu), cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(fmt));
-        if (e != cudaSuccess) return e;
+        const Kernel k = pick(type, fmt, glu);
+        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      smem_bytes(fmt))) != cudaSuccess)
+          return e;
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[2];
+        pair_launch(&cfg, attr, fmt, 1, nullptr);
+        cfg.numAttrs = 1;
+        int n = 0;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, k, &cfg)) != cudaSuccess) return e;
+        least = n < least ? n : least;
       }
+  if (least < 1) return cudaErrorInvalidConfiguration;
+  g_pairs[dev % 64] = least;
   return cudaSuccess;
 }
 
 cudaError_t launch_experts_tc(const ExpertCall& c, const CUtensorMap& x64, const CUtensorMap& x16,
-                              int sms, unsigned int* status, cudaStream_t s) {
+                              unsigned int* status, cudaStream_t s) {
   Args a;
   a.plane = c.plane;
   a.scale = reinterpret_cast<const float*>(c.plane + c.g.scale_off);
@@ -659,10 +807,15 @@ cudaError_t launch_experts_tc(const ExpertCall& c, const CUtensorMap& x64, const
   a.vec = (reinterpret_cast<uintptr_t>(c.Y) | (uintptr_t)(c.ldy * 2)) % 16 == 0;
   // at most this many tiles
   const long long tiles =
-      (c.items / kTileN + (c.items < c.E ? c.items : c.E)) * (long long)c.g.bands;
-  const unsigned grid = (unsigned)(tiles < sms ? (tiles > 0 ? tiles : 1) : sms);
-  return launch_pdl(pick(c.type, c.fmt, c.swiglu), dim3(grid), dim3(kThreads),
-                    (size_t)smem_bytes(c.fmt), s, x64, x16, a, status);
+      (c.items / kTileN + (c.items < c.E ? c.items : c.E) + 1) * (long long)((c.g.bands + 1) / 2);
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const long long most = g_pairs[dev % 64];
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  pair_launch(&cfg, attr, c.fmt, (unsigned)(tiles < most ? tiles : most), s);
+  return cudaLaunchKernelEx(&cfg, pick(c.type, c.fmt, c.swiglu), x64, x16, a, status);
 }
 
 // ------------------------------------------------------- x in item order ---

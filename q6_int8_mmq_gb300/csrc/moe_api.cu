@@ -175,10 +175,6 @@ int q6_experts_mmq(int fmt, const void* plane, int E, int M, int K, int swiglu, 
     if (need && (!workspace || workspace_bytes < need))
       return fail(Q6_ESIZE, "the product needs a workspace of %zu bytes", need);
     if (need && !aligned(workspace, 256)) return fail(Q6_EALIGN, "workspace must be 256-byte aligned");
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return fail(Q6_ECUDA, "SM count: %s", cudaGetErrorString(e));
     const void* x = need ? workspace : X;
     const int64_t n = need ? items : nx, ld = need ? K : ldx;
     CUtensorMap x64, x16;
@@ -188,7 +184,7 @@ int q6_experts_mmq(int fmt, const void* plane, int E, int M, int K, int swiglu, 
     if (need && (rc = launched(q6::launch_sort_rows(c, K, workspace, (cudaStream_t)s), "row sort")))
       return rc;
     if (path_out) *path_out = Q6_PATH_EXPERTS_TC;
-    return launched(q6::launch_experts_tc(c, x64, x16, sms, status, (cudaStream_t)s),
+    return launched(q6::launch_experts_tc(c, x64, x16, status, (cudaStream_t)s),
                     "grouped product");
   }
   if (path_out) *path_out = Q6_PATH_EXPERTS_FEW;

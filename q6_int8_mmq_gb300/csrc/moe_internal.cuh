@@ -152,7 +152,7 @@ cudaError_t experts_tc_prepare();
 // x64, x16: tensor maps of the items' rows, 64 x 64 and 64 x 16
 // (encode_rows_map). c.X, c.gather and c.rows are not used.
 cudaError_t launch_experts_tc(const ExpertCall& c, const CUtensorMap& x64, const CUtensorMap& x16,
-                              int sms, unsigned int* status, cudaStream_t s);
+                              unsigned int* status, cudaStream_t s);
 // out [items][K] = the items' rows of X.
 cudaError_t launch_sort_rows(const ExpertCall& c, int K, void* out, cudaStream_t s);
 // The tensor map of 16-bit rows [n][ld] read as boxes of 64 elements x
