@@ -20,48 +20,31 @@
 // was measured at about 60 cycles a request, 4000 for the 256 rows of a stage
 // whose MMAs take 512.
 //
-// Warp roles (16 warps, persistent CTAs, one per SM):
+// Warp roles (20 warps, persistent CTAs, one per SM):
 //   0      loads x
-//   1      CTA 0: issues the pair's MMAs; CTA 1: tells CTA 0 which x stages
-//          have arrived
+//   1      in CTA 0, issues the pair's MMAs
 //   2      TMEM allocation
 //   3      streams the packed weights, one super-block a stage
 //   4-11   dequantise: warps 4-7 the even, 8-11 the odd halves (128 of K) of
 //          the super-blocks
-//   12-15  epilogue
+//   12-19  epilogue: warps 12-15 items 0-127 of a tile, 16-19 the others (or
+//          every other tile of up to 128 items)
 // TMEM: columns 0-255 two accumulators of 128 items (or one of 256), 256-511
 // four A slots of 128 of K.
 // Every wait is bounded (see q6_internal.cuh), and the pair meets once more
 // before either CTA leaves.
-#include <stdint.h>
-
-// Barriers of a pair are waited on with cluster scope.
-namespace q6 {
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity);
-}
-#define MBAR_POLL mbar_try_wait_cluster
 #include "moe_internal.cuh"
 
 namespace q6 {
-
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kTileN = 256;
 constexpr int kXStages = 4, kXStage = 32 * 1024;
-constexpr int kWStages = 3;
+// Packed super-blocks in flight: 54 KB of either format.
+template <int kFmt>
+constexpr int kWStagesOf = kFmt == Q6_FMT_Q4K ? 3 : 2;
+constexpr int kMaxWStages = 3;
 constexpr int kASlots = 4, kACols = 64, kACol0 = 256;
 constexpr int kTmemCols = 512;
 
@@ -70,7 +53,7 @@ enum : uint32_t { kSiteXEmpty = 32, kSiteXFull, kSiteWEmpty, kSiteWFull, kSiteAE
 
 struct Bars {
   uint64_t x_full[kXStages], x_empty[kXStages];
-  uint64_t w_full[kWStages], w_empty[kWStages];
+  uint64_t w_full[kMaxWStages], w_empty[kMaxWStages];
   uint64_t a_full[kASlots], a_empty[kASlots];
   uint64_t d_full[2], d_empty[2];
   uint64_t drain;
@@ -92,9 +75,19 @@ template <int kFmt>
 constexpr int kWTile = kFmt == Q6_FMT_Q4K ? kQ4Tile : kQ6Tile;
 constexpr int kOutWarp = 2048;  // epilogue staging of a warp: 32 items of 64 bytes
 template <int kFmt>
-constexpr int kSmemBytes = 1024 + kXStages * kXStage + kWStages * kWTile<kFmt> + 4 * kOutWarp +
+constexpr int kSmemBytes = 1024 + kXStages * kXStage + kWStagesOf<kFmt> * kWTile<kFmt> + 8 * kOutWarp +
                            (kMaxGroups + 1) * 4 + 12 + (int)sizeof(Bars);
 
+// True in one lane of the converged warp. TMA and MMA instructions take their
+// operands from uniform registers: one elected lane on values that all lanes
+// share issues them several times faster than a lane's own branch.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
   asm volatile(
@@ -141,12 +134,15 @@ __device__ __forceinline__ void arrive_leader_tmem(uint64_t* bar) {
       "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [ra];\n\t}\n" ::"r"(smem_u32(bar))
       : "memory");
 }
-// Arrives once on `bar` of CTA 0 of the pair.
-__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+// A TMA load into this CTA that counts on `bar` of CTA 0 of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                                 int c0, int c1) {
   asm volatile(
       "{\n\t.reg .b32 ra;\n\t"
-      "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n\t}\n" ::"r"(smem_u32(bar))
+      "mapa.shared::cluster.u32 ra, %2, 0;\n\t"
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [ra];\n\t}\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
       : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -169,16 +165,12 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31, %32};" ::"r"(addr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(addr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31])
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
@@ -206,15 +198,6 @@ __device__ __forceinline__ void store_tiles_t(uint32_t addr, uint32_t a, uint32_
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
                "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
-}
-
-// True in one lane of the converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(p));
-  return p != 0;
 }
 
 // Instruction descriptor: f16 or bf16 operands, f32 accumulation, M = 256.
@@ -271,28 +254,24 @@ struct Half<Q6_FMT_Q4K> {
     sc = h ? (head.w & 0x0F0F0F0Fu) | ((head.y >> 2) & 0x30303030u) : head.y & 0x3F3F3F3Fu;
     mn = h ? ((head.w >> 4) & 0x0F0F0F0Fu) | ((head.z >> 2) & 0x30303030u) : head.z & 0x3F3F3F3Fu;
   }
-  // 64 of K (chunks 2 * part and 2 * part + 1 of the half) as 32 words. A code
-  // at bit p becomes 2^(23-p) + q; the offset goes with the min (its rounding
-  // is at most 2^-12 of the scale).
+  // Chunk cc of the half (32 of K) as 16 words. A code at bit p becomes
+  // 2^(23-p) + q; the offset goes with the min (its rounding is at most 2^-12
+  // of the scale).
   template <typename T>
-  __device__ __forceinline__ void expand(int part, uint32_t (&out)[32]) const {
+  __device__ __forceinline__ void expand(int cc, uint32_t (&out)[16]) const {
+    const float s = d * byte_f32(sc, cc), m = -dm * byte_f32(mn, cc);
+    const float c11 = fmaf(-4096.0f, s, m), c15 = fmaf(-256.0f, s, m), c19 = fmaf(-16.0f, s, m),
+                c12 = fmaf(-2048.0f, s, m);
+    const uint64_t ss = f2(s, s), k11 = f2(c11, c11), k15 = f2(c15, c15), k19 = f2(c19, c19),
+                   k12 = f2(c12, c12);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int cc = 2 * part + c;
-      const float s = d * byte_f32(sc, cc), m = -dm * byte_f32(mn, cc);
-      const float c11 = fmaf(-4096.0f, s, m), c15 = fmaf(-256.0f, s, m), c19 = fmaf(-16.0f, s, m),
-                  c12 = fmaf(-2048.0f, s, m);
-      const uint64_t ss = f2(s, s), k11 = f2(c11, c11), k15 = f2(c15, c15), k19 = f2(c19, c19),
-                     k12 = f2(c12, c12);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t w = word4(q[t], cc), a = w << 11, b = w >> 5, e = w >> 16;
-        uint32_t* o = out + 16 * c + 4 * t;
-        o[0] = round2<T>(fma_f2(f2(code_f32(a, 0x7800u, 0x45800000u), code_f32(b, 0x7800u, 0x45800000u)), ss, k11));
-        o[1] = round2<T>(fma_f2(f2(code_f32(a, 0x78000u, 0x43800000u), code_f32(b, 0x78000u, 0x43800000u)), ss, k15));
-        o[2] = round2<T>(fma_f2(f2(code_f32(a, 0x780000u, 0x41800000u), code_f32(b, 0x780000u, 0x41800000u)), ss, k19));
-        o[3] = round2<T>(fma_f2(f2(code_f32(w, 0xF000u, 0x45000000u), code_f32(e, 0xF000u, 0x45000000u)), ss, k12));
-      }
+    for (int t = 0; t < 4; ++t) {
+      const uint32_t w = word4(q[t], cc), a = w << 11, b = w >> 5, e = w >> 16;
+      uint32_t* o = out + 4 * t;
+      o[0] = round2<T>(fma_f2(f2(code_f32(a, 0x7800u, 0x45800000u), code_f32(b, 0x7800u, 0x45800000u)), ss, k11));
+      o[1] = round2<T>(fma_f2(f2(code_f32(a, 0x78000u, 0x43800000u), code_f32(b, 0x78000u, 0x43800000u)), ss, k15));
+      o[2] = round2<T>(fma_f2(f2(code_f32(a, 0x780000u, 0x41800000u), code_f32(b, 0x780000u, 0x41800000u)), ss, k19));
+      o[3] = round2<T>(fma_f2(f2(code_f32(w, 0xF000u, 0x45000000u), code_f32(e, 0xF000u, 0x45000000u)), ss, k12));
     }
   }
 };
@@ -314,27 +293,23 @@ struct Half<Q6_FMT_Q6K> {
     d = __half2float(reinterpret_cast<const __half*>(tile + 13 * 2048)[row]) * inv;
   }
   template <typename T>
-  __device__ __forceinline__ void expand(int part, uint32_t (&out)[32]) const {
+  __device__ __forceinline__ void expand(int cc, uint32_t (&out)[16]) const {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int cc = 2 * part + c;
+    for (int sub = 0; sub < 2; ++sub) {  // runs 0, 1 and 2, 3 of the chunk
+      const float s = d * (byte_f32(sc[sub], cc) - 128.0f);
+      // codes at bits 12 and 16: 2048 + q and 128 + q, and q - 32
+      const uint64_t ss = f2(s, s), k = f2(-2080.0f * s, -160.0f * s);
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {  // runs 0, 1 and 2, 3 of the chunk
-        const float s = d * (byte_f32(sc[sub], cc) - 128.0f);
-        // codes at bits 12 and 16: 2048 + q and 128 + q, and q - 32
-        const uint64_t ss = f2(s, s), k = f2(-2080.0f * s, -160.0f * s);
+      for (int t = 2 * sub; t < 2 * sub + 2; ++t) {
+        const uint32_t w = word4(q[t], cc), hw = cc < 2 ? high[t].x : high[t].y;
 #pragma unroll
-        for (int t = 2 * sub; t < 2 * sub + 2; ++t) {
-          const uint32_t w = word4(q[t], cc), hw = cc < 2 ? high[t].x : high[t].y;
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const int at = 2 * ((cc % 2) * 4 + m);
-            const uint32_t hi = at < 4 ? hw << (4 - at) : hw >> (at - 4);
-            const uint32_t v = ((w >> (4 * m)) & 0x000F000Fu) | (hi & 0x00300030u);
-            out[16 * c + 4 * t + m] =
-                round2<T>(fma_f2(f2(code_f32(v << 12, 0x3F000u, 0x45000000u),
-                                    code_f32(v, 0x3F0000u, 0x43000000u)), ss, k));
-          }
+        for (int m = 0; m < 4; ++m) {
+          const int at = 2 * ((cc % 2) * 4 + m);
+          const uint32_t hi = at < 4 ? hw << (4 - at) : hw >> (at - 4);
+          const uint32_t v = ((w >> (4 * m)) & 0x000F000Fu) | (hi & 0x00300030u);
+          out[4 * t + m] =
+              round2<T>(fma_f2(f2(code_f32(v << 12, 0x3F000u, 0x45000000u),
+                                  code_f32(v, 0x3F0000u, 0x43000000u)), ss, k));
         }
       }
     }
@@ -380,20 +355,24 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* start, int t) 
 __device__ __forceinline__ int band_of(const Args& a, int pair, int rank) {
   return min(2 * pair + rank, a.bands - 1);
 }
-// log2 of the 64-of-K blocks an x stage holds (n / 2 rows of 128 bytes each).
+// A CTA's n / 2 rows of x come as one box of 16, 32, 64 or 128 rows (the rows
+// past n / 2 are loaded and not used: one request a block is worth more than
+// the bytes; requests by several lanes took about 150 cycles each).
+__device__ __forceinline__ int box_of(int n) { return n > 128 ? 3 : n > 64 ? 2 : n > 32 ? 1 : 0; }
+// log2 of the 64-of-K blocks an x stage holds.
 __device__ __forceinline__ int stage_shift(int n) { return n > 128 ? 1 : 2; }
 
 template <typename T, int kFmt, bool kGlu>
 __global__ void __launch_bounds__(kThreads, 1)
-experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
-                  const __grid_constant__ CUtensorMap tmX16, const Args a, unsigned int* status) {
+experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned int* status) {
+  constexpr int kWStages = kWStagesOf<kFmt>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* xring = smem;
   uint8_t* wring = smem + kXStages * kXStage;
   uint8_t* out_stage = wring + kWStages * kWTile<kFmt>;
-  int* start = reinterpret_cast<int*>(out_stage + 4 * kOutWarp);
+  int* start = reinterpret_cast<int*>(out_stage + 8 * kOutWarp);
   Bars* bars = reinterpret_cast<Bars*>(
       (reinterpret_cast<uintptr_t>(start + kMaxGroups + 1) + 7) & ~static_cast<uintptr_t>(7));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -402,7 +381,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kXStages; ++i) {
-      mbar_init(&bars->x_full[i], rank ? 1 : 2);  // CTA 0: its own copies and CTA 1's word
+      mbar_init(&bars->x_full[i], 1);  // both CTAs' copies, in CTA 0
       mbar_init(&bars->x_empty[i], 1);
     }
     for (int i = 0; i < kWStages; ++i) {
@@ -420,8 +399,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     mbar_fence_init();
-    tma_prefetch_desc(&tmX64);
-    tma_prefetch_desc(&tmX16);
+    for (int i = 0; i < RowMaps::kCount; ++i) tma_prefetch_desc(&maps.box[i]);
   }
   if (warp == 2) {
     tmem_alloc_pair(&bars->tmem_base, kTmemCols);
@@ -457,23 +435,22 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
     int g = 0;  // stages issued
     for (int t = cluster; t < total && ok; t += clusters) {
       const Tile w = tile_at(a, start, t);
-      // lane l < loads: one request, of 64 rows or of 16 past the last whole 64
       const int rows = w.n / 2;  // this CTA's
-      const int whole = rows / 64, loads = whole + rows % 64 / 16;
-      const int row = lane < whole ? 64 * lane : 64 * whole + 16 * (lane - whole);
+      const int box = box_of(w.n);
       const int shift = stage_shift(w.n);
+      const int row0 = __shfl_sync(0xffffffffu, (int)w.first + rank * rows, 0);
+      const int block = (16 << box) * 128;
       for (int k = 0; k < 4 * a.sbs; k += 1 << shift) {
         const int slot = g % kXStages;
         if (!(ok = mbar_wait_warp(&bars->x_empty[slot], ((g / kXStages) & 1) ^ 1, abort_flag, status,
                                   kSiteXEmpty)))
           break;
-        if (lane == 0) mbar_arrive_expect_tx(&bars->x_full[slot], (uint32_t)(rows * 128) << shift);
-        __syncwarp();
-        if (lane < loads)
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&bars->x_full[slot], (uint32_t)(2 * block) << shift);
           for (int b = 0; b < 1 << shift; ++b)
-            tma_load_2d(xring + slot * kXStage + (b * rows + row) * 128,
-                        lane < whole ? &tmX64 : &tmX16, &bars->x_full[slot], (k + b) * 64,
-                        (int)w.first + rank * rows + row);
+            tma_load_2d_pair(xring + slot * kXStage + b * block, &maps.box[box], &bars->x_full[slot],
+                        (k + b) * 64, row0);
+        }
         __syncwarp();
         ++g;
       }
@@ -482,65 +459,52 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
     for (int k = g > kXStages ? g - kXStages : 0; k < g && ok; ++k)
       ok = mbar_wait_warp(&bars->x_empty[k % kXStages], (k / kXStages) & 1, abort_flag, status,
                           kSiteXEmpty);
-    if (!ok && lane == 0) {  // copies in flight land before the CTA exits
+    if (!ok && lane == 0) {
+      // Copies in flight land before the CTA exits: CTA 0 waits for those it
+      // counts; a copy whose stage CTA 0 has not opened is given 1 ms.
       volatile int no_abort = 0;
-      for (int k = g > kXStages ? g - kXStages : 0; k < g; ++k)
+      for (int k = g > kXStages ? g - kXStages : 0; k < g && rank == 0; ++k)
         mbar_wait_bounded(&bars->x_full[k % kXStages], (k / kXStages) & 1, &no_abort, status,
                           kSiteXFull);
+      for (const long long t0 = clock64(); clock64() - t0 < 2100000;) {
+      }
     }
   } else if (warp == 3) {
     // ------------------------------------------------------- packed weights --
-    if (lane == 0) {
-      int g = 0;
-      for (int t = cluster; t < total && ok; t += clusters) {
-        const Tile w = tile_at(a, start, t);
-        const uint8_t* src =
-            a.plane + ((size_t)w.expert * a.bands + band_of(a, w.pair, rank)) *
-                          (size_t)a.sbs * kWTile<kFmt>;
-        for (int sb = 0; sb < a.sbs; ++sb) {
-          const int slot = g % kWStages;
-          if (!(ok = mbar_wait_bounded(&bars->w_empty[slot], ((g / kWStages) & 1) ^ 1, abort_flag,
-                                       status, kSiteWEmpty)))
-            break;
+    int g = 0;
+    for (int t = cluster; t < total && ok; t += clusters) {
+      const Tile w = tile_at(a, start, t);
+      const size_t band = (size_t)w.expert * a.bands + band_of(a, w.pair, rank);
+      const uint8_t* src = a.plane + __shfl_sync(0xffffffffu, band, 0) * (size_t)a.sbs * kWTile<kFmt>;
+      for (int sb = 0; sb < a.sbs; ++sb) {
+        const int slot = g % kWStages;
+        if (!(ok = mbar_wait_warp(&bars->w_empty[slot], ((g / kWStages) & 1) ^ 1, abort_flag, status,
+                                  kSiteWEmpty)))
+          break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&bars->w_full[slot], kWTile<kFmt>);
-          bulk_load(wring + slot * kWTile<kFmt>, src + (size_t)sb * kWTile<kFmt>, kWTile<kFmt>,
-                    &bars->w_full[slot]);
-          ++g;
+          bulk_load(wring + slot * kWTile<kFmt>, src, kWTile<kFmt>, &bars->w_full[slot]);
         }
-      }
-      if (!ok) {
-        volatile int no_abort = 0;
-        for (int k = g > kWStages ? g - kWStages : 0; k < g; ++k)
-          mbar_wait_bounded(&bars->w_full[k % kWStages], (k / kWStages) & 1, &no_abort, status,
-                            kSiteWFull);
+        __syncwarp();
+        src += kWTile<kFmt>;
+        ++g;
       }
     }
-  } else if (warp == 1 && rank == 1) {
-    // ------------------------------------------- CTA 1: its x has arrived --
-    if (lane == 0) {
-      int g = 0;
-      for (int t = cluster; t < total && ok; t += clusters) {
-        const int stages = 4 * a.sbs >> stage_shift(tile_at(a, start, t).n);
-        for (int k = 0; k < stages; ++k, ++g) {
-          const int slot = g % kXStages;
-          if (!(ok = mbar_wait_bounded(&bars->x_full[slot], (g / kXStages) & 1, abort_flag, status,
-                                       kSiteXFull)))
-            break;
-          arrive_leader(&bars->x_full[slot]);
-        }
-      }
+    if (!ok && lane == 0) {
+      volatile int no_abort = 0;
+      for (int k = g > kWStages ? g - kWStages : 0; k < g; ++k)
+        mbar_wait_bounded(&bars->w_full[k % kWStages], (k / kWStages) & 1, &no_abort, status,
+                          kSiteWFull);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------------------------ MMA --
-    // The whole warp walks the stages on values that are the same in all
-    // lanes, one elected lane issues: the MMA takes its addresses from uniform
-    // registers, and values of a single lane's own branch have to be moved
-    // there one by one (measured: 700 cycles for the issue of 64 of K).
+    // (Issued from one lane's own branch, 64 of K took 700 cycles.)
     int gx = 0, ga = 0, next = 0, uses0 = 0, uses1 = 0;
     for (int t = cluster; t < total && ok; t += clusters) {
       const int n = __shfl_sync(0xffffffffu, tile_at(a, start, t).n, 0);
       const int mask = (1 << stage_shift(n)) - 1;
       const uint32_t idesc = idesc_of<T>(n);
+      const int x_block = (16 << box_of(n)) * 128;
       const bool both = n > 128, first = both || next == 0, second = both || next == 1;
       if (first)
         ok = mbar_wait_warp(&bars->d_empty[0], (uses0 & 1) ^ 1, abort_flag, status, kSiteDEmpty);
@@ -561,7 +525,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
                                                   status, kSiteXFull)))
             break;
           tc_fence_after();
-          const uint32_t b = sw128_desc_lo(smem_u32(xring) + xs * kXStage + block * n * 64);
+          const uint32_t b = sw128_desc_lo(smem_u32(xring) + xs * kXStage + block * x_block);
           const uint32_t at = tmem + (uint32_t)(kACol0 + as * kACols + half * 32);
           if (elect_one()) {
 #pragma unroll
@@ -612,10 +576,10 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
         tc_fence_after();
         const uint32_t dst = tmem + lanes + (uint32_t)(kACol0 + as * kACols);
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          uint32_t v[32];
-          half.template expand<T>(part, v);
-          tmem_st32(dst + 32 * part, v);
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t v[16];
+          half.template expand<T>(cc, v);
+          tmem_st16(dst + 16 * cc, v);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->w_empty[ws]);
@@ -634,95 +598,93 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
     // Thread (r, c) of a warp, r = lane / 4, holds rows 16 h + r and 16 h + 8 +
     // r of its 32 and items 8 j + 2 c, + 1: pairs of items go to shared memory
     // transposed, [item][row], and from there to Y in 16-byte pieces.
-    const int q = warp % 4;
+    const int q = warp % 4, me = (warp - 12) / 4;   // me: the accumulator half
     T* Y = static_cast<T*>(a.Y);
     constexpr int kCols = kGlu ? 16 : 32;          // output features of a warp
     constexpr int kUnits = kCols / 8;              // 16-byte units of an item
-    uint8_t* stage = out_stage + q * kOutWarp;
+    uint8_t* stage = out_stage + (warp - 12) * kOutWarp;
     // items of no expert: zeros
     for (long long i = a.offsets[a.E] + (long long)blockIdx.x; i < a.offsets[a.E + 1];
          i += gridDim.x)
-      for (int m = 32 * q + lane; m < a.out; m += 128) Y[i * a.ldy + m] = from_f32<T>(0.0f);
-    int next = 0, uses[2] = {0, 0};
+      for (int m = 128 * me + 32 * q + lane; m < a.out; m += 256)
+        Y[i * a.ldy + m] = from_f32<T>(0.0f);
+    int next = 0, uses = 0;
     for (int t = cluster; t < total && ok; t += clusters) {
       const Tile w = tile_at(a, start, t);
+      const bool both = w.n > 128, here = both || next == me;
+      next = both ? 0 : next ^ 1;
+      if (!here) continue;
       const int band = band_of(a, w.pair, rank);
       const bool mine = 2 * w.pair + rank < a.bands;
       const float* sc = a.scale + ((size_t)w.expert * a.bands + band) * kBand + 32 * q + (lane >> 2);
       const float scale[4] = {sc[0], sc[8], sc[16], sc[24]};
-      const bool both = w.n > 128;
-      const int d0 = both ? 0 : next;
-      const int m0 = (band * 4 + q) * kCols;     // this warp's first output feature
-      for (int d = d0; d <= (both ? 1 : d0); ++d) {
-        if (!(ok = mbar_wait_warp(&bars->d_full[d], uses[d] & 1, abort_flag, status, kSiteDFull)))
-          break;
-        ++uses[d];
-        tc_fence_after();
-        const int c1 = both ? (d ? w.n : 128) : w.n;
-        for (int c0 = both ? 128 * d : 0; c0 < c1; c0 += 32) {
-          uint32_t v[2][16];
-          const uint32_t src =
-              tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(both ? c0 : 128 * d0 + c0);
-          tmem_ld_frag(src, v[0]);
-          tmem_ld_frag(src + (16u << 16), v[1]);
-          tmem_wait_frag(v[0], v[1]);
-          if (c0 + 32 >= c1) {  // the accumulator is in registers
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_leader_tmem(&bars->d_empty[d]);
-          }
-          __syncwarp();  // the last piece has left the staging
-          uint32_t p[4][4];  // [j][unit]: item pairs of 8-row blocks
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float f[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                f[e] = __uint_as_float(v[h][4 * j + e]) * scale[2 * h + e / 2];
-              if constexpr (kGlu) {
-                p[j][h] = pack2<T>(silu(f[0]) * f[2], silu(f[1]) * f[3]);
-              } else {
-                p[j][2 * h] = pack2<T>(f[0], f[1]);
-                p[j][2 * h + 1] = pack2<T>(f[2], f[3]);
-              }
-            }
-          if constexpr (kGlu) {
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              const int item = 8 * (j + (lane >> 4)) + (lane & 7), unit = (lane >> 3) & 1;
-              store_tiles_t(smem_u32(stage + item * 32 + (unit ^ ((item >> 2) & 1)) * 16), p[j][0],
-                            p[j][1], p[j + 1][0], p[j + 1][1]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int item = 8 * j + (lane & 7), unit = lane >> 3;
-              store_tiles_t(smem_u32(stage + item * 64 + (unit ^ ((item >> 1) & 3)) * 16), p[j][0],
-                            p[j][1], p[j][2], p[j][3]);
-            }
-          }
+      const int m0 = (band * 4 + q) * kCols;       // this warp's first output feature
+      const int item0 = both ? 128 * me : 0;
+      const int cols = min(128, w.n - item0), count = mine ? w.count - item0 : 0;
+      const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(128 * me);
+      if (!(ok = mbar_wait_warp(&bars->d_full[me], uses & 1, abort_flag, status, kSiteDFull))) break;
+      ++uses;
+      tc_fence_after();
+      for (int c0 = 0; c0 < cols; c0 += 32) {
+        uint32_t v[2][16];
+        tmem_ld_frag(src + c0, v[0]);
+        tmem_ld_frag(src + c0 + (16u << 16), v[1]);
+        tmem_wait_frag(v[0], v[1]);
+        if (c0 + 32 >= cols) {  // the accumulator is in registers
+          tc_fence_before();
           __syncwarp();
+          if (lane == 0) arrive_leader_tmem(&bars->d_empty[me]);
+        }
+        __syncwarp();  // the last piece has left the staging
+        uint32_t p[4][4];  // [j][unit]: item pairs of 8-row blocks
 #pragma unroll
-          for (int i = lane; i < 32 * kUnits; i += 32) {
-            const int item = i / kUnits, unit = i % kUnits, m = m0 + 8 * unit;
-            const int at = kGlu ? unit ^ ((item >> 2) & 1) : unit ^ ((item >> 1) & 3);
-            const uint4 u = *reinterpret_cast<const uint4*>(stage + (item * kUnits + at) * 16);
-            if (c0 + item >= w.count || m >= a.out || !mine) continue;
-            T* y = Y + (w.first + c0 + item) * a.ldy + m;
-            if (a.vec && m + 8 <= a.out) {
-              *reinterpret_cast<uint4*>(y) = u;
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              f[e] = __uint_as_float(v[h][4 * j + e]) * scale[2 * h + e / 2];
+            if constexpr (kGlu) {
+              p[j][h] = pack2<T>(silu(f[0]) * f[2], silu(f[1]) * f[3]);
             } else {
-              const T* one = reinterpret_cast<const T*>(&u);
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (m + e < a.out) y[e] = one[e];
+              p[j][2 * h] = pack2<T>(f[0], f[1]);
+              p[j][2 * h + 1] = pack2<T>(f[2], f[3]);
             }
+          }
+        if constexpr (kGlu) {
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            const int item = 8 * (j + (lane >> 4)) + (lane & 7), unit = (lane >> 3) & 1;
+            store_tiles_t(smem_u32(stage + item * 32 + (unit ^ ((item >> 2) & 1)) * 16), p[j][0],
+                          p[j][1], p[j + 1][0], p[j + 1][1]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int item = 8 * j + (lane & 7), unit = lane >> 3;
+            store_tiles_t(smem_u32(stage + item * 64 + (unit ^ ((item >> 1) & 3)) * 16), p[j][0],
+                          p[j][1], p[j][2], p[j][3]);
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = lane; i < 32 * kUnits; i += 32) {
+          const int item = i / kUnits, unit = i % kUnits, m = m0 + 8 * unit;
+          const int at = kGlu ? unit ^ ((item >> 2) & 1) : unit ^ ((item >> 1) & 3);
+          const uint4 u = *reinterpret_cast<const uint4*>(stage + (item * kUnits + at) * 16);
+          if (c0 + item >= count || m >= a.out) continue;
+          T* y = Y + (w.first + item0 + c0 + item) * a.ldy + m;
+          if (a.vec && m + 8 <= a.out) {
+            *reinterpret_cast<uint4*>(y) = u;
+          } else {
+            const T* one = reinterpret_cast<const T*>(&u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (m + e < a.out) y[e] = one[e];
           }
         }
       }
-      next = both ? 0 : next ^ 1;
     }
   }
   tc_fence_before();
@@ -734,7 +696,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmX64,
   }
 }
 
-typedef void (*Kernel)(const CUtensorMap, const CUtensorMap, const Args, unsigned int*);
+typedef void (*Kernel)(const RowMaps, const Args, unsigned int*);
 template <typename T>
 Kernel pick_t(int fmt, int swiglu) {
   if (fmt == Q6_FMT_Q4K)
@@ -796,8 +758,8 @@ cudaError_t experts_tc_prepare() {
   return cudaSuccess;
 }
 
-cudaError_t launch_experts_tc(const ExpertCall& c, const CUtensorMap& x64, const CUtensorMap& x16,
-                              unsigned int* status, cudaStream_t s) {
+cudaError_t launch_experts_tc(const ExpertCall& c, const RowMaps& x, unsigned int* status,
+                              cudaStream_t s) {
   Args a;
   a.plane = c.plane;
   a.scale = reinterpret_cast<const float*>(c.plane + c.g.scale_off);
@@ -815,7 +777,7 @@ cudaError_t launch_experts_tc(const ExpertCall& c, const CUtensorMap& x64, const
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   pair_launch(&cfg, attr, c.fmt, (unsigned)(tiles < most ? tiles : most), s);
-  return cudaLaunchKernelEx(&cfg, pick(c.type, c.fmt, c.swiglu), x64, x16, a, status);
+  return cudaLaunchKernelEx(&cfg, pick(c.type, c.fmt, c.swiglu), x, a, status);
 }
 
 // ------------------------------------------------------- x in item order ---

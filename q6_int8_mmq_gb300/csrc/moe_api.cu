@@ -177,15 +177,12 @@ int q6_experts_mmq(int fmt, const void* plane, int E, int M, int K, int swiglu, 
     if (need && !aligned(workspace, 256)) return fail(Q6_EALIGN, "workspace must be 256-byte aligned");
     const void* x = need ? workspace : X;
     const int64_t n = need ? items : nx, ld = need ? K : ldx;
-    CUtensorMap x64, x16;
-    if ((rc = q6::encode_rows_map(&x64, type, x, n, K, ld, 64)) ||
-        (rc = q6::encode_rows_map(&x16, type, x, n, K, ld, 16)))
-      return rc;
+    q6::RowMaps maps;
+    if ((rc = q6::encode_row_maps(&maps, type, x, n, K, ld))) return rc;
     if (need && (rc = launched(q6::launch_sort_rows(c, K, workspace, (cudaStream_t)s), "row sort")))
       return rc;
     if (path_out) *path_out = Q6_PATH_EXPERTS_TC;
-    return launched(q6::launch_experts_tc(c, x64, x16, status, (cudaStream_t)s),
-                    "grouped product");
+    return launched(q6::launch_experts_tc(c, maps, status, (cudaStream_t)s), "grouped product");
   }
   if (path_out) *path_out = Q6_PATH_EXPERTS_FEW;
   return launched(q6::launch_experts_few(c, (cudaStream_t)s), "grouped product");

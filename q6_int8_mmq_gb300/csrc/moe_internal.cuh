@@ -149,16 +149,18 @@ struct ExpertCall {
 cudaError_t experts_few_prepare();
 cudaError_t launch_experts_few(const ExpertCall& c, cudaStream_t s);
 cudaError_t experts_tc_prepare();
-// x64, x16: tensor maps of the items' rows, 64 x 64 and 64 x 16
-// (encode_rows_map). c.X, c.gather and c.rows are not used.
-cudaError_t launch_experts_tc(const ExpertCall& c, const CUtensorMap& x64, const CUtensorMap& x16,
-                              unsigned int* status, cudaStream_t s);
+// Tensor maps of 16-bit rows [n][ld] as boxes of 64 elements x 16, 32, 64 and
+// 128 rows with the 128-byte swizzle.
+struct RowMaps {
+  static constexpr int kCount = 4;
+  CUtensorMap box[kCount];
+};
+int encode_row_maps(RowMaps* maps, int type, const void* X, long long n, int K, long long ld);
+// x: the items' rows in order; c.X, c.gather and c.rows are not used.
+cudaError_t launch_experts_tc(const ExpertCall& c, const RowMaps& x, unsigned int* status,
+                              cudaStream_t s);
 // out [items][K] = the items' rows of X.
 cudaError_t launch_sort_rows(const ExpertCall& c, int K, void* out, cudaStream_t s);
-// The tensor map of 16-bit rows [n][ld] read as boxes of 64 elements x
-// `box_rows` rows with the 128-byte swizzle (api.cu).
-int encode_rows_map(CUtensorMap* map, int type, const void* X, long long n, int K, long long ld,
-                    int box_rows);
 
 }  // namespace q6
 
