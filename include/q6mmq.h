@@ -563,9 +563,9 @@ int q6_pack_experts(int fmt, const uint8_t *raw, int E, int M, int K, int swiglu
  *   items : the grouping's number of items (offsets[E + 1]).
  *   workspace : device, 256-byte aligned, at least
  *       q6_experts_workspace_bytes() (NULL when that is 0): the rows of X in
- *       item order, where the tensor cores run on gathered rows.
+ *       item order as binary16 and their scales, for the tensor cores.
  *   path_out : NULL or receives the Q6_PATH_EXPERTS_* that ran. */
-int q6_experts_workspace_bytes(int E, int K, int64_t items, int gather, size_t *bytes);
+int q6_experts_workspace_bytes(int E, int K, int type, int64_t items, int gather, size_t *bytes);
 int q6_experts_mmq(int fmt, const void *plane, int E, int M, int K, int swiglu, const void *X,
                    int type, int64_t nx, int64_t ldx, int gather, const int32_t *offsets,
                    const int32_t *rows, int64_t items, void *Y, int64_t ldy, void *workspace,

@@ -75,7 +75,7 @@ SIGNATURES = [
     ("q6_moe_route", _I, [_P, _I, _I, _I, _L, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     ("q6_expert_plane_bytes", _I, [_I, _I, _I, _I, _I, _SZ]),
     ("q6_pack_experts", _I, [_I, _P, _I, _I, _I, _I, _P, _P]),
-    ("q6_experts_workspace_bytes", _I, [_I, _I, _L, _I, _SZ]),
+    ("q6_experts_workspace_bytes", _I, [_I, _I, _I, _L, _I, _SZ]),
     ("q6_experts_mmq", _I, [_I, _P, _I, _I, _I, _I, _P, _I, _L, _L, _I, _P, _P, _L, _P, _L, _P,
                             ctypes.c_size_t, _IP, _P]),
     ("q6_moe_combine", _I, [_P, _I, _L, _P, _P, _I, _I, _I, _P, _L, _P, _L, _P]),

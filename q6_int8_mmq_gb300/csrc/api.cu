@@ -196,12 +196,10 @@ int require_device(unsigned int** status) {
   return rc;
 }
 int readable_raw(const uint8_t* raw, const uint8_t** src) { return device_readable(raw, src); }
-int encode_row_maps(RowMaps* maps, int type, const void* X, long long n, int K, long long ld) {
+int encode_row_maps(RowMaps* maps, const void* X, long long n, int K, long long ld) {
   for (int i = 0; i < RowMaps::kCount; ++i) {
-    const int rc = encode_2d(&maps->box[i],
-                             type == Q6_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                             X, (uint64_t)K, (uint64_t)n, (uint64_t)ld * 2, 64, 16u << i,
+    const int rc = encode_2d(&maps->box[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, X, (uint64_t)K,
+                             (uint64_t)n, (uint64_t)ld * 2, 64, 16u << i,
                              CU_TENSOR_MAP_SWIZZLE_128B, "X");
     if (rc) return rc;
   }

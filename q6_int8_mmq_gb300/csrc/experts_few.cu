@@ -59,24 +59,10 @@ __device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
                : "l"(p));
   return v;
 }
-__device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
 constexpr uint32_t kH2_32 = 0x50005000u;        // (32, 32)
 constexpr uint32_t kH2_m32768 = 0xF800F800u;    // (-32768, -32768)
 constexpr uint32_t kH2_m36864 = 0xF880F880u;    // (-36864, -36864)
 constexpr uint32_t kH2_m2p19 = 0x80208020u;     // (-2^-19, -2^-19)
-
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
 
 // One lane's share of one super-block of 16 rows: rows g and g + 8.
 template <int kFmt>
@@ -141,7 +127,7 @@ __device__ __forceinline__ void multiply(const Block<Q6_FMT_Q4K>& b, const uint4
     uint32_t a[2][4];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const uint32_t w = word(b.q[r][c / 4], c % 4);
+      const uint32_t w = word4(b.q[r][c / 4], c % 4);
       const uint32_t s1 = __byte_perm(sc[r][c / 4], 0x64u, 0x4040u | (c % 4) << 8 | (c % 4));
       const uint32_t s = hfma2u(s1, kH2_32, kH2_m32768);  // 32 * sc
 #pragma unroll
@@ -180,18 +166,15 @@ __device__ __forceinline__ void multiply(const Block<Q6_FMT_Q6K>& b, const uint4
     uint32_t a[2][4];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const uint32_t w = word(b.q[r][c / 4], c % 4);
-      const uint32_t hw = word(b.high[r], c / 2);
+      const uint32_t w = word4(b.q[r][c / 4], c % 4);
+      const uint32_t hw = word4(b.high[r], c / 2);
       const uint32_t sw = c < 4 ? b.sc[r].x : b.sc[r].y;
       const uint32_t s1 = __byte_perm(sw, 0x64u, 0x4040u | (c % 4) << 8 | (c % 4));
       const uint32_t s = hfma2u(s1, kH2_32, kH2_m36864);  // 32 * sc
       const uint32_t o = hmul2u(s, kH2_m2p19);             // -32 * 2^-24 * 32 * sc
+      q6_pairs(w, hw, c % 2, a[r]);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int at = 2 * ((c % 2) * 4 + m);
-        const uint32_t hi = at < 4 ? hw << (4 - at) : hw >> (at - 4);
-        a[r][m] = hfma2u(((w >> (4 * m)) & 0x000F000Fu) | (hi & 0x00300030u), s, o);
-      }
+      for (int m = 0; m < 4; ++m) a[r][m] = hfma2u(a[r][m], s, o);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -230,7 +213,7 @@ __device__ __forceinline__ void stage_x(const Args& a, long long first, int vali
       const uint4 v = *reinterpret_cast<const uint4*>(X + r * a.ldx + (sb0 + sb) * 256 + lane * 8);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 p = unpack2<T>(word(v, i));
+        const float2 p = unpack2<T>(word4(v, i));
         f[2 * i] = p.x, f[2 * i + 1] = p.y;
       }
     }

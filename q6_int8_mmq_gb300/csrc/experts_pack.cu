@@ -69,7 +69,7 @@ expert_pack_kernel(const uint8_t* raw, int M, int swiglu, int bands, int sbs, ui
       uint32_t w[4] = {};
       for (int c = 0; c < 8; ++c)
         for (int i = 0; i < 8; ++i)
-          w[c / 2] |= (code(32 * c + 8 * t + i) >> 4) << (2 * ((c % 2) * 4 + i / 2) + 16 * (i % 2));
+          w[c / 2] |= (code(32 * c + 8 * t + i) >> 4) << (4 * (i / 2) + 2 * (c % 2) + 16 * (i % 2));
       unit(8 + t, w);
     }
     uint32_t w[4] = {};
@@ -103,7 +103,7 @@ expert_scale_kernel(const uint8_t* plane, int sbs, float* scale) {
     }
     if (v > most && v < 1e30f) most = v;  // an infinite or NaN scale shows whatever e is
   }
-  scale[band * kBand + row] = most > 0.0f ? ldexpf(1.0f, ilogbf(most) + 1 - 15) : 1.0f;
+  scale[band * kBand + row] = most > 0.0f ? ldexpf(1.0f, ilogbf(most) + 1 - 10) : 1.0f;
 }
 
 template <int kRaw>

@@ -11,14 +11,22 @@
 // (measured, 8192 items of 11008 x 4096: 621 us alone).
 //
 // The weights are dequantised inside the kernel, once per tile: thread =
-// weight row, f32 arithmetic (w = d * sc * q - dmin * m times a power of two
-// of the row), one rounding to the activations' 16-bit type, the result
-// stored straight into TMEM, where the MMA takes its A operand from. Packed
-// weights are all that memory and shared memory ever see. x comes in item
-// order (a gathering call copies the rows into its workspace first) by TMA,
-// as 128-byte-swizzled K-major tiles. TMA's own row gather (4 rows a request)
-// was measured at about 60 cycles a request, 4000 for the 256 rows of a stage
-// whose MMAs take 512.
+// weight row, binary16 pairs, the result stored straight into TMEM, where the
+// MMA takes its A operand from. Packed weights are all that memory and shared
+// memory ever see. A code is the binary16 subnormal q * 2^-24; with sc * 2^9
+// it makes sc * q exactly, and one fused multiply-add with d and -dmin * m
+// (all times a power of two of the row) makes the weight: what is rounded to
+// 11 bits is dmin * m and the weight (q6_K: sc * (q - 32) beyond 2048, and the
+// weight), an eighth of the rounding of a bf16 Y. For a binary16 Y that would
+// show, so there the weight is formed in f32 and rounded once (2.6 instead of
+// 1.8 instructions a weight; q6_K 3.8 instead of 2.4).
+//
+// x comes as binary16 in item order: bf16 rows scaled by a power of two (exact
+// down to 2^-32 of the row's largest value), gathered ones copied, by a kernel
+// before this one; binary16 rows that are in order are read where they are.
+// TMA loads them as 128-byte-swizzled K-major tiles. (Gathering with TMA's own
+// row gather, 4 rows a request, was measured at about 60 cycles a request,
+// 4000 for the 256 rows of a stage whose MMAs take 512.)
 //
 // Warp roles (20 warps, persistent CTAs, one per SM):
 //   0      loads x
@@ -64,6 +72,7 @@ struct Bars {
 struct Args {
   const uint8_t* plane;
   const float* scale;  // 2^e per plane row
+  const float* xscale;  // per item, or NULL: 1
   const int32_t* offsets;
   void* Y;
   long long ldy;
@@ -200,16 +209,21 @@ __device__ __forceinline__ void store_tiles_t(uint32_t addr, uint32_t a, uint32_
                : "memory");
 }
 
-// Instruction descriptor: f16 or bf16 operands, f32 accumulation, M = 256.
-template <typename T>
-__device__ __forceinline__ uint32_t idesc_of(int n) {
-  const uint32_t type = sizeof(T) == 2 && __is_same(T, __nv_bfloat16) ? 1u : 0u;
-  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(n >> 3) << 17) | (16u << 24);
+// ------------------------------------------------------------ dequantising ---
+constexpr uint32_t kH2_512 = 0x60006000u, kH2_256 = 0x5C005C00u, kH2_m2p19 = 0x80208020u;
+
+// A byte of a word as a binary16 pair, plus 1024.
+__device__ __forceinline__ uint32_t byte_h2(uint32_t w, int i) {
+  return __byte_perm(w, 0x64u, 0x4040u | i << 8 | i);
+}
+// v * 2^k as a binary16 pair (both halves).
+__device__ __forceinline__ uint32_t splat_h2(float v) {
+  const __half2 h = __float2half2_rn(v);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// ------------------------------------------------------------ dequantising ---
-// q + offset as a float from a code in bits p.. of x: the exponent of
-// 2^(23 - p) makes the code's lowest bit a 1.
+// The same in f32: a code in bits p.. of x, with the exponent of 2^(23 - p)
+// above it, is the float 2^(23 - p) + code.
 __device__ __forceinline__ float code_f32(uint32_t x, uint32_t mask, uint32_t magic) {
   return __uint_as_float((x & mask) | magic);
 }
@@ -218,19 +232,13 @@ __device__ __forceinline__ uint64_t f2(float a, float b) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+// a * b + c on two floats, then rounded to a binary16 pair.
+__device__ __forceinline__ uint32_t fma_round(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-template <typename T>
-__device__ __forceinline__ uint32_t round2(uint64_t v) {
-  float a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-  return pack2<T>(a, b);
-}
-__device__ __forceinline__ uint32_t word4(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+  return pack2<__half>(x, y);
 }
 __device__ __forceinline__ float byte_f32(uint32_t w, int i) {
   return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | i)) - 8388608.0f;
@@ -242,36 +250,50 @@ struct Half;
 template <>
 struct Half<Q6_FMT_Q4K> {
   uint4 q[4];
-  uint32_t sc, mn;
-  float d, dm;
+  uint32_t sc, mn, d, dm;
+  float df, dmf;
   __device__ __forceinline__ void load(const uint8_t* tile, int row, int h, float inv) {
     const uint4* p = reinterpret_cast<const uint4*>(tile) + row;
     const uint4 head = p[0];
 #pragma unroll
     for (int t = 0; t < 4; ++t) q[t] = p[(1 + 2 * t + h) * kBand];
     const float2 dd = unpack2<__half>(head.x);
-    d = dd.x * inv, dm = dd.y * inv;
+    df = dd.x * inv, dmf = -dd.y * inv;
+    d = splat_h2(df * 32768.0f), dm = splat_h2(dmf);
     sc = h ? (head.w & 0x0F0F0F0Fu) | ((head.y >> 2) & 0x30303030u) : head.y & 0x3F3F3F3Fu;
     mn = h ? ((head.w >> 4) & 0x0F0F0F0Fu) | ((head.z >> 2) & 0x30303030u) : head.z & 0x3F3F3F3Fu;
   }
-  // Chunk cc of the half (32 of K) as 16 words. A code at bit p becomes
-  // 2^(23-p) + q; the offset goes with the min (its rounding is at most 2^-12
-  // of the scale).
-  template <typename T>
+  // Chunk cc of the half (32 of K) as 16 words.
   __device__ __forceinline__ void expand(int cc, uint32_t (&out)[16]) const {
-    const float s = d * byte_f32(sc, cc), m = -dm * byte_f32(mn, cc);
+    const uint32_t s = hmul2u(hsub2u(byte_h2(sc, cc), kH2_1024), kH2_512);   // sc * 2^9
+    const uint32_t m = hmul2u(hsub2u(byte_h2(mn, cc), kH2_1024), dm);        // -dmin * m
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint32_t w = word4(q[t], cc);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        out[4 * t + i] = hfma2u(hmul2u((w >> (4 * i)) & 0x000F000Fu, s), d, m);
+    }
+  }
+  // The offsets of the codes go with the min (rounded to at most 2^-12 of the
+  // scale).
+  __device__ __forceinline__ void expand_f32(int cc, uint32_t (&out)[16]) const {
+    const float s = df * byte_f32(sc, cc), m = dmf * byte_f32(mn, cc);
     const float c11 = fmaf(-4096.0f, s, m), c15 = fmaf(-256.0f, s, m), c19 = fmaf(-16.0f, s, m),
                 c12 = fmaf(-2048.0f, s, m);
-    const uint64_t ss = f2(s, s), k11 = f2(c11, c11), k15 = f2(c15, c15), k19 = f2(c19, c19),
-                   k12 = f2(c12, c12);
+    const uint64_t ss = f2(s, s);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const uint32_t w = word4(q[t], cc), a = w << 11, b = w >> 5, e = w >> 16;
       uint32_t* o = out + 4 * t;
-      o[0] = round2<T>(fma_f2(f2(code_f32(a, 0x7800u, 0x45800000u), code_f32(b, 0x7800u, 0x45800000u)), ss, k11));
-      o[1] = round2<T>(fma_f2(f2(code_f32(a, 0x78000u, 0x43800000u), code_f32(b, 0x78000u, 0x43800000u)), ss, k15));
-      o[2] = round2<T>(fma_f2(f2(code_f32(a, 0x780000u, 0x41800000u), code_f32(b, 0x780000u, 0x41800000u)), ss, k19));
-      o[3] = round2<T>(fma_f2(f2(code_f32(w, 0xF000u, 0x45000000u), code_f32(e, 0xF000u, 0x45000000u)), ss, k12));
+      o[0] = fma_round(f2(code_f32(a, 0x7800u, 0x45800000u), code_f32(b, 0x7800u, 0x45800000u)), ss,
+                       f2(c11, c11));
+      o[1] = fma_round(f2(code_f32(a, 0x78000u, 0x43800000u), code_f32(b, 0x78000u, 0x43800000u)),
+                       ss, f2(c15, c15));
+      o[2] = fma_round(f2(code_f32(a, 0x780000u, 0x41800000u), code_f32(b, 0x780000u, 0x41800000u)),
+                       ss, f2(c19, c19));
+      o[3] = fma_round(f2(code_f32(w, 0xF000u, 0x45000000u), code_f32(e, 0xF000u, 0x45000000u)), ss,
+                       f2(c12, c12));
     }
   }
 };
@@ -279,8 +301,8 @@ template <>
 struct Half<Q6_FMT_Q6K> {
   uint4 q[4];
   uint2 high[4];
-  uint32_t sc[2];
-  float d;
+  uint32_t sc[2], d;
+  float df;
   __device__ __forceinline__ void load(const uint8_t* tile, int row, int h, float inv) {
     const uint4* p = reinterpret_cast<const uint4*>(tile) + row;
 #pragma unroll
@@ -290,36 +312,44 @@ struct Half<Q6_FMT_Q6K> {
     }
     const uint32_t* s = reinterpret_cast<const uint32_t*>(p + 12 * kBand);
     sc[0] = s[h], sc[1] = s[2 + h];
-    d = __half2float(reinterpret_cast<const __half*>(tile + 13 * 2048)[row]) * inv;
+    df = __half2float(reinterpret_cast<const __half*>(tile + 13 * 2048)[row]) * inv;
+    d = splat_h2(df * 65536.0f);
   }
-  template <typename T>
   __device__ __forceinline__ void expand(int cc, uint32_t (&out)[16]) const {
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {  // runs 0, 1 and 2, 3 of the chunk
-      const float s = d * (byte_f32(sc[sub], cc) - 128.0f);
-      // codes at bits 12 and 16: 2048 + q and 128 + q, and q - 32
+      const uint32_t s = hmul2u(hsub2u(byte_h2(sc[sub], cc), kH2_1152), kH2_256);  // sc * 2^8
+      const uint32_t o = hmul2u(s, kH2_m2p19);                                     // -32 * 2^-24 * s
+#pragma unroll
+      for (int t = 2 * sub; t < 2 * sub + 2; ++t) {
+        uint32_t v[4];
+        q6_pairs(word4(q[t], cc), cc < 2 ? high[t].x : high[t].y, cc % 2, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[4 * t + i] = hmul2u(hfma2u(v[i], s, o), d);
+      }
+    }
+  }
+  // Codes at bits 12 and 16: 2048 + q and 128 + q, less the offset and 32.
+  __device__ __forceinline__ void expand_f32(int cc, uint32_t (&out)[16]) const {
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      const float s = df * (byte_f32(sc[sub], cc) - 128.0f);
       const uint64_t ss = f2(s, s), k = f2(-2080.0f * s, -160.0f * s);
 #pragma unroll
       for (int t = 2 * sub; t < 2 * sub + 2; ++t) {
-        const uint32_t w = word4(q[t], cc), hw = cc < 2 ? high[t].x : high[t].y;
+        uint32_t v[4];
+        q6_pairs(word4(q[t], cc), cc < 2 ? high[t].x : high[t].y, cc % 2, v);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const int at = 2 * ((cc % 2) * 4 + m);
-          const uint32_t hi = at < 4 ? hw << (4 - at) : hw >> (at - 4);
-          const uint32_t v = ((w >> (4 * m)) & 0x000F000Fu) | (hi & 0x00300030u);
-          out[4 * t + m] =
-              round2<T>(fma_f2(f2(code_f32(v << 12, 0x3F000u, 0x45000000u),
-                                  code_f32(v, 0x3F0000u, 0x43000000u)), ss, k));
-        }
+        for (int i = 0; i < 4; ++i)
+          out[4 * t + i] = fma_round(f2(code_f32(v[i] << 12, 0x3F000u, 0x45000000u),
+                                        code_f32(v[i], 0x3F0000u, 0x43000000u)), ss, k);
       }
     }
   }
 };
 
-// x / (1 + exp(-x)), within 2^-20 (exp(-x) past f32 gives 0, as in the limit).
-__device__ __forceinline__ float silu(float x) {
-  return x * __frcp_rn(1.0f + __expf(-x));
-}
+// x / (1 + exp(-x)), within 2^-20 (0 below -87, where it is under 2^-118).
+__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
 
 // ---------------------------------------------------------------- schedule ---
 struct Tile {
@@ -361,6 +391,47 @@ __device__ __forceinline__ int band_of(const Args& a, int pair, int rank) {
 __device__ __forceinline__ int box_of(int n) { return n > 128 ? 3 : n > 64 ? 2 : n > 32 ? 1 : 0; }
 // log2 of the 64-of-K blocks an x stage holds.
 __device__ __forceinline__ int stage_shift(int n) { return n > 128 ? 1 : 2; }
+
+// The MMAs of one tile, by the whole MMA warp; kShift = stage_shift(n).
+struct MmaState {
+  int x, a;  // x stages and A slots used so far
+};
+template <int kShift>
+__device__ __forceinline__ bool tile_mmas(MmaState& st, Bars* bars, const uint8_t* xring,
+                                          uint32_t tmem, uint32_t d_tmem, int n, int sbs,
+                                          volatile int* abort_flag, unsigned int* status) {
+  // f16 operands, f32 accumulation, M = 256
+  const uint32_t idesc = idesc_f16_f32(256, n);
+  const uint32_t x_block = (uint32_t)(16 << box_of(n)) * 128 >> 4;  // in descriptor units
+  const uint32_t x0 = sw128_desc_lo(smem_u32(xring));
+  for (int sb = 0; sb < sbs; ++sb) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {  // A slots: 128 of K
+      const int xs = st.x % kXStages, as = st.a % kASlots;
+      if (kShift == 1 || u == 0)
+        if (!mbar_wait_warp(&bars->x_full[xs], (st.x / kXStages) & 1, abort_flag, status,
+                            kSiteXFull))
+          return false;
+      if (!mbar_wait_warp(&bars->a_full[as], (st.a / kASlots) & 1, abort_flag, status, kSiteAFull))
+        return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t b = x0 + xs * (kXStage >> 4) + (kShift == 1 ? 0 : 2 * u) * x_block;
+        const uint32_t at = tmem + (uint32_t)(kACol0 + as * kACols);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          umma_f16_pair(d_tmem, at + 8 * i, b + (i / 4) * x_block + 2 * (i % 4), idesc,
+                        (uint32_t)(sb > 0 || u > 0 || i > 0));
+        commit_pair(&bars->a_empty[as]);
+        if (kShift == 1 || u == 1) commit_pair(&bars->x_empty[xs]);
+      }
+      __syncwarp();
+      ++st.a;
+      if (kShift == 1 || u == 1) ++st.x;
+    }
+  }
+  return true;
+}
 
 template <typename T, int kFmt, bool kGlu>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -499,12 +570,10 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
   } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------------------------ MMA --
     // (Issued from one lane's own branch, 64 of K took 700 cycles.)
-    int gx = 0, ga = 0, next = 0, uses0 = 0, uses1 = 0;
+    MmaState st = {0, 0};
+    int next = 0, uses0 = 0, uses1 = 0;
     for (int t = cluster; t < total && ok; t += clusters) {
-      const int n = __shfl_sync(0xffffffffu, tile_at(a, start, t).n, 0);
-      const int mask = (1 << stage_shift(n)) - 1;
-      const uint32_t idesc = idesc_of<T>(n);
-      const int x_block = (16 << box_of(n)) * 128;
+      const int n = (int)__reduce_max_sync(0xffffffffu, (unsigned)tile_at(a, start, t).n);
       const bool both = n > 128, first = both || next == 0, second = both || next == 1;
       if (first)
         ok = mbar_wait_warp(&bars->d_empty[0], (uses0 & 1) ^ 1, abort_flag, status, kSiteDEmpty);
@@ -513,33 +582,8 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
       if (!ok) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem + (first ? 0u : 128u);
-      for (int u = 0; u < 2 * a.sbs; ++u) {  // A slots: 128 of K
-        const int as = ga % kASlots;
-        if (!(ok = mbar_wait_warp(&bars->a_full[as], (ga / kASlots) & 1, abort_flag, status,
-                                  kSiteAFull)))
-          break;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int block = (2 * u + half) & mask, xs = gx % kXStages;
-          if (block == 0 && !(ok = mbar_wait_warp(&bars->x_full[xs], (gx / kXStages) & 1, abort_flag,
-                                                  status, kSiteXFull)))
-            break;
-          tc_fence_after();
-          const uint32_t b = sw128_desc_lo(smem_u32(xring) + xs * kXStage + block * x_block);
-          const uint32_t at = tmem + (uint32_t)(kACol0 + as * kACols + half * 32);
-          if (elect_one()) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              umma_f16_pair(d_tmem, at + 8 * i, b + 2 * i, idesc, (uint32_t)(u > 0 || half > 0 || i > 0));
-            if (block == mask) commit_pair(&bars->x_empty[xs]);
-            if (half) commit_pair(&bars->a_empty[as]);
-          }
-          __syncwarp();
-          if (block == mask) ++gx;
-        }
-        if (!ok) break;
-        ++ga;
-      }
+      ok = both ? tile_mmas<1>(st, bars, xring, tmem, d_tmem, n, a.sbs, abort_flag, status)
+                : tile_mmas<2>(st, bars, xring, tmem, d_tmem, n, a.sbs, abort_flag, status);
       if (!ok) break;
       if (elect_one()) {
         if (first) commit_pair(&bars->d_full[0]);
@@ -578,7 +622,10 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) {
           uint32_t v[16];
-          half.template expand<T>(cc, v);
+          if constexpr (__is_same(T, __half))
+            half.expand_f32(cc, v);
+          else
+            half.expand(cc, v);
           tmem_st16(dst + 16 * cc, v);
         }
         __syncwarp();
@@ -602,6 +649,7 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
     T* Y = static_cast<T*>(a.Y);
     constexpr int kCols = kGlu ? 16 : 32;          // output features of a warp
     constexpr int kUnits = kCols / 8;              // 16-byte units of an item
+    constexpr bool kScaled = !__is_same(T, __half);
     uint8_t* stage = out_stage + (warp - 12) * kOutWarp;
     // items of no expert: zeros
     for (long long i = a.offsets[a.E] + (long long)blockIdx.x; i < a.offsets[a.E + 1];
@@ -622,10 +670,24 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
       const int item0 = both ? 128 * me : 0;
       const int cols = min(128, w.n - item0), count = mine ? w.count - item0 : 0;
       const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(128 * me);
+      // lane l holds the scales of items l, 32 + l, ...
+      float xs[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        xs[k] = kScaled && 32 * k + lane < count ? a.xscale[w.first + item0 + 32 * k + lane] : 1.0f;
+      // this lane's first 16-byte unit of a piece, and the step to its next
+      constexpr int kStep = 32 / kUnits;
+      const int item = lane / kUnits, unit = lane % kUnits, m = m0 + 8 * unit;
+      T* y = Y + (w.first + item0 + item) * a.ldy + m;
+      const long long step = (long long)kStep * a.ldy;
+      const bool whole = a.vec && m + 8 <= a.out;
       if (!(ok = mbar_wait_warp(&bars->d_full[me], uses & 1, abort_flag, status, kSiteDFull))) break;
       ++uses;
       tc_fence_after();
-      for (int c0 = 0; c0 < cols; c0 += 32) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c0 = 32 * k;
+        if (c0 >= cols) break;
         uint32_t v[2][16];
         tmem_ld_frag(src + c0, v[0]);
         tmem_ld_frag(src + c0 + (16u << 16), v[1]);
@@ -635,16 +697,18 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
           __syncwarp();
           if (lane == 0) arrive_leader_tmem(&bars->d_empty[me]);
         }
-        __syncwarp();  // the last piece has left the staging
         uint32_t p[4][4];  // [j][unit]: item pairs of 8-row blocks
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j) {
+          const float x0 = kScaled ? __shfl_sync(0xffffffffu, xs[k], 8 * j + 2 * (lane & 3)) : 1.0f;
+          const float x1 =
+              kScaled ? __shfl_sync(0xffffffffu, xs[k], 8 * j + 2 * (lane & 3) + 1) : 1.0f;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float f[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              f[e] = __uint_as_float(v[h][4 * j + e]) * scale[2 * h + e / 2];
+              f[e] = __uint_as_float(v[h][4 * j + e]) * scale[2 * h + e / 2] * (e % 2 ? x1 : x0);
             if constexpr (kGlu) {
               p[j][h] = pack2<T>(silu(f[0]) * f[2], silu(f[1]) * f[3]);
             } else {
@@ -652,30 +716,31 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
               p[j][2 * h + 1] = pack2<T>(f[2], f[3]);
             }
           }
+        }
+        __syncwarp();  // the last piece has left the staging
         if constexpr (kGlu) {
 #pragma unroll
           for (int j = 0; j < 4; j += 2) {
-            const int item = 8 * (j + (lane >> 4)) + (lane & 7), unit = (lane >> 3) & 1;
-            store_tiles_t(smem_u32(stage + item * 32 + (unit ^ ((item >> 2) & 1)) * 16), p[j][0],
-                          p[j][1], p[j + 1][0], p[j + 1][1]);
+            const int i = 8 * (j + (lane >> 4)) + (lane & 7), u = (lane >> 3) & 1;
+            store_tiles_t(smem_u32(stage + i * 32 + (u ^ ((i >> 2) & 1)) * 16), p[j][0], p[j][1],
+                          p[j + 1][0], p[j + 1][1]);
           }
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int item = 8 * j + (lane & 7), unit = lane >> 3;
-            store_tiles_t(smem_u32(stage + item * 64 + (unit ^ ((item >> 1) & 3)) * 16), p[j][0],
-                          p[j][1], p[j][2], p[j][3]);
+            const int i = 8 * j + (lane & 7), u = lane >> 3;
+            store_tiles_t(smem_u32(stage + i * 64 + (u ^ ((i >> 1) & 3)) * 16), p[j][0], p[j][1],
+                          p[j][2], p[j][3]);
           }
         }
         __syncwarp();
 #pragma unroll
-        for (int i = lane; i < 32 * kUnits; i += 32) {
-          const int item = i / kUnits, unit = i % kUnits, m = m0 + 8 * unit;
-          const int at = kGlu ? unit ^ ((item >> 2) & 1) : unit ^ ((item >> 1) & 3);
-          const uint4 u = *reinterpret_cast<const uint4*>(stage + (item * kUnits + at) * 16);
-          if (c0 + item >= count || m >= a.out) continue;
-          T* y = Y + (w.first + item0 + c0 + item) * a.ldy + m;
-          if (a.vec && m + 8 <= a.out) {
+        for (int r = 0; r < kUnits; ++r, y += step) {
+          const int i = item + kStep * r;
+          const int at = kGlu ? unit ^ ((i >> 2) & 1) : unit ^ ((i >> 1) & 3);
+          const uint4 u = *reinterpret_cast<const uint4*>(stage + (i * kUnits + at) * 16);
+          if (c0 + i >= count) continue;
+          if (whole) {
             *reinterpret_cast<uint4*>(y) = u;
           } else {
             const T* one = reinterpret_cast<const T*>(&u);
@@ -758,11 +823,12 @@ cudaError_t experts_tc_prepare() {
   return cudaSuccess;
 }
 
-cudaError_t launch_experts_tc(const ExpertCall& c, const RowMaps& x, unsigned int* status,
-                              cudaStream_t s) {
+cudaError_t launch_experts_tc(const ExpertCall& c, const RowMaps& x, const float* scale,
+                              unsigned int* status, cudaStream_t s) {
   Args a;
   a.plane = c.plane;
   a.scale = reinterpret_cast<const float*>(c.plane + c.g.scale_off);
+  a.xscale = scale;
   a.offsets = c.offsets;
   a.Y = c.Y, a.ldy = c.ldy;
   a.E = c.E, a.bands = c.g.bands, a.sbs = c.g.sbs, a.out = c.g.out;
@@ -782,29 +848,73 @@ cudaError_t launch_experts_tc(const ExpertCall& c, const RowMaps& x, unsigned in
 
 // ------------------------------------------------------- x in item order ---
 namespace {
-constexpr int kSortThreads = 256;
-// out[i] = X[rows[i]], rows of `units` 16-byte units; `per` threads a row.
-__global__ void __launch_bounds__(kSortThreads)
-sort_rows_kernel(const uint4* X, long long ldx, const int32_t* rows, long long items, int units,
-                 int per, uint4* out) {
+constexpr int kRowThreads = 256;
+// One warp an item: xh[i] = its row of X as binary16, bf16 rows times 2^-e with
+// the largest finite value in [2^14, 2^15), and scale[i] = 2^e.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads)
+expert_rows_kernel(const T* X, long long ldx, const int32_t* rows, long long items, int units,
+                   uint4* xh, float* scale) {
   griddep_wait();
   griddep_launch_dependents();
-  const long long i = (long long)blockIdx.x * (kSortThreads / per) + threadIdx.x / per;
+  const long long i = (long long)blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32;
   if (i >= items) return;
-  const uint4* src = X + rows[i] * ldx;
-  uint4* dst = out + i * units;
+  const int lane = threadIdx.x & 31;
+  const uint4* src = reinterpret_cast<const uint4*>(X + (rows ? rows[i] : i) * ldx);
+  uint4* dst = xh + i * units;
+  if constexpr (__is_same(T, __half)) {
 #pragma unroll 4
-  for (int u = threadIdx.x % per; u < units; u += per) dst[u] = src[u];
+    for (int u = lane; u < units; u += 32) dst[u] = src[u];
+  } else {
+    // 16 units at a time stay in registers; longer rows are read again
+    constexpr int kKeep = 16;
+    uint4 v[kKeep];
+    uint32_t most = 0;  // of the values' bits without the sign, infinities and NaN left out
+    auto size = [&](const uint4& u) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w = word4(u, k) & 0x7FFF7FFFu, lo = w & 0xFFFFu, hi = w >> 16;
+        if (lo < 0x7F80u) most = max(most, lo);
+        if (hi < 0x7F80u) most = max(most, hi);
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k)
+      if (lane + 32 * k < units) size(v[k] = src[lane + 32 * k]);
+    for (int u = lane + 32 * kKeep; u < units; u += 32) size(src[u]);
+    most = __reduce_max_sync(0xffffffffu, most);
+    // 2^e and 2^-e normal numbers
+    const int e = min(max((int)(most >> 7) - 127 - 14, -116), 118);
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+    auto half = [&](const uint4& u) {
+      uint32_t h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack2<T>(word4(u, k));
+        h[k] = pack2<__half>(f.x * down, f.y * down);
+      }
+      return make_uint4(h[0], h[1], h[2], h[3]);
+    };
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k)
+      if (lane + 32 * k < units) dst[lane + 32 * k] = half(v[k]);
+    for (int u = lane + 32 * kKeep; u < units; u += 32) dst[u] = half(src[u]);
+    if (lane == 0) scale[i] = __uint_as_float((uint32_t)(127 + e) << 23);
+  }
 }
 }  // namespace
 
-cudaError_t launch_sort_rows(const ExpertCall& c, int K, void* out, cudaStream_t s) {
-  const int units = K / 8;
-  const int per = units >= 128 ? 64 : 32;
-  const long long rows = kSortThreads / per;
-  return launch_pdl(sort_rows_kernel, dim3((unsigned)((c.items + rows - 1) / rows)),
-                    dim3(kSortThreads), 0, s, static_cast<const uint4*>(c.X), c.ldx / 8, c.rows,
-                    c.items, units, per, static_cast<uint4*>(out));
+cudaError_t launch_expert_rows(const ExpertCall& c, int K, __half* xh, float* scale,
+                               cudaStream_t s) {
+  const int32_t* rows = c.gather ? c.rows : nullptr;
+  const dim3 grid((unsigned)((c.items + kRowThreads / 32 - 1) / (kRowThreads / 32)));
+  uint4* out = reinterpret_cast<uint4*>(xh);
+  return c.type == Q6_TYPE_BF16
+             ? launch_pdl(expert_rows_kernel<__nv_bfloat16>, grid, dim3(kRowThreads), 0, s,
+                          static_cast<const __nv_bfloat16*>(c.X), c.ldx, rows, c.items, K / 8, out,
+                          scale)
+             : launch_pdl(expert_rows_kernel<__half>, grid, dim3(kRowThreads), 0, s,
+                          static_cast<const __half*>(c.X), c.ldx, rows, c.items, K / 8, out, scale);
 }
 
 }  // namespace q6

@@ -60,9 +60,12 @@ int check_experts(int fmt, int E, int M, int K, int swiglu) {
 // Items an expert, on average, up to which the few-token kernel runs.
 constexpr int kFewItems = 12;
 bool on_tensor_cores(int64_t items, int E) { return items > kFewItems * (int64_t)E; }
-// Bytes of the X rows in item order that the tensor-core path reads.
-size_t sorted_bytes(int64_t items, int E, int K, int gather) {
-  return gather && on_tensor_cores(items, E) ? (size_t)items * (size_t)K * 2 : 0;
+// Bytes of the binary16 rows in item order that the tensor-core path makes (0:
+// it reads X itself), and where their scales follow.
+size_t rows_bytes(int64_t items, int K) { return q6::round_up((size_t)items * (size_t)K * 2, 256); }
+size_t experts_bytes(int64_t items, int E, int K, int type, int gather) {
+  if (!on_tensor_cores(items, E) || (type == Q6_TYPE_F16 && !gather)) return 0;
+  return rows_bytes(items, K) + (type == Q6_TYPE_BF16 ? (size_t)items * 4 : 0);
 }
 
 bool half_type(int type) { return type == Q6_TYPE_BF16 || type == Q6_TYPE_F16; }
@@ -137,10 +140,10 @@ int q6_pack_experts(int fmt, const uint8_t* raw, int E, int M, int K, int swiglu
                   "expert pack");
 }
 
-int q6_experts_workspace_bytes(int E, int K, int64_t items, int gather, size_t* bytes) {
-  if (E < 1 || K < 1 || K % 256 || items < 0 || !bytes)
-    return fail(Q6_EINVAL, "E >= 1, K a multiple of 256, items >= 0, bytes not NULL");
-  *bytes = sorted_bytes(items, E, K, gather);
+int q6_experts_workspace_bytes(int E, int K, int type, int64_t items, int gather, size_t* bytes) {
+  if (E < 1 || K < 1 || K % 256 || !half_type(type) || items < 0 || !bytes)
+    return fail(Q6_EINVAL, "E >= 1, K a multiple of 256, type bf16 or f16, items >= 0, bytes not NULL");
+  *bytes = experts_bytes(items, E, K, type, gather);
   return Q6_OK;
 }
 
@@ -171,18 +174,24 @@ int q6_experts_mmq(int fmt, const void* plane, int E, int M, int K, int swiglu, 
   c.offsets = offsets, c.rows = rows, c.items = items;
   c.Y = Y, c.ldy = ldy;
   if (on_tensor_cores(items, E)) {
-    const size_t need = sorted_bytes(items, E, K, gather);
+    const size_t need = experts_bytes(items, E, K, type, gather);
     if (need && (!workspace || workspace_bytes < need))
       return fail(Q6_ESIZE, "the product needs a workspace of %zu bytes", need);
     if (need && !aligned(workspace, 256)) return fail(Q6_EALIGN, "workspace must be 256-byte aligned");
-    const void* x = need ? workspace : X;
-    const int64_t n = need ? items : nx, ld = need ? K : ldx;
+    __half* xh = static_cast<__half*>(workspace);
+    float* scale = nullptr;
+    if (type == Q6_TYPE_BF16)
+      scale = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + rows_bytes(items, K));
     q6::RowMaps maps;
-    if ((rc = q6::encode_row_maps(&maps, type, x, n, K, ld))) return rc;
-    if (need && (rc = launched(q6::launch_sort_rows(c, K, workspace, (cudaStream_t)s), "row sort")))
+    if ((rc = need ? q6::encode_row_maps(&maps, xh, items, K, K)
+                   : q6::encode_row_maps(&maps, X, nx, K, ldx)))
+      return rc;
+    if (need && (rc = launched(q6::launch_expert_rows(c, K, xh, scale, (cudaStream_t)s),
+                               "expert rows")))
       return rc;
     if (path_out) *path_out = Q6_PATH_EXPERTS_TC;
-    return launched(q6::launch_experts_tc(c, maps, status, (cudaStream_t)s), "grouped product");
+    return launched(q6::launch_experts_tc(c, maps, scale, status, (cudaStream_t)s),
+                    "grouped product");
   }
   if (path_out) *path_out = Q6_PATH_EXPERTS_FEW;
   return launched(q6::launch_experts_few(c, (cudaStream_t)s), "grouped product");

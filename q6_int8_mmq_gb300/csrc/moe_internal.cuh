@@ -80,6 +80,21 @@ __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
 
 namespace q6 {
 
+// binary16 pairs.
+__device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t word4(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
 // ------------------------------------------------------------ expert plane ---
 // Packed K-quant experts: per expert and band of 128 plane rows, one tile per
 // super-block (256 elements of K), tiles in the order [expert][band][super-
@@ -95,18 +110,30 @@ namespace q6 {
 // chunks 4h..4h+3.
 //   q4_K (9 units): 0: d, dmin (f16) and the 12 raw scale bytes; 1 + j: words.
 //   q6_K (13 units and 256 bytes): j: low-nibble words; 8 + t: the 2-bit
-//     fields of run t, word c/2, pair (c % 2) * 4 + m at bit 2 * that of each
-//     half; 12: the 16 scales plus 128, those of even sub-blocks first; then
-//     d (f16) of the 128 rows.
+//     fields of run t, word c/2, pair m at bit 4 m + 2 (c % 2) of each half;
+//     12: the 16 scales plus 128, those of even sub-blocks first; then d (f16)
+//     of the 128 rows.
 // After the tiles, f32 [E][bands * 128]: 2^e of each row, with e such that
-// every weight of the row times 2^-e is below 2^15 (a binary16 operand plane
-// keeps 11 bits of the large ones and loses only what is 2^-24 of them).
+// every weight of the row times 2^-e is below 2^10 (as binary16 the large ones
+// keep 11 bits, and nothing above 2^-34 of them is lost).
 //
 // Plane rows: the weight's rows, or for gate/up weights (M = 2H raw rows, the
 // H gate rows first) blocks of 16: 8 gate rows, then their 8 up rows.
 constexpr int kBand = 128;
 constexpr int kQ4Tile = 9 * 2048;
 constexpr int kQ6Tile = 13 * 2048 + 256;
+
+// The 6-bit codes of a run of a q6_K chunk (c % 2 = odd), pairs in halves:
+// word w of low nibbles, word h of 2-bit fields.
+__device__ __forceinline__ void q6_pairs(uint32_t w, uint32_t h, int odd, uint32_t (&v)[4]) {
+  // nibbles 0 and 2 with their fields above them, then 1 and 3
+  const uint32_t even = (w & 0x0F0F0F0Fu) | ((h << (odd ? 2 : 4)) & ~0x0F0F0F0Fu);
+  const uint32_t rest = ((w >> 4) & 0x0F0F0F0Fu) | ((odd ? h >> 2 : h) & ~0x0F0F0F0Fu);
+  v[0] = even & 0x003F003Fu;
+  v[1] = rest & 0x003F003Fu;
+  v[2] = (even >> 8) & 0x003F003Fu;
+  v[3] = (rest >> 8) & 0x003F003Fu;
+}
 
 struct ExpertGeom {
   int rows;        // plane rows
@@ -149,18 +176,21 @@ struct ExpertCall {
 cudaError_t experts_few_prepare();
 cudaError_t launch_experts_few(const ExpertCall& c, cudaStream_t s);
 cudaError_t experts_tc_prepare();
-// Tensor maps of 16-bit rows [n][ld] as boxes of 64 elements x 16, 32, 64 and
+// Tensor maps of binary16 rows [n][ld] as boxes of 64 elements x 16, 32, 64 and
 // 128 rows with the 128-byte swizzle.
 struct RowMaps {
   static constexpr int kCount = 4;
   CUtensorMap box[kCount];
 };
-int encode_row_maps(RowMaps* maps, int type, const void* X, long long n, int K, long long ld);
-// x: the items' rows in order; c.X, c.gather and c.rows are not used.
-cudaError_t launch_experts_tc(const ExpertCall& c, const RowMaps& x, unsigned int* status,
-                              cudaStream_t s);
-// out [items][K] = the items' rows of X.
-cudaError_t launch_sort_rows(const ExpertCall& c, int K, void* out, cudaStream_t s);
+int encode_row_maps(RowMaps* maps, const void* X, long long n, int K, long long ld);
+// x: the items' rows as binary16 in order, scale (nullable): f32 [items], what
+// each is multiplied with. c.X, c.gather and c.rows are not used.
+cudaError_t launch_experts_tc(const ExpertCall& c, const RowMaps& x, const float* scale,
+                              unsigned int* status, cudaStream_t s);
+// The items' rows of X as binary16 in item order: xh [items][K], and for bf16
+// (scaled by a power of two of the row) scale [items], that power.
+cudaError_t launch_expert_rows(const ExpertCall& c, int K, __half* xh, float* scale,
+                               cudaStream_t s);
 
 }  // namespace q6
 

@@ -249,9 +249,9 @@ def pack_experts(raw, fmt: str, E: int, M: int, K: int, swiglu: bool = False, st
 
 
 @functools.lru_cache(maxsize=256)
-def experts_workspace_bytes(E: int, K: int, items: int, gather: bool) -> int:
+def experts_workspace_bytes(E: int, K: int, type: int, items: int, gather: bool) -> int:
     b = ctypes.c_size_t()
-    _check(load().q6_experts_workspace_bytes(E, K, items, int(gather), ctypes.byref(b)))
+    _check(load().q6_experts_workspace_bytes(E, K, type, items, int(gather), ctypes.byref(b)))
     return b.value
 
 
@@ -279,7 +279,7 @@ def experts_mmq(w: ExpertWeights, X, groups: Groups, gather: bool = True, out=No
             out = torch.empty(shape, dtype=X.dtype, device=dev)
     else:
         _tensor(out, "out", X.dtype, shape, dev, rows=True)
-    need, ws = experts_workspace_bytes(w.E, w.K, items, bool(gather)), None
+    need, ws = experts_workspace_bytes(w.E, w.K, code, items, bool(gather)), None
     if need:
         with _on(stream):
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
