@@ -848,27 +848,32 @@ cudaError_t launch_experts_tc(const ExpertCall& c, const RowMaps& x, const float
 
 // ------------------------------------------------------- x in item order ---
 namespace {
-constexpr int kRowThreads = 256;
-// One warp an item: xh[i] = its row of X as binary16, bf16 rows times 2^-e with
-// the largest finite value in [2^14, 2^15), and scale[i] = 2^e.
+constexpr int kRowThreads = 128;
+// One block an item: xh[i] = its row of X as binary16, bf16 rows times 2^-e
+// with the largest finite value in [2^14, 2^15), and scale[i] = 2^e.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads)
-expert_rows_kernel(const T* X, long long ldx, const int32_t* rows, long long items, int units,
-                   uint4* xh, float* scale) {
+expert_rows_kernel(const T* X, long long ldx, const int32_t* rows, int units, uint4* xh,
+                   float* scale) {
+  constexpr int kKeep = 4;  // units a thread keeps in registers; longer rows are read again
+  __shared__ uint32_t part[kRowThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
-  const long long i = (long long)blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32;
-  if (i >= items) return;
-  const int lane = threadIdx.x & 31;
+  const long long i = blockIdx.x;
   const uint4* src = reinterpret_cast<const uint4*>(X + (rows ? rows[i] : i) * ldx);
   uint4* dst = xh + i * units;
+  uint4 v[kKeep];
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const int u = threadIdx.x + kRowThreads * k;
+    v[k] = u < units ? src[u] : make_uint4(0, 0, 0, 0);
+  }
   if constexpr (__is_same(T, __half)) {
-#pragma unroll 4
-    for (int u = lane; u < units; u += 32) dst[u] = src[u];
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k)
+      if (threadIdx.x + kRowThreads * k < units) dst[threadIdx.x + kRowThreads * k] = v[k];
+    for (int u = threadIdx.x + kRowThreads * kKeep; u < units; u += kRowThreads) dst[u] = src[u];
   } else {
-    // 16 units at a time stay in registers; longer rows are read again
-    constexpr int kKeep = 16;
-    uint4 v[kKeep];
     uint32_t most = 0;  // of the values' bits without the sign, infinities and NaN left out
     auto size = [&](const uint4& u) {
 #pragma unroll
@@ -879,10 +884,13 @@ expert_rows_kernel(const T* X, long long ldx, const int32_t* rows, long long ite
       }
     };
 #pragma unroll
-    for (int k = 0; k < kKeep; ++k)
-      if (lane + 32 * k < units) size(v[k] = src[lane + 32 * k]);
-    for (int u = lane + 32 * kKeep; u < units; u += 32) size(src[u]);
+    for (int k = 0; k < kKeep; ++k) size(v[k]);
+    for (int u = threadIdx.x + kRowThreads * kKeep; u < units; u += kRowThreads) size(src[u]);
     most = __reduce_max_sync(0xffffffffu, most);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = most;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kRowThreads / 32; ++k) most = max(most, part[k]);
     // 2^e and 2^-e normal numbers
     const int e = min(max((int)(most >> 7) - 127 - 14, -116), 118);
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
@@ -897,9 +905,10 @@ expert_rows_kernel(const T* X, long long ldx, const int32_t* rows, long long ite
     };
 #pragma unroll
     for (int k = 0; k < kKeep; ++k)
-      if (lane + 32 * k < units) dst[lane + 32 * k] = half(v[k]);
-    for (int u = lane + 32 * kKeep; u < units; u += 32) dst[u] = half(src[u]);
-    if (lane == 0) scale[i] = __uint_as_float((uint32_t)(127 + e) << 23);
+      if (threadIdx.x + kRowThreads * k < units) dst[threadIdx.x + kRowThreads * k] = half(v[k]);
+    for (int u = threadIdx.x + kRowThreads * kKeep; u < units; u += kRowThreads)
+      dst[u] = half(src[u]);
+    if (threadIdx.x == 0) scale[i] = __uint_as_float((uint32_t)(127 + e) << 23);
   }
 }
 }  // namespace
@@ -907,14 +916,13 @@ expert_rows_kernel(const T* X, long long ldx, const int32_t* rows, long long ite
 cudaError_t launch_expert_rows(const ExpertCall& c, int K, __half* xh, float* scale,
                                cudaStream_t s) {
   const int32_t* rows = c.gather ? c.rows : nullptr;
-  const dim3 grid((unsigned)((c.items + kRowThreads / 32 - 1) / (kRowThreads / 32)));
+  const dim3 grid((unsigned)c.items);
   uint4* out = reinterpret_cast<uint4*>(xh);
   return c.type == Q6_TYPE_BF16
              ? launch_pdl(expert_rows_kernel<__nv_bfloat16>, grid, dim3(kRowThreads), 0, s,
-                          static_cast<const __nv_bfloat16*>(c.X), c.ldx, rows, c.items, K / 8, out,
-                          scale)
+                          static_cast<const __nv_bfloat16*>(c.X), c.ldx, rows, K / 8, out, scale)
              : launch_pdl(expert_rows_kernel<__half>, grid, dim3(kRowThreads), 0, s,
-                          static_cast<const __half*>(c.X), c.ldx, rows, c.items, K / 8, out, scale);
+                          static_cast<const __half*>(c.X), c.ldx, rows, K / 8, out, scale);
 }
 
 }  // namespace q6
