@@ -197,56 +197,69 @@ __device__ __forceinline__ void multiply(const Block<Q6_FMT_Q6K>& b, const uint4
   }
 }
 
-// Stages super-blocks sb0..sb0+count-1 of tokens tok0.. (zeros past `valid`):
-// one warp per (token, super-block), 8 elements a lane.
+// Stages super-blocks sb0..sb0+count-1 of the `valid` tokens: one warp per
+// (token, super-block), 8 elements a lane, kBatch of them in flight. What is
+// past `valid` stays unwritten: it only meets columns that are not stored.
 template <typename T, int NT>
 __device__ __forceinline__ void stage_x(const Args& a, long long first, int valid, int sb0,
                                         int count, uint4* xs, uint32_t* sums, float* scale) {
-  constexpr int kTok = 8 * NT;
+  constexpr int kTok = 8 * NT, kBatch = 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const T* X = static_cast<const T*>(a.X);
-  for (int w = warp; w < kTok * count; w += kWarps) {
-    const int n = w % kTok, sb = w / kTok;
-    float f[8] = {};
-    if (n < valid) {
+  const T* X = static_cast<const T*>(a.X) + lane * 8;
+  const int total = valid * count;
+  for (int w0 = warp; w0 < total; w0 += kWarps * kBatch) {
+    uint4 v[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int w = w0 + b * kWarps;
+      if (w >= total) break;
+      const int n = w / count, sb = w - n * count;
       const long long r = a.gather ? a.rows[first + n] : first + n;
-      const uint4 v = *reinterpret_cast<const uint4*>(X + r * a.ldx + (sb0 + sb) * 256 + lane * 8);
+      v[b] = *reinterpret_cast<const uint4*>(X + r * a.ldx + (sb0 + sb) * 256);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int w = w0 + b * kWarps;
+      if (w >= total) break;
+      const int n = w / count, sb = w - n * count;
+      float f[8];
+      float most = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 p = unpack2<T>(word4(v, i));
+        const float2 p = unpack2<T>(word4(v[b], i));
         f[2 * i] = p.x, f[2 * i + 1] = p.y;
       }
-    }
-    float most = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float m = fabsf(f[i]);
-      if (m < __int_as_float(0x7f800000)) most = fmaxf(most, m);
-    }
-    // non-negative floats order as their bits
-    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
-    // 2^e with most * 2^-e in [2^9, 2^10), e within [-116, 118] so that both
-    // 2^e and 2^-e are normal
-    const int e = min(max((int)(__float_as_uint(most) >> 23) - 127 - 9, -116), 118);
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-    uint32_t h[4];
-    float s = 0.0f;
+      for (int i = 0; i < 8; ++i) {
+        const float m = fabsf(f[i]);
+        if (m < __int_as_float(0x7f800000)) most = fmaxf(most, m);
+      }
+      // non-negative floats order as their bits
+      most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+      // 2^e with most * 2^-e in [2^9, 2^10), e within [-116, 118] so that both
+      // 2^e and 2^-e are normal
+      const int e = min(max((int)(__float_as_uint(most) >> 23) - 127 - 9, -116), 118);
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+      uint32_t h[4];
+      float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[i] = pack2<__half>(f[2 * i] * down, f[2 * i + 1] * down);
-      const float2 p = unpack2<__half>(h[i]);
-      s += p.x + p.y;
+      for (int i = 0; i < 4; ++i) {
+        h[i] = pack2<__half>(f[2 * i] * down, f[2 * i + 1] * down);
+        const float2 p = unpack2<__half>(h[i]);
+        s += p.x + p.y;
+      }
+      xs[((sb * 8 + (lane >> 2)) * kTok + n) * 4 + (lane & 3)] =
+          make_uint4(h[0], h[1], h[2], h[3]);
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      if ((lane & 3) == 0) {
+        __half* p = reinterpret_cast<__half*>(sums + (sb * kTok + n) * 8);
+        const __half hi = __float2half_rn(s);
+        p[lane >> 2] = hi;
+        p[8 + (lane >> 2)] = __float2half_rn(s - __half2float(hi));
+      }
+      if (lane == 0) scale[sb * kTok + n] = __uint_as_float((uint32_t)(127 + e) << 23);
     }
-    xs[((sb * 8 + (lane >> 2)) * kTok + n) * 4 + (lane & 3)] = make_uint4(h[0], h[1], h[2], h[3]);
-    s += __shfl_xor_sync(0xffffffffu, s, 1);
-    s += __shfl_xor_sync(0xffffffffu, s, 2);
-    if ((lane & 3) == 0) {
-      __half* p = reinterpret_cast<__half*>(sums + (sb * kTok + n) * 8);
-      const __half hi = __float2half_rn(s);
-      p[lane >> 2] = hi;
-      p[8 + (lane >> 2)] = __float2half_rn(s - __half2float(hi));
-    }
-    if (lane == 0) scale[sb * kTok + n] = __uint_as_float((uint32_t)(127 + e) << 23);
   }
 }
 
@@ -391,9 +404,9 @@ cudaError_t launch_experts_few(const ExpertCall& c, cudaStream_t s) {
   a.Y = c.Y, a.ldy = c.ldy;
   a.E = c.E, a.plane_rows = c.g.rows, a.bands = c.g.bands, a.sbs = c.g.sbs, a.out = c.g.out;
   const unsigned experts = (unsigned)(c.items < c.E ? c.items : c.E);
-  // the most rows a CTA (x is staged less often) that leaves four CTAs an SM
-  int R = 8;
-  while (R > 1 && (size_t)experts * (size_t)((c.g.rows + 16 * R - 1) / (16 * R)) < 4 * 152) R /= 2;
+  // the fewest rows a CTA with which all CTAs run at a time (two an SM)
+  int R = 1;
+  while (R < 8 && (size_t)experts * (size_t)((c.g.rows + 16 * R - 1) / (16 * R)) > 2 * 152) R *= 2;
   a.row_groups = R;
   const dim3 grid((unsigned)((c.g.rows + 16 * R - 1) / (16 * R)), experts);
   // what the launch needs of the shared memory: one stage of x, or the sums

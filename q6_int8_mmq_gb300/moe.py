@@ -14,8 +14,8 @@ import ctypes
 import dataclasses
 import functools
 
-from . import (PATH_NAMES, Q6_EINVAL, Q6Error, _check, _ptr, _row_stride, _same_device, _stream,
-               _tensor, load)
+from . import (PATH_NAMES, Q6_EINVAL, Q6Error, _check, _ptr, _row_stride, _same_device, _tensor,
+               load)
 
 FORMATS = {"q4_K": 4, "q6_K": 6}
 BLOCK_BYTES = {"q4_K": 144, "q6_K": 210}
@@ -47,6 +47,17 @@ def _rows2d(t, name, width=None):
         raise Q6Error(Q6_EINVAL, f"{name} must have shape [rows, {width or 'columns'}], not "
                                  f"{tuple(t.shape)}")
     return t.shape[0]
+
+
+def _stream(stream, device):
+    """The raw handle of the stream a call runs on: `stream`, or the current
+    one of the tensors' device, which has to be the current device."""
+    import torch
+    if torch.cuda.current_device() != device.index:
+        raise Q6Error(Q6_EINVAL, f"the tensors are on {device}, the current device is "
+                                 f"cuda:{torch.cuda.current_device()}")
+    return torch.cuda.current_stream(device.index).cuda_stream if stream is None else (
+        stream.cuda_stream)
 
 
 def _on(stream):
@@ -126,7 +137,7 @@ def group_rows(ids, n_groups: int, out: Groups | None = None, stream=None) -> Gr
     ws = out.workspace
     _check(load().q6_group_rows(ids.data_ptr(), N, per_row, n_groups, out.offsets.data_ptr(),
                                 out.rows.data_ptr(), out.pos.data_ptr(), _ptr(ws),
-                                0 if ws is None else ws.numel(), _stream(stream)))
+                                0 if ws is None else ws.numel(), _stream(stream, ids.device)))
     return out
 
 
@@ -177,7 +188,8 @@ def moe_route(logits, topk: int, renormalize: bool = True, out: Route | None = N
     _check(load().q6_moe_route(logits.data_ptr(), code, N, E, _row_stride(logits), topk,
                                int(bool(renormalize)), out.ids.data_ptr(), out.weights.data_ptr(),
                                g.offsets.data_ptr(), g.rows.data_ptr(), g.pos.data_ptr(),
-                               _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+                               _ptr(ws), 0 if ws is None else ws.numel(),
+                               _stream(stream, logits.device)))
     return out
 
 
@@ -242,7 +254,7 @@ def pack_experts(raw, fmt: str, E: int, M: int, K: int, swiglu: bool = False, st
         plane = torch.empty(need, dtype=torch.uint8, device=dev)
         s = stream if stream is not None else torch.cuda.current_stream(dev)
         _check(load().q6_pack_experts(FORMATS[fmt], _ptr(raw), E, M, K, int(swiglu), _ptr(plane),
-                                      _stream(s)))
+                                      s.cuda_stream))
         if on_host:
             s.synchronize()      # the kernel has read the host bytes
     return ExpertWeights(fmt, E, M, K, swiglu, plane)
@@ -288,7 +300,7 @@ def experts_mmq(w: ExpertWeights, X, groups: Groups, gather: bool = True, out=No
                                  X.data_ptr(), code, nx, _row_stride(X), int(bool(gather)),
                                  groups.offsets.data_ptr(), groups.rows.data_ptr(), items,
                                  out.data_ptr(), _row_stride(out), _ptr(ws), need,
-                                 ctypes.byref(path), _stream(stream)))
+                                 ctypes.byref(path), _stream(stream, dev)))
     return out, PATH_NAMES.get(path.value, str(path.value))
 
 
@@ -316,7 +328,7 @@ def moe_combine(Y, pos, weights, shared=None, out=None, stream=None):
     _check(load().q6_moe_combine(Y.data_ptr(), code, _row_stride(Y), pos.data_ptr(),
                                  weights.data_ptr(), N, topk, M, _ptr(shared),
                                  0 if shared is None else _row_stride(shared), out.data_ptr(),
-                                 _row_stride(out), _stream(stream)))
+                                 _row_stride(out), _stream(stream, dev)))
     return out
 
 
@@ -379,5 +391,5 @@ def lora_add(adapters: LoraAdapters, X, groups: Groups, Y, out=None, stream=None
                               _types()[A.dtype], L, r, M, K, X.data_ptr(), code, _row_stride(X),
                               groups.offsets.data_ptr(), groups.rows.data_ptr(), N, Y.data_ptr(),
                               _row_stride(Y), out.data_ptr(), _row_stride(out), ws.data_ptr(),
-                              need, _stream(stream)))
+                              need, _stream(stream, dev)))
     return out
