@@ -75,7 +75,7 @@ int device_state(DevState** out) {
     if ((e = q6::mmq_tc_prepare()) || (e = q6::mmq_skinny_prepare()) ||
         (e = q6::mmq_sync_prepare()) || (e = q6::q4k_skinny_mma_prepare()) ||
         (e = q6::q4k_skinny_prepare()) || (e = q6::experts_few_prepare()) ||
-        (e = q6::experts_tc_prepare()))
+        (e = q6::experts_tc_prepare()) || (e = q6::lora_prepare()))
       return cuda_fail(e, "cudaFuncSetAttribute");
     if (!encoder()) return fail(Q6_ECUDA, "cuTensorMapEncodeTiled entry point not found");
     st.arch_ok = 1;

@@ -3,9 +3,12 @@
 // Tokens come grouped by adapter, so a tile of up to 16 or 32 tokens shares
 // one A and one B.
 //
-// Two kernels. Shrink: T[i] = scale[a] A[a] x (K long, r wide), K split over
-// the warps of a CTA and, when there are few tiles, over CTAs too; the parts
-// are added in a fixed order. Expand: out = Y + B[a] T (r long, M wide).
+// Two kernels. Shrink: T[i] = scale[a] A[a] x (K long, r wide). For few tokens
+// an adapter a CTA takes up to 16 of them and splits K over its warps; for
+// many it takes 64, x and A coming through shared memory in four stages. K is
+// also split over CTAs while there are few tiles; the parts are added in a
+// fixed order. Expand: out = Y + B[a] T (r long, M wide), B in blocks of
+// columns through shared memory, the loads of Y issued before the products.
 //
 // Both on warp-level tf32 MMAs. f16 and bf16 values are tf32 values as they
 // are; an f32 factor (x, T) is split into a tf32 value and a tf32 remainder
@@ -107,10 +110,10 @@ __device__ __forceinline__ Tile find_tile(const int32_t* offsets, int G, int row
 }
 
 // T: part [split][item][r]. Grid (tiles, K splits, rank blocks).
-template <typename TX, typename TW, int RT>
+template <typename TX, typename TW>
 __global__ void __launch_bounds__(kThreads)
 shrink_kernel(const LoraCall c) {
-  constexpr int kRows = 16 * RT;
+  constexpr int RT = 1, kRows = 16 * RT;
   constexpr bool kSplit = sizeof(TX) == 4;
   __shared__ float red[kWarps / 2][kRows][kRankBlock + 4];
   griddep_wait();
@@ -220,115 +223,301 @@ shrink_kernel(const LoraCall c) {
   }
 }
 
-constexpr int kColsWarp = 32;  // columns a warp takes at a time
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool copy) {
+  // copy == false fills with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(copy ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+// kCount values of shared memory as f32.
+template <typename T, int kCount>
+__device__ __forceinline__ void shared_f32(const void* p, float (&f)[kCount]) {
+  uint32_t w[kCount / 2];
+  if constexpr (kCount == 8) {
+    const uint4 v = *static_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (kCount == 4) {
+    const uint2 v = *static_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *static_cast<const uint32_t*>(p);
+  }
+#pragma unroll
+  for (int i = 0; i < kCount / 2; ++i) {
+    const float2 v = unpack2<T>(w[i]);
+    f[2 * i] = v.x, f[2 * i + 1] = v.y;
+  }
+}
 
-// out = Y + B T. Grid (tiles, column blocks of `cols`). JV: ranks a lane loads
-// at a time (r is a multiple of 4 * JV). kVec: 16-byte rows of Y and out.
-template <typename TW, int RT, int JV, bool kVec>
-__global__ void __launch_bounds__(kThreads)
-expand_kernel(const LoraCall c, int cols) {
-  constexpr int kRows = 16 * RT;
-  extern __shared__ float ts[];  // T of the tile: [kRows][r + 4]
+// Shrink for many tokens an adapter. Grid (tiles of 64 items, K splits, rank
+// blocks); warp w: items 16 (w % 4).., ranks 32 (w / 4)... Stages of 64 of K:
+// x [64][64], A [64 ranks][64]; the 16-byte units of a row are exchanged by
+// the row's lowest bit so that two rows' fragment loads meet no bank twice.
+constexpr int kBigRows = 64, kBigStages = 4;
+template <typename TX, typename TW>
+constexpr int kBigStageBytes = kBigRows * 64 * (int)sizeof(TX) + kRankBlock * 64 * (int)sizeof(TW);
+
+template <typename TX, typename TW>
+__global__ void __launch_bounds__(kThreads, 2)
+shrink_big_kernel(const LoraCall c) {
+  constexpr bool kSplit = sizeof(TX) == 4;
+  constexpr int kXUnits = 64 * (int)sizeof(TX) / 16, kXSwap = kSplit ? 1 : 4;
+  constexpr int kXBytes = kBigRows * 64 * (int)sizeof(TX), kStage = kBigStageBytes<TX, TW>;
+  extern __shared__ uint4 big_smem[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(big_smem);
   griddep_wait();
-  const Tile tile = find_tile(c.offsets, c.L, kRows, blockIdx.x);
-  if (tile.group < 0) return;
-  const int m1 = min(c.M, ((int)blockIdx.y + 1) * cols);
-  if (tile.group == c.L) {  // tokens without an adapter
-    if (c.out == c.Y) return;
-    for (int n = 0; n < tile.count; ++n) {
-      const long long row = c.rows[tile.first + n];
-      for (int m = (int)blockIdx.y * cols + threadIdx.x; m < m1; m += blockDim.x)
-        c.out[row * c.ldo + m] = c.Y[row * c.ldy + m];
-    }
-    return;
-  }
+  griddep_launch_dependents();
+  const Tile tile = find_tile(c.offsets, c.L, kBigRows, blockIdx.x);
+  if (tile.group < 0 || tile.group == c.L) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int ld = c.r + 4;
-  for (int i = threadIdx.x; i < kRows * c.r; i += blockDim.x) {
-    const int n = i / c.r, j = i % c.r;
-    float v = 0.0f;
-    if (n < tile.count)
-      for (int s = 0; s < c.splits; ++s)
-        v += c.part[((size_t)s * c.items + tile.first + n) * c.r + j];
-    ts[n * ld + j] = v;
+  const int j0 = blockIdx.z * kRankBlock, ranks = min(kRankBlock, c.r - j0);
+  // this CTA's stages of 64 of K
+  const int stages = (c.K + 63) / 64;
+  const int s0 = (int)((long long)stages * blockIdx.y / gridDim.y);
+  const int s1 = (int)((long long)stages * (blockIdx.y + 1) / gridDim.y);
+  // what a thread copies: units (row, u) of x and of A; rows past the end
+  // repeat the last
+  constexpr int kXCopies = kBigRows * kXUnits / kThreads, kACopies = kRankBlock * 8 / kThreads;
+  const TX* xsrc[kXCopies];
+  const TW* asrc[kACopies];
+#pragma unroll
+  for (int i = 0; i < kXCopies; ++i) {
+    const int row = (threadIdx.x + i * kThreads) / kXUnits, u = (threadIdx.x + i * kThreads) % kXUnits;
+    xsrc[i] = static_cast<const TX*>(c.X) +
+              c.rows[tile.first + min(row, tile.count - 1)] * c.ldx + u * (16 / (int)sizeof(TX));
   }
-  __syncthreads();
-  long long row[RT][2];
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+  for (int i = 0; i < kACopies; ++i) {
+    const int row = (threadIdx.x + i * kThreads) / 8, u = (threadIdx.x + i * kThreads) % 8;
+    asrc[i] = static_cast<const TW*>(c.A) +
+              ((size_t)tile.group * c.r + j0 + min(row, ranks - 1)) * (size_t)c.K + u * 8;
+  }
+  auto load = [&](int s) {
+    if (s < s1) {
+      uint8_t* x = smem + (s - s0) % kBigStages * kStage;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int n = 16 * i + 8 * h + g;
-      row[i][h] = n < tile.count ? c.rows[tile.first + n] : -1;
+      for (int i = 0; i < kXCopies; ++i) {
+        const int row = (threadIdx.x + i * kThreads) / kXUnits;
+        const int u = (threadIdx.x + i * kThreads) % kXUnits;
+        const bool in = s * 64 + u * (16 / (int)sizeof(TX)) < c.K;
+        cp_async16(x + (row * kXUnits + (u ^ ((row & 1) * kXSwap))) * 16,
+                   in ? xsrc[i] + (size_t)s * 64 : xsrc[i], in);
+      }
+#pragma unroll
+      for (int i = 0; i < kACopies; ++i) {
+        const int row = (threadIdx.x + i * kThreads) / 8, u = (threadIdx.x + i * kThreads) % 8;
+        const bool in = s * 64 + u * 8 < c.K;
+        cp_async16(x + kXBytes + (row * 8 + (u ^ ((row & 1) * 4))) * 16,
+                   in ? asrc[i] + (size_t)s * 64 : asrc[i], in);
+      }
     }
-  const TW* B = static_cast<const TW*>(c.B) + (size_t)tile.group * c.M * (size_t)c.r;
-  for (int m0 = (int)blockIdx.y * cols + warp * kColsWarp; m0 < m1;
-       m0 += (int)(blockDim.x / 32) * kColsWarp) {
-    // column of this lane in MMA tile p: slots 2t, 2t + 1 of tiles 2q and
-    // 2q + 1 are the four consecutive columns 16 q + 4 t..
-    float acc[RT][4][4] = {};
-    for (int j0 = 0; j0 < c.r; j0 += 4 * JV) {
-      float w[4][JV];
+    cp_async_commit();
+  };
+  const int row0 = 16 * (warp % 4), rank0 = 32 * (warp / 4);
+  const int nj = min(4, (ranks - rank0 + 7) / 8);
+  float acc[4][4] = {};
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int m = m0 + 16 * (p / 2) + 4 * (g / 2) + 2 * (p % 2) + g % 2;
-        if (m < c.M) {
-          load_16<TW, JV>(B + (size_t)m * c.r + j0 + JV * t, w[p]);
+  for (int s = 0; s < kBigStages - 1; ++s) load(s0 + s);
+  for (int s = s0; s < s1; ++s) {
+    cp_async_wait<kBigStages - 2>();
+    __syncthreads();  // stage s is there, stage s - 1 has been read
+    load(s + kBigStages - 1);
+    const uint8_t* x = smem + (s - s0) % kBigStages * kStage;
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {  // 32 of K: 8 consecutive ones a lane
+      float f[2][8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = row0 + 8 * h + g;
+        if constexpr (kSplit) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int u = (8 * step + 2 * t + q) ^ (row & 1);
+            const float4 v = *reinterpret_cast<const float4*>(x + (row * kXUnits + u) * 16);
+            f[h][4 * q] = v.x, f[h][4 * q + 1] = v.y, f[h][4 * q + 2] = v.z, f[h][4 * q + 3] = v.w;
+          }
         } else {
-#pragma unroll
-          for (int q = 0; q < JV; ++q) w[p][q] = 0.0f;
+          shared_f32<TX, 8>(x + (row * kXUnits + ((4 * step + t) ^ ((row & 1) * 4))) * 16, f[h]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+      for (int j = 0; j < 4; ++j) {
+        if (j >= nj) break;
+        float w[8];
+        const int row = rank0 + 8 * j + g;
+        shared_f32<TW, 8>(x + kXBytes + (row * 8 + ((4 * step + t) ^ ((row & 1) * 4))) * 16, w);
+        float p[4] = {};
 #pragma unroll
-        for (int q = 0; q < JV / 2; ++q) {
-          const float2 f0 = *reinterpret_cast<const float2*>(ts + (16 * i + g) * ld + j0 + JV * t + 2 * q);
-          const float2 f1 =
-              *reinterpret_cast<const float2*>(ts + (16 * i + 8 + g) * ld + j0 + JV * t + 2 * q);
-          const float v[4] = {f0.x, f1.x, f0.y, f1.y};
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t b0 = __float_as_uint(w[2 * q]), b1 = __float_as_uint(w[2 * q + 1]);
+          const float v[4] = {f[0][2 * q], f[1][2 * q], f[0][2 * q + 1], f[1][2 * q + 1]};
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float a, b;
             tf32_split(v[e], a, b);
-            hi[e] = __float_as_uint(a);
+            hi[e] = __float_as_uint(kSplit ? a : v[e]);
             lo[e] = __float_as_uint(b);
           }
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const uint32_t b0 = __float_as_uint(w[p][2 * q]), b1 = __float_as_uint(w[p][2 * q + 1]);
-            mma_tf32(acc[i][p], lo, b0, b1);
-            mma_tf32(acc[i][p], hi, b0, b1);
-          }
+          mma_tf32(p, hi, b0, b1);
+          if constexpr (kSplit) mma_tf32(p, lo, b0, b1);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] += p[e];
+      }
     }
+  }
+  cp_async_wait<0>();
+  const float scale = c.scale[tile.group];
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (row[i][h] < 0) continue;
-        const float* y = c.Y + row[i][h] * c.ldy;
-        float* o = c.out + row[i][h] * c.ldo;
+    for (int h = 0; h < 2; ++h) {
+      const int n = row0 + 8 * h + g;
+      if (j < nj && n < tile.count) {
+        float* p = c.part + ((size_t)blockIdx.y * c.items + tile.first + n) * c.r + j0 + rank0 +
+                   8 * j + 2 * t;
+        *reinterpret_cast<float2*>(p) = make_float2(scale * acc[j][2 * h], scale * acc[j][2 * h + 1]);
+      }
+    }
+}
+
+constexpr int kColsWarp = 64;  // columns a warp takes at a time
+
+// Bytes of a column of B in shared memory: half a bank line off, so that
+// neighbouring columns' fragment loads do not meet.
+__host__ __device__ constexpr int b_pitch(int r) { return 2 * r + (2 * r % 128 == 0 ? 64 : 0); }
+
+// out = Y + B T. Grid (tiles of 16 * RW items, column parts); RW row warps
+// times col_warps column warps. JV: ranks a lane loads at a time (r is a
+// multiple of 4 * JV). kVec: 16-byte rows of Y and out.
+template <typename TW, int RW, int JV, bool kVec>
+__global__ void __launch_bounds__(kThreads, 2)
+expand_kernel(const LoraCall c, int col_warps, int part_cols) {
+  constexpr int kRows = 16 * RW;
+  extern __shared__ uint4 expand_smem[];
+  float* ts = reinterpret_cast<float*>(expand_smem);  // T of the tile: [kRows][r + 4]
+  const int ld = c.r + 4, pitch = b_pitch(c.r), width = kColsWarp * col_warps;
+  uint8_t* bs = reinterpret_cast<uint8_t*>(ts + kRows * ld);  // two blocks of `width` columns
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int m_begin = (int)blockIdx.y * part_cols, m_end = min(c.M, m_begin + part_cols);
+  griddep_wait();
+  const Tile tile = find_tile(c.offsets, c.L, kRows, blockIdx.x);
+  if (tile.group < 0) return;
+  const bool none = tile.group == c.L;  // tokens without an adapter: Y alone
+  if (none && c.out == c.Y) return;
+  const TW* B = static_cast<const TW*>(c.B) + (size_t)tile.group * c.M * (size_t)c.r;
+  const int units = c.r / 8;  // 16-byte units of a column
+  auto load = [&](int m0, int buf) {
+    const int n = none ? 0 : min(width, m_end - m0) * units;
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+      cp_async16(bs + buf * width * pitch + i / units * pitch + i % units * 16,
+                 B + (size_t)m0 * c.r + (size_t)i * 8, true);
+    cp_async_commit();
+  };
+  load(m_begin, 0);
+  for (int i = threadIdx.x; i < kRows * c.r; i += blockDim.x) {
+    const int n = i / c.r, j = i % c.r;
+    float v = 0.0f;
+    if (n < tile.count && !none)
+      for (int s = 0; s < c.splits; ++s)
+        v += c.part[((size_t)s * c.items + tile.first + n) * c.r + j];
+    ts[n * ld + j] = v;
+  }
+  const int rw = warp % RW, cw = warp / RW;
+  const float* ys[2];
+  float* os[2];
+  bool has[2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int m = m0 + 16 * q + 4 * t;
-          const float v[4] = {acc[i][2 * q][2 * h], acc[i][2 * q][2 * h + 1],
-                              acc[i][2 * q + 1][2 * h], acc[i][2 * q + 1][2 * h + 1]};
-          if (kVec) {
-            if (m < c.M) {
-              const float4 a = *reinterpret_cast<const float4*>(y + m);
-              *reinterpret_cast<float4*>(o + m) =
-                  make_float4(a.x + v[0], a.y + v[1], a.z + v[2], a.w + v[3]);
-            }
-          } else {
+  for (int h = 0; h < 2; ++h) {
+    const int n = 16 * rw + 8 * h + g;
+    has[h] = n < tile.count;
+    const long long row = c.rows[tile.first + (has[h] ? n : 0)];
+    ys[h] = c.Y + row * c.ldy;
+    os[h] = c.out + row * c.ldo;
+  }
+  int buf = 0;
+  for (int m0 = m_begin; m0 < m_end; m0 += width, buf ^= 1) {
+    if (m0 + width < m_end) {
+      load(m0 + width, buf ^ 1);
+    } else {
+      cp_async_commit();
+    }
+    // MMA tile p's slots 2t, 2t + 1 with those of tile p + 1 are the four
+    // consecutive columns 16 (p / 2) + 4 t..
+    const int m = m0 + cw * kColsWarp + 4 * t;
+    float4 y[2][4];
+    if (kVec) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (m + e < c.M) o[m + e] = y[m + e] + v[e];
-          }
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          y[h][q] = has[h] && m + 16 * q < m_end
+                        ? __ldcs(reinterpret_cast<const float4*>(ys[h] + m + 16 * q))
+                        : make_float4(0, 0, 0, 0);
+    }
+    cp_async_wait<1>();
+    __syncthreads();  // the block (and, before the first, T) is there
+    float acc[8][4] = {};
+    const uint8_t* b = bs + buf * width * pitch + cw * kColsWarp * pitch;
+    for (int j0 = 0; j0 < c.r && !none; j0 += 4 * JV) {
+      uint32_t hi[JV / 2][4], lo[JV / 2][4];
+#pragma unroll
+      for (int q = 0; q < JV / 2; ++q) {
+        const float* p = ts + (16 * rw + g) * ld + j0 + JV * t + 2 * q;
+        const float2 f0 = *reinterpret_cast<const float2*>(p);
+        const float2 f1 = *reinterpret_cast<const float2*>(p + 8 * ld);
+        const float v[4] = {f0.x, f1.x, f0.y, f1.y};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x, r;
+          tf32_split(v[e], x, r);
+          hi[q][e] = __float_as_uint(x);
+          lo[q][e] = __float_as_uint(r);
         }
       }
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        // columns past M hold what the buffer held: they are not stored
+        const int col = 16 * (p / 2) + 4 * (g / 2) + 2 * (p % 2) + g % 2;
+        float w[JV];
+        shared_f32<TW, JV>(b + col * pitch + (j0 + JV * t) * 2, w);
+#pragma unroll
+        for (int q = 0; q < JV / 2; ++q) {
+          const uint32_t b0 = __float_as_uint(w[2 * q]), b1 = __float_as_uint(w[2 * q + 1]);
+          mma_tf32(acc[p], lo[q], b0, b1);
+          mma_tf32(acc[p], hi[q], b0, b1);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!has[h]) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int at = m + 16 * q;
+        const float v[4] = {acc[2 * q][2 * h], acc[2 * q][2 * h + 1], acc[2 * q + 1][2 * h],
+                            acc[2 * q + 1][2 * h + 1]};
+        if (kVec) {
+          const float4 a = y[h][q];
+          if (at < m_end)
+            __stcs(reinterpret_cast<float4*>(os[h] + at),
+                   make_float4(a.x + v[0], a.y + v[1], a.z + v[2], a.w + v[3]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (at + e < m_end) os[h][at + e] = ys[h][at + e] + v[e];
+        }
+      }
+    }
+    __syncthreads();  // the block has been read
   }
+  cp_async_wait<0>();
 }
 
 // The most tiles `items` items in L groups (and the section without one) can
@@ -337,38 +526,76 @@ long long most_tiles(long long items, int L, int rows) {
   const long long t = items / rows + L + 1;
   return t < items ? t : items;
 }
-int tile_rows(long long items, int L) {
-  // 32-row tiles once the groups average more than 16 items
-  return items > 16ll * L ? 32 : 16;
-}
+// Many tokens an adapter: more than 16 on average.
+bool many(long long items, int L) { return items > 16ll * L; }
 
 template <typename TX, typename TW>
 cudaError_t shrink(const LoraCall& c, cudaStream_t s) {
-  const int rows = tile_rows(c.items, c.L);
-  const dim3 grid((unsigned)most_tiles(c.items, c.L, rows), (unsigned)c.splits,
+  const bool big = many(c.items, c.L);
+  const dim3 grid((unsigned)most_tiles(c.items, c.L, big ? kBigRows : 16), (unsigned)c.splits,
                   (unsigned)((c.r + kRankBlock - 1) / kRankBlock));
-  return launch_pdl(rows == 32 ? shrink_kernel<TX, TW, 2> : shrink_kernel<TX, TW, 1>, grid,
-                    dim3(kThreads), 0, s, c);
+  if (big)
+    return launch_pdl(shrink_big_kernel<TX, TW>, grid, dim3(kThreads),
+                      (size_t)kBigStages * kBigStageBytes<TX, TW>, s, c);
+  return launch_pdl(shrink_kernel<TX, TW>, grid, dim3(kThreads), 0, s, c);
 }
 
-template <typename TW, int RT, int JV>
-cudaError_t expand_v(const LoraCall& c, bool vec, cudaStream_t s) {
-  const long long tiles = most_tiles(c.items, c.L, 16 * RT);
-  // column blocks: as wide as leaves about four CTAs an SM, so that T is
-  // staged less often
-  int cols = 1024;
-  while (cols > 64 && tiles * ((c.M + cols - 1) / cols) < 4 * 152) cols /= 2;
-  const dim3 grid((unsigned)tiles, (unsigned)((c.M + cols - 1) / cols));
-  const int threads = cols >= 256 ? kThreads : cols;
-  const size_t smem = (size_t)16 * RT * (c.r + 4) * 4;
-  return launch_pdl(vec ? expand_kernel<TW, RT, JV, true> : expand_kernel<TW, RT, JV, false>, grid,
-                    dim3(threads), smem, s, c, cols);
+size_t expand_smem_bytes(int rows, int r, int col_warps) {
+  return (size_t)rows * (r + 4) * 4 + (size_t)2 * kColsWarp * col_warps * b_pitch(r);
 }
-template <typename TW, int RT>
+constexpr size_t kExpandSmem = 112 * 1024;  // two CTAs an SM where that is enough
+constexpr int kExpandSmemMax = 227 * 1024;
+static_assert(128 * (Q6_LORA_MAX_RANK + 4) * 4 + 2 * kColsWarp * b_pitch(Q6_LORA_MAX_RANK) <=
+                  kExpandSmemMax, "128 items at the largest rank");
+
+template <typename TW, int RW, int JV>
+cudaError_t expand_v(const LoraCall& c, bool vec, cudaStream_t s) {
+  const long long tiles = most_tiles(c.items, c.L, 16 * RW);
+  int col_warps = kWarps / RW;
+  while (col_warps > 1 && (expand_smem_bytes(16 * RW, c.r, col_warps) > kExpandSmem ||
+                           kColsWarp * col_warps >= 2 * c.M))
+    col_warps /= 2;
+  // column parts: as many as fill the SMs twice, whole blocks each
+  const int width = kColsWarp * col_warps, blocks = (c.M + width - 1) / width;
+  long long parts = (2 * 152 + tiles - 1) / tiles;
+  if (parts > blocks) parts = blocks;
+  const int part_cols = (int)((blocks + parts - 1) / parts) * width;
+  const dim3 grid((unsigned)tiles, (unsigned)((c.M + part_cols - 1) / part_cols));
+  return launch_pdl(vec ? expand_kernel<TW, RW, JV, true> : expand_kernel<TW, RW, JV, false>, grid,
+                    dim3(32 * RW * col_warps), expand_smem_bytes(16 * RW, c.r, col_warps), s, c,
+                    col_warps, part_cols);
+}
+template <typename TW, int RW>
 cudaError_t expand_r(const LoraCall& c, bool vec, cudaStream_t s) {
-  return c.r % 32 == 0   ? expand_v<TW, RT, 8>(c, vec, s)
-         : c.r % 16 == 0 ? expand_v<TW, RT, 4>(c, vec, s)
-                         : expand_v<TW, RT, 2>(c, vec, s);
+  return c.r % 32 == 0   ? expand_v<TW, RW, 8>(c, vec, s)
+         : c.r % 16 == 0 ? expand_v<TW, RW, 4>(c, vec, s)
+                         : expand_v<TW, RW, 2>(c, vec, s);
+}
+
+template <typename TW, int RW>
+cudaError_t prepare_expand() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto* k) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmemMax);
+  };
+  set(expand_kernel<TW, RW, 8, true>), set(expand_kernel<TW, RW, 8, false>);
+  set(expand_kernel<TW, RW, 4, true>), set(expand_kernel<TW, RW, 4, false>);
+  set(expand_kernel<TW, RW, 2, true>), set(expand_kernel<TW, RW, 2, false>);
+  return e;
+}
+template <typename TW>
+cudaError_t prepare_t() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto* k, int bytes) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  set(shrink_big_kernel<float, TW>, kBigStages * kBigStageBytes<float, TW>);
+  set(shrink_big_kernel<__nv_bfloat16, TW>, kBigStages * kBigStageBytes<__nv_bfloat16, TW>);
+  set(shrink_big_kernel<__half, TW>, kBigStages * kBigStageBytes<__half, TW>);
+  if (e == cudaSuccess) e = prepare_expand<TW, 1>();
+  if (e == cudaSuccess) e = prepare_expand<TW, 8>();
+  return e;
 }
 
 template <typename TW>
@@ -379,20 +606,25 @@ cudaError_t lora_t(const LoraCall& c, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const uintptr_t bits = reinterpret_cast<uintptr_t>(c.Y) | reinterpret_cast<uintptr_t>(c.out) |
                          (uintptr_t)(c.ldy * 4) | (uintptr_t)(c.ldo * 4) | (uintptr_t)(c.M * 4);
-  return tile_rows(c.items, c.L) == 32 ? expand_r<TW, 2>(c, bits % 16 == 0, s)
-                                       : expand_r<TW, 1>(c, bits % 16 == 0, s);
+  return many(c.items, c.L) ? expand_r<TW, 8>(c, bits % 16 == 0, s)
+                            : expand_r<TW, 1>(c, bits % 16 == 0, s);
 }
 
 }  // namespace
 
 int lora_splits(long long items, int L, int r, int K) {
   // K parts over CTAs until there are about two CTAs an SM, at least 256 of K
-  // (one step a warp) each
-  const int rows = tile_rows(items, L);
-  const long long tiles = most_tiles(items, L, rows) * ((r + kRankBlock - 1) / kRankBlock);
-  int splits = 1;
-  while (splits < 16 && tiles * splits < 2 * 152 && (K / (2 * splits)) >= 256) splits *= 2;
-  return splits;
+  // each
+  const long long tiles = most_tiles(items, L, many(items, L) ? kBigRows : 16) *
+                          ((r + kRankBlock - 1) / kRankBlock);
+  long long splits = (2 * 152 + tiles - 1) / tiles;
+  if (splits > K / 256) splits = K / 256;
+  return splits < 1 ? 1 : splits > 16 ? 16 : (int)splits;
+}
+
+cudaError_t lora_prepare() {
+  const cudaError_t e = prepare_t<__nv_bfloat16>();
+  return e == cudaSuccess ? prepare_t<__half>() : e;
 }
 
 cudaError_t launch_lora(const LoraCall& c, cudaStream_t s) {

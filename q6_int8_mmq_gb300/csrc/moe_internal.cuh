@@ -219,6 +219,7 @@ struct LoraCall {
 // Parts the shrink product splits K into (its workspace is splits * items * r
 // f32 values).
 int lora_splits(long long items, int L, int r, int K);
+cudaError_t lora_prepare();
 cudaError_t launch_lora(const LoraCall& c, cudaStream_t s);
 
 }  // namespace q6
