@@ -8,7 +8,7 @@
 // many it takes 64, x and A coming through shared memory in four stages. K is
 // also split over CTAs while there are few tiles; the parts are added in a
 // fixed order. Expand: out = Y + B[a] T (r long, M wide), B in blocks of
-// columns through shared memory, the loads of Y issued before the products.
+// columns through shared memory, Y loaded a block ahead.
 //
 // Both on warp-level tf32 MMAs. f16 and bf16 values are tf32 values as they
 // are; an f32 factor (x, T) is split into a tf32 value and a tf32 remainder
@@ -389,9 +389,9 @@ shrink_big_kernel(const LoraCall c) {
 
 constexpr int kColsWarp = 64;  // columns a warp takes at a time
 
-// Bytes of a column of B in shared memory: half a bank line off, so that
-// neighbouring columns' fragment loads do not meet.
-__host__ __device__ constexpr int b_pitch(int r) { return 2 * r + (2 * r % 128 == 0 ? 64 : 0); }
+// Bytes of a column of B in shared memory: four neighbouring columns' fragment
+// loads (32 bytes each) fall on different banks.
+__host__ __device__ constexpr int b_pitch(int r) { return 2 * r + (2 * r % 64 == 0 ? 32 : 0); }
 
 // out = Y + B T. Grid (tiles of 16 * RW items, column parts); RW row warps
 // times col_warps column warps. JV: ranks a lane loads at a time (r is a
@@ -421,13 +421,24 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
     cp_async_commit();
   };
   load(m_begin, 0);
-  for (int i = threadIdx.x; i < kRows * c.r; i += blockDim.x) {
-    const int n = i / c.r, j = i % c.r;
-    float v = 0.0f;
-    if (n < tile.count && !none)
-      for (int s = 0; s < c.splits; ++s)
-        v += c.part[((size_t)s * c.items + tile.first + n) * c.r + j];
-    ts[n * ld + j] = v;
+  // T, four ranks at a time, the parts' loads in flight together
+  for (int i = threadIdx.x; i < kRows * (c.r / 4); i += blockDim.x) {
+    const int n = i / (c.r / 4), j = i % (c.r / 4) * 4;
+    float4 v = make_float4(0, 0, 0, 0);
+    if (n < tile.count && !none) {
+      const float* p = c.part + (size_t)(tile.first + n) * c.r + j;
+      const size_t step = (size_t)c.items * c.r;
+      for (int s0 = 0; s0 < c.splits; s0 += 8) {
+        float4 w[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          w[s] = s0 + s < c.splits ? *reinterpret_cast<const float4*>(p + (s0 + s) * step)
+                                   : make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) v.x += w[s].x, v.y += w[s].y, v.z += w[s].z, v.w += w[s].w;
+      }
+    }
+    *reinterpret_cast<float4*>(ts + n * ld + j) = v;
   }
   const int rw = warp % RW, cw = warp / RW;
   const float* ys[2];
@@ -441,6 +452,18 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
     ys[h] = c.Y + row * c.ldy;
     os[h] = c.out + row * c.ldo;
   }
+  // MMA tile p's slots 2t, 2t + 1 with those of tile p + 1 are the four
+  // consecutive columns 16 (p / 2) + 4 t..
+  const int col0 = cw * kColsWarp + 4 * t;
+  auto load_y = [&](int h, int m) {
+    return kVec && has[h] && m < m_end ? __ldcs(reinterpret_cast<const float4*>(ys[h] + m))
+                                       : make_float4(0, 0, 0, 0);
+  };
+  float4 y[2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) y[h][q] = load_y(h, m_begin + col0 + 16 * q);
   int buf = 0;
   for (int m0 = m_begin; m0 < m_end; m0 += width, buf ^= 1) {
     if (m0 + width < m_end) {
@@ -448,19 +471,7 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
     } else {
       cp_async_commit();
     }
-    // MMA tile p's slots 2t, 2t + 1 with those of tile p + 1 are the four
-    // consecutive columns 16 (p / 2) + 4 t..
-    const int m = m0 + cw * kColsWarp + 4 * t;
-    float4 y[2][4];
-    if (kVec) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          y[h][q] = has[h] && m + 16 * q < m_end
-                        ? __ldcs(reinterpret_cast<const float4*>(ys[h] + m + 16 * q))
-                        : make_float4(0, 0, 0, 0);
-    }
+    const int m = m0 + col0;
     cp_async_wait<1>();
     __syncthreads();  // the block (and, before the first, T) is there
     float acc[8][4] = {};
@@ -496,8 +507,7 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
       }
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (!has[h]) continue;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int at = m + 16 * q;
@@ -505,16 +515,16 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
                             acc[2 * q + 1][2 * h + 1]};
         if (kVec) {
           const float4 a = y[h][q];
-          if (at < m_end)
+          if (has[h] && at < m_end)
             __stcs(reinterpret_cast<float4*>(os[h] + at),
                    make_float4(a.x + v[0], a.y + v[1], a.z + v[2], a.w + v[3]));
+          y[h][q] = load_y(h, at + width);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (at + e < m_end) os[h][at + e] = ys[h][at + e] + v[e];
+            if (has[h] && at + e < m_end) os[h][at + e] = ys[h][at + e] + v[e];
         }
       }
-    }
     __syncthreads();  // the block has been read
   }
   cp_async_wait<0>();
@@ -567,9 +577,7 @@ cudaError_t expand_v(const LoraCall& c, bool vec, cudaStream_t s) {
 }
 template <typename TW, int RW>
 cudaError_t expand_r(const LoraCall& c, bool vec, cudaStream_t s) {
-  return c.r % 32 == 0   ? expand_v<TW, RW, 8>(c, vec, s)
-         : c.r % 16 == 0 ? expand_v<TW, RW, 4>(c, vec, s)
-                         : expand_v<TW, RW, 2>(c, vec, s);
+  return c.r % 16 == 0 ? expand_v<TW, RW, 4>(c, vec, s) : expand_v<TW, RW, 2>(c, vec, s);
 }
 
 template <typename TW, int RW>
@@ -579,7 +587,6 @@ cudaError_t prepare_expand() {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmemMax);
   };
-  set(expand_kernel<TW, RW, 8, true>), set(expand_kernel<TW, RW, 8, false>);
   set(expand_kernel<TW, RW, 4, true>), set(expand_kernel<TW, RW, 4, false>);
   set(expand_kernel<TW, RW, 2, true>), set(expand_kernel<TW, RW, 2, false>);
   return e;
@@ -594,7 +601,7 @@ cudaError_t prepare_t() {
   set(shrink_big_kernel<__nv_bfloat16, TW>, kBigStages * kBigStageBytes<__nv_bfloat16, TW>);
   set(shrink_big_kernel<__half, TW>, kBigStages * kBigStageBytes<__half, TW>);
   if (e == cudaSuccess) e = prepare_expand<TW, 1>();
-  if (e == cudaSuccess) e = prepare_expand<TW, 8>();
+  if (e == cudaSuccess) e = prepare_expand<TW, 2>();
   return e;
 }
 
@@ -606,7 +613,7 @@ cudaError_t lora_t(const LoraCall& c, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const uintptr_t bits = reinterpret_cast<uintptr_t>(c.Y) | reinterpret_cast<uintptr_t>(c.out) |
                          (uintptr_t)(c.ldy * 4) | (uintptr_t)(c.ldo * 4) | (uintptr_t)(c.M * 4);
-  return many(c.items, c.L) ? expand_r<TW, 8>(c, bits % 16 == 0, s)
+  return many(c.items, c.L) ? expand_r<TW, 2>(c, bits % 16 == 0, s)
                             : expand_r<TW, 1>(c, bits % 16 == 0, s);
 }
 
