@@ -10,10 +10,10 @@
 // fixed order. Expand: out = Y + B[a] T (r long, M wide), B in blocks of
 // columns through shared memory, Y loaded a block ahead.
 //
-// Both on warp-level tf32 MMAs. f16 and bf16 values are tf32 values as they
-// are; an f32 factor (x, T) is split into a tf32 value and a tf32 remainder
-// and multiplied twice (2^-21 of it is lost). The products are short next to
-// the bytes: 2 r flops for each 4 to 8 bytes of X and Y.
+// Both on warp-level MMAs with f32 accumulation, the 16-bit factors as they
+// are. An f32 factor (x, T) beside bf16 is split into three bf16 values, 8
+// bits each and together exact; beside f16 (whose range is too small for the
+// parts) into a tf32 value and a tf32 remainder, which loses 2^-21 of it.
 //
 // The order of k inside an MMA is free, so a lane takes consecutive k (or
 // rank) values of its row in 16-byte loads and the MMAs use them two by two.
@@ -37,6 +37,32 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// D += A (16 x 16) * B (16 x 8), 16-bit operands of type T.
+template <typename T>
+__device__ __forceinline__ void mma_16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                       uint32_t b1) {
+  if constexpr (__is_same(T, __half))
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// A pair of f32 values as three bf16 pairs that add up to it.
+__device__ __forceinline__ void bf16_split3(float x, float y, uint32_t (&p)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+    p[i] = __byte_perm(a, b, 0x7632u);  // the upper halves
+    x -= __uint_as_float(a & 0xFFFF0000u);
+    y -= __uint_as_float(b & 0xFFFF0000u);
+  }
 }
 
 // kCount consecutive values as f32.
@@ -330,7 +356,11 @@ shrink_big_kernel(const LoraCall c) {
     const uint8_t* x = smem + (s - s0) % kBigStages * kStage;
 #pragma unroll
     for (int step = 0; step < 2; ++step) {  // 32 of K: 8 consecutive ones a lane
-      float f[2][8];
+      // MMA i of 16 of K takes values 4 i.. of the lane's 8: a[i][part] its A
+      // operand, the rows' values as they are or their parts
+      constexpr bool kRaw = __is_same(TX, TW), kThree = kSplit && !__is_same(TW, __half);
+      uint4 xw[2];    // kRaw
+      float f[2][8];  // otherwise
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int row = row0 + 8 * h + g;
@@ -342,30 +372,64 @@ shrink_big_kernel(const LoraCall c) {
             f[h][4 * q] = v.x, f[h][4 * q + 1] = v.y, f[h][4 * q + 2] = v.z, f[h][4 * q + 3] = v.w;
           }
         } else {
-          shared_f32<TX, 8>(x + (row * kXUnits + ((4 * step + t) ^ ((row & 1) * 4))) * 16, f[h]);
+          const uint8_t* p = x + (row * kXUnits + ((4 * step + t) ^ ((row & 1) * 4))) * 16;
+          if constexpr (kRaw)
+            xw[h] = *reinterpret_cast<const uint4*>(p);
+          else
+            shared_f32<TX, 8>(p, f[h]);
         }
+      }
+      uint32_t three[2][3][4];  // [MMA][part][register]
+      if constexpr (kThree) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // row e % 2, the pair 2 i + e / 2
+            uint32_t p[3];
+            const int k = 2 * (2 * i + e / 2);
+            bf16_split3(f[e % 2][k], f[e % 2][k + 1], p);
+#pragma unroll
+            for (int s = 0; s < 3; ++s) three[i][s][e] = p[s];
+          }
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j >= nj) break;
-        float w[8];
         const int row = rank0 + 8 * j + g;
-        shared_f32<TW, 8>(x + kXBytes + (row * 8 + ((4 * step + t) ^ ((row & 1) * 4))) * 16, w);
+        const uint8_t* wp = x + kXBytes + (row * 8 + ((4 * step + t) ^ ((row & 1) * 4))) * 16;
         float p[4] = {};
+        if constexpr (kRaw || kThree) {
+          const uint4 w = *reinterpret_cast<const uint4*>(wp);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t b0 = __float_as_uint(w[2 * q]), b1 = __float_as_uint(w[2 * q + 1]);
-          const float v[4] = {f[0][2 * q], f[1][2 * q], f[0][2 * q + 1], f[1][2 * q + 1]};
-          uint32_t hi[4], lo[4];
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t b0 = word4(w, 2 * i), b1 = word4(w, 2 * i + 1);
+            if constexpr (kRaw) {
+              const uint32_t a[4] = {word4(xw[0], 2 * i), word4(xw[1], 2 * i),
+                                     word4(xw[0], 2 * i + 1), word4(xw[1], 2 * i + 1)};
+              mma_16<TW>(p, a, b0, b1);
+            } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float a, b;
-            tf32_split(v[e], a, b);
-            hi[e] = __float_as_uint(kSplit ? a : v[e]);
-            lo[e] = __float_as_uint(b);
+              for (int s = 2; s >= 0; --s) mma_16<TW>(p, three[i][s], b0, b1);
+            }
           }
-          mma_tf32(p, hi, b0, b1);
-          if constexpr (kSplit) mma_tf32(p, lo, b0, b1);
+        } else {
+          float w[8];
+          shared_f32<TW, 8>(wp, w);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t b0 = __float_as_uint(w[2 * q]), b1 = __float_as_uint(w[2 * q + 1]);
+            const float v[4] = {f[0][2 * q], f[1][2 * q], f[0][2 * q + 1], f[1][2 * q + 1]};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float a, b;
+              tf32_split(v[e], a, b);
+              hi[e] = __float_as_uint(kSplit ? a : v[e]);
+              lo[e] = __float_as_uint(b);
+            }
+            if constexpr (kSplit) mma_tf32(p, lo, b0, b1);
+            mma_tf32(p, hi, b0, b1);
+          }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[j][e] += p[e];
@@ -477,32 +541,53 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
     float acc[8][4] = {};
     const uint8_t* b = bs + buf * width * pitch + cw * kColsWarp * pitch;
     for (int j0 = 0; j0 < c.r && !none; j0 += 4 * JV) {
-      uint32_t hi[JV / 2][4], lo[JV / 2][4];
+      constexpr bool kThree = JV == 4 && !__is_same(TW, __half);
+      uint32_t hi[JV / 2][4], lo[JV / 2][4], three[3][4];
+      float v[JV / 2][4];  // T of rows g, g + 8, two ranks each
 #pragma unroll
       for (int q = 0; q < JV / 2; ++q) {
         const float* p = ts + (16 * rw + g) * ld + j0 + JV * t + 2 * q;
         const float2 f0 = *reinterpret_cast<const float2*>(p);
         const float2 f1 = *reinterpret_cast<const float2*>(p + 8 * ld);
-        const float v[4] = {f0.x, f1.x, f0.y, f1.y};
+        v[q][0] = f0.x, v[q][1] = f1.x, v[q][2] = f0.y, v[q][3] = f1.y;
+      }
+      if constexpr (kThree) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x, r;
-          tf32_split(v[e], x, r);
-          hi[q][e] = __float_as_uint(x);
-          lo[q][e] = __float_as_uint(r);
+        for (int e = 0; e < 4; ++e) {  // row e % 2, the pair e / 2
+          uint32_t p[3];
+          bf16_split3(v[e / 2][e % 2], v[e / 2][2 + e % 2], p);
+#pragma unroll
+          for (int s = 0; s < 3; ++s) three[s][e] = p[s];
         }
+      } else {
+#pragma unroll
+        for (int q = 0; q < JV / 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x, r;
+            tf32_split(v[q][e], x, r);
+            hi[q][e] = __float_as_uint(x);
+            lo[q][e] = __float_as_uint(r);
+          }
       }
 #pragma unroll
       for (int p = 0; p < 8; ++p) {
         // columns past M hold what the buffer held: they are not stored
         const int col = 16 * (p / 2) + 4 * (g / 2) + 2 * (p % 2) + g % 2;
-        float w[JV];
-        shared_f32<TW, JV>(b + col * pitch + (j0 + JV * t) * 2, w);
+        const uint8_t* wp = b + col * pitch + (j0 + JV * t) * 2;
+        if constexpr (kThree) {
+          const uint2 w = *reinterpret_cast<const uint2*>(wp);
 #pragma unroll
-        for (int q = 0; q < JV / 2; ++q) {
-          const uint32_t b0 = __float_as_uint(w[2 * q]), b1 = __float_as_uint(w[2 * q + 1]);
-          mma_tf32(acc[p], lo[q], b0, b1);
-          mma_tf32(acc[p], hi[q], b0, b1);
+          for (int s = 2; s >= 0; --s) mma_16<TW>(acc[p], three[s], w.x, w.y);
+        } else {
+          float w[JV];
+          shared_f32<TW, JV>(wp, w);
+#pragma unroll
+          for (int q = 0; q < JV / 2; ++q) {
+            const uint32_t b0 = __float_as_uint(w[2 * q]), b1 = __float_as_uint(w[2 * q + 1]);
+            mma_tf32(acc[p], lo[q], b0, b1);
+            mma_tf32(acc[p], hi[q], b0, b1);
+          }
         }
       }
     }
@@ -565,9 +650,9 @@ cudaError_t expand_v(const LoraCall& c, bool vec, cudaStream_t s) {
   while (col_warps > 1 && (expand_smem_bytes(16 * RW, c.r, col_warps) > kExpandSmem ||
                            kColsWarp * col_warps >= 2 * c.M))
     col_warps /= 2;
-  // column parts: as many as fill the SMs twice, whole blocks each
+  // column parts: about four CTAs an SM (two run at a time), whole blocks each
   const int width = kColsWarp * col_warps, blocks = (c.M + width - 1) / width;
-  long long parts = (2 * 152 + tiles - 1) / tiles;
+  long long parts = (4 * 152 + tiles - 1) / tiles;
   if (parts > blocks) parts = blocks;
   const int part_cols = (int)((blocks + parts - 1) / parts) * width;
   const dim3 grid((unsigned)tiles, (unsigned)((c.M + part_cols - 1) / part_cols));
