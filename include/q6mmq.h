@@ -521,7 +521,7 @@ int q4k_mmq(const void *plane, const uint16_t *wq, int M, int K, const int8_t *X
 int q6_group_workspace_bytes(int N, int per_row, int groups, size_t *bytes);
 
 /* Groups items by ids [N][per_row] (device int32); an id outside 0 ..
- * groups - 1 belongs to no group. workspace: device, 4-byte aligned, at least
+ * groups - 1 belongs to no group. workspace: device, 16-byte aligned, at least
  * q6_group_workspace_bytes() (may be NULL when that is 0). */
 int q6_group_rows(const int32_t *ids, int N, int per_row, int groups, int32_t *offsets,
                   int32_t *rows, int32_t *pos, void *workspace, size_t workspace_bytes,

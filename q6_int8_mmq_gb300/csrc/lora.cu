@@ -705,11 +705,11 @@ cudaError_t lora_t(const LoraCall& c, cudaStream_t s) {
 }  // namespace
 
 int lora_splits(long long items, int L, int r, int K) {
-  // K parts over CTAs until there are about two CTAs an SM, at least 256 of K
-  // each
+  // K parts over CTAs, at least 256 of K each, as many as run at a time (two
+  // CTAs an SM)
   const long long tiles = most_tiles(items, L, many(items, L) ? kBigRows : 16) *
                           ((r + kRankBlock - 1) / kRankBlock);
-  long long splits = (2 * 152 + tiles - 1) / tiles;
+  long long splits = 2 * 152 / tiles;
   if (splits > K / 256) splits = K / 256;
   return splits < 1 ? 1 : splits > 16 ? 16 : (int)splits;
 }

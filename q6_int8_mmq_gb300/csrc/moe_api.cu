@@ -34,13 +34,13 @@ int check_group(int N, int per_row, int groups) {
 }
 size_t group_bytes(int N, int per_row, int groups) {
   const int blocks = q6::group_blocks((long long)N * per_row, N);
-  return blocks > 1 ? (size_t)blocks * (size_t)(groups + 1) * 4 : 0;
+  return blocks > 1 ? (size_t)blocks * (size_t)q6::group_hist_ld(groups) * 4 : 0;
 }
 int check_group_buffers(const void* offsets, const void* rows, const void* pos, const void* ws,
                         size_t ws_bytes, size_t need, int N) {
   if (!offsets || (N > 0 && (!rows || !pos))) return fail(Q6_EINVAL, "null pointer");
-  if (!aligned(offsets, 4) || !aligned(rows, 4) || !aligned(pos, 4) || !aligned(ws, 4))
-    return fail(Q6_EALIGN, "offsets, rows, pos and the workspace must be 4-byte aligned");
+  if (!aligned(offsets, 4) || !aligned(rows, 4) || !aligned(pos, 4) || !aligned(ws, 16))
+    return fail(Q6_EALIGN, "offsets, rows and pos must be 4-byte, the workspace 16-byte aligned");
   if (need && (!ws || ws_bytes < need))
     return fail(Q6_ESIZE, "the grouping needs a workspace of %zu bytes", need);
   return Q6_OK;

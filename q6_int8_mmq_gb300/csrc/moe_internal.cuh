@@ -25,6 +25,8 @@ inline int group_blocks(long long items, int N) {
   if (items <= kGroupSingle || N <= 1) return 1;
   return N < kGroupBlocks ? N : kGroupBlocks;
 }
+// Row length of the blocks' counts: groups and the section of none, padded.
+__host__ __device__ constexpr int group_hist_ld(int G) { return (G + 4) / 4 * 4; }
 cudaError_t launch_route(const void* logits, int type, int N, int E, long long ldl, int topk,
                          int renorm, int32_t* ids, float* weights, int32_t* offsets,
                          int32_t* rows, int32_t* pos, int32_t* hist, cudaStream_t s);

@@ -11,9 +11,10 @@
 // Grouping: a stable counting sort of the items (token n, slot j) by id. Each
 // block owns a contiguous range of tokens and counts its ids in shared memory
 // (integer counts: the order of the atomics does not show). A second kernel
-// adds up the counts of the blocks before it and places its items in order,
-// 32 at a time, each behind the equal ids on lower lanes. A call of few items
-// does all of it in one block of the first kernel.
+// adds up the counts of the blocks before it and places its items, two threads
+// each, behind the equal ids before them in the block (counted one against
+// the other in shared memory: 512 items are 32 steps of eight ids). A call of
+// few items does all of it in one block of the first kernel.
 //
 // Bound: a few dependent latencies, not bytes (8191 tokens of 256 bf16
 // logits are 4.2 MB, 0.6 us of memory time).
@@ -24,8 +25,11 @@
 namespace q6 {
 namespace {
 
-constexpr int kRouteThreads = 512;
 constexpr int kPlaceThreads = 1024;
+constexpr int kCountThreads = 512;
+// Threads of a routing block with V logits a lane (its registers).
+template <int V>
+constexpr int kRouteThreadsOf = V <= 8 ? 1024 : 512;
 
 // Order-preserving key of a float; 0 (below every key of a number) for -inf
 // and NaN. -0 counts as +0.
@@ -47,74 +51,93 @@ __device__ __forceinline__ void block_rows(int N, int& n0, int& n1) {
 // The exclusive prefix sum of smem counts cnt[0..G] (G + 1 values) into
 // base[0..G], by the whole block; base[G + 1] is the total.
 __device__ void block_scan(const int* cnt, int* base, int G) {
-  // one warp, 32 counts a step: at most 33 steps
-  if (threadIdx.x < 32) {
-    int run = 0;
-    for (int i0 = 0; i0 <= G; i0 += 32) {
-      const int i = i0 + (int)threadIdx.x;
-      const int v = i <= G ? cnt[i] : 0;
-      int x = v;
+  __shared__ int warps[32];
+  const int per = (G + (int)blockDim.x) / (int)blockDim.x;  // consecutive values a thread
+  const int i0 = (int)threadIdx.x * per, i1 = min(i0 + per, G + 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int mine = 0;
+  for (int i = i0; i < i1; ++i) mine += cnt[i];
+  int x = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if ((int)threadIdx.x >= o) x += y;
-      }
-      if (i <= G) base[i] = run + x - v;
-      run += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (threadIdx.x == 0) base[G + 1] = run;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
+  if (lane == 31) warps[warp] = x;
+  __syncthreads();
+  int before = x - mine;
+  for (int w = 0; w < warp; ++w) before += warps[w];
+  for (int i = i0; i < i1; ++i) {
+    base[i] = before;
+    before += cnt[i];
+  }
+  if (threadIdx.x == blockDim.x - 1) base[G + 1] = before;
   __syncthreads();
 }
 
-// Places the items of rows n0..n1-1 in order: warp 0 takes 32 a step, each
-// behind the equal ids on lower lanes; base[g] runs ahead.
+// Places the items of rows n0..n1-1 in order, blockDim.x / 2 at a time, two
+// threads an item; base[g] runs ahead. ids_s holds that many ids.
 __device__ void place_items(const int32_t* ids, int n0, int n1, int per_row, int G, int* base,
-                            int32_t* rows, int32_t* pos) {
-  if (threadIdx.x >= 32) return;
-  const int lane = threadIdx.x;
-  const long long i1 = (long long)n1 * per_row;
-  for (long long i0 = (long long)n0 * per_row; i0 < i1; i0 += 32) {
-    const long long i = i0 + lane;
+                            int* ids_s, int32_t* rows, int32_t* pos) {
+  const int me = threadIdx.x / 2, half = threadIdx.x % 2, chunk = (int)blockDim.x / 2;
+  const long long end = (long long)n1 * per_row;
+  for (long long i0 = (long long)n0 * per_row; i0 < end; i0 += chunk) {
+    const long long i = i0 + me;
     int g = -1;
-    if (i < i1) {
+    if (i < end) {
       g = ids[i];
       if (g < 0 || g >= G) g = G;
     }
-    const unsigned same = __match_any_sync(0xffffffffu, g);
+    if (half == 0) ids_s[me] = g;
+    __syncthreads();
+    // equal ids before mine: whole groups of eight, every other one by each of
+    // the two threads, then what is left
+    int before = 0;
     if (g >= 0) {
-      const int before = __popc(same & ((1u << lane) - 1u));
-      const int at = base[g] + before;
+      const int4* v = reinterpret_cast<const int4*>(ids_s);
+      for (int k = half; k < me / 8; k += 2) {
+        const int4 a = v[2 * k], b = v[2 * k + 1];
+        before += (a.x == g) + (a.y == g) + (a.z == g) + (a.w == g) + (b.x == g) + (b.y == g) +
+                  (b.z == g) + (b.w == g);
+      }
+      for (int k = me / 8 * 8 + half; k < me; k += 2) before += ids_s[k] == g;
+    }
+    before += __shfl_xor_sync(0xffffffffu, before, 1);
+    int at = 0;
+    if (g >= 0) at = base[g] + before;
+    __syncthreads();
+    if (g >= 0 && half == 0) {
       rows[at] = (int)(i / per_row);
       pos[i] = g < G ? at : -1;
-      __syncwarp(same);
-      if (before == 0) base[g] += __popc(same);
+      if (i0 + chunk < end) atomicAdd(&base[g], 1);
     }
-    __syncwarp();
+    if (i0 + chunk < end) __syncthreads();
   }
 }
 
 // Ends a counting kernel: a grid of one block scans and places at once, any
 // other leaves its counts in hist[block][G + 1].
 __device__ void finish_counts(const int32_t* ids, int n0, int n1, int per_row, int G, int* cnt,
-                              int* base, int32_t* offsets, int32_t* rows, int32_t* pos,
-                              int32_t* hist) {
+                              int* base, int* ids_s, int32_t* offsets, int32_t* rows,
+                              int32_t* pos, int32_t* hist) {
   if (gridDim.x == 1) {
     block_scan(cnt, base, G);
     for (int g = threadIdx.x; g <= G + 1; g += blockDim.x) offsets[g] = base[g];
     __syncthreads();
-    place_items(ids, n0, n1, per_row, G, base, rows, pos);
+    place_items(ids, n0, n1, per_row, G, base, ids_s, rows, pos);
   } else {
-    for (int g = threadIdx.x; g <= G; g += blockDim.x)
-      hist[(size_t)blockIdx.x * (G + 1) + g] = cnt[g];
+    const int ld = group_hist_ld(G);  // past G: zeros
+    for (int g = threadIdx.x; g < ld; g += blockDim.x)
+      hist[(size_t)blockIdx.x * ld + g] = g <= G ? cnt[g] : 0;
   }
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kRouteThreads)
+__global__ void __launch_bounds__(kRouteThreadsOf<V>)
 route_kernel(const T* logits, int N, int E, long long ldl, int topk, int renorm, int32_t* ids,
              float* weights, int32_t* offsets, int32_t* rows, int32_t* pos, int32_t* hist) {
   __shared__ int cnt[kMaxGroups + 1], base[kMaxGroups + 2];
+  __shared__ __align__(16) int ids_s[512];
   griddep_wait();
   griddep_launch_dependents();
   for (int g = threadIdx.x; g <= E; g += blockDim.x) cnt[g] = 0;
@@ -122,7 +145,7 @@ route_kernel(const T* logits, int N, int E, long long ldl, int topk, int renorm,
   int n0, n1;
   block_rows(N, n0, n1);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int n = n0 + warp; n < n1; n += kRouteThreads / 32) {
+  for (int n = n0 + warp; n < n1; n += (int)blockDim.x / 32) {
     const T* row = logits + (size_t)n * ldl;
     uint32_t key[V];
     float x[V];
@@ -176,13 +199,14 @@ route_kernel(const T* logits, int N, int E, long long ldl, int topk, int renorm,
     }
   }
   __syncthreads();
-  finish_counts(ids, n0, n1, topk, E, cnt, base, offsets, rows, pos, hist);
+  finish_counts(ids, n0, n1, topk, E, cnt, base, ids_s, offsets, rows, pos, hist);
 }
 
-__global__ void __launch_bounds__(kRouteThreads)
+__global__ void __launch_bounds__(kCountThreads)
 count_kernel(const int32_t* ids, int N, int per_row, int G, int32_t* offsets, int32_t* rows,
              int32_t* pos, int32_t* hist) {
   __shared__ int cnt[kMaxGroups + 1], base[kMaxGroups + 2];
+  __shared__ __align__(16) int ids_s[512];
   griddep_wait();
   griddep_launch_dependents();
   for (int g = threadIdx.x; g <= G; g += blockDim.x) cnt[g] = 0;
@@ -195,7 +219,7 @@ count_kernel(const int32_t* ids, int N, int per_row, int G, int32_t* offsets, in
     atomicAdd(&cnt[g < 0 || g >= G ? G : g], 1);
   }
   __syncthreads();
-  finish_counts(ids, n0, n1, per_row, G, cnt, base, offsets, rows, pos, hist);
+  finish_counts(ids, n0, n1, per_row, G, cnt, base, ids_s, offsets, rows, pos, hist);
 }
 
 // The second kernel of a large grouping: this block's first place in every
@@ -203,26 +227,32 @@ count_kernel(const int32_t* ids, int N, int per_row, int G, int32_t* offsets, in
 __global__ void __launch_bounds__(kPlaceThreads)
 place_kernel(const int32_t* ids, int N, int per_row, int G, int32_t* offsets, int32_t* rows,
              int32_t* pos, const int32_t* hist) {
-  __shared__ int cnt[kMaxGroups + 1], before[kMaxGroups + 1], base[kMaxGroups + 2];
-  for (int g = threadIdx.x; g <= G; g += blockDim.x) cnt[g] = before[g] = 0;
+  __shared__ int cnt[kMaxGroups + 4], before[kMaxGroups + 4], base[kMaxGroups + 2];
+  __shared__ __align__(16) int ids_s[kPlaceThreads / 2];
+  const int ld = group_hist_ld(G);
+  for (int g = threadIdx.x; g < ld; g += blockDim.x) cnt[g] = before[g] = 0;
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  // several threads a group when there are few groups, each over its share of
-  // the blocks
-  const int parts = max(1, (int)blockDim.x / (G + 1));
-  for (int w = threadIdx.x; w < (G + 1) * parts; w += blockDim.x) {
-    const int g = w % (G + 1), p = w / (G + 1);
-    const int b1 = (int)((long long)gridDim.x * (p + 1) / parts);
-    int all = 0, low = 0;
+  // four groups a thread, several threads for the same four, each over its
+  // share of the blocks
+  const int quads = ld / 4, parts = max(1, (int)blockDim.x / quads);
+  for (int w = threadIdx.x; w < quads * parts; w += blockDim.x) {
+    const int q = w % quads, p = w / quads;
+    const int b1 = (int)gridDim.x * (p + 1) / parts;
+    int all[4] = {}, low[4] = {};
 #pragma unroll 8
-    for (int b = (int)((long long)gridDim.x * p / parts); b < b1; ++b) {
-      const int c = hist[(size_t)b * (G + 1) + g];
-      all += c;
-      low += b < (int)blockIdx.x ? c : 0;
+    for (int b = (int)gridDim.x * p / parts; b < b1; ++b) {
+      const int4 c = *reinterpret_cast<const int4*>(hist + (size_t)b * ld + 4 * q);
+      const int m = b < (int)blockIdx.x ? -1 : 0;
+      all[0] += c.x, all[1] += c.y, all[2] += c.z, all[3] += c.w;
+      low[0] += c.x & m, low[1] += c.y & m, low[2] += c.z & m, low[3] += c.w & m;
     }
-    atomicAdd(&cnt[g], all);
-    atomicAdd(&before[g], low);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (all[k]) atomicAdd(&cnt[4 * q + k], all[k]);
+      if (low[k]) atomicAdd(&before[4 * q + k], low[k]);
+    }
   }
   __syncthreads();
   block_scan(cnt, base, G);
@@ -233,14 +263,17 @@ place_kernel(const int32_t* ids, int N, int per_row, int G, int32_t* offsets, in
   __syncthreads();
   int n0, n1;
   block_rows(N, n0, n1);
-  place_items(ids, n0, n1, per_row, G, base, rows, pos);
+  place_items(ids, n0, n1, per_row, G, base, ids_s, rows, pos);
 }
 
 template <typename T, int V>
 cudaError_t route_v(const void* logits, int N, int E, long long ldl, int topk, int renorm,
                     int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* pos,
                     int32_t* hist, int blocks, cudaStream_t s) {
-  return launch_pdl(route_kernel<T, V>, dim3(blocks), dim3(kRouteThreads), 0, s,
+  // a warp a token where one block has few
+  const int threads = blocks == 1 && N < kRouteThreadsOf<V> / 32 ? (N < 4 ? 128 : 32 * N)
+                                                                 : kRouteThreadsOf<V>;
+  return launch_pdl(route_kernel<T, V>, dim3(blocks), dim3(threads), 0, s,
                     static_cast<const T*>(logits), N, E, ldl, topk, renorm, ids, weights, offsets,
                     rows, pos, hist);
 }
@@ -291,7 +324,7 @@ cudaError_t launch_route(const void* logits, int type, int N, int E, long long l
 cudaError_t launch_group(const int32_t* ids, int N, int per_row, int G, int32_t* offsets,
                          int32_t* rows, int32_t* pos, int32_t* hist, cudaStream_t s) {
   const int blocks = group_blocks((long long)N * per_row, N);
-  const cudaError_t e = launch_pdl(count_kernel, dim3(blocks), dim3(kRouteThreads), 0, s, ids, N,
+  const cudaError_t e = launch_pdl(count_kernel, dim3(blocks), dim3(kCountThreads), 0, s, ids, N,
                                    per_row, G, offsets, rows, pos, hist);
   if (e != cudaSuccess || blocks == 1) return e;
   return place(ids, N, per_row, G, offsets, rows, pos, hist, blocks, s);

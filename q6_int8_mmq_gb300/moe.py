@@ -56,8 +56,28 @@ def _stream(stream, device):
     if torch.cuda.current_device() != device.index:
         raise Q6Error(Q6_EINVAL, f"the tensors are on {device}, the current device is "
                                  f"cuda:{torch.cuda.current_device()}")
-    return torch.cuda.current_stream(device.index).cuda_stream if stream is None else (
-        stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return _current_stream()(device.index)
+
+
+@functools.lru_cache(maxsize=None)
+def _current_stream():
+    """device index -> the current stream's raw handle (without a stream
+    object, where this PyTorch can)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _plain(t, dtype, shape, device):
+    """Whether t is a contiguous tensor of this dtype and shape on this device:
+    what _tensor() accepts, decided quickly. Anything else goes to _tensor()."""
+    try:
+        return (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                and t.device == device)
+    except AttributeError:
+        return False
 
 
 def _on(stream):
@@ -99,13 +119,8 @@ class Groups:
         if need and self.workspace is None:
             raise Q6Error(Q6_EINVAL, f"this grouping needs a workspace of {need} bytes")
 
-    @property
-    def items(self):
-        return self.N * self.per_row
-
-    @property
-    def device(self):
-        return self.offsets.device
+        object.__setattr__(self, "items", n)
+        object.__setattr__(self, "device", self.offsets.device)
 
 
 def alloc_groups(N: int, per_row: int, n_groups: int, device=None) -> Groups:
@@ -278,7 +293,8 @@ def experts_mmq(w: ExpertWeights, X, groups: Groups, gather: bool = True, out=No
     code = _type(X, "X", half=True)
     nx = _rows2d(X, "X", w.K)
     dev, items = w.device, groups.items
-    _tensor(X, "X", X.dtype, (nx, w.K), dev, rows=True)
+    if not _plain(X, X.dtype, (nx, w.K), dev):
+        _tensor(X, "X", X.dtype, (nx, w.K), dev, rows=True)
     if groups.n_groups != w.E or groups.device != dev:
         raise Q6Error(Q6_EINVAL, f"a grouping of {groups.n_groups} groups on {groups.device} for "
                                  f"{w.E} experts on {dev}")
@@ -289,7 +305,7 @@ def experts_mmq(w: ExpertWeights, X, groups: Groups, gather: bool = True, out=No
     if out is None:
         with _on(stream):
             out = torch.empty(shape, dtype=X.dtype, device=dev)
-    else:
+    elif not _plain(out, X.dtype, shape, dev):
         _tensor(out, "out", X.dtype, shape, dev, rows=True)
     need, ws = experts_workspace_bytes(w.E, w.K, code, items, bool(gather)), None
     if need:
@@ -316,14 +332,16 @@ def moe_combine(Y, pos, weights, shared=None, out=None, stream=None):
     if not isinstance(pos, torch.Tensor) or pos.dim() != 2:
         raise Q6Error(Q6_EINVAL, "pos must be a 2-D torch tensor [N, topk]")
     N, topk = pos.shape
-    _tensor(pos, "pos", torch.int32, (N, topk), dev)
-    _tensor(weights, "weights", torch.float32, (N, topk), dev)
-    if shared is not None:
+    if not _plain(pos, torch.int32, (N, topk), dev):
+        _tensor(pos, "pos", torch.int32, (N, topk), dev)
+    if not _plain(weights, torch.float32, (N, topk), dev):
+        _tensor(weights, "weights", torch.float32, (N, topk), dev)
+    if shared is not None and not _plain(shared, torch.float32, (N, M), dev):
         _tensor(shared, "shared", torch.float32, (N, M), dev, rows=True)
     if out is None:
         with _on(stream):
             out = torch.empty((N, M), dtype=Y.dtype, device=dev)
-    else:
+    elif not _plain(out, Y.dtype, (N, M), dev):
         _tensor(out, "out", Y.dtype, (N, M), dev, rows=True)
     _check(load().q6_moe_combine(Y.data_ptr(), code, _row_stride(Y), pos.data_ptr(),
                                  weights.data_ptr(), N, topk, M, _ptr(shared),
@@ -376,17 +394,22 @@ def lora_add(adapters: LoraAdapters, X, groups: Groups, Y, out=None, stream=None
     L, r, K = A.shape
     M, dev, N = adapters.B.shape[1], A.device, groups.items
     code = _type(X, "X")
-    _tensor(X, "X", X.dtype, (N, K), dev, rows=True)
+    if not _plain(X, X.dtype, (N, K), dev):
+        _tensor(X, "X", X.dtype, (N, K), dev, rows=True)
     if groups.n_groups != L or groups.per_row != 1 or groups.device != dev:
         raise Q6Error(Q6_EINVAL, f"adapters need one id a token in {L} groups on {dev}")
-    _tensor(Y, "Y", torch.float32, (N, M), dev, rows=True)
+    if not _plain(Y, torch.float32, (N, M), dev):
+        _tensor(Y, "Y", torch.float32, (N, M), dev, rows=True)
     if out is None:
         out = Y
-    else:
+    elif not _plain(out, torch.float32, (N, M), dev):
         _tensor(out, "out", torch.float32, (N, M), dev, rows=True)
     need = lora_workspace_bytes(N, L, r, K)
-    with _on(stream):
+    if stream is None:
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        with _on(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _check(load().q6_lora_add(A.data_ptr(), adapters.B.data_ptr(), adapters.scale.data_ptr(),
                               _types()[A.dtype], L, r, M, K, X.data_ptr(), code, _row_stride(X),
                               groups.offsets.data_ptr(), groups.rows.data_ptr(), N, Y.data_ptr(),
