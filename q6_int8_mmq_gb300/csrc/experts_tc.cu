@@ -39,6 +39,12 @@
 //          every other tile of up to 128 items)
 // TMEM: columns 0-255 two accumulators of 128 items (or one of 256), 256-511
 // four A slots of 128 of K.
+// The walk is in units: 128 of K for tiles of more than 128 items, 256 for
+// others. A unit has one x stage and one or two A slots; one barrier says that
+// all of it is there (both CTAs' copies and dequantised halves), another that
+// its MMAs are through. (A wait costs the MMA warp about 120 cycles and a
+// commit 150 or more, a unit's MMAs at 128 items 1024: with separate barriers
+// for x and A and 128 of K each, 1023 tokens over 64 experts took 119 us.)
 // Every wait is bounded (see q6_internal.cuh), and the pair meets once more
 // before either CTA leaves.
 #include "moe_internal.cuh"
@@ -48,7 +54,7 @@ namespace {
 
 constexpr int kThreads = 640;
 constexpr int kTileN = 256;
-constexpr int kXStages = 4, kXStage = 32 * 1024;
+constexpr int kUnits = 4, kXStage = 32 * 1024;  // units in flight; an x stage each
 // Packed super-blocks in flight: 54 KB of either format.
 template <int kFmt>
 constexpr int kWStagesOf = kFmt == Q6_FMT_Q4K ? 3 : 2;
@@ -56,18 +62,21 @@ constexpr int kMaxWStages = 3;
 constexpr int kASlots = 4, kACols = 64, kACol0 = 256;
 constexpr int kTmemCols = 512;
 
-enum : uint32_t { kSiteXEmpty = 32, kSiteXFull, kSiteWEmpty, kSiteWFull, kSiteAEmpty, kSiteAFull,
-                  kSiteDEmpty, kSiteDFull, kSiteDrain };
+enum : uint32_t { kSiteReady = 32, kSiteDone, kSiteWEmpty, kSiteWFull, kSiteDEmpty, kSiteDFull,
+                  kSiteDrain };
 
 struct Bars {
-  uint64_t x_full[kXStages], x_empty[kXStages];
+  uint64_t ready[kUnits], done[kUnits];
   uint64_t w_full[kMaxWStages], w_empty[kMaxWStages];
-  uint64_t a_full[kASlots], a_empty[kASlots];
   uint64_t d_full[2], d_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
 };
+// Arrivals that make a unit ready: the x copies' opening, and 16 of the
+// dequantising warps (one for each of 16 warps and half super-blocks, or two
+// for each of 8).
+constexpr int kReadyArrivals = 17;
 
 struct Args {
   const uint8_t* plane;
@@ -84,7 +93,7 @@ template <int kFmt>
 constexpr int kWTile = kFmt == Q6_FMT_Q4K ? kQ4Tile : kQ6Tile;
 constexpr int kOutWarp = 2048;  // epilogue staging of a warp: 32 items of 64 bytes
 template <int kFmt>
-constexpr int kSmemBytes = 1024 + kXStages * kXStage + kWStagesOf<kFmt> * kWTile<kFmt> + 8 * kOutWarp +
+constexpr int kSmemBytes = 1024 + kUnits * kXStage + kWStagesOf<kFmt> * kWTile<kFmt> + 8 * kOutWarp +
                            (kMaxGroups + 1) * 4 + 12 + (int)sizeof(Bars);
 
 // True in one lane of the converged warp. TMA and MMA instructions take their
@@ -132,15 +141,17 @@ __device__ __forceinline__ void commit_own(uint64_t* bar) {
           smem_u32(bar))
       : "memory");
 }
-// Arrives once on `bar` of CTA 0 of the pair after this thread's tcgen05 loads
+// Arrives `count` times on `bar` of CTA 0 of the pair after this warp's tcgen05 loads
 // or stores, which the tcgen05 waits and fences around the barrier order;
 // nothing else is published, so the arrival needs no release (one of cluster
 // scope was measured at 1300 cycles behind the packed-weight reads).
-__device__ __forceinline__ void arrive_leader_tmem(uint64_t* bar) {
+__device__ __forceinline__ void arrive_leader_tmem(uint64_t* bar, uint32_t count = 1) {
   asm volatile(
       "{\n\t.reg .b32 ra;\n\t"
       "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
-      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [ra];\n\t}\n" ::"r"(smem_u32(bar))
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [ra], %1;\n\t}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(count)
       : "memory");
 }
 // A TMA load into this CTA that counts on `bar` of CTA 0 of the pair.
@@ -389,12 +400,12 @@ __device__ __forceinline__ int band_of(const Args& a, int pair, int rank) {
 // past n / 2 are loaded and not used: one request a block is worth more than
 // the bytes; requests by several lanes took about 150 cycles each).
 __device__ __forceinline__ int box_of(int n) { return n > 128 ? 3 : n > 64 ? 2 : n > 32 ? 1 : 0; }
-// log2 of the 64-of-K blocks an x stage holds.
-__device__ __forceinline__ int stage_shift(int n) { return n > 128 ? 1 : 2; }
+// log2 of a unit's 64-of-K blocks.
+__device__ __forceinline__ int unit_shift(int n) { return n > 128 ? 1 : 2; }
 
-// The MMAs of one tile, by the whole MMA warp; kShift = stage_shift(n).
+// The MMAs of one tile, by the whole MMA warp; kShift = unit_shift(n).
 struct MmaState {
-  int x, a;  // x stages and A slots used so far
+  int unit, a;  // units and A slots used so far
 };
 template <int kShift>
 __device__ __forceinline__ bool tile_mmas(MmaState& st, Bars* bars, const uint8_t* xring,
@@ -404,31 +415,26 @@ __device__ __forceinline__ bool tile_mmas(MmaState& st, Bars* bars, const uint8_
   const uint32_t idesc = idesc_f16_f32(256, n);
   const uint32_t x_block = (uint32_t)(16 << box_of(n)) * 128 >> 4;  // in descriptor units
   const uint32_t x0 = sw128_desc_lo(smem_u32(xring));
-  for (int sb = 0; sb < sbs; ++sb) {
+  const int units = 4 * sbs >> kShift;
+  for (int u = 0; u < units; ++u) {
+    const int slot = st.unit % kUnits;
+    if (!mbar_wait_warp(&bars->ready[slot], (st.unit / kUnits) & 1, abort_flag, status, kSiteReady))
+      return false;
+    tc_fence_after();
+    if (elect_one()) {
+      const uint32_t b = x0 + slot * (kXStage >> 4);
+      // A slots of a unit of 256 of K are neighbours: super-blocks begin at an
+      // even slot
+      const uint32_t at = tmem + (uint32_t)(kACol0 + st.a % kASlots * kACols);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {  // A slots: 128 of K
-      const int xs = st.x % kXStages, as = st.a % kASlots;
-      if (kShift == 1 || u == 0)
-        if (!mbar_wait_warp(&bars->x_full[xs], (st.x / kXStages) & 1, abort_flag, status,
-                            kSiteXFull))
-          return false;
-      if (!mbar_wait_warp(&bars->a_full[as], (st.a / kASlots) & 1, abort_flag, status, kSiteAFull))
-        return false;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t b = x0 + xs * (kXStage >> 4) + (kShift == 1 ? 0 : 2 * u) * x_block;
-        const uint32_t at = tmem + (uint32_t)(kACol0 + as * kACols);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          umma_f16_pair(d_tmem, at + 8 * i, b + (i / 4) * x_block + 2 * (i % 4), idesc,
-                        (uint32_t)(sb > 0 || u > 0 || i > 0));
-        commit_pair(&bars->a_empty[as]);
-        if (kShift == 1 || u == 1) commit_pair(&bars->x_empty[xs]);
-      }
-      __syncwarp();
-      ++st.a;
-      if (kShift == 1 || u == 1) ++st.x;
+      for (int i = 0; i < 4 << kShift; ++i)
+        umma_f16_pair(d_tmem, at + 8 * i, b + (i / 4) * x_block + 2 * (i % 4), idesc,
+                      (uint32_t)(u > 0 || i > 0));
+      commit_pair(&bars->done[slot]);
     }
+    __syncwarp();
+    ++st.unit;
+    st.a += kShift;
   }
   return true;
 }
@@ -441,7 +447,7 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* xring = smem;
-  uint8_t* wring = smem + kXStages * kXStage;
+  uint8_t* wring = smem + kUnits * kXStage;
   uint8_t* out_stage = wring + kWStages * kWTile<kFmt>;
   int* start = reinterpret_cast<int*>(out_stage + 8 * kOutWarp);
   Bars* bars = reinterpret_cast<Bars*>(
@@ -451,17 +457,13 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
   volatile int* abort_flag = &bars->abort;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kXStages; ++i) {
-      mbar_init(&bars->x_full[i], 1);  // both CTAs' copies, in CTA 0
-      mbar_init(&bars->x_empty[i], 1);
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&bars->ready[i], kReadyArrivals);  // used in CTA 0
+      mbar_init(&bars->done[i], 1);
     }
     for (int i = 0; i < kWStages; ++i) {
       mbar_init(&bars->w_full[i], 1);
       mbar_init(&bars->w_empty[i], 8);
-    }
-    for (int i = 0; i < kASlots; ++i) {
-      mbar_init(&bars->a_full[i], 8);  // both CTAs' warps, in CTA 0
-      mbar_init(&bars->a_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->d_full[i], 1);
@@ -503,40 +505,36 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
 
   if (warp == 0) {
     // --------------------------------------------------------------- load x --
-    int g = 0;  // stages issued
+    int g = 0;  // units opened
     for (int t = cluster; t < total && ok; t += clusters) {
       const Tile w = tile_at(a, start, t);
       const int rows = w.n / 2;  // this CTA's
       const int box = box_of(w.n);
-      const int shift = stage_shift(w.n);
+      const int shift = unit_shift(w.n);
       const int row0 = __shfl_sync(0xffffffffu, (int)w.first + rank * rows, 0);
       const int block = (16 << box) * 128;
       for (int k = 0; k < 4 * a.sbs; k += 1 << shift) {
-        const int slot = g % kXStages;
-        if (!(ok = mbar_wait_warp(&bars->x_empty[slot], ((g / kXStages) & 1) ^ 1, abort_flag, status,
-                                  kSiteXEmpty)))
+        const int slot = g % kUnits;
+        if (!(ok = mbar_wait_warp(&bars->done[slot], ((g / kUnits) & 1) ^ 1, abort_flag, status,
+                                  kSiteDone)))
           break;
         if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(&bars->x_full[slot], (uint32_t)(2 * block) << shift);
+          if (rank == 0) mbar_arrive_expect_tx(&bars->ready[slot], (uint32_t)(2 * block) << shift);
           for (int b = 0; b < 1 << shift; ++b)
-            tma_load_2d_pair(xring + slot * kXStage + b * block, &maps.box[box], &bars->x_full[slot],
-                        (k + b) * 64, row0);
+            tma_load_2d_pair(xring + slot * kXStage + b * block, &maps.box[box], &bars->ready[slot],
+                             (k + b) * 64, row0);
         }
         __syncwarp();
         ++g;
       }
     }
-    // the last stages' releases reach this CTA before it leaves
-    for (int k = g > kXStages ? g - kXStages : 0; k < g && ok; ++k)
-      ok = mbar_wait_warp(&bars->x_empty[k % kXStages], (k / kXStages) & 1, abort_flag, status,
-                          kSiteXEmpty);
+    // the last units' MMAs are through, and this CTA has been told, before it
+    // leaves
+    for (int k = g > kUnits ? g - kUnits : 0; k < g && ok; ++k)
+      ok = mbar_wait_warp(&bars->done[k % kUnits], (k / kUnits) & 1, abort_flag, status, kSiteDone);
     if (!ok && lane == 0) {
-      // Copies in flight land before the CTA exits: CTA 0 waits for those it
-      // counts; a copy whose stage CTA 0 has not opened is given 1 ms.
-      volatile int no_abort = 0;
-      for (int k = g > kXStages ? g - kXStages : 0; k < g && rank == 0; ++k)
-        mbar_wait_bounded(&bars->x_full[k % kXStages], (k / kXStages) & 1, &no_abort, status,
-                          kSiteXFull);
+      // Copies in flight land before the CTA exits. They count on a barrier
+      // that other arrivals complete too, so they are given 1 ms.
       for (const long long t0 = clock64(); clock64() - t0 < 2100000;) {
       }
     }
@@ -603,20 +601,27 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
     // ----------------------------------------------------------- dequantise --
     const int h = (warp - 4) / 4, row = 32 * (warp % 4) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
-    int gw = 0;
+    int gw = 0, unit = 0;
+    int last1 = -1, last2 = -1;  // units of this warp's last two halves, in this and the other slot
     for (int t = cluster; t < total && ok; t += clusters) {
       const Tile w = tile_at(a, start, t);
+      const bool split = unit_shift(w.n) == 1;  // a unit for each half
       const float inv = 1.0f / a.scale[((size_t)w.expert * a.bands + band_of(a, w.pair, rank)) * kBand + row];
       for (int sb = 0; sb < a.sbs; ++sb, ++gw) {
-        const int ws = gw % kWStages, ga = 2 * gw + h, as = ga % kASlots;
+        const int ws = gw % kWStages, as = (2 * gw + h) % kASlots;
+        const int mine = split ? unit + h : unit;
+        unit += split ? 2 : 1;
         if (!(ok = mbar_wait_warp(&bars->w_full[ws], (gw / kWStages) & 1, abort_flag, status,
                                   kSiteWFull)))
           break;
         Half<kFmt> half;
         half.load(wring + ws * kWTile<kFmt>, row, h, inv);
-        if (!(ok = mbar_wait_warp(&bars->a_empty[as], ((ga / kASlots) & 1) ^ 1, abort_flag, status,
-                                  kSiteAEmpty)))
+        // The slot's last unit is at most kUnits back, so its barrier has not
+        // gone further.
+        if (last2 >= 0 && !(ok = mbar_wait_warp(&bars->done[last2 % kUnits], (last2 / kUnits) & 1,
+                                                abort_flag, status, kSiteDone)))
           break;
+        last2 = last1, last1 = mine;
         tc_fence_after();
         const uint32_t dst = tmem + lanes + (uint32_t)(kACol0 + as * kACols);
 #pragma unroll
@@ -633,13 +638,9 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader_tmem(&bars->a_full[as]);
+        if (lane == 0) arrive_leader_tmem(&bars->ready[mine % kUnits], split ? 2 : 1);
       }
     }
-    // the last A slots' releases reach this CTA before it leaves
-    for (int k = gw > 2 ? gw - 2 : 0; k < gw && ok; ++k)
-      ok = mbar_wait_warp(&bars->a_empty[(2 * k + h) % kASlots], ((2 * k + h) / kASlots) & 1,
-                          abort_flag, status, kSiteAEmpty);
   } else if (warp >= 12) {
     // ------------------------------------------------------------- epilogue --
     // Thread (r, c) of a warp, r = lane / 4, holds rows 16 h + r and 16 h + 8 +
@@ -648,7 +649,7 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
     const int q = warp % 4, me = (warp - 12) / 4;   // me: the accumulator half
     T* Y = static_cast<T*>(a.Y);
     constexpr int kCols = kGlu ? 16 : 32;          // output features of a warp
-    constexpr int kUnits = kCols / 8;              // 16-byte units of an item
+    constexpr int kPieces = kCols / 8;              // 16-byte units of an item
     constexpr bool kScaled = !__is_same(T, __half);
     uint8_t* stage = out_stage + (warp - 12) * kOutWarp;
     // items of no expert: zeros
@@ -676,8 +677,8 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
       for (int k = 0; k < 4; ++k)
         xs[k] = kScaled && 32 * k + lane < count ? a.xscale[w.first + item0 + 32 * k + lane] : 1.0f;
       // this lane's first 16-byte unit of a piece, and the step to its next
-      constexpr int kStep = 32 / kUnits;
-      const int item = lane / kUnits, unit = lane % kUnits, m = m0 + 8 * unit;
+      constexpr int kStep = 32 / kPieces;
+      const int item = lane / kPieces, unit = lane % kPieces, m = m0 + 8 * unit;
       T* y = Y + (w.first + item0 + item) * a.ldy + m;
       const long long step = (long long)kStep * a.ldy;
       const bool whole = a.vec && m + 8 <= a.out;
@@ -735,10 +736,10 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
         }
         __syncwarp();
 #pragma unroll
-        for (int r = 0; r < kUnits; ++r, y += step) {
+        for (int r = 0; r < kPieces; ++r, y += step) {
           const int i = item + kStep * r;
           const int at = kGlu ? unit ^ ((i >> 2) & 1) : unit ^ ((i >> 1) & 3);
-          const uint4 u = *reinterpret_cast<const uint4*>(stage + (i * kUnits + at) * 16);
+          const uint4 u = *reinterpret_cast<const uint4*>(stage + (i * kPieces + at) * 16);
           if (c0 + i >= count) continue;
           if (whole) {
             *reinterpret_cast<uint4*>(y) = u;
