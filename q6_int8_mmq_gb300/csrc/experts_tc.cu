@@ -18,8 +18,8 @@
 // (all times a power of two of the row) makes the weight: what is rounded to
 // 11 bits is dmin * m and the weight (q6_K: sc * (q - 32) beyond 2048, and the
 // weight), an eighth of the rounding of a bf16 Y. For a binary16 Y that would
-// show, so there the weight is formed in f32 and rounded once (2.6 instead of
-// 1.8 instructions a weight; q6_K 3.8 instead of 2.4).
+// show, so there the weight is rounded once (q4_K in f32, 2.6 instead of 1.7
+// instructions a weight; q6_K with sc * d in two terms, 3.4 instead of 2.6).
 //
 // x comes as binary16 in item order: bf16 rows scaled by a power of two (exact
 // down to 2^-32 of the row's largest value), gathered ones copied, by a kernel
@@ -221,7 +221,8 @@ __device__ __forceinline__ void store_tiles_t(uint32_t addr, uint32_t a, uint32_
 }
 
 // ------------------------------------------------------------ dequantising ---
-constexpr uint32_t kH2_512 = 0x60006000u, kH2_256 = 0x5C005C00u, kH2_m2p19 = 0x80208020u;
+constexpr uint32_t kH2_512 = 0x60006000u, kH2_256 = 0x5C005C00u, kH2_m2p19 = 0x80208020u,
+                   kH2_1_16 = 0x2C002C00u, kH2_1056 = 0x64206420u;
 
 // A byte of a word as a binary16 pair, plus 1024.
 __device__ __forceinline__ uint32_t byte_h2(uint32_t w, int i) {
@@ -277,18 +278,20 @@ struct Half<Q6_FMT_Q4K> {
   // Chunk cc of the half (32 of K) as 16 words.
   __device__ __forceinline__ void expand(int cc, uint32_t (&out)[16]) const {
     const uint32_t s = hmul2u(hsub2u(byte_h2(sc, cc), kH2_1024), kH2_512);   // sc * 2^9
+    const uint32_t s16 = hmul2u(s, kH2_1_16);  // for codes four bits up
     const uint32_t m = hmul2u(hsub2u(byte_h2(mn, cc), kH2_1024), dm);        // -dmin * m
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const uint32_t w = word4(q[t], cc);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        out[4 * t + i] = hfma2u(hmul2u((w >> (4 * i)) & 0x000F000Fu, s), d, m);
+      const uint32_t w = word4(q[t], cc), w8 = w >> 8;
+      out[4 * t] = hfma2u(hmul2u(w & 0x000F000Fu, s), d, m);
+      out[4 * t + 1] = hfma2u(hmul2u(w & 0x00F000F0u, s16), d, m);
+      out[4 * t + 2] = hfma2u(hmul2u(w8 & 0x000F000Fu, s), d, m);
+      out[4 * t + 3] = hfma2u(hmul2u(w8 & 0x00F000F0u, s16), d, m);
     }
   }
-  // The offsets of the codes go with the min (rounded to at most 2^-12 of the
+  // In f32, rounded once. The offsets of the codes go with the min (rounded to at most 2^-12 of the
   // scale).
-  __device__ __forceinline__ void expand_f32(int cc, uint32_t (&out)[16]) const {
+  __device__ __forceinline__ void expand_once(int cc, uint32_t (&out)[16]) const {
     const float s = df * byte_f32(sc, cc), m = dmf * byte_f32(mn, cc);
     const float c11 = fmaf(-4096.0f, s, m), c15 = fmaf(-256.0f, s, m), c19 = fmaf(-16.0f, s, m),
                 c12 = fmaf(-2048.0f, s, m);
@@ -340,20 +343,22 @@ struct Half<Q6_FMT_Q6K> {
       }
     }
   }
-  // Codes at bits 12 and 16: 2048 + q and 128 + q, less the offset and 32.
-  __device__ __forceinline__ void expand_f32(int cc, uint32_t (&out)[16]) const {
+  // The scale sc * d as two binary16 terms: their sum and so the weight is
+  // rounded once.
+  __device__ __forceinline__ void expand_once(int cc, uint32_t (&out)[16]) const {
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
       const float s = df * (byte_f32(sc[sub], cc) - 128.0f);
-      const uint64_t ss = f2(s, s), k = f2(-2080.0f * s, -160.0f * s);
+      const uint32_t hi = splat_h2(s), lo = splat_h2(s - unpack2<__half>(hi).x);
 #pragma unroll
       for (int t = 2 * sub; t < 2 * sub + 2; ++t) {
         uint32_t v[4];
         q6_pairs(word4(q[t], cc), cc < 2 ? high[t].x : high[t].y, cc % 2, v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          out[4 * t + i] = fma_round(f2(code_f32(v[i] << 12, 0x3F000u, 0x45000000u),
-                                        code_f32(v[i], 0x3F0000u, 0x43000000u)), ss, k);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t c = hsub2u(v[i] | kH2_1024, kH2_1056);  // q - 32
+          out[4 * t + i] = hfma2u(c, hi, hmul2u(c, lo));
+        }
       }
     }
   }
@@ -628,7 +633,7 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
         for (int cc = 0; cc < 4; ++cc) {
           uint32_t v[16];
           if constexpr (__is_same(T, __half))
-            half.expand_f32(cc, v);
+            half.expand_once(cc, v);
           else
             half.expand(cc, v);
           tmem_st16(dst + 16 * cc, v);
