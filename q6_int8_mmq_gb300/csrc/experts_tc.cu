@@ -20,6 +20,9 @@
 // weight), an eighth of the rounding of a bf16 Y. For a binary16 Y that would
 // show, so there the weight is rounded once (q4_K in f32, 2.6 instead of 1.7
 // instructions a weight; q6_K with sc * d in two terms, 3.4 instead of 2.6).
+// In a binary16 silu(gate) * up the roundings of both products would still
+// add up to 1.7 times that of Y; there a weight is a pair of binary16 values
+// in two A slots, and every x tile meets both.
 //
 // x comes as binary16 in item order: bf16 rows scaled by a power of two (exact
 // down to 2^-32 of the row's largest value), gathered ones copied, by a kernel
@@ -39,8 +42,8 @@
 //          every other tile of up to 128 items)
 // TMEM: columns 0-255 two accumulators of 128 items (or one of 256), 256-511
 // four A slots of 128 of K.
-// The walk is in units: 128 of K for tiles of more than 128 items, 256 for
-// others. A unit has one x stage and one or two A slots; one barrier says that
+// The walk is in units: 128 of K for tiles of more than 128 items (or weights
+// in pairs), 256 for others. A unit has one x stage and one or two A slots; one barrier says that
 // all of it is there (both CTAs' copies and dequantised halves), another that
 // its MMAs are through. (A wait costs the MMA warp about 120 cycles and a
 // commit 150 or more, a unit's MMAs at 128 items 1024: with separate barriers
@@ -244,12 +247,14 @@ __device__ __forceinline__ uint64_t f2(float a, float b) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
   return r;
 }
-// a * b + c on two floats, then rounded to a binary16 pair.
-__device__ __forceinline__ uint32_t fma_round(uint64_t a, uint64_t b, uint64_t c) {
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t round_f2(uint64_t v) {
   float x, y;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
   return pack2<__half>(x, y);
 }
 __device__ __forceinline__ float byte_f32(uint32_t w, int i) {
@@ -289,25 +294,42 @@ struct Half<Q6_FMT_Q4K> {
       out[4 * t + 3] = hfma2u(hmul2u(w8 & 0x00F000F0u, s16), d, m);
     }
   }
-  // In f32, rounded once. The offsets of the codes go with the min (rounded to at most 2^-12 of the
-  // scale).
+  // In f32, rounded once. The offsets of the codes go with the min (rounded to
+  // at most 2^-12 of the scale).
   __device__ __forceinline__ void expand_once(int cc, uint32_t (&out)[16]) const {
+    expand_f32<false>(cc, out, out);
+  }
+  // In f32, as two binary16 values (the min beside a code without an offset).
+  __device__ __forceinline__ void expand_pair(int cc, uint32_t (&out)[16],
+                                              uint32_t (&rest)[16]) const {
+    expand_f32<true>(cc, out, rest);
+  }
+  template <bool kTwo>
+  __device__ __forceinline__ void expand_f32(int cc, uint32_t (&out)[16],
+                                             uint32_t (&rest)[16]) const {
     const float s = df * byte_f32(sc, cc), m = dmf * byte_f32(mn, cc);
     const float c11 = fmaf(-4096.0f, s, m), c15 = fmaf(-256.0f, s, m), c19 = fmaf(-16.0f, s, m),
                 c12 = fmaf(-2048.0f, s, m);
     const uint64_t ss = f2(s, s);
+    auto weight = [&](float lo, float hi, float offset, float c, int i) {
+      if (kTwo) {  // the code alone is exact, and so are few bits times s: one rounding, at 2^-24
+        const uint64_t v = fma_f2(f2(lo - offset, hi - offset), ss, f2(m, m));
+        float a, b;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+        out[i] = pack2<__half>(a, b);
+        const float2 h = unpack2<__half>(out[i]);
+        rest[i] = pack2<__half>(a - h.x, b - h.y);
+      } else {
+        out[i] = round_f2(fma_f2(f2(lo, hi), ss, f2(c, c)));
+      }
+    };
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const uint32_t w = word4(q[t], cc), a = w << 11, b = w >> 5, e = w >> 16;
-      uint32_t* o = out + 4 * t;
-      o[0] = fma_round(f2(code_f32(a, 0x7800u, 0x45800000u), code_f32(b, 0x7800u, 0x45800000u)), ss,
-                       f2(c11, c11));
-      o[1] = fma_round(f2(code_f32(a, 0x78000u, 0x43800000u), code_f32(b, 0x78000u, 0x43800000u)),
-                       ss, f2(c15, c15));
-      o[2] = fma_round(f2(code_f32(a, 0x780000u, 0x41800000u), code_f32(b, 0x780000u, 0x41800000u)),
-                       ss, f2(c19, c19));
-      o[3] = fma_round(f2(code_f32(w, 0xF000u, 0x45000000u), code_f32(e, 0xF000u, 0x45000000u)), ss,
-                       f2(c12, c12));
+      weight(code_f32(a, 0x7800u, 0x45800000u), code_f32(b, 0x7800u, 0x45800000u), 4096.0f, c11, 4 * t);
+      weight(code_f32(a, 0x78000u, 0x43800000u), code_f32(b, 0x78000u, 0x43800000u), 256.0f, c15, 4 * t + 1);
+      weight(code_f32(a, 0x780000u, 0x41800000u), code_f32(b, 0x780000u, 0x41800000u), 16.0f, c19, 4 * t + 2);
+      weight(code_f32(w, 0xF000u, 0x45000000u), code_f32(e, 0xF000u, 0x45000000u), 2048.0f, c12, 4 * t + 3);
     }
   }
 };
@@ -362,6 +384,28 @@ struct Half<Q6_FMT_Q6K> {
       }
     }
   }
+  // The weight and what it was rounded by.
+  __device__ __forceinline__ void expand_pair(int cc, uint32_t (&out)[16],
+                                              uint32_t (&rest)[16]) const {
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      const float s = df * (byte_f32(sc[sub], cc) - 128.0f);
+      const uint32_t hi = splat_h2(s), lo = splat_h2(s - unpack2<__half>(hi).x);
+#pragma unroll
+      for (int t = 2 * sub; t < 2 * sub + 2; ++t) {
+        uint32_t v[4];
+        q6_pairs(word4(q[t], cc), cc < 2 ? high[t].x : high[t].y, cc % 2, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t c = hsub2u(v[i] | kH2_1024, kH2_1056);  // q - 32
+          const uint32_t w = hfma2u(c, hi, hmul2u(c, lo));
+          out[4 * t + i] = w;
+          // c * hi - w is exact (17 bits less the upper 11)
+          rest[4 * t + i] = hfma2u(c, lo, hfma2u(c, hi, w ^ 0x80008000u));
+        }
+      }
+    }
+  }
 };
 
 // x / (1 + exp(-x)), within 2^-20 (0 below -87, where it is under 2^-118).
@@ -405,14 +449,19 @@ __device__ __forceinline__ int band_of(const Args& a, int pair, int rank) {
 // past n / 2 are loaded and not used: one request a block is worth more than
 // the bytes; requests by several lanes took about 150 cycles each).
 __device__ __forceinline__ int box_of(int n) { return n > 128 ? 3 : n > 64 ? 2 : n > 32 ? 1 : 0; }
+// Whether a weight is two binary16 values.
+template <typename T, bool kGlu>
+constexpr bool kPair = __is_same(T, __half) && kGlu;
 // log2 of a unit's 64-of-K blocks.
-__device__ __forceinline__ int unit_shift(int n) { return n > 128 ? 1 : 2; }
+template <bool kTwo>
+__device__ __forceinline__ int unit_shift(int n) { return kTwo || n > 128 ? 1 : 2; }
 
-// The MMAs of one tile, by the whole MMA warp; kShift = unit_shift(n).
+// The MMAs of one tile, by the whole MMA warp; kShift = unit_shift(n). kTwo:
+// weights in pairs, the second ones in the next A slot.
 struct MmaState {
   int unit, a;  // units and A slots used so far
 };
-template <int kShift>
+template <int kShift, bool kTwo>
 __device__ __forceinline__ bool tile_mmas(MmaState& st, Bars* bars, const uint8_t* xring,
                                           uint32_t tmem, uint32_t d_tmem, int n, int sbs,
                                           volatile int* abort_flag, unsigned int* status) {
@@ -428,18 +477,19 @@ __device__ __forceinline__ bool tile_mmas(MmaState& st, Bars* bars, const uint8_
     tc_fence_after();
     if (elect_one()) {
       const uint32_t b = x0 + slot * (kXStage >> 4);
-      // A slots of a unit of 256 of K are neighbours: super-blocks begin at an
-      // even slot
+      // two A slots of a unit are neighbours, the first an even one
       const uint32_t at = tmem + (uint32_t)(kACol0 + st.a % kASlots * kACols);
 #pragma unroll
-      for (int i = 0; i < 4 << kShift; ++i)
-        umma_f16_pair(d_tmem, at + 8 * i, b + (i / 4) * x_block + 2 * (i % 4), idesc,
-                      (uint32_t)(u > 0 || i > 0));
+      for (int i = 0; i < 4 << kShift; ++i) {
+        const uint32_t bi = b + (i / 4) * x_block + 2 * (i % 4);
+        umma_f16_pair(d_tmem, at + 8 * i, bi, idesc, (uint32_t)(u > 0 || i > 0));
+        if (kTwo) umma_f16_pair(d_tmem, at + kACols + 8 * i, bi, idesc, 1u);
+      }
       commit_pair(&bars->done[slot]);
     }
     __syncwarp();
     ++st.unit;
-    st.a += kShift;
+    st.a += kTwo ? 2 : kShift;
   }
   return true;
 }
@@ -508,6 +558,7 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
   const int total = start[a.E] * ((a.bands + 1) / 2);
   bool ok = true;
 
+  constexpr bool kTwo = kPair<T, kGlu>;
   if (warp == 0) {
     // --------------------------------------------------------------- load x --
     int g = 0;  // units opened
@@ -515,7 +566,7 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
       const Tile w = tile_at(a, start, t);
       const int rows = w.n / 2;  // this CTA's
       const int box = box_of(w.n);
-      const int shift = unit_shift(w.n);
+      const int shift = unit_shift<kTwo>(w.n);
       const int row0 = __shfl_sync(0xffffffffu, (int)w.first + rank * rows, 0);
       const int block = (16 << box) * 128;
       for (int k = 0; k < 4 * a.sbs; k += 1 << shift) {
@@ -585,8 +636,9 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
       if (!ok) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem + (first ? 0u : 128u);
-      ok = both ? tile_mmas<1>(st, bars, xring, tmem, d_tmem, n, a.sbs, abort_flag, status)
-                : tile_mmas<2>(st, bars, xring, tmem, d_tmem, n, a.sbs, abort_flag, status);
+      ok = both || kTwo
+               ? tile_mmas<1, kTwo>(st, bars, xring, tmem, d_tmem, n, a.sbs, abort_flag, status)
+               : tile_mmas<2, false>(st, bars, xring, tmem, d_tmem, n, a.sbs, abort_flag, status);
       if (!ok) break;
       if (elect_one()) {
         if (first) commit_pair(&bars->d_full[0]);
@@ -610,10 +662,12 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
     int last1 = -1, last2 = -1;  // units of this warp's last two halves, in this and the other slot
     for (int t = cluster; t < total && ok; t += clusters) {
       const Tile w = tile_at(a, start, t);
-      const bool split = unit_shift(w.n) == 1;  // a unit for each half
+      const bool split = unit_shift<kTwo>(w.n) == 1;  // a unit for each half
       const float inv = 1.0f / a.scale[((size_t)w.expert * a.bands + band_of(a, w.pair, rank)) * kBand + row];
       for (int sb = 0; sb < a.sbs; ++sb, ++gw) {
-        const int ws = gw % kWStages, as = (2 * gw + h) % kASlots;
+        const int ws = gw % kWStages;
+        // in pairs, each half super-block has the same two slots again
+        const int as = kTwo ? 2 * h : (2 * gw + h) % kASlots, last = kTwo ? last1 : last2;
         const int mine = split ? unit + h : unit;
         unit += split ? 2 : 1;
         if (!(ok = mbar_wait_warp(&bars->w_full[ws], (gw / kWStages) & 1, abort_flag, status,
@@ -623,8 +677,8 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
         half.load(wring + ws * kWTile<kFmt>, row, h, inv);
         // The slot's last unit is at most kUnits back, so its barrier has not
         // gone further.
-        if (last2 >= 0 && !(ok = mbar_wait_warp(&bars->done[last2 % kUnits], (last2 / kUnits) & 1,
-                                                abort_flag, status, kSiteDone)))
+        if (last >= 0 && !(ok = mbar_wait_warp(&bars->done[last % kUnits], (last / kUnits) & 1,
+                                               abort_flag, status, kSiteDone)))
           break;
         last2 = last1, last1 = mine;
         tc_fence_after();
@@ -632,10 +686,15 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) {
           uint32_t v[16];
-          if constexpr (__is_same(T, __half))
+          if constexpr (kTwo) {
+            uint32_t rest[16];
+            half.expand_pair(cc, v, rest);
+            tmem_st16(dst + kACols + 16 * cc, rest);
+          } else if constexpr (__is_same(T, __half)) {
             half.expand_once(cc, v);
-          else
+          } else {
             half.expand(cc, v);
+          }
           tmem_st16(dst + 16 * cc, v);
         }
         __syncwarp();
