@@ -59,6 +59,7 @@ __device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
                : "l"(p));
   return v;
 }
+constexpr uint32_t kH2_1_16 = 0x2C002C00u;      // (1/16, 1/16)
 constexpr uint32_t kH2_32 = 0x50005000u;        // (32, 32)
 constexpr uint32_t kH2_m32768 = 0xF800F800u;    // (-32768, -32768)
 constexpr uint32_t kH2_m36864 = 0xF880F880u;    // (-36864, -36864)
@@ -130,8 +131,11 @@ __device__ __forceinline__ void multiply(const Block<Q6_FMT_Q4K>& b, const uint4
       const uint32_t w = word4(b.q[r][c / 4], c % 4);
       const uint32_t s1 = __byte_perm(sc[r][c / 4], 0x64u, 0x4040u | (c % 4) << 8 | (c % 4));
       const uint32_t s = hfma2u(s1, kH2_32, kH2_m32768);  // 32 * sc
-#pragma unroll
-      for (int m = 0; m < 4; ++m) a[r][m] = hmul2u((w >> (4 * m)) & 0x000F000Fu, s);
+      const uint32_t s16 = hmul2u(s, kH2_1_16), w8 = w >> 8;  // for codes four bits up
+      a[r][0] = hmul2u(w & 0x000F000Fu, s);
+      a[r][1] = hmul2u(w & 0x00F000F0u, s16);
+      a[r][2] = hmul2u(w8 & 0x000F000Fu, s);
+      a[r][3] = hmul2u(w8 & 0x00F000F0u, s16);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
