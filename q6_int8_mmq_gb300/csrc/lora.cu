@@ -3,12 +3,15 @@
 // Tokens come grouped by adapter, so a tile of up to 16 or 32 tokens shares
 // one A and one B.
 //
-// Two kernels. Shrink: T[i] = scale[a] A[a] x (K long, r wide). For few tokens
-// an adapter a CTA takes up to 16 of them and splits K over its warps; for
-// many it takes 64, x and A coming through shared memory in four stages. K is
-// also split over CTAs while there are few tiles; the parts are added in a
-// fixed order. Expand: out = Y + B[a] T (r long, M wide), B in blocks of
-// columns through shared memory, Y loaded a block ahead.
+// Shrink: T[i] = scale[a] A[a] x (K long, r wide). Expand: out = Y + B[a] T (r
+// long, M wide), B in blocks of columns through shared memory, Y loaded a block
+// ahead. For few tokens an adapter one kernel does both: a CTA has up to 16
+// tokens and a part of the columns, splits K over its 16 warps, and computes T
+// again for each column part (A comes from L2 then; two kernels with K split
+// over CTAs took 22 us for 47 tokens of 24 adapters of rank 32, 4096 x 11008).
+// For many tokens an adapter there are two: shrink takes 64 tokens a CTA, x and
+// A coming through shared memory in four stages, K split over CTAs and the parts
+// added in a fixed order by expand, which takes 32.
 //
 // Both on warp-level MMAs with f32 accumulation, the 16-bit factors as they
 // are. An f32 factor (x, T) beside bf16 is split into three bf16 values, 8
@@ -65,42 +68,6 @@ __device__ __forceinline__ void bf16_split3(float x, float y, uint32_t (&p)[3]) 
   }
 }
 
-// kCount consecutive values as f32.
-template <int kCount>
-__device__ __forceinline__ void load_f32(const float* p, float (&f)[kCount]) {
-#pragma unroll
-  for (int i = 0; i < kCount / 4; ++i) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
-    f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
-  }
-}
-template <typename T, int kCount>
-__device__ __forceinline__ void load_16(const T* p, float (&f)[kCount]) {
-  uint32_t w[kCount / 2];
-  if constexpr (kCount == 8) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else if constexpr (kCount == 4) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    w[0] = v.x, w[1] = v.y;
-  } else {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-  }
-#pragma unroll
-  for (int i = 0; i < kCount / 2; ++i) {
-    const float2 v = unpack2<T>(w[i]);
-    f[2 * i] = v.x, f[2 * i + 1] = v.y;
-  }
-}
-template <int kCount>
-__device__ __forceinline__ void load_f32(const __nv_bfloat16* p, float (&f)[kCount]) {
-  load_16(p, f);
-}
-template <int kCount>
-__device__ __forceinline__ void load_f32(const __half* p, float (&f)[kCount]) {
-  load_16(p, f);
-}
-
 // The tile-th tile of kRows items, counted group by group (G = the section of
 // items without an adapter): its group (-1 past the end), first item and
 // number of items. Called by whole warps.
@@ -135,120 +102,6 @@ __device__ __forceinline__ Tile find_tile(const int32_t* offsets, int G, int row
   return Tile{-1, 0, 0};
 }
 
-// T: part [split][item][r]. Grid (tiles, K splits, rank blocks).
-template <typename TX, typename TW>
-__global__ void __launch_bounds__(kThreads)
-shrink_kernel(const LoraCall c) {
-  constexpr int RT = 1, kRows = 16 * RT;
-  constexpr bool kSplit = sizeof(TX) == 4;
-  __shared__ float red[kWarps / 2][kRows][kRankBlock + 4];
-  griddep_wait();
-  griddep_launch_dependents();
-  const Tile tile = find_tile(c.offsets, c.L, kRows, blockIdx.x);
-  if (tile.group < 0 || tile.group == c.L) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int j0 = blockIdx.z * kRankBlock, nj = min(kRankBlock, c.r - j0) / 8;
-  const TX* x[RT][2];
-  bool has[RT][2];
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int n = 16 * i + 8 * h + g;
-      has[i][h] = n < tile.count;
-      const long long row = c.rows[tile.first + (has[i][h] ? n : 0)];
-      x[i][h] = static_cast<const TX*>(c.X) + row * c.ldx;
-    }
-  const TW* A = static_cast<const TW*>(c.A) +
-                ((size_t)tile.group * c.r + j0 + g) * (size_t)c.K;
-  float acc[RT][kRankBlock / 8][4] = {};
-  // K in steps of 32, dealt out to (split, warp) in turn
-  for (int k0 = ((int)blockIdx.y * kWarps + warp) * 32; k0 < c.K;
-       k0 += (int)gridDim.y * kWarps * 32) {
-    const int k = k0 + 8 * t;
-    float f[RT][2][8];
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (has[i][h]) {
-          load_f32<8>(x[i][h] + k, f[i][h]);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) f[i][h][q] = 0.0f;
-        }
-      }
-#pragma unroll
-    for (int j = 0; j < kRankBlock / 8; ++j) {
-      if (j >= nj) break;
-      float w[8];
-      load_16<TW, 8>(A + (size_t)j * 8 * c.K + k, w);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        float p[4] = {};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t b0 = __float_as_uint(w[2 * q]), b1 = __float_as_uint(w[2 * q + 1]);
-          const float v[4] = {f[i][0][2 * q], f[i][1][2 * q], f[i][0][2 * q + 1],
-                              f[i][1][2 * q + 1]};
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float a, b;
-            tf32_split(v[e], a, b);
-            hi[e] = __float_as_uint(kSplit ? a : v[e]);
-            lo[e] = __float_as_uint(b);
-          }
-          mma_tf32(p, hi, b0, b1);
-          if constexpr (kSplit) mma_tf32(p, lo, b0, b1);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] += p[e];
-      }
-    }
-  }
-  // the warps' parts, halved three times: warp w takes warp w + half's
-  for (int half = kWarps / 2; half; half /= 2) {
-    if (warp >= half && warp < 2 * half) {
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int j = 0; j < kRankBlock / 8; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (j < nj) red[warp - half][16 * i + g + 8 * (e / 2)][8 * j + 2 * t + e % 2] = acc[i][j][e];
-    }
-    __syncthreads();
-    if (warp < half) {
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int j = 0; j < kRankBlock / 8; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (j < nj) acc[i][j][e] += red[warp][16 * i + g + 8 * (e / 2)][8 * j + 2 * t + e % 2];
-    }
-    __syncthreads();
-  }
-  if (warp == 0) {
-    const float scale = c.scale[tile.group];
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < kRankBlock / 8; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int n = 16 * i + 8 * h + g;
-          if (j < nj && n < tile.count) {
-            float* p = c.part + ((size_t)blockIdx.y * c.items + tile.first + n) * c.r + j0 + 8 * j +
-                       2 * t;
-            *reinterpret_cast<float2*>(p) =
-                make_float2(scale * acc[i][j][2 * h], scale * acc[i][j][2 * h + 1]);
-          }
-        }
-  }
-}
-
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool copy) {
   // copy == false fills with zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
@@ -279,6 +132,81 @@ __device__ __forceinline__ void shared_f32(const void* p, float (&f)[kCount]) {
     f[2 * i] = v.x, f[2 * i + 1] = v.y;
   }
 }
+
+// 32 of K of two rows of x (g and g + 8 of a 16-row tile), 8 consecutive values
+// a lane, ready for the products with as many of A.
+template <typename TX, typename TW>
+struct XPart {
+  static constexpr bool kRaw = __is_same(TX, TW);  // the 16-bit words as they are
+  static constexpr bool kThree = sizeof(TX) == 4 && !__is_same(TW, __half);
+  static constexpr int kWords = 2 * (int)sizeof(TX);
+  uint32_t w[2][kWords];  // the rows' values
+  uint32_t three[2][3][4];  // [MMA][part][register]
+
+  __device__ __forceinline__ void put(int row, int i, const uint4& v) {
+    w[row][4 * i] = v.x, w[row][4 * i + 1] = v.y, w[row][4 * i + 2] = v.z, w[row][4 * i + 3] = v.w;
+  }
+  // Value k (0..7) of a row.
+  __device__ __forceinline__ float value(int row, int k) const {
+    if constexpr (sizeof(TX) == 4) {
+      return __uint_as_float(w[row][k]);
+    } else {
+      const float2 f = unpack2<TX>(w[row][k / 2]);
+      return k % 2 ? f.y : f.x;
+    }
+  }
+  __device__ __forceinline__ void prepare() {
+    if constexpr (kThree) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // row e % 2, the pair 2 i + e / 2
+          uint32_t p[3];
+          const int k = 2 * (2 * i + e / 2);
+          bf16_split3(value(e % 2, k), value(e % 2, k + 1), p);
+#pragma unroll
+          for (int s = 0; s < 3; ++s) three[i][s][e] = p[s];
+        }
+    }
+  }
+  // acc += this times 8 rows of A: a's words are the same 8 of K of row g.
+  __device__ __forceinline__ void multiply(const uint4& a, float (&acc)[4]) const {
+    float p[4] = {};
+    if constexpr (kRaw || kThree) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t b0 = word4(a, 2 * i), b1 = word4(a, 2 * i + 1);
+        if constexpr (kRaw) {
+          const uint32_t x[4] = {w[0][2 * i], w[1][2 * i], w[0][2 * i + 1], w[1][2 * i + 1]};
+          mma_16<TW>(p, x, b0, b1);
+        } else {
+#pragma unroll
+          for (int s = 2; s >= 0; --s) mma_16<TW>(p, three[i][s], b0, b1);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 b = unpack2<TW>(word4(a, q));
+        const float v[4] = {value(0, 2 * q), value(1, 2 * q), value(0, 2 * q + 1),
+                            value(1, 2 * q + 1)};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x, y;
+          tf32_split(v[e], x, y);
+          hi[e] = __float_as_uint(sizeof(TX) == 4 ? x : v[e]);
+          lo[e] = __float_as_uint(y);
+        }
+        if constexpr (sizeof(TX) == 4)
+          mma_tf32(p, lo, __float_as_uint(b.x), __float_as_uint(b.y));
+        mma_tf32(p, hi, __float_as_uint(b.x), __float_as_uint(b.y));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += p[e];
+  }
+};
 
 // Shrink for many tokens an adapter. Grid (tiles of 64 items, K splits, rank
 // blocks); warp w: items 16 (w % 4).., ranks 32 (w / 4)... Stages of 64 of K:
@@ -355,12 +283,8 @@ shrink_big_kernel(const LoraCall c) {
     load(s + kBigStages - 1);
     const uint8_t* x = smem + (s - s0) % kBigStages * kStage;
 #pragma unroll
-    for (int step = 0; step < 2; ++step) {  // 32 of K: 8 consecutive ones a lane
-      // MMA i of 16 of K takes values 4 i.. of the lane's 8: a[i][part] its A
-      // operand, the rows' values as they are or their parts
-      constexpr bool kRaw = __is_same(TX, TW), kThree = kSplit && !__is_same(TW, __half);
-      uint4 xw[2];    // kRaw
-      float f[2][8];  // otherwise
+    for (int step = 0; step < 2; ++step) {  // 32 of K
+      XPart<TX, TW> xp;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int row = row0 + 8 * h + g;
@@ -368,71 +292,20 @@ shrink_big_kernel(const LoraCall c) {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const int u = (8 * step + 2 * t + q) ^ (row & 1);
-            const float4 v = *reinterpret_cast<const float4*>(x + (row * kXUnits + u) * 16);
-            f[h][4 * q] = v.x, f[h][4 * q + 1] = v.y, f[h][4 * q + 2] = v.z, f[h][4 * q + 3] = v.w;
+            xp.put(h, q, *reinterpret_cast<const uint4*>(x + (row * kXUnits + u) * 16));
           }
         } else {
-          const uint8_t* p = x + (row * kXUnits + ((4 * step + t) ^ ((row & 1) * 4))) * 16;
-          if constexpr (kRaw)
-            xw[h] = *reinterpret_cast<const uint4*>(p);
-          else
-            shared_f32<TX, 8>(p, f[h]);
+          const int u = (4 * step + t) ^ ((row & 1) * 4);
+          xp.put(h, 0, *reinterpret_cast<const uint4*>(x + (row * kXUnits + u) * 16));
         }
       }
-      uint32_t three[2][3][4];  // [MMA][part][register]
-      if constexpr (kThree) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {  // row e % 2, the pair 2 i + e / 2
-            uint32_t p[3];
-            const int k = 2 * (2 * i + e / 2);
-            bf16_split3(f[e % 2][k], f[e % 2][k + 1], p);
-#pragma unroll
-            for (int s = 0; s < 3; ++s) three[i][s][e] = p[s];
-          }
-      }
+      xp.prepare();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j >= nj) break;
         const int row = rank0 + 8 * j + g;
-        const uint8_t* wp = x + kXBytes + (row * 8 + ((4 * step + t) ^ ((row & 1) * 4))) * 16;
-        float p[4] = {};
-        if constexpr (kRaw || kThree) {
-          const uint4 w = *reinterpret_cast<const uint4*>(wp);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t b0 = word4(w, 2 * i), b1 = word4(w, 2 * i + 1);
-            if constexpr (kRaw) {
-              const uint32_t a[4] = {word4(xw[0], 2 * i), word4(xw[1], 2 * i),
-                                     word4(xw[0], 2 * i + 1), word4(xw[1], 2 * i + 1)};
-              mma_16<TW>(p, a, b0, b1);
-            } else {
-#pragma unroll
-              for (int s = 2; s >= 0; --s) mma_16<TW>(p, three[i][s], b0, b1);
-            }
-          }
-        } else {
-          float w[8];
-          shared_f32<TW, 8>(wp, w);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t b0 = __float_as_uint(w[2 * q]), b1 = __float_as_uint(w[2 * q + 1]);
-            const float v[4] = {f[0][2 * q], f[1][2 * q], f[0][2 * q + 1], f[1][2 * q + 1]};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float a, b;
-              tf32_split(v[e], a, b);
-              hi[e] = __float_as_uint(kSplit ? a : v[e]);
-              lo[e] = __float_as_uint(b);
-            }
-            if constexpr (kSplit) mma_tf32(p, lo, b0, b1);
-            mma_tf32(p, hi, b0, b1);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] += p[e];
+        const int u = (4 * step + t) ^ ((row & 1) * 4);
+        xp.multiply(*reinterpret_cast<const uint4*>(x + kXBytes + (row * 8 + u) * 16), acc[j]);
       }
     }
   }
@@ -457,12 +330,90 @@ constexpr int kColsWarp = 64;  // columns a warp takes at a time
 // loads (32 bytes each) fall on different banks.
 __host__ __device__ constexpr int b_pitch(int r) { return 2 * r + (2 * r % 64 == 0 ? 32 : 0); }
 
+constexpr int kFusedThreads = 512, kFusedWarps = kFusedThreads / 32;
+constexpr int kFusedSum = (kFusedWarps / 2) * 16 * (kRankBlock + 4) * 4;  // bytes of its partial sums
+
+// T of a tile of up to 16 items into ts [16][ld], by all warps of a CTA, K dealt
+// out to them 32 at a time; red: kFusedSum bytes.
+template <typename TX, typename TW>
+__device__ __forceinline__ void shrink_tile(const LoraCall& c, const Tile& tile, float* ts, int ld,
+                                            float* red) {
+  constexpr int kLoads = (int)sizeof(TX) / 2, kLd = kRankBlock + 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const TX* x[2];
+  bool has[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    has[h] = 8 * h + g < tile.count;
+    x[h] = static_cast<const TX*>(c.X) + c.rows[tile.first + (has[h] ? 8 * h + g : 0)] * c.ldx + 8 * t;
+  }
+  const float scale = c.scale[tile.group];
+  for (int j0 = 0; j0 < c.r; j0 += kRankBlock) {
+    const int nj = min(kRankBlock, c.r - j0) / 8;
+    const TW* A = static_cast<const TW*>(c.A) +
+                  ((size_t)tile.group * c.r + j0 + g) * (size_t)c.K + 8 * t;
+    float acc[kRankBlock / 8][4] = {};
+    for (int k = warp * 32; k < c.K; k += kFusedWarps * 32) {
+      XPart<TX, TW> xp;
+      uint4 w[kRankBlock / 8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q)
+          xp.put(h, q, has[h] ? __ldg(reinterpret_cast<const uint4*>(x[h] + k) + q)
+                              : make_uint4(0, 0, 0, 0));
+#pragma unroll
+      for (int j = 0; j < kRankBlock / 8; ++j)
+        if (j < nj) w[j] = __ldg(reinterpret_cast<const uint4*>(A + (size_t)j * 8 * c.K + k));
+      xp.prepare();
+#pragma unroll
+      for (int j = 0; j < kRankBlock / 8; ++j)
+        if (j < nj) xp.multiply(w[j], acc[j]);
+    }
+    // the warps' parts, halved until one has them all
+    for (int half = kFusedWarps / 2; half; half /= 2) {
+#pragma unroll
+      for (int j = 0; j < kRankBlock / 8; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float2* p = reinterpret_cast<float2*>(red + ((warp % half) * 16 + 8 * h + g) * kLd + 8 * j + 2 * t);
+          if (j < nj && warp >= half && warp < 2 * half)
+            *p = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+        }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kRankBlock / 8; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2* p =
+              reinterpret_cast<const float2*>(red + ((warp % half) * 16 + 8 * h + g) * kLd + 8 * j + 2 * t);
+          if (j < nj && warp < half) acc[j][2 * h] += p->x, acc[j][2 * h + 1] += p->y;
+        }
+      __syncthreads();
+    }
+    if (warp == 0) {
+#pragma unroll
+      for (int j = 0; j < kRankBlock / 8; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (j < nj)
+            *reinterpret_cast<float2*>(ts + (8 * h + g) * ld + j0 + 8 * j + 2 * t) =
+                make_float2(scale * acc[j][2 * h], scale * acc[j][2 * h + 1]);
+    }
+  }
+}
+
 // out = Y + B T. Grid (tiles of 16 * RW items, column parts); RW row warps
 // times col_warps column warps. JV: ranks a lane loads at a time (r is a
-// multiple of 4 * JV). kVec: 16-byte rows of Y and out.
-template <typename TW, int RW, int JV, bool kVec>
-__global__ void __launch_bounds__(kThreads, 2)
+// multiple of 4 * JV). kVec: 16-byte rows of Y and out. With TX (a type of X,
+// RW = 1) it makes T itself and has kFusedThreads threads; with void T comes
+// from shrink's parts.
+template <typename TX, typename TW, int RW, int JV, bool kVec>
+__global__ void __launch_bounds__(__is_same(TX, void) ? kThreads : kFusedThreads,
+                                  __is_same(TX, void) ? 2 : 1)
 expand_kernel(const LoraCall c, int col_warps, int part_cols) {
+  constexpr bool kFused = !__is_same(TX, void);
+  static_assert(!kFused || RW == 1, "the fused kernel has tiles of 16 items");
   constexpr int kRows = 16 * RW;
   extern __shared__ uint4 expand_smem[];
   float* ts = reinterpret_cast<float*>(expand_smem);  // T of the tile: [kRows][r + 4]
@@ -471,6 +422,7 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int m_begin = (int)blockIdx.y * part_cols, m_end = min(c.M, m_begin + part_cols);
   griddep_wait();
+  if (kFused) griddep_launch_dependents();
   const Tile tile = find_tile(c.offsets, c.L, kRows, blockIdx.x);
   if (tile.group < 0) return;
   const bool none = tile.group == c.L;  // tokens without an adapter: Y alone
@@ -485,24 +437,29 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
     cp_async_commit();
   };
   load(m_begin, 0);
-  // T, four ranks at a time, the parts' loads in flight together
-  for (int i = threadIdx.x; i < kRows * (c.r / 4); i += blockDim.x) {
-    const int n = i / (c.r / 4), j = i % (c.r / 4) * 4;
-    float4 v = make_float4(0, 0, 0, 0);
-    if (n < tile.count && !none) {
-      const float* p = c.part + (size_t)(tile.first + n) * c.r + j;
-      const size_t step = (size_t)c.items * c.r;
-      for (int s0 = 0; s0 < c.splits; s0 += 8) {
-        float4 w[8];
+  if constexpr (kFused) {
+    if (!none)
+      shrink_tile<TX, TW>(c, tile, ts, ld, reinterpret_cast<float*>(bs + 2 * width * pitch));
+  } else {
+    // T, four ranks at a time, the parts' loads in flight together
+    for (int i = threadIdx.x; i < kRows * (c.r / 4); i += blockDim.x) {
+      const int n = i / (c.r / 4), j = i % (c.r / 4) * 4;
+      float4 v = make_float4(0, 0, 0, 0);
+      if (n < tile.count && !none) {
+        const float* p = c.part + (size_t)(tile.first + n) * c.r + j;
+        const size_t step = (size_t)c.items * c.r;
+        for (int s0 = 0; s0 < c.splits; s0 += 8) {
+          float4 w[8];
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-          w[s] = s0 + s < c.splits ? *reinterpret_cast<const float4*>(p + (s0 + s) * step)
-                                   : make_float4(0, 0, 0, 0);
+          for (int s = 0; s < 8; ++s)
+            w[s] = s0 + s < c.splits ? *reinterpret_cast<const float4*>(p + (s0 + s) * step)
+                                     : make_float4(0, 0, 0, 0);
 #pragma unroll
-        for (int s = 0; s < 8; ++s) v.x += w[s].x, v.y += w[s].y, v.z += w[s].z, v.w += w[s].w;
+          for (int s = 0; s < 8; ++s) v.x += w[s].x, v.y += w[s].y, v.z += w[s].z, v.w += w[s].w;
+        }
       }
+      *reinterpret_cast<float4*>(ts + n * ld + j) = v;
     }
-    *reinterpret_cast<float4*>(ts + n * ld + j) = v;
   }
   const int rw = warp % RW, cw = warp / RW;
   const float* ys[2];
@@ -511,7 +468,7 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int n = 16 * rw + 8 * h + g;
-    has[h] = n < tile.count;
+    has[h] = n < tile.count && cw < col_warps;
     const long long row = c.rows[tile.first + (has[h] ? n : 0)];
     ys[h] = c.Y + row * c.ldy;
     os[h] = c.out + row * c.ldo;
@@ -540,7 +497,7 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
     __syncthreads();  // the block (and, before the first, T) is there
     float acc[8][4] = {};
     const uint8_t* b = bs + buf * width * pitch + cw * kColsWarp * pitch;
-    for (int j0 = 0; j0 < c.r && !none; j0 += 4 * JV) {
+    for (int j0 = 0; j0 < c.r && !none && cw < col_warps; j0 += 4 * JV) {
       constexpr bool kThree = JV == 4 && !__is_same(TW, __half);
       uint32_t hi[JV / 2][4], lo[JV / 2][4], three[3][4];
       float v[JV / 2][4];  // T of rows g, g + 8, two ranks each
@@ -626,13 +583,10 @@ bool many(long long items, int L) { return items > 16ll * L; }
 
 template <typename TX, typename TW>
 cudaError_t shrink(const LoraCall& c, cudaStream_t s) {
-  const bool big = many(c.items, c.L);
-  const dim3 grid((unsigned)most_tiles(c.items, c.L, big ? kBigRows : 16), (unsigned)c.splits,
+  const dim3 grid((unsigned)most_tiles(c.items, c.L, kBigRows), (unsigned)c.splits,
                   (unsigned)((c.r + kRankBlock - 1) / kRankBlock));
-  if (big)
-    return launch_pdl(shrink_big_kernel<TX, TW>, grid, dim3(kThreads),
-                      (size_t)kBigStages * kBigStageBytes<TX, TW>, s, c);
-  return launch_pdl(shrink_kernel<TX, TW>, grid, dim3(kThreads), 0, s, c);
+  return launch_pdl(shrink_big_kernel<TX, TW>, grid, dim3(kThreads),
+                    (size_t)kBigStages * kBigStageBytes<TX, TW>, s, c);
 }
 
 size_t expand_smem_bytes(int rows, int r, int col_warps) {
@@ -640,75 +594,94 @@ size_t expand_smem_bytes(int rows, int r, int col_warps) {
 }
 constexpr size_t kExpandSmem = 112 * 1024;  // two CTAs an SM where that is enough
 constexpr int kExpandSmemMax = 227 * 1024;
-static_assert(128 * (Q6_LORA_MAX_RANK + 4) * 4 + 2 * kColsWarp * b_pitch(Q6_LORA_MAX_RANK) <=
-                  kExpandSmemMax, "128 items at the largest rank");
+constexpr int kBigRw = 2;  // row warps of the expand kernel for many tokens
+static_assert(16 * (Q6_LORA_MAX_RANK + 4) * 4 + 2 * kColsWarp * b_pitch(Q6_LORA_MAX_RANK) + kFusedSum <=
+                  kExpandSmemMax, "16 items at the largest rank");
+static_assert(16 * kBigRw * (Q6_LORA_MAX_RANK + 4) * 4 + 2 * kColsWarp * b_pitch(Q6_LORA_MAX_RANK) <=
+                  kExpandSmemMax, "the largest rank");
 
-template <typename TW, int RW, int JV>
+// The expand kernel for many tokens (TX void) or the fused one.
+template <typename TX, typename TW, int JV>
 cudaError_t expand_v(const LoraCall& c, bool vec, cudaStream_t s) {
+  constexpr bool kFused = !__is_same(TX, void);
+  constexpr int RW = kFused ? 1 : kBigRw;
   const long long tiles = most_tiles(c.items, c.L, 16 * RW);
-  int col_warps = kWarps / RW;
-  while (col_warps > 1 && (expand_smem_bytes(16 * RW, c.r, col_warps) > kExpandSmem ||
-                           kColsWarp * col_warps >= 2 * c.M))
+  const size_t extra = kFused ? kFusedSum : 0;
+  // column parts: about four CTAs an SM (two run at a time), or one of the
+  // fused kernel, which makes T again in each; then the widest block that is
+  // not wider than a part and leaves room
+  const int cols = (c.M + kColsWarp - 1) / kColsWarp;  // in warps' columns
+  long long parts = kFused ? 152 / tiles : (4 * 152 + tiles - 1) / tiles;
+  parts = parts < 1 ? 1 : parts > cols ? cols : parts;
+  int col_warps = kFused ? kFusedWarps : kWarps / RW;
+  while (col_warps > 1 &&
+         (expand_smem_bytes(16 * RW, c.r, col_warps) + extra > (kFused ? kExpandSmemMax : kExpandSmem) ||
+          col_warps >= 2 * ((cols + parts - 1) / parts)))
     col_warps /= 2;
-  // column parts: about four CTAs an SM (two run at a time), whole blocks each
   const int width = kColsWarp * col_warps, blocks = (c.M + width - 1) / width;
-  long long parts = (4 * 152 + tiles - 1) / tiles;
   if (parts > blocks) parts = blocks;
   const int part_cols = (int)((blocks + parts - 1) / parts) * width;
   const dim3 grid((unsigned)tiles, (unsigned)((c.M + part_cols - 1) / part_cols));
-  return launch_pdl(vec ? expand_kernel<TW, RW, JV, true> : expand_kernel<TW, RW, JV, false>, grid,
-                    dim3(32 * RW * col_warps), expand_smem_bytes(16 * RW, c.r, col_warps), s, c,
-                    col_warps, part_cols);
+  return launch_pdl(vec ? expand_kernel<TX, TW, RW, JV, true> : expand_kernel<TX, TW, RW, JV, false>,
+                    grid, dim3(kFused ? kFusedThreads : 32 * RW * col_warps),
+                    expand_smem_bytes(16 * RW, c.r, col_warps) + extra, s, c, col_warps, part_cols);
 }
-template <typename TW, int RW>
-cudaError_t expand_r(const LoraCall& c, bool vec, cudaStream_t s) {
-  return c.r % 16 == 0 ? expand_v<TW, RW, 4>(c, vec, s) : expand_v<TW, RW, 2>(c, vec, s);
+template <typename TX, typename TW>
+cudaError_t expand(const LoraCall& c, cudaStream_t s) {
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(c.Y) | reinterpret_cast<uintptr_t>(c.out) |
+                         (uintptr_t)(c.ldy * 4) | (uintptr_t)(c.ldo * 4) | (uintptr_t)(c.M * 4);
+  const bool vec = bits % 16 == 0;
+  return c.r % 16 == 0 ? expand_v<TX, TW, 4>(c, vec, s) : expand_v<TX, TW, 2>(c, vec, s);
 }
 
-template <typename TW, int RW>
+template <typename TX, typename TW>
 cudaError_t prepare_expand() {
+  constexpr int RW = __is_same(TX, void) ? kBigRw : 1;
   cudaError_t e = cudaSuccess;
   auto set = [&](auto* k) {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmemMax);
   };
-  set(expand_kernel<TW, RW, 4, true>), set(expand_kernel<TW, RW, 4, false>);
-  set(expand_kernel<TW, RW, 2, true>), set(expand_kernel<TW, RW, 2, false>);
+  set(expand_kernel<TX, TW, RW, 4, true>), set(expand_kernel<TX, TW, RW, 4, false>);
+  set(expand_kernel<TX, TW, RW, 2, true>), set(expand_kernel<TX, TW, RW, 2, false>);
   return e;
+}
+template <typename TX, typename TW>
+cudaError_t prepare_x() {
+  cudaError_t e = cudaFuncSetAttribute(shrink_big_kernel<TX, TW>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kBigStages * kBigStageBytes<TX, TW>);
+  return e == cudaSuccess ? prepare_expand<TX, TW>() : e;
 }
 template <typename TW>
 cudaError_t prepare_t() {
-  cudaError_t e = cudaSuccess;
-  auto set = [&](auto* k, int bytes) {
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  };
-  set(shrink_big_kernel<float, TW>, kBigStages * kBigStageBytes<float, TW>);
-  set(shrink_big_kernel<__nv_bfloat16, TW>, kBigStages * kBigStageBytes<__nv_bfloat16, TW>);
-  set(shrink_big_kernel<__half, TW>, kBigStages * kBigStageBytes<__half, TW>);
-  if (e == cudaSuccess) e = prepare_expand<TW, 1>();
-  if (e == cudaSuccess) e = prepare_expand<TW, 2>();
+  cudaError_t e = prepare_expand<void, TW>();
+  if (e == cudaSuccess) e = prepare_x<float, TW>();
+  if (e == cudaSuccess) e = prepare_x<__nv_bfloat16, TW>();
+  if (e == cudaSuccess) e = prepare_x<__half, TW>();
   return e;
 }
 
+template <typename TX, typename TW>
+cudaError_t lora_x(const LoraCall& c, cudaStream_t s) {
+  if (!many(c.items, c.L)) return expand<TX, TW>(c, s);
+  const cudaError_t e = shrink<TX, TW>(c, s);
+  return e == cudaSuccess ? expand<void, TW>(c, s) : e;
+}
 template <typename TW>
 cudaError_t lora_t(const LoraCall& c, cudaStream_t s) {
-  const cudaError_t e = c.xtype == Q6_TYPE_F32    ? shrink<float, TW>(c, s)
-                        : c.xtype == Q6_TYPE_BF16 ? shrink<__nv_bfloat16, TW>(c, s)
-                                                  : shrink<__half, TW>(c, s);
-  if (e != cudaSuccess) return e;
-  const uintptr_t bits = reinterpret_cast<uintptr_t>(c.Y) | reinterpret_cast<uintptr_t>(c.out) |
-                         (uintptr_t)(c.ldy * 4) | (uintptr_t)(c.ldo * 4) | (uintptr_t)(c.M * 4);
-  return many(c.items, c.L) ? expand_r<TW, 2>(c, bits % 16 == 0, s)
-                            : expand_r<TW, 1>(c, bits % 16 == 0, s);
+  return c.xtype == Q6_TYPE_F32    ? lora_x<float, TW>(c, s)
+         : c.xtype == Q6_TYPE_BF16 ? lora_x<__nv_bfloat16, TW>(c, s)
+                                   : lora_x<__half, TW>(c, s);
 }
 
 }  // namespace
 
 int lora_splits(long long items, int L, int r, int K) {
+  if (!many(items, L)) return 0;
   // K parts over CTAs, at least 256 of K each, as many as run at a time (two
   // CTAs an SM)
-  const long long tiles = most_tiles(items, L, many(items, L) ? kBigRows : 16) *
-                          ((r + kRankBlock - 1) / kRankBlock);
+  const long long tiles = most_tiles(items, L, kBigRows) * ((r + kRankBlock - 1) / kRankBlock);
   long long splits = 2 * 152 / tiles;
   if (splits > K / 256) splits = K / 256;
   return splits < 1 ? 1 : splits > 16 ? 16 : (int)splits;

@@ -255,7 +255,7 @@ int q6_lora_add(const void* A, const void* B, const float* scale, int type, int 
   q6::LoraCall c;
   c.splits = q6::lora_splits(items, L, r, K);
   const size_t need = (size_t)c.splits * (size_t)items * (size_t)r * 4;
-  if (!workspace || workspace_bytes < need)
+  if (need && (!workspace || workspace_bytes < need))
     return fail(Q6_ESIZE, "the adapters need a workspace of %zu bytes", need);
   if ((rc = q6::require_device(nullptr))) return rc;
   c.A = A, c.B = B, c.scale = scale, c.type = type;

@@ -219,7 +219,7 @@ struct LoraCall {
   int splits;
 };
 // Parts the shrink product splits K into (its workspace is splits * items * r
-// f32 values).
+// f32 values); 0 where one kernel does it all.
 int lora_splits(long long items, int L, int r, int K);
 cudaError_t lora_prepare();
 cudaError_t launch_lora(const LoraCall& c, cudaStream_t s);

@@ -404,15 +404,13 @@ def lora_add(adapters: LoraAdapters, X, groups: Groups, Y, out=None, stream=None
         out = Y
     elif not _plain(out, torch.float32, (N, M), dev):
         _tensor(out, "out", torch.float32, (N, M), dev, rows=True)
-    need = lora_workspace_bytes(N, L, r, K)
-    if stream is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    else:
+    need, ws = lora_workspace_bytes(N, L, r, K), None
+    if need:
         with _on(stream):
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _check(load().q6_lora_add(A.data_ptr(), adapters.B.data_ptr(), adapters.scale.data_ptr(),
                               _types()[A.dtype], L, r, M, K, X.data_ptr(), code, _row_stride(X),
                               groups.offsets.data_ptr(), groups.rows.data_ptr(), N, Y.data_ptr(),
-                              _row_stride(Y), out.data_ptr(), _row_stride(out), ws.data_ptr(),
+                              _row_stride(Y), out.data_ptr(), _row_stride(out), _ptr(ws),
                               need, _stream(stream, dev)))
     return out
