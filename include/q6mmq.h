@@ -590,7 +590,7 @@ int q6_moe_combine(const void *Y, int type, int64_t ldy, const int32_t *pos, con
  *       L, N = items).
  *   Y, out : device f32, ldy, ldo >= M; out may be Y (in place).
  *   workspace : device, 16-byte aligned, at least q6_lora_workspace_bytes()
- *       (NULL when that is 0: up to 16 tokens an adapter on average). */
+ *       (NULL when that is 0: up to 8 tokens an adapter on average). */
 int q6_lora_workspace_bytes(int64_t items, int L, int r, int K, size_t *bytes);
 int q6_lora_add(const void *A, const void *B, const float *scale, int type, int L, int r, int M,
                 int K, const void *X, int xtype, int64_t ldx, const int32_t *offsets,

@@ -4,19 +4,24 @@
 // one A and one B.
 //
 // Shrink: T[i] = scale[a] A[a] x (K long, r wide). Expand: out = Y + B[a] T (r
-// long, M wide), B in blocks of columns through shared memory, Y loaded a block
-// ahead. For few tokens an adapter one kernel does both: a CTA has up to 16
-// tokens and a part of the columns, splits K over its 16 warps, and computes T
-// again for each column part (A comes from L2 then; two kernels with K split
-// over CTAs took 22 us for 47 tokens of 24 adapters of rank 32, 4096 x 11008).
-// For many tokens an adapter there are two: shrink takes 64 tokens a CTA, x and
-// A coming through shared memory in four stages, K split over CTAs and the parts
-// added in a fixed order by expand, which takes 32.
+// long, M wide).
 //
-// Both on warp-level MMAs with f32 accumulation, the 16-bit factors as they
-// are. An f32 factor (x, T) beside bf16 is split into three bf16 values, 8
-// bits each and together exact; beside f16 (whose range is too small for the
-// parts) into a tf32 value and a tf32 remainder, which loses 2^-21 of it.
+// Up to 8 tokens an adapter on average, one kernel does both on FMAs: a cluster
+// of CTAs has up to 4 tokens of one adapter, each CTA a part of the columns and
+// a part of K, whose sums they exchange through distributed shared memory. An
+// MMA's 16 rows would be empty but for those tokens, and the loads are what
+// counts: for 47 tokens of 24 adapters of rank 32 at 4096 x 11008, two MMA
+// kernels with T in memory took 22 us, one MMA kernel that made T in each CTA
+// 23 us, the same on FMAs 20 us.
+//
+// Beyond that there are two kernels on warp-level MMAs: shrink takes 64 tokens a
+// CTA, x and A coming through shared memory in four stages, K split over CTAs
+// and the parts added in a fixed order by expand, which takes 32 tokens, B in
+// blocks of columns through shared memory and Y loaded a block ahead. MMAs with
+// f32 accumulation, the 16-bit factors as they are; an f32 factor (x, T) beside
+// bf16 is split into three bf16 values, 8 bits each and together exact; beside
+// f16 (whose range is too small for the parts) into a tf32 value and a tf32
+// remainder, which loses 2^-21 of it.
 //
 // The order of k inside an MMA is free, so a lane takes consecutive k (or
 // rank) values of its row in 16-byte loads and the MMAs use them two by two.
@@ -218,7 +223,7 @@ constexpr int kBigStageBytes = kBigRows * 64 * (int)sizeof(TX) + kRankBlock * 64
 
 template <typename TX, typename TW>
 __global__ void __launch_bounds__(kThreads, 2)
-shrink_big_kernel(const LoraCall c) {
+shrink_kernel(const LoraCall c) {
   constexpr bool kSplit = sizeof(TX) == 4;
   constexpr int kXUnits = 64 * (int)sizeof(TX) / 16, kXSwap = kSplit ? 1 : 4;
   constexpr int kXBytes = kBigRows * 64 * (int)sizeof(TX), kStage = kBigStageBytes<TX, TW>;
@@ -330,90 +335,219 @@ constexpr int kColsWarp = 64;  // columns a warp takes at a time
 // loads (32 bytes each) fall on different banks.
 __host__ __device__ constexpr int b_pitch(int r) { return 2 * r + (2 * r % 64 == 0 ? 32 : 0); }
 
-constexpr int kFusedThreads = 512, kFusedWarps = kFusedThreads / 32;
-constexpr int kFusedSum = (kFusedWarps / 2) * 16 * (kRankBlock + 4) * 4;  // bytes of its partial sums
+constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32;
+constexpr int kFewItems = 4;  // of a tile
 
-// T of a tile of up to 16 items into ts [16][ld], by all warps of a CTA, K dealt
-// out to them 32 at a time; red: kFusedSum bytes.
-template <typename TX, typename TW>
-__device__ __forceinline__ void shrink_tile(const LoraCall& c, const Tile& tile, float* ts, int ld,
-                                            float* red) {
-  constexpr int kLoads = (int)sizeof(TX) / 2, kLd = kRankBlock + 4;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const TX* x[2];
-  bool has[2];
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// *p of CTA `rank` of the cluster.
+__device__ __forceinline__ float load_cluster(const float* p, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\t"
+      "mapa.shared::cluster.u32 ra, %1, %2;\n\t"
+      "ld.shared::cluster.f32 %0, [ra];\n\t}\n"
+      : "=f"(v)
+      : "r"(smem_u32(p)), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// A tile of up to kTok items' sums over this warp's K for ranks 8 j + g, j < nj,
+// on FMAs (an MMA's 16 rows would be empty but for one to four, and splitting f32
+// values for it costs more than the products): lane (g, t) takes 8 consecutive of
+// 32 values of K, kSteps times those loaded together. This is warp `warp` of the
+// `warps` that share K; sum[tok][8 j + g] is its own.
+template <typename TX, typename TW, int kTok, int kNj>
+__device__ __forceinline__ void shrink_fma(const LoraCall& c, const Tile& tile, const TW* A, int nj,
+                                           int warp, int warps, float* sum) {
+  constexpr int kSteps = 8 / kNj / kTok > 1 ? 8 / kNj / kTok : 1;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const TX* x[kTok];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    has[h] = 8 * h + g < tile.count;
-    x[h] = static_cast<const TX*>(c.X) + c.rows[tile.first + (has[h] ? 8 * h + g : 0)] * c.ldx + 8 * t;
+  for (int n = 0; n < kTok; ++n)
+    x[n] = static_cast<const TX*>(c.X) + c.rows[tile.first + min(n, tile.count - 1)] * c.ldx + 8 * t;
+  float acc[kTok][kNj] = {};
+  for (int k0 = warp * 32 * kSteps; k0 < c.K; k0 += warps * 32 * kSteps) {
+    uint4 xw[kSteps][kTok][sizeof(TX) / 2], w[kSteps][kNj];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const bool in = k0 + 32 * s < c.K;
+#pragma unroll
+      for (int j = 0; j < kNj; ++j)
+        w[s][j] = j < nj && in
+                      ? __ldg(reinterpret_cast<const uint4*>(A + (size_t)j * 8 * c.K + k0 + 32 * s))
+                      : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int n = 0; n < kTok; ++n)
+#pragma unroll
+        for (int q = 0; q < (int)sizeof(TX) / 2; ++q)
+          xw[s][n][q] = in ? __ldg(reinterpret_cast<const uint4*>(x[n] + k0 + 32 * s) + q)
+                           : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      float f[kTok][8];
+#pragma unroll
+      for (int n = 0; n < kTok; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(TX) == 4) {
+            f[n][2 * i] = __uint_as_float(word4(xw[s][n][i / 2], 2 * i % 4));
+            f[n][2 * i + 1] = __uint_as_float(word4(xw[s][n][i / 2], 2 * i % 4 + 1));
+          } else {
+            const float2 v = unpack2<TX>(word4(xw[s][n][0], i));
+            f[n][2 * i] = v.x, f[n][2 * i + 1] = v.y;
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < kNj; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 a = unpack2<TW>(word4(w[s][j], i));
+#pragma unroll
+          for (int n = 0; n < kTok; ++n)
+            acc[n][j] = fmaf(a.y, f[n][2 * i + 1], fmaf(a.x, f[n][2 * i], acc[n][j]));
+        }
+    }
   }
-  const float scale = c.scale[tile.group];
-  for (int j0 = 0; j0 < c.r; j0 += kRankBlock) {
+#pragma unroll
+  for (int n = 0; n < kTok; ++n)
+#pragma unroll
+    for (int j = 0; j < kNj; ++j) {
+      float v = acc[n][j];
+      v += __shfl_xor_sync(0xffffffffu, v, 1);
+      v += __shfl_xor_sync(0xffffffffu, v, 2);
+      if (t == 0 && j < nj) sum[n * kRankBlock + 8 * j + g] = v;
+    }
+}
+template <typename TX, typename TW, int kTok>
+__device__ __forceinline__ void shrink_few(const LoraCall& c, const Tile& tile, const TW* A, int nj,
+                                           int rank, int ranks, float* red) {
+  const int warp = threadIdx.x >> 5, warps = ranks * kFewWarps;
+  float* sum = red + warp * kTok * kRankBlock;
+  if (nj <= 2)
+    shrink_fma<TX, TW, kTok, 2>(c, tile, A, nj, rank * kFewWarps + warp, warps, sum);
+  else if (nj <= 4)
+    shrink_fma<TX, TW, kTok, 4>(c, tile, A, nj, rank * kFewWarps + warp, warps, sum);
+  else
+    shrink_fma<TX, TW, kTok, 8>(c, tile, A, nj, rank * kFewWarps + warp, warps, sum);
+}
+
+// Both products for tiles of up to kFewItems items. Grid (tiles, column parts),
+// clusters of `ranks` column parts.
+template <typename TX, typename TW>
+__global__ void __launch_bounds__(kFewThreads, 1)
+lora_few_kernel(const LoraCall c, int part_cols, int ranks) {
+  __shared__ float red[kFewWarps * kFewItems * kRankBlock];
+  __shared__ float mine[kFewItems * Q6_LORA_MAX_RANK];              // this CTA's sums [item][r]
+  __shared__ __align__(16) float ts[kFewItems * Q6_LORA_MAX_RANK];  // T [item][r]
+  griddep_wait();
+  griddep_launch_dependents();
+  const Tile tile = find_tile(c.offsets, c.L, kFewItems, blockIdx.x);
+  if (tile.group < 0) return;
+  const bool none = tile.group == c.L;  // tokens without an adapter: Y alone
+  if (none && c.out == c.Y) return;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int tok = tile.count == 1 ? 1 : kFewItems, rank = (int)blockIdx.y % ranks;
+  for (int j0 = 0; j0 < c.r && !none; j0 += kRankBlock) {
     const int nj = min(kRankBlock, c.r - j0) / 8;
     const TW* A = static_cast<const TW*>(c.A) +
                   ((size_t)tile.group * c.r + j0 + g) * (size_t)c.K + 8 * t;
-    float acc[kRankBlock / 8][4] = {};
-    for (int k = warp * 32; k < c.K; k += kFusedWarps * 32) {
-      XPart<TX, TW> xp;
-      uint4 w[kRankBlock / 8];
+    if (tok == 1)
+      shrink_few<TX, TW, 1>(c, tile, A, nj, rank, ranks, red);
+    else
+      shrink_few<TX, TW, kFewItems>(c, tile, A, nj, rank, ranks, red);
+    __syncthreads();
+    for (int i = threadIdx.x; i < tok * 8 * nj; i += kFewThreads) {
+      const int n = i / (8 * nj), j = i % (8 * nj);
+      float v = 0.0f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int q = 0; q < kLoads; ++q)
-          xp.put(h, q, has[h] ? __ldg(reinterpret_cast<const uint4*>(x[h] + k) + q)
-                              : make_uint4(0, 0, 0, 0));
-#pragma unroll
-      for (int j = 0; j < kRankBlock / 8; ++j)
-        if (j < nj) w[j] = __ldg(reinterpret_cast<const uint4*>(A + (size_t)j * 8 * c.K + k));
-      xp.prepare();
-#pragma unroll
-      for (int j = 0; j < kRankBlock / 8; ++j)
-        if (j < nj) xp.multiply(w[j], acc[j]);
+      for (int w = 0; w < kFewWarps; ++w) v += red[(w * tok + n) * kRankBlock + j];
+      mine[n * c.r + j0 + j] = v;
     }
-    // the warps' parts, halved until one has them all
-    for (int half = kFusedWarps / 2; half; half /= 2) {
+    __syncthreads();
+  }
+  if (!none) {
+    cluster_sync_all();  // all CTAs' sums are there
+    for (int i = threadIdx.x; i < tok * c.r; i += kFewThreads) {
+      float v = 0.0f;
+      for (int k = 0; k < ranks; ++k) v += load_cluster(mine + i, (uint32_t)k);
+      ts[i] = c.scale[tile.group] * v;
+    }
+    cluster_sync_all();  // and have been read (no CTA leaves before)
+  }
+  const float* ys[kFewItems];
+  float* os[kFewItems];
 #pragma unroll
-      for (int j = 0; j < kRankBlock / 8; ++j)
+  for (int n = 0; n < kFewItems; ++n) {
+    const long long row = c.rows[tile.first + min(n, tile.count - 1)];
+    ys[n] = c.Y + row * c.ldy;
+    os[n] = c.out + row * c.ldo;
+  }
+  // kCols columns a thread, their rows of B against T, 32 ranks at a time
+  constexpr int kCols = 2;
+  const TW* B = static_cast<const TW*>(c.B) + (size_t)tile.group * c.M * (size_t)c.r;
+  const int m1 = min(c.M, ((int)blockIdx.y + 1) * part_cols);
+  for (int m0 = (int)blockIdx.y * part_cols + threadIdx.x; m0 < m1; m0 += kCols * kFewThreads) {
+    float y[kCols][kFewItems], add[kCols][kFewItems] = {};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float2* p = reinterpret_cast<float2*>(red + ((warp % half) * 16 + 8 * h + g) * kLd + 8 * j + 2 * t);
-          if (j < nj && warp >= half && warp < 2 * half)
-            *p = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+    for (int p = 0; p < kCols; ++p)
+#pragma unroll
+      for (int n = 0; n < kFewItems; ++n)
+        y[p][n] = n < tile.count && m0 + p * kFewThreads < m1 ? ys[n][m0 + p * kFewThreads] : 0.0f;
+    for (int j0 = 0; j0 < c.r && !none; j0 += 32) {
+      uint4 w[kCols][4];
+#pragma unroll
+      for (int p = 0; p < kCols; ++p)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int m = m0 + p * kFewThreads;
+          w[p][u] = j0 + 8 * u < c.r && m < m1
+                        ? __ldg(reinterpret_cast<const uint4*>(B + (size_t)m * c.r + j0 + 8 * u))
+                        : make_uint4(0, 0, 0, 0);
         }
-      __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kRankBlock / 8; ++j)
+      for (int u = 0; u < 4; ++u) {
+        if (j0 + 8 * u >= c.r) break;
+        float f[kCols][8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float2* p =
-              reinterpret_cast<const float2*>(red + ((warp % half) * 16 + 8 * h + g) * kLd + 8 * j + 2 * t);
-          if (j < nj && warp < half) acc[j][2 * h] += p->x, acc[j][2 * h + 1] += p->y;
+        for (int p = 0; p < kCols; ++p)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 v = unpack2<TW>(word4(w[p][u], i));
+            f[p][2 * i] = v.x, f[p][2 * i + 1] = v.y;
+          }
+#pragma unroll
+        for (int n = 0; n < kFewItems; ++n) {
+          if (n >= tok) break;
+          const float4* q = reinterpret_cast<const float4*>(ts + n * c.r + j0 + 8 * u);
+          const float4 a = q[0], b = q[1];
+          const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int p = 0; p < kCols; ++p)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) add[p][n] = fmaf(f[p][i], v[i], add[p][n]);
         }
-      __syncthreads();
+      }
     }
-    if (warp == 0) {
 #pragma unroll
-      for (int j = 0; j < kRankBlock / 8; ++j)
+    for (int p = 0; p < kCols; ++p)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (j < nj)
-            *reinterpret_cast<float2*>(ts + (8 * h + g) * ld + j0 + 8 * j + 2 * t) =
-                make_float2(scale * acc[j][2 * h], scale * acc[j][2 * h + 1]);
-    }
+      for (int n = 0; n < kFewItems; ++n)
+        if (n < tile.count && m0 + p * kFewThreads < m1)
+          os[n][m0 + p * kFewThreads] = y[p][n] + add[p][n];
   }
 }
 
 // out = Y + B T. Grid (tiles of 16 * RW items, column parts); RW row warps
 // times col_warps column warps. JV: ranks a lane loads at a time (r is a
-// multiple of 4 * JV). kVec: 16-byte rows of Y and out. With TX (a type of X,
-// RW = 1) it makes T itself and has kFusedThreads threads; with void T comes
-// from shrink's parts.
-template <typename TX, typename TW, int RW, int JV, bool kVec>
-__global__ void __launch_bounds__(__is_same(TX, void) ? kThreads : kFusedThreads,
-                                  __is_same(TX, void) ? 2 : 1)
+// multiple of 4 * JV). kVec: 16-byte rows of Y and out.
+template <typename TW, int RW, int JV, bool kVec>
+__global__ void __launch_bounds__(kThreads, 2)
 expand_kernel(const LoraCall c, int col_warps, int part_cols) {
-  constexpr bool kFused = !__is_same(TX, void);
-  static_assert(!kFused || RW == 1, "the fused kernel has tiles of 16 items");
   constexpr int kRows = 16 * RW;
   extern __shared__ uint4 expand_smem[];
   float* ts = reinterpret_cast<float*>(expand_smem);  // T of the tile: [kRows][r + 4]
@@ -422,7 +556,6 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int m_begin = (int)blockIdx.y * part_cols, m_end = min(c.M, m_begin + part_cols);
   griddep_wait();
-  if (kFused) griddep_launch_dependents();
   const Tile tile = find_tile(c.offsets, c.L, kRows, blockIdx.x);
   if (tile.group < 0) return;
   const bool none = tile.group == c.L;  // tokens without an adapter: Y alone
@@ -437,29 +570,24 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
     cp_async_commit();
   };
   load(m_begin, 0);
-  if constexpr (kFused) {
-    if (!none)
-      shrink_tile<TX, TW>(c, tile, ts, ld, reinterpret_cast<float*>(bs + 2 * width * pitch));
-  } else {
-    // T, four ranks at a time, the parts' loads in flight together
-    for (int i = threadIdx.x; i < kRows * (c.r / 4); i += blockDim.x) {
-      const int n = i / (c.r / 4), j = i % (c.r / 4) * 4;
-      float4 v = make_float4(0, 0, 0, 0);
-      if (n < tile.count && !none) {
-        const float* p = c.part + (size_t)(tile.first + n) * c.r + j;
-        const size_t step = (size_t)c.items * c.r;
-        for (int s0 = 0; s0 < c.splits; s0 += 8) {
-          float4 w[8];
+  // T, four ranks at a time, the parts' loads in flight together
+  for (int i = threadIdx.x; i < kRows * (c.r / 4); i += blockDim.x) {
+    const int n = i / (c.r / 4), j = i % (c.r / 4) * 4;
+    float4 v = make_float4(0, 0, 0, 0);
+    if (n < tile.count && !none) {
+      const float* p = c.part + (size_t)(tile.first + n) * c.r + j;
+      const size_t step = (size_t)c.items * c.r;
+      for (int s0 = 0; s0 < c.splits; s0 += 8) {
+        float4 w[8];
 #pragma unroll
-          for (int s = 0; s < 8; ++s)
-            w[s] = s0 + s < c.splits ? *reinterpret_cast<const float4*>(p + (s0 + s) * step)
-                                     : make_float4(0, 0, 0, 0);
+        for (int s = 0; s < 8; ++s)
+          w[s] = s0 + s < c.splits ? *reinterpret_cast<const float4*>(p + (s0 + s) * step)
+                                   : make_float4(0, 0, 0, 0);
 #pragma unroll
-          for (int s = 0; s < 8; ++s) v.x += w[s].x, v.y += w[s].y, v.z += w[s].z, v.w += w[s].w;
-        }
+        for (int s = 0; s < 8; ++s) v.x += w[s].x, v.y += w[s].y, v.z += w[s].z, v.w += w[s].w;
       }
-      *reinterpret_cast<float4*>(ts + n * ld + j) = v;
     }
+    *reinterpret_cast<float4*>(ts + n * ld + j) = v;
   }
   const int rw = warp % RW, cw = warp / RW;
   const float* ys[2];
@@ -468,7 +596,7 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int n = 16 * rw + 8 * h + g;
-    has[h] = n < tile.count && cw < col_warps;
+    has[h] = n < tile.count;
     const long long row = c.rows[tile.first + (has[h] ? n : 0)];
     ys[h] = c.Y + row * c.ldy;
     os[h] = c.out + row * c.ldo;
@@ -497,7 +625,7 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
     __syncthreads();  // the block (and, before the first, T) is there
     float acc[8][4] = {};
     const uint8_t* b = bs + buf * width * pitch + cw * kColsWarp * pitch;
-    for (int j0 = 0; j0 < c.r && !none && cw < col_warps; j0 += 4 * JV) {
+    for (int j0 = 0; j0 < c.r && !none; j0 += 4 * JV) {
       constexpr bool kThree = JV == 4 && !__is_same(TW, __half);
       uint32_t hi[JV / 2][4], lo[JV / 2][4], three[3][4];
       float v[JV / 2][4];  // T of rows g, g + 8, two ranks each
@@ -578,95 +706,97 @@ long long most_tiles(long long items, int L, int rows) {
   const long long t = items / rows + L + 1;
   return t < items ? t : items;
 }
-// Many tokens an adapter: more than 16 on average.
-bool many(long long items, int L) { return items > 16ll * L; }
+// Many tokens an adapter: more than 8 on average.
+bool many(long long items, int L) { return items > 8ll * L; }
 
 template <typename TX, typename TW>
 cudaError_t shrink(const LoraCall& c, cudaStream_t s) {
   const dim3 grid((unsigned)most_tiles(c.items, c.L, kBigRows), (unsigned)c.splits,
                   (unsigned)((c.r + kRankBlock - 1) / kRankBlock));
-  return launch_pdl(shrink_big_kernel<TX, TW>, grid, dim3(kThreads),
+  return launch_pdl(shrink_kernel<TX, TW>, grid, dim3(kThreads),
                     (size_t)kBigStages * kBigStageBytes<TX, TW>, s, c);
 }
 
 size_t expand_smem_bytes(int rows, int r, int col_warps) {
   return (size_t)rows * (r + 4) * 4 + (size_t)2 * kColsWarp * col_warps * b_pitch(r);
 }
-constexpr size_t kExpandSmem = 112 * 1024;  // two CTAs an SM where that is enough
-constexpr int kExpandSmemMax = 227 * 1024;
-constexpr int kBigRw = 2;  // row warps of the expand kernel for many tokens
-static_assert(16 * (Q6_LORA_MAX_RANK + 4) * 4 + 2 * kColsWarp * b_pitch(Q6_LORA_MAX_RANK) + kFusedSum <=
-                  kExpandSmemMax, "16 items at the largest rank");
+constexpr size_t kExpandSmem = 112 * 1024;  // two CTAs an SM
+constexpr int kBigRw = 2;  // row warps of the expand kernel
 static_assert(16 * kBigRw * (Q6_LORA_MAX_RANK + 4) * 4 + 2 * kColsWarp * b_pitch(Q6_LORA_MAX_RANK) <=
-                  kExpandSmemMax, "the largest rank");
+                  kExpandSmem, "the largest rank");
 
-// The expand kernel for many tokens (TX void) or the fused one.
-template <typename TX, typename TW, int JV>
+template <typename TW, int JV>
 cudaError_t expand_v(const LoraCall& c, bool vec, cudaStream_t s) {
-  constexpr bool kFused = !__is_same(TX, void);
-  constexpr int RW = kFused ? 1 : kBigRw;
+  constexpr int RW = kBigRw;
   const long long tiles = most_tiles(c.items, c.L, 16 * RW);
-  const size_t extra = kFused ? kFusedSum : 0;
-  // column parts: about four CTAs an SM (two run at a time), or one of the
-  // fused kernel, which makes T again in each; then the widest block that is
-  // not wider than a part and leaves room
-  const int cols = (c.M + kColsWarp - 1) / kColsWarp;  // in warps' columns
-  long long parts = kFused ? 152 / tiles : (4 * 152 + tiles - 1) / tiles;
-  parts = parts < 1 ? 1 : parts > cols ? cols : parts;
-  int col_warps = kFused ? kFusedWarps : kWarps / RW;
-  while (col_warps > 1 &&
-         (expand_smem_bytes(16 * RW, c.r, col_warps) + extra > (kFused ? kExpandSmemMax : kExpandSmem) ||
-          col_warps >= 2 * ((cols + parts - 1) / parts)))
+  int col_warps = kWarps / RW;
+  while (col_warps > 1 && (expand_smem_bytes(16 * RW, c.r, col_warps) > kExpandSmem ||
+                           kColsWarp * col_warps >= 2 * c.M))
     col_warps /= 2;
+  // column parts: about four CTAs an SM (two run at a time), whole blocks each
   const int width = kColsWarp * col_warps, blocks = (c.M + width - 1) / width;
+  long long parts = (4 * 152 + tiles - 1) / tiles;
   if (parts > blocks) parts = blocks;
   const int part_cols = (int)((blocks + parts - 1) / parts) * width;
   const dim3 grid((unsigned)tiles, (unsigned)((c.M + part_cols - 1) / part_cols));
-  return launch_pdl(vec ? expand_kernel<TX, TW, RW, JV, true> : expand_kernel<TX, TW, RW, JV, false>,
-                    grid, dim3(kFused ? kFusedThreads : 32 * RW * col_warps),
-                    expand_smem_bytes(16 * RW, c.r, col_warps) + extra, s, c, col_warps, part_cols);
+  return launch_pdl(vec ? expand_kernel<TW, RW, JV, true> : expand_kernel<TW, RW, JV, false>, grid,
+                    dim3(32 * RW * col_warps), expand_smem_bytes(16 * RW, c.r, col_warps), s, c,
+                    col_warps, part_cols);
 }
-template <typename TX, typename TW>
+template <typename TW>
 cudaError_t expand(const LoraCall& c, cudaStream_t s) {
   const uintptr_t bits = reinterpret_cast<uintptr_t>(c.Y) | reinterpret_cast<uintptr_t>(c.out) |
                          (uintptr_t)(c.ldy * 4) | (uintptr_t)(c.ldo * 4) | (uintptr_t)(c.M * 4);
   const bool vec = bits % 16 == 0;
-  return c.r % 16 == 0 ? expand_v<TX, TW, 4>(c, vec, s) : expand_v<TX, TW, 2>(c, vec, s);
+  return c.r % 16 == 0 ? expand_v<TW, 4>(c, vec, s) : expand_v<TW, 2>(c, vec, s);
 }
 
 template <typename TX, typename TW>
-cudaError_t prepare_expand() {
-  constexpr int RW = __is_same(TX, void) ? kBigRw : 1;
-  cudaError_t e = cudaSuccess;
-  auto set = [&](auto* k) {
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmemMax);
-  };
-  set(expand_kernel<TX, TW, RW, 4, true>), set(expand_kernel<TX, TW, RW, 4, false>);
-  set(expand_kernel<TX, TW, RW, 2, true>), set(expand_kernel<TX, TW, RW, 2, false>);
-  return e;
+cudaError_t few(const LoraCall& c, cudaStream_t s) {
+  // column parts: one CTA an SM, at least 128 columns; clusters of up to 8
+  const long long tiles = most_tiles(c.items, c.L, kFewItems);
+  long long parts = 152 / tiles;
+  if (parts > c.M / 128) parts = c.M / 128;
+  int ranks = 1;
+  while (ranks < 8 && 2 * ranks <= parts) ranks *= 2;
+  parts = parts < 1 ? 1 : parts / ranks * ranks;
+  const int cols = (int)((c.M + parts - 1) / parts + 31) / 32 * 32;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)tiles, (unsigned)parts);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = (unsigned)ranks;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, lora_few_kernel<TX, TW>, c, cols, ranks);
 }
-template <typename TX, typename TW>
-cudaError_t prepare_x() {
-  cudaError_t e = cudaFuncSetAttribute(shrink_big_kernel<TX, TW>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kBigStages * kBigStageBytes<TX, TW>);
-  return e == cudaSuccess ? prepare_expand<TX, TW>() : e;
-}
+
 template <typename TW>
 cudaError_t prepare_t() {
-  cudaError_t e = prepare_expand<void, TW>();
-  if (e == cudaSuccess) e = prepare_x<float, TW>();
-  if (e == cudaSuccess) e = prepare_x<__nv_bfloat16, TW>();
-  if (e == cudaSuccess) e = prepare_x<__half, TW>();
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto* k, int bytes) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  set(expand_kernel<TW, kBigRw, 4, true>, kExpandSmem), set(expand_kernel<TW, kBigRw, 4, false>, kExpandSmem);
+  set(expand_kernel<TW, kBigRw, 2, true>, kExpandSmem), set(expand_kernel<TW, kBigRw, 2, false>, kExpandSmem);
+  set(shrink_kernel<float, TW>, kBigStages * kBigStageBytes<float, TW>);
+  set(shrink_kernel<__nv_bfloat16, TW>, kBigStages * kBigStageBytes<__nv_bfloat16, TW>);
+  set(shrink_kernel<__half, TW>, kBigStages * kBigStageBytes<__half, TW>);
   return e;
 }
 
 template <typename TX, typename TW>
 cudaError_t lora_x(const LoraCall& c, cudaStream_t s) {
-  if (!many(c.items, c.L)) return expand<TX, TW>(c, s);
+  if (!many(c.items, c.L)) return few<TX, TW>(c, s);
   const cudaError_t e = shrink<TX, TW>(c, s);
-  return e == cudaSuccess ? expand<void, TW>(c, s) : e;
+  return e == cudaSuccess ? expand<TW>(c, s) : e;
 }
 template <typename TW>
 cudaError_t lora_t(const LoraCall& c, cudaStream_t s) {
