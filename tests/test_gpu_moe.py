@@ -377,3 +377,65 @@ def test_refusals(rng):
         with pytest.raises(q6.Q6Error):
             call()
             pytest.fail(f"call {i} was accepted")
+
+
+@pytest.mark.parametrize("tokens", [1, 5, 200])
+def test_example_layer(tokens):
+    """The example's layer against 64 bits. Its int8 activations dominate: a value's step is 1/127
+    of its block's largest, about 3, so the rounding error is 3 / 127 / sqrt(12) of a unit value,
+    0.7 %; the experts' part has bf16 activations (2^-9 each way) and results."""
+    import importlib
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                                    "examples"))
+    assert importlib.import_module("moe_layer").check(tokens) <= 0.015
+
+
+# ------------------------------------------------- offsets that pass 32 bits ---
+
+@pytest.mark.parametrize("N", [2, 600])
+def test_experts_plane_past_4_gib(rng, N):
+    E, M, K = 40, 16384, 16384
+    gen = torch.Generator("cuda").manual_seed(N)
+    raw = torch.randint(0, 256, (E, M, K // 256, 144), generator=gen, device="cuda",
+                        dtype=torch.uint8)
+    d = torch.tensor([1e-4, 7e-4], device="cuda").half().view(torch.uint8)
+    raw[..., 0:4] = d
+    w = q6.pack_experts(raw, "q4_K", E, M, K)
+    assert w.plane.numel() > 1 << 32
+    rows = np.array([0, 1, 127, 128, 9000, M - 2, M - 1])
+    some = raw[E - 1, torch.from_numpy(rows).cuda()].cpu().numpy().reshape(1, len(rows), -1)
+    del raw
+    X = cuda(rng.standard_normal((N, K)), "bf16")
+    ids = np.full((N, 1), E - 1)
+    Y, path = q6.experts_mmq(w, X, q6.group_rows(cuda(ids.astype(np.int32)), E))
+    assert path == ("experts_few" if N == 2 else "experts_tc")
+    q6.sync_status()
+    want, bound = ref.experts(some, "q4_K", f64(X), np.zeros_like(ids), 1, False, True, "bf16")
+    check(Y[:, torch.from_numpy(rows).cuda()], want, bound)
+
+
+def test_combine_past_2_31_values():
+    N, topk, M = 70000, 8, 4096
+    Y = torch.zeros((N * topk, M), dtype=torch.bfloat16, device="cuda")
+    assert Y.numel() > 1 << 31
+    Y[-topk:] = torch.arange(1, topk + 1, device="cuda")[:, None]
+    pos = torch.arange(N * topk, dtype=torch.int32, device="cuda").view(N, topk)
+    out = q6.moe_combine(Y, pos, torch.ones((N, topk), device="cuda"))
+    assert (out[-1] == 36).all() and not out[:-1].any()
+
+
+def test_lora_past_2_31_values(rng):
+    N, K, M, r = 140000, 16384, 24, 8
+    X = torch.zeros((N, K), dtype=torch.bfloat16, device="cuda")
+    assert X.numel() > 1 << 31
+    last = cuda(rng.standard_normal((3, K)), "bf16")
+    X[-3:] = last
+    A, B = cuda(rng.standard_normal((2, r, K)) / 128, "bf16"), cuda(rng.standard_normal((2, M, r)), "bf16")
+    scale, Y = torch.ones(2, device="cuda"), torch.zeros((N, M), device="cuda")
+    ids = np.ones(N, np.int64)
+    out = q6.lora_add(q6.LoraAdapters(A, B, scale), X, q6.group_rows(cuda(ids.astype(np.int32)), 2), Y)
+    want, bound = ref.lora(np.zeros((3, M)), f64(last), f64(A), f64(B), f64(scale), ids[:3])
+    check(out[-3:], want, bound)
+    assert not out[:-3].any()
