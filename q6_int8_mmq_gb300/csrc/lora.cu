@@ -16,9 +16,11 @@
 //
 // Beyond that there are two kernels on warp-level MMAs: shrink takes 64 tokens a
 // CTA, x and A coming through shared memory in four stages, K split over CTAs
-// and the parts added in a fixed order by expand, which takes 32 tokens, B in
-// blocks of columns through shared memory and Y loaded a block ahead. MMAs with
-// f32 accumulation, the 16-bit factors as they are; an f32 factor (x, T) beside
+// and the parts added in a fixed order by expand, which takes 32 tokens, T split
+// once, and whose warps each walk columns of their own, B copied and Y loaded a
+// block ahead (sharing B among the warps of a CTA, with a barrier per block, took
+// 73 instead of 68 us for 3314 tokens, rank 64, 11008 columns). MMAs with f32
+// accumulation, the 16-bit factors as they are; an f32 factor (x, T) beside
 // bf16 is split into three bf16 values, 8 bits each and together exact; beside
 // f16 (whose range is too small for the parts) into a tf32 value and a tf32
 // remainder, which loses 2^-21 of it.
@@ -329,12 +331,6 @@ shrink_kernel(const LoraCall c) {
     }
 }
 
-constexpr int kColsWarp = 64;  // columns a warp takes at a time
-
-// Bytes of a column of B in shared memory: four neighbouring columns' fragment
-// loads (32 bytes each) fall on different banks.
-__host__ __device__ constexpr int b_pitch(int r) { return 2 * r + (2 * r % 64 == 0 ? 32 : 0); }
-
 constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32;
 constexpr int kFewItems = 4;  // of a tile
 
@@ -542,39 +538,90 @@ lora_few_kernel(const LoraCall c, int part_cols, int ranks) {
   }
 }
 
-// out = Y + B T. Grid (tiles of 16 * RW items, column parts); RW row warps
-// times col_warps column warps. JV: ranks a lane loads at a time (r is a
-// multiple of 4 * JV). kVec: 16-byte rows of Y and out.
-template <typename TW, int RW, int JV, bool kVec>
+// Expand for many tokens. A tile is 32 items; a CTA's warps take 32 columns each
+// of its part in turn.
+constexpr int kExpandRows = 32, kColsWarp = 32;  // a thread a column: blockDim.x is the width
+// Bytes of a column of B in shared memory: four neighbouring columns' fragment
+// loads (32 bytes each) fall on different banks.
+__host__ __device__ constexpr int b_pitch(int r) { return 2 * r + (2 * r % 64 == 0 ? 32 : 0); }
+// T in shared memory as the MMAs' factors: three bf16 parts [3][32][r + 8], or a
+// tf32 value and the remainder [2][32][r + 4].
+template <typename TW>
+constexpr bool kThreeParts = !__is_same(TW, __half);
+template <typename TW>
+__host__ __device__ constexpr int t_pitch(int r) { return kThreeParts<TW> ? 2 * (r + 8) : 4 * (r + 4); }
+template <typename TW>
+constexpr int expand_smem(int r, int warps) {
+  return (kThreeParts<TW> ? 3 : 2) * kExpandRows * t_pitch<TW>(r) + 2 * kColsWarp * warps * b_pitch(r);
+}
+// Warps of a CTA: 8, or as many as leave room for two CTAs an SM; 4 of one where
+// two do not fit (rank 256).
+constexpr int kExpandSmem = 112 * 1024, kExpandSmemMax = 227 * 1024;
+template <typename TW>
+constexpr int expand_warps(int r) {
+  for (int w = kWarps; w > 1; w /= 2)
+    if (expand_smem<TW>(r, w) <= kExpandSmem) return w;
+  return 4;
+}
+static_assert(expand_smem<__nv_bfloat16>(Q6_LORA_MAX_RANK, 4) <= kExpandSmemMax &&
+                  expand_smem<__half>(Q6_LORA_MAX_RANK, 4) <= kExpandSmemMax, "the largest rank");
+
+// Grid (tiles, column parts). JV: ranks a lane loads at a time (r is a multiple
+// of 4 * JV). kVec: 16-byte rows of Y and out.
+template <typename TW, int JV, bool kVec>
 __global__ void __launch_bounds__(kThreads, 2)
-expand_kernel(const LoraCall c, int col_warps, int part_cols) {
-  constexpr int kRows = 16 * RW;
-  extern __shared__ uint4 expand_smem[];
-  float* ts = reinterpret_cast<float*>(expand_smem);  // T of the tile: [kRows][r + 4]
-  const int ld = c.r + 4, pitch = b_pitch(c.r), width = kColsWarp * col_warps;
-  uint8_t* bs = reinterpret_cast<uint8_t*>(ts + kRows * ld);  // two blocks of `width` columns
+expand_kernel(const LoraCall c, int part_cols) {
+  constexpr bool kThree = kThreeParts<TW>;
+  constexpr int kParts = kThree ? 3 : 2;
+  extern __shared__ uint4 smem_raw[];
+  uint8_t* ts = reinterpret_cast<uint8_t*>(smem_raw);
+  const int ld = t_pitch<TW>(c.r), pitch = b_pitch(c.r), width = (int)blockDim.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int m_begin = (int)blockIdx.y * part_cols, m_end = min(c.M, m_begin + part_cols);
+  // this warp's two blocks of B
+  uint8_t* bs = ts + kParts * kExpandRows * ld + warp * 2 * kColsWarp * pitch;
+  const int m_end = min(c.M, ((int)blockIdx.y + 1) * part_cols);
+  const int m_first = (int)blockIdx.y * part_cols + warp * kColsWarp;
   griddep_wait();
-  const Tile tile = find_tile(c.offsets, c.L, kRows, blockIdx.x);
+  const Tile tile = find_tile(c.offsets, c.L, kExpandRows, blockIdx.x);
   if (tile.group < 0) return;
   const bool none = tile.group == c.L;  // tokens without an adapter: Y alone
   if (none && c.out == c.Y) return;
   const TW* B = static_cast<const TW*>(c.B) + (size_t)tile.group * c.M * (size_t)c.r;
   const int units = c.r / 8;  // 16-byte units of a column
-  auto load = [&](int m0, int buf) {
-    const int n = none ? 0 : min(width, m_end - m0) * units;
-    for (int i = threadIdx.x; i < n; i += blockDim.x)
-      cp_async16(bs + buf * width * pitch + i / units * pitch + i % units * 16,
+  auto load_b = [&](int m0, int buf) {
+    const int n = none || m0 >= m_end ? 0 : min(kColsWarp, m_end - m0) * units;
+    for (int i = lane; i < n; i += 32)
+      cp_async16(bs + buf * kColsWarp * pitch + i / units * pitch + i % units * 16,
                  B + (size_t)m0 * c.r + (size_t)i * 8, true);
     cp_async_commit();
   };
-  load(m_begin, 0);
+  load_b(m_first, 0);
+  const float* ys[4];  // rows g, g + 8, g + 16, g + 24 of the tile
+  float* os[4];
+  bool has[4];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    has[h] = 8 * h + g < tile.count;
+    const long long row = c.rows[tile.first + (has[h] ? 8 * h + g : 0)];
+    ys[h] = c.Y + row * c.ldy;
+    os[h] = c.out + row * c.ldo;
+  }
+  auto load_y = [&](int h, int m) {
+    return kVec && has[h] && m < m_end ? __ldcs(reinterpret_cast<const float4*>(ys[h] + m))
+                                       : make_float4(0, 0, 0, 0);
+  };
+  // MMA tile p's slots 2t, 2t + 1 with those of tile p + 1 are the four
+  // consecutive columns 16 (p / 2) + 4 t..
+  float4 y[4][2];
+#pragma unroll
+  for (int h = 0; h < 4; ++h)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) y[h][q] = load_y(h, m_first + 4 * t + 16 * q);
   // T, four ranks at a time, the parts' loads in flight together
-  for (int i = threadIdx.x; i < kRows * (c.r / 4); i += blockDim.x) {
+  for (int i = threadIdx.x; i < kExpandRows * (c.r / 4) && !none; i += width) {
     const int n = i / (c.r / 4), j = i % (c.r / 4) * 4;
     float4 v = make_float4(0, 0, 0, 0);
-    if (n < tile.count && !none) {
+    if (n < tile.count) {
       const float* p = c.part + (size_t)(tile.first + n) * c.r + j;
       const size_t step = (size_t)c.items * c.r;
       for (int s0 = 0; s0 < c.splits; s0 += 8) {
@@ -587,102 +634,98 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
         for (int s = 0; s < 8; ++s) v.x += w[s].x, v.y += w[s].y, v.z += w[s].z, v.w += w[s].w;
       }
     }
-    *reinterpret_cast<float4*>(ts + n * ld + j) = v;
-  }
-  const int rw = warp % RW, cw = warp / RW;
-  const float* ys[2];
-  float* os[2];
-  bool has[2];
+    uint8_t* to = ts + n * ld;
+    if constexpr (kThree) {
+      uint32_t a[3], b[3];
+      bf16_split3(v.x, v.y, a);
+      bf16_split3(v.z, v.w, b);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int n = 16 * rw + 8 * h + g;
-    has[h] = n < tile.count;
-    const long long row = c.rows[tile.first + (has[h] ? n : 0)];
-    ys[h] = c.Y + row * c.ldy;
-    os[h] = c.out + row * c.ldo;
-  }
-  // MMA tile p's slots 2t, 2t + 1 with those of tile p + 1 are the four
-  // consecutive columns 16 (p / 2) + 4 t..
-  const int col0 = cw * kColsWarp + 4 * t;
-  auto load_y = [&](int h, int m) {
-    return kVec && has[h] && m < m_end ? __ldcs(reinterpret_cast<const float4*>(ys[h] + m))
-                                       : make_float4(0, 0, 0, 0);
-  };
-  float4 y[2][4];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) y[h][q] = load_y(h, m_begin + col0 + 16 * q);
-  int buf = 0;
-  for (int m0 = m_begin; m0 < m_end; m0 += width, buf ^= 1) {
-    if (m0 + width < m_end) {
-      load(m0 + width, buf ^ 1);
+      for (int s = 0; s < 3; ++s)
+        *reinterpret_cast<uint2*>(to + s * kExpandRows * ld + 2 * j) = make_uint2(a[s], b[s]);
     } else {
-      cp_async_commit();
+      float4 hi, lo;
+      tf32_split(v.x, hi.x, lo.x), tf32_split(v.y, hi.y, lo.y);
+      tf32_split(v.z, hi.z, lo.z), tf32_split(v.w, hi.w, lo.w);
+      *reinterpret_cast<float4*>(to + 4 * j) = hi;
+      *reinterpret_cast<float4*>(to + kExpandRows * ld + 4 * j) = lo;
     }
-    const int m = m0 + col0;
-    cp_async_wait<1>();
-    __syncthreads();  // the block (and, before the first, T) is there
-    float acc[8][4] = {};
-    const uint8_t* b = bs + buf * width * pitch + cw * kColsWarp * pitch;
+  }
+  __syncthreads();
+  int buf = 0;
+  for (int m0 = m_first; m0 < m_end; m0 += width, buf ^= 1) {
+    cp_async_wait<0>();
+    __syncwarp();  // all lanes' copies of the block are there, the other block has been read
+    load_b(m0 + width, buf ^ 1);
+    float acc[2][4][4] = {};
+    const uint8_t* b = bs + buf * kColsWarp * pitch;
     for (int j0 = 0; j0 < c.r && !none; j0 += 4 * JV) {
-      constexpr bool kThree = JV == 4 && !__is_same(TW, __half);
-      uint32_t hi[JV / 2][4], lo[JV / 2][4], three[3][4];
-      float v[JV / 2][4];  // T of rows g, g + 8, two ranks each
+      // columns past M hold what the buffer held: they are not stored
+      auto col_at = [&](int p) {
+        return b + (16 * (p / 2) + 4 * (g / 2) + 2 * (p % 2) + g % 2) * pitch + (j0 + JV * t) * 2;
+      };
+      if constexpr (kThree && JV == 4) {
+        uint32_t a[2][3][4];
 #pragma unroll
-      for (int q = 0; q < JV / 2; ++q) {
-        const float* p = ts + (16 * rw + g) * ld + j0 + JV * t + 2 * q;
-        const float2 f0 = *reinterpret_cast<const float2*>(p);
-        const float2 f1 = *reinterpret_cast<const float2*>(p + 8 * ld);
-        v[q][0] = f0.x, v[q][1] = f1.x, v[q][2] = f0.y, v[q][3] = f1.y;
-      }
-      if constexpr (kThree) {
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // row e % 2, the pair e / 2
-          uint32_t p[3];
-          bf16_split3(v[e / 2][e % 2], v[e / 2][2 + e % 2], p);
+          for (int s = 0; s < 3; ++s)
 #pragma unroll
-          for (int s = 0; s < 3; ++s) three[s][e] = p[s];
+            for (int h = 0; h < 2; ++h) {
+              const uint2 v = *reinterpret_cast<const uint2*>(
+                  ts + (s * kExpandRows + 16 * i + 8 * h + g) * ld + (j0 + 4 * t) * 2);
+              a[i][s][h] = v.x, a[i][s][2 + h] = v.y;
+            }
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint2 w = *reinterpret_cast<const uint2*>(col_at(p));
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int s = 2; s >= 0; --s) mma_16<TW>(acc[i][p], a[i][s], w.x, w.y);
         }
       } else {
+        // tf32: the parts as they are (bf16 ones are tf32 values too)
+        uint32_t a[kParts][JV / 2][2][4];
 #pragma unroll
-        for (int q = 0; q < JV / 2; ++q)
+        for (int s = 0; s < kParts; ++s)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x, r;
-            tf32_split(v[q][e], x, r);
-            hi[q][e] = __float_as_uint(x);
-            lo[q][e] = __float_as_uint(r);
-          }
-      }
+          for (int q = 0; q < JV / 2; ++q)
 #pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        // columns past M hold what the buffer held: they are not stored
-        const int col = 16 * (p / 2) + 4 * (g / 2) + 2 * (p % 2) + g % 2;
-        const uint8_t* wp = b + col * pitch + (j0 + JV * t) * 2;
-        if constexpr (kThree) {
-          const uint2 w = *reinterpret_cast<const uint2*>(wp);
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int s = 2; s >= 0; --s) mma_16<TW>(acc[p], three[s], w.x, w.y);
-        } else {
+              for (int h = 0; h < 2; ++h) {
+                const uint8_t* p = ts + (s * kExpandRows + 16 * i + 8 * h + g) * ld;
+                const int j = j0 + JV * t + 2 * q;
+                float2 v;
+                if constexpr (kThree)
+                  v = unpack2<__nv_bfloat16>(*reinterpret_cast<const uint32_t*>(p + 2 * j));
+                else
+                  v = *reinterpret_cast<const float2*>(p + 4 * j);
+                a[s][q][i][h] = __float_as_uint(v.x), a[s][q][i][2 + h] = __float_as_uint(v.y);
+              }
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
           float w[JV];
-          shared_f32<TW, JV>(wp, w);
+          shared_f32<TW, JV>(col_at(p), w);
 #pragma unroll
-          for (int q = 0; q < JV / 2; ++q) {
-            const uint32_t b0 = __float_as_uint(w[2 * q]), b1 = __float_as_uint(w[2 * q + 1]);
-            mma_tf32(acc[p], lo[q], b0, b1);
-            mma_tf32(acc[p], hi[q], b0, b1);
-          }
+          for (int q = 0; q < JV / 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int s = kParts - 1; s >= 0; --s)
+                mma_tf32(acc[i][p], a[s][q][i], __float_as_uint(w[2 * q]),
+                         __float_as_uint(w[2 * q + 1]));
         }
       }
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 4; ++h)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int at = m + 16 * q;
-        const float v[4] = {acc[2 * q][2 * h], acc[2 * q][2 * h + 1], acc[2 * q + 1][2 * h],
-                            acc[2 * q + 1][2 * h + 1]};
+      for (int q = 0; q < 2; ++q) {
+        const int at = m0 + 4 * t + 16 * q;
+        const float(&lo)[4] = acc[h / 2][2 * q], (&hi)[4] = acc[h / 2][2 * q + 1];
+        const int e = 2 * (h % 2);
+        const float v[4] = {lo[e], lo[e + 1], hi[e], hi[e + 1]};
         if (kVec) {
           const float4 a = y[h][q];
           if (has[h] && at < m_end)
@@ -691,11 +734,10 @@ expand_kernel(const LoraCall c, int col_warps, int part_cols) {
           y[h][q] = load_y(h, at + width);
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (has[h] && at + e < m_end) os[h][at + e] = ys[h][at + e] + v[e];
+          for (int k = 0; k < 4; ++k)
+            if (has[h] && at + k < m_end) os[h][at + k] = ys[h][at + k] + v[k];
         }
       }
-    __syncthreads();  // the block has been read
   }
   cp_async_wait<0>();
 }
@@ -717,31 +759,18 @@ cudaError_t shrink(const LoraCall& c, cudaStream_t s) {
                     (size_t)kBigStages * kBigStageBytes<TX, TW>, s, c);
 }
 
-size_t expand_smem_bytes(int rows, int r, int col_warps) {
-  return (size_t)rows * (r + 4) * 4 + (size_t)2 * kColsWarp * col_warps * b_pitch(r);
-}
-constexpr size_t kExpandSmem = 112 * 1024;  // two CTAs an SM
-constexpr int kBigRw = 2;  // row warps of the expand kernel
-static_assert(16 * kBigRw * (Q6_LORA_MAX_RANK + 4) * 4 + 2 * kColsWarp * b_pitch(Q6_LORA_MAX_RANK) <=
-                  kExpandSmem, "the largest rank");
-
 template <typename TW, int JV>
 cudaError_t expand_v(const LoraCall& c, bool vec, cudaStream_t s) {
-  constexpr int RW = kBigRw;
-  const long long tiles = most_tiles(c.items, c.L, 16 * RW);
-  int col_warps = kWarps / RW;
-  while (col_warps > 1 && (expand_smem_bytes(16 * RW, c.r, col_warps) > kExpandSmem ||
-                           kColsWarp * col_warps >= 2 * c.M))
-    col_warps /= 2;
-  // column parts: about four CTAs an SM (two run at a time), whole blocks each
-  const int width = kColsWarp * col_warps, blocks = (c.M + width - 1) / width;
-  long long parts = (4 * 152 + tiles - 1) / tiles;
+  const long long tiles = most_tiles(c.items, c.L, kExpandRows);
+  const int warps = expand_warps<TW>(c.r), width = kColsWarp * warps;
+  // column parts: about two CTAs an SM (as run at a time), whole blocks each
+  const int blocks = (c.M + width - 1) / width;
+  long long parts = (2 * 152 + tiles - 1) / tiles;
   if (parts > blocks) parts = blocks;
   const int part_cols = (int)((blocks + parts - 1) / parts) * width;
   const dim3 grid((unsigned)tiles, (unsigned)((c.M + part_cols - 1) / part_cols));
-  return launch_pdl(vec ? expand_kernel<TW, RW, JV, true> : expand_kernel<TW, RW, JV, false>, grid,
-                    dim3(32 * RW * col_warps), expand_smem_bytes(16 * RW, c.r, col_warps), s, c,
-                    col_warps, part_cols);
+  return launch_pdl(vec ? expand_kernel<TW, JV, true> : expand_kernel<TW, JV, false>, grid,
+                    dim3(32 * warps), (size_t)expand_smem<TW>(c.r, warps), s, c, part_cols);
 }
 template <typename TW>
 cudaError_t expand(const LoraCall& c, cudaStream_t s) {
@@ -784,8 +813,9 @@ cudaError_t prepare_t() {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
-  set(expand_kernel<TW, kBigRw, 4, true>, kExpandSmem), set(expand_kernel<TW, kBigRw, 4, false>, kExpandSmem);
-  set(expand_kernel<TW, kBigRw, 2, true>, kExpandSmem), set(expand_kernel<TW, kBigRw, 2, false>, kExpandSmem);
+  constexpr int kMost = kExpandSmemMax;
+  set(expand_kernel<TW, 4, true>, kMost), set(expand_kernel<TW, 4, false>, kMost);
+  set(expand_kernel<TW, 2, true>, kMost), set(expand_kernel<TW, 2, false>, kMost);
   set(shrink_kernel<float, TW>, kBigStages * kBigStageBytes<float, TW>);
   set(shrink_kernel<__nv_bfloat16, TW>, kBigStages * kBigStageBytes<__nv_bfloat16, TW>);
   set(shrink_kernel<__half, TW>, kBigStages * kBigStageBytes<__half, TW>);
