@@ -57,8 +57,11 @@ int check_experts(int fmt, int E, int M, int K, int swiglu) {
   return Q6_OK;
 }
 
-// Items an expert, on average, up to which the few-token kernel runs.
-constexpr int kFewItems = 12;
+// Items an expert, on average, up to which the few-token kernel runs. Measured,
+// few-token kernel / tensor cores, q4_K, 64 experts of 1536 x 2048: 30.8 / 32.9 us
+// at 2, 47.0 / 35.2 us at 4, 148 / 42.5 us at 16; 8 experts of 4096 x 4096: 24.6 /
+// 31.7, 33.6 / 32.4 and 79.9 / 32.4 us; q6_K crosses at the same place.
+constexpr int kFewItems = 3;
 bool on_tensor_cores(int64_t items, int E) { return items > kFewItems * (int64_t)E; }
 // Bytes of the binary16 rows in item order that the tensor-core path makes (0:
 // it reads X itself), and where their scales follow.
