@@ -13,13 +13,16 @@
 // The weights are dequantised inside the kernel, once per tile: thread =
 // weight row, binary16 pairs, the result stored straight into TMEM, where the
 // MMA takes its A operand from. Packed weights are all that memory and shared
-// memory ever see. A code is the binary16 subnormal q * 2^-24; with sc * 2^9
-// it makes sc * q exactly, and one fused multiply-add with d and -dmin * m
-// (all times a power of two of the row) makes the weight: what is rounded to
-// 11 bits is dmin * m and the weight (q6_K: sc * (q - 32) beyond 2048, and the
-// weight), an eighth of the rounding of a bf16 Y. For a binary16 Y that would
-// show, so there the weight is rounded once (q4_K in f32, 2.6 instead of 1.7
-// instructions a weight; q6_K with sc * d in two terms, 3.4 instead of 2.6).
+// memory ever see. A code is the binary16 subnormal q * 2^-24 and a weight one
+// fused multiply-add of it with sc * d and -dmin * m, all times a power of two of
+// the row (the largest possible weight of a row just below 2^-5): what is rounded
+// to 11 bits is sc * d, dmin * m and the weight, each an eighth of the rounding of
+// a bf16 Y. (Rates, cycles a warp instruction of one scheduler: binary16 pairs 2,
+// integer logic and shifts 2, on two pipes; f32 1. With sc * q exact and d
+// multiplied in after that, 2.7 instead of 2 instructions a pair, 8 experts of
+// 4096 x 4096 took 28.8 instead of 27.0 us.) For a binary16 Y that would
+// show, so there the weight is rounded once (q4_K in f32, 2.6 instructions a
+// weight; q6_K with sc * d in two terms, 3.4).
 // In a binary16 silu(gate) * up the roundings of both products would still
 // add up to 1.7 times that of Y; there a weight is a pair of binary16 values
 // in two A slots, and every x tile meets both.
@@ -36,15 +39,19 @@
 //   1      in CTA 0, issues the pair's MMAs
 //   2      TMEM allocation
 //   3      streams the packed weights, one super-block a stage
-//   4-11   dequantise: warps 4-7 the even, 8-11 the odd halves (128 of K) of
-//          the super-blocks
+//   4-11   dequantise: warps 4-7 the even, 8-11 the odd super-blocks. A group
+//          waits, loads and hands over for about as long as it calculates, and
+//          the other's calculation fills that time; when both worked on the
+//          halves of one super-block they did everything at the same time (1350
+//          instead of 1050 cycles a super-block with few items). Sixteen warps
+//          instead of eight, by halves or quarters, with 72 registers: not faster.
 //   12-19  epilogue: warps 12-15 items 0-127 of a tile, 16-19 the others (or
 //          every other tile of up to 128 items)
 // TMEM: columns 0-255 two accumulators of 128 items (or one of 256), 256-511
 // four A slots of 128 of K.
 // The walk is in units: 128 of K for tiles of more than 128 items (or weights
-// in pairs), 256 for others. A unit has one x stage and one or two A slots; one barrier says that
-// all of it is there (both CTAs' copies and dequantised halves), another that
+// in pairs), 256 for others. A unit has one x stage and one or two A slots; one
+// barrier says that all of it is there (both CTAs' copies and dequantised halves), another that
 // its MMAs are through. (A wait costs the MMA warp about 120 cycles and a
 // commit 150 or more, a unit's MMAs at 128 items 1024: with separate barriers
 // for x and A and 128 of K each, 1023 tokens over 64 experts took 119 us.)
@@ -57,11 +64,14 @@ namespace {
 
 constexpr int kThreads = 640;
 constexpr int kTileN = 256;
-constexpr int kUnits = 4, kXStage = 32 * 1024;  // units in flight; an x stage each
-// Packed super-blocks in flight: 54 KB of either format.
+// Units in flight, and those with their x in shared memory; packed super-blocks
+// there, of either format what is left. (With a fourth x stage q6_K keeps two
+// super-blocks, half of what HBM's latency wants: 8 experts of 4096 x 4096 with
+// 32 items each took 43.5 instead of 34.7 us.)
+constexpr int kUnits = 4, kXStages = 3, kXStage = 32 * 1024;
 template <int kFmt>
-constexpr int kWStagesOf = kFmt == Q6_FMT_Q4K ? 3 : 2;
-constexpr int kMaxWStages = 3;
+constexpr int kWStages = kFmt == Q6_FMT_Q4K ? 5 : 4;
+constexpr int kMaxWStages = 5;
 constexpr int kASlots = 4, kACols = 64, kACol0 = 256;
 constexpr int kTmemCols = 512;
 
@@ -76,10 +86,9 @@ struct Bars {
   uint32_t tmem_base;
   int abort;
 };
-// Arrivals that make a unit ready: the x copies' opening, and 16 of the
-// dequantising warps (one for each of 16 warps and half super-blocks, or two
-// for each of 8).
-constexpr int kReadyArrivals = 17;
+// Arrivals that make a unit ready: the x copies' opening, and the pair's eight
+// warps that dequantise it.
+constexpr int kReadyArrivals = 9;
 
 struct Args {
   const uint8_t* plane;
@@ -90,14 +99,15 @@ struct Args {
   long long ldy;
   int E, bands, sbs, out;
   int vec;  // Y and its rows are 16-byte aligned
+  int early;  // the kernel before is expert_rows_kernel: only x depends on it
 };
 
 template <int kFmt>
 constexpr int kWTile = kFmt == Q6_FMT_Q4K ? kQ4Tile : kQ6Tile;
 constexpr int kOutWarp = 2048;  // epilogue staging of a warp: 32 items of 64 bytes
 template <int kFmt>
-constexpr int kSmemBytes = 1024 + kUnits * kXStage + kWStagesOf<kFmt> * kWTile<kFmt> + 8 * kOutWarp +
-                           (kMaxGroups + 1) * 4 + 12 + (int)sizeof(Bars);
+constexpr int kSmemBytes = 1024 + kXStages * kXStage + kWStages<kFmt> * kWTile<kFmt> + 8 * kOutWarp +
+                           2 * (kMaxGroups + 1) * 4 + (int)sizeof(Bars);
 
 // True in one lane of the converged warp. TMA and MMA instructions take their
 // operands from uniform registers: one elected lane on values that all lanes
@@ -144,17 +154,15 @@ __device__ __forceinline__ void commit_own(uint64_t* bar) {
           smem_u32(bar))
       : "memory");
 }
-// Arrives `count` times on `bar` of CTA 0 of the pair after this warp's tcgen05 loads
-// or stores, which the tcgen05 waits and fences around the barrier order;
+// Arrives on `bar` of CTA 0 of the pair after this warp's tcgen05 loads or stores, which the tcgen05 waits and fences around the barrier order;
 // nothing else is published, so the arrival needs no release (one of cluster
 // scope was measured at 1300 cycles behind the packed-weight reads).
-__device__ __forceinline__ void arrive_leader_tmem(uint64_t* bar, uint32_t count = 1) {
+__device__ __forceinline__ void arrive_leader_tmem(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .b32 ra;\n\t"
       "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
-      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [ra], %1;\n\t}\n" ::"r"(
-          smem_u32(bar)),
-      "r"(count)
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [ra];\n\t}\n" ::"r"(
+          smem_u32(bar))
       : "memory");
 }
 // A TMA load into this CTA that counts on `bar` of CTA 0 of the pair.
@@ -224,7 +232,7 @@ __device__ __forceinline__ void store_tiles_t(uint32_t addr, uint32_t a, uint32_
 }
 
 // ------------------------------------------------------------ dequantising ---
-constexpr uint32_t kH2_512 = 0x60006000u, kH2_256 = 0x5C005C00u, kH2_m2p19 = 0x80208020u,
+constexpr uint32_t kH2_2m15 = 0x02000200u, kH2_m2p19 = 0x80208020u,
                    kH2_1_16 = 0x2C002C00u, kH2_1056 = 0x64206420u;
 
 // A byte of a word as a binary16 pair, plus 1024.
@@ -276,22 +284,22 @@ struct Half<Q6_FMT_Q4K> {
     for (int t = 0; t < 4; ++t) q[t] = p[(1 + 2 * t + h) * kBand];
     const float2 dd = unpack2<__half>(head.x);
     df = dd.x * inv, dmf = -dd.y * inv;
-    d = splat_h2(df * 32768.0f), dm = splat_h2(dmf);
+    d = splat_h2(df * 512.0f), dm = splat_h2(dmf);
     sc = h ? (head.w & 0x0F0F0F0Fu) | ((head.y >> 2) & 0x30303030u) : head.y & 0x3F3F3F3Fu;
     mn = h ? ((head.w >> 4) & 0x0F0F0F0Fu) | ((head.z >> 2) & 0x30303030u) : head.z & 0x3F3F3F3Fu;
   }
   // Chunk cc of the half (32 of K) as 16 words.
   __device__ __forceinline__ void expand(int cc, uint32_t (&out)[16]) const {
-    const uint32_t s = hmul2u(hsub2u(byte_h2(sc, cc), kH2_1024), kH2_512);   // sc * 2^9
+    const uint32_t s = hmul2u(hsub2u(byte_h2(sc, cc), kH2_1024), d);  // sc * d * 2^9
     const uint32_t s16 = hmul2u(s, kH2_1_16);  // for codes four bits up
-    const uint32_t m = hmul2u(hsub2u(byte_h2(mn, cc), kH2_1024), dm);        // -dmin * m
+    const uint32_t m = hmul2u(hmul2u(hsub2u(byte_h2(mn, cc), kH2_1024), dm), kH2_2m15);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const uint32_t w = word4(q[t], cc), w8 = w >> 8;
-      out[4 * t] = hfma2u(hmul2u(w & 0x000F000Fu, s), d, m);
-      out[4 * t + 1] = hfma2u(hmul2u(w & 0x00F000F0u, s16), d, m);
-      out[4 * t + 2] = hfma2u(hmul2u(w8 & 0x000F000Fu, s), d, m);
-      out[4 * t + 3] = hfma2u(hmul2u(w8 & 0x00F000F0u, s16), d, m);
+      out[4 * t] = hfma2u(w & 0x000F000Fu, s, m);
+      out[4 * t + 1] = hfma2u(w & 0x00F000F0u, s16, m);
+      out[4 * t + 2] = hfma2u(w8 & 0x000F000Fu, s, m);
+      out[4 * t + 3] = hfma2u(w8 & 0x00F000F0u, s16, m);
     }
   }
   // In f32, rounded once. The offsets of the codes go with the min (rounded to
@@ -349,19 +357,19 @@ struct Half<Q6_FMT_Q6K> {
     const uint32_t* s = reinterpret_cast<const uint32_t*>(p + 12 * kBand);
     sc[0] = s[h], sc[1] = s[2 + h];
     df = __half2float(reinterpret_cast<const __half*>(tile + 13 * 2048)[row]) * inv;
-    d = splat_h2(df * 65536.0f);
+    d = splat_h2(df * 512.0f);
   }
   __device__ __forceinline__ void expand(int cc, uint32_t (&out)[16]) const {
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {  // runs 0, 1 and 2, 3 of the chunk
-      const uint32_t s = hmul2u(hsub2u(byte_h2(sc[sub], cc), kH2_1152), kH2_256);  // sc * 2^8
+      const uint32_t s = hmul2u(hsub2u(byte_h2(sc[sub], cc), kH2_1152), d);  // sc * d * 2^9
       const uint32_t o = hmul2u(s, kH2_m2p19);                                     // -32 * 2^-24 * s
 #pragma unroll
       for (int t = 2 * sub; t < 2 * sub + 2; ++t) {
         uint32_t v[4];
         q6_pairs(word4(q[t], cc), cc < 2 ? high[t].x : high[t].y, cc % 2, v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) out[4 * t + i] = hmul2u(hfma2u(v[i], s, o), d);
+        for (int i = 0; i < 4; ++i) out[4 * t + i] = hfma2u(v[i], s, o);
       }
     }
   }
@@ -420,8 +428,11 @@ struct Tile {
 __device__ __forceinline__ int tiles_of(int count) { return (count + kTileN - 1) / kTileN; }
 
 // Tile t of the list ordered by (expert, item tile, band pair); start[e] is
-// the number of (expert, item tile)s before expert e.
-__device__ __forceinline__ Tile tile_at(const Args& a, const int* start, int t) {
+// the number of (expert, item tile)s before expert e. Nothing past the last tile.
+__device__ __forceinline__ Tile tile_at(const Args& a, const int* start, const int* offs, int t,
+                                        int total) {
+  Tile r = {};
+  if (t >= total) return r;
   const int pairs = (a.bands + 1) / 2;
   const int item_tile = t / pairs;
   int lo = 0, hi = a.E;  // start[lo] <= item_tile < start[hi]
@@ -430,9 +441,8 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* start, int t) 
     if (start[mid] <= item_tile) lo = mid;
     else hi = mid;
   }
-  Tile r;
   r.expert = lo, r.pair = t % pairs;
-  const int begin = a.offsets[lo], count = a.offsets[lo + 1] - begin;
+  const int begin = offs[lo], count = offs[lo + 1] - begin;
   const int parts = tiles_of(count), j = item_tile - start[lo];
   // equal parts, in steps of 32 (their last may hold less, but never nothing)
   r.n = ((count + parts - 1) / parts + 31) / 32 * 32;
@@ -476,7 +486,7 @@ __device__ __forceinline__ bool tile_mmas(MmaState& st, Bars* bars, const uint8_
       return false;
     tc_fence_after();
     if (elect_one()) {
-      const uint32_t b = x0 + slot * (kXStage >> 4);
+      const uint32_t b = x0 + st.unit % kXStages * (kXStage >> 4);
       // two A slots of a unit are neighbours, the first an even one
       const uint32_t at = tmem + (uint32_t)(kACol0 + st.a % kASlots * kACols);
 #pragma unroll
@@ -497,16 +507,16 @@ __device__ __forceinline__ bool tile_mmas(MmaState& st, Bars* bars, const uint8_
 template <typename T, int kFmt, bool kGlu>
 __global__ void __launch_bounds__(kThreads, 1)
 experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned int* status) {
-  constexpr int kWStages = kWStagesOf<kFmt>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* xring = smem;
-  uint8_t* wring = smem + kUnits * kXStage;
-  uint8_t* out_stage = wring + kWStages * kWTile<kFmt>;
+  uint8_t* wring = smem + kXStages * kXStage;
+  uint8_t* out_stage = wring + kWStages<kFmt> * kWTile<kFmt>;
   int* start = reinterpret_cast<int*>(out_stage + 8 * kOutWarp);
-  Bars* bars = reinterpret_cast<Bars*>(
-      (reinterpret_cast<uintptr_t>(start + kMaxGroups + 1) + 7) & ~static_cast<uintptr_t>(7));
+  int* offs = start + kMaxGroups + 1;  // a copy of the offsets
+  Bars* bars = reinterpret_cast<Bars*>(offs + kMaxGroups + 1);
+  static_assert(2 * (kMaxGroups + 1) * 4 % 8 == 0, "barriers are 8-byte aligned");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
   volatile int* abort_flag = &bars->abort;
@@ -516,9 +526,9 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
       mbar_init(&bars->ready[i], kReadyArrivals);  // used in CTA 0
       mbar_init(&bars->done[i], 1);
     }
-    for (int i = 0; i < kWStages; ++i) {
+    for (int i = 0; i < kWStages<kFmt>; ++i) {
       mbar_init(&bars->w_full[i], 1);
-      mbar_init(&bars->w_empty[i], 8);
+      mbar_init(&bars->w_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->d_full[i], 1);
@@ -532,13 +542,17 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
   if (warp == 2) {
     tmem_alloc_pair(&bars->tmem_base, kTmemCols);
   }
-  griddep_wait();
+  // The kernel before has passed its own wait once this one runs, so all before it
+  // is in memory: where it made nothing but the rows of x, only their readers wait.
+  if (!a.early) griddep_wait();
   griddep_launch_dependents();
+  for (int e = threadIdx.x; e <= a.E; e += kThreads) offs[e] = a.offsets[e];
+  __syncthreads();
   if (warp == 3) {  // start[]: the running number of (expert, item tile) pairs
     int run = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
-      const int v = e < a.E ? tiles_of(a.offsets[e + 1] - a.offsets[e]) : 0;
+      const int v = e < a.E ? tiles_of(offs[e + 1] - offs[e]) : 0;
       int x = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -556,29 +570,38 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   const int total = start[a.E] * ((a.bands + 1) / 2);
+  // Each role works out its next tile while it has one: between two tiles that
+  // would stand still for 1300 cycles.
+  Tile next = tile_at(a, start, offs, cluster, total);
+  auto take = [&](int t) {
+    const Tile w = next;
+    next = tile_at(a, start, offs, t + clusters, total);
+    return w;
+  };
   bool ok = true;
 
   constexpr bool kTwo = kPair<T, kGlu>;
   if (warp == 0) {
     // --------------------------------------------------------------- load x --
+    griddep_wait();
     int g = 0;  // units opened
     for (int t = cluster; t < total && ok; t += clusters) {
-      const Tile w = tile_at(a, start, t);
+      const Tile w = take(t);
       const int rows = w.n / 2;  // this CTA's
       const int box = box_of(w.n);
       const int shift = unit_shift<kTwo>(w.n);
       const int row0 = __shfl_sync(0xffffffffu, (int)w.first + rank * rows, 0);
       const int block = (16 << box) * 128;
       for (int k = 0; k < 4 * a.sbs; k += 1 << shift) {
-        const int slot = g % kUnits;
-        if (!(ok = mbar_wait_warp(&bars->done[slot], ((g / kUnits) & 1) ^ 1, abort_flag, status,
-                                  kSiteDone)))
+        const int slot = g % kUnits, last = g - kXStages;  // last: the unit before in this x stage
+        if (last >= 0 && !(ok = mbar_wait_warp(&bars->done[last % kUnits], (last / kUnits) & 1,
+                                               abort_flag, status, kSiteDone)))
           break;
         if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&bars->ready[slot], (uint32_t)(2 * block) << shift);
           for (int b = 0; b < 1 << shift; ++b)
-            tma_load_2d_pair(xring + slot * kXStage + b * block, &maps.box[box], &bars->ready[slot],
-                             (k + b) * 64, row0);
+            tma_load_2d_pair(xring + g % kXStages * kXStage + b * block, &maps.box[box],
+                             &bars->ready[slot], (k + b) * 64, row0);
         }
         __syncwarp();
         ++g;
@@ -596,14 +619,13 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
     }
   } else if (warp == 3) {
     // ------------------------------------------------------- packed weights --
-    int g = 0;
+    int slot = 0, round = 0, g = 0;  // g: stages filled
     for (int t = cluster; t < total && ok; t += clusters) {
-      const Tile w = tile_at(a, start, t);
+      const Tile w = take(t);
       const size_t band = (size_t)w.expert * a.bands + band_of(a, w.pair, rank);
       const uint8_t* src = a.plane + __shfl_sync(0xffffffffu, band, 0) * (size_t)a.sbs * kWTile<kFmt>;
       for (int sb = 0; sb < a.sbs; ++sb) {
-        const int slot = g % kWStages;
-        if (!(ok = mbar_wait_warp(&bars->w_empty[slot], ((g / kWStages) & 1) ^ 1, abort_flag, status,
+        if (!(ok = mbar_wait_warp(&bars->w_empty[slot], (round & 1) ^ 1, abort_flag, status,
                                   kSiteWEmpty)))
           break;
         if (elect_one()) {
@@ -613,22 +635,23 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
         __syncwarp();
         src += kWTile<kFmt>;
         ++g;
+        if (++slot == kWStages<kFmt>) slot = 0, ++round;
       }
     }
     if (!ok && lane == 0) {
       volatile int no_abort = 0;
-      for (int k = g > kWStages ? g - kWStages : 0; k < g; ++k)
-        mbar_wait_bounded(&bars->w_full[k % kWStages], (k / kWStages) & 1, &no_abort, status,
+      for (int k = g > kWStages<kFmt> ? g - kWStages<kFmt> : 0; k < g; ++k)
+        mbar_wait_bounded(&bars->w_full[k % kWStages<kFmt>], (k / kWStages<kFmt>) & 1, &no_abort, status,
                           kSiteWFull);
     }
   } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------------------------ MMA --
     // (Issued from one lane's own branch, 64 of K took 700 cycles.)
     MmaState st = {0, 0};
-    int next = 0, uses0 = 0, uses1 = 0;
+    int turn = 0, uses0 = 0, uses1 = 0;
     for (int t = cluster; t < total && ok; t += clusters) {
-      const int n = (int)__reduce_max_sync(0xffffffffu, (unsigned)tile_at(a, start, t).n);
-      const bool both = n > 128, first = both || next == 0, second = both || next == 1;
+      const int n = (int)__reduce_max_sync(0xffffffffu, (unsigned)take(t).n);
+      const bool both = n > 128, first = both || turn == 0, second = both || turn == 1;
       if (first)
         ok = mbar_wait_warp(&bars->d_empty[0], (uses0 & 1) ^ 1, abort_flag, status, kSiteDEmpty);
       if (second && ok)
@@ -646,7 +669,7 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
       }
       __syncwarp();
       uses0 += first, uses1 += second;
-      next = both ? 0 : next ^ 1;
+      turn = both ? 0 : turn ^ 1;
     }
     if (elect_one()) {
       commit_own(&bars->drain);
@@ -656,53 +679,66 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
     __syncwarp();
   } else if (warp >= 4 && warp < 12) {
     // ----------------------------------------------------------- dequantise --
-    const int h = (warp - 4) / 4, row = 32 * (warp % 4) + lane;
+    const int me = (warp - 4) / 4, row = 32 * (warp % 4) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
-    int gw = 0, unit = 0;
-    int last1 = -1, last2 = -1;  // units of this warp's last two halves, in this and the other slot
+    int ws = me, round = 0;  // stage of this group's next super-block
+    int gw = 0, unit = 0;  // super-blocks and units of both groups so far
+    int last1 = -1, last2 = -1;  // units of this warp's last two halves
+    auto scale_of = [&](const Tile& w) {
+      return a.scale[((size_t)w.expert * a.bands + band_of(a, w.pair, rank)) * kBand + row];
+    };
+    float scale = total > cluster ? scale_of(next) : 1.0f;
     for (int t = cluster; t < total && ok; t += clusters) {
-      const Tile w = tile_at(a, start, t);
+      const Tile w = take(t);
       const bool split = unit_shift<kTwo>(w.n) == 1;  // a unit for each half
-      const float inv = 1.0f / a.scale[((size_t)w.expert * a.bands + band_of(a, w.pair, rank)) * kBand + row];
-      for (int sb = 0; sb < a.sbs; ++sb, ++gw) {
-        const int ws = gw % kWStages;
-        // in pairs, each half super-block has the same two slots again
-        const int as = kTwo ? 2 * h : (2 * gw + h) % kASlots, last = kTwo ? last1 : last2;
-        const int mine = split ? unit + h : unit;
-        unit += split ? 2 : 1;
-        if (!(ok = mbar_wait_warp(&bars->w_full[ws], (gw / kWStages) & 1, abort_flag, status,
+      const float inv = 1.0f / scale;
+      if (t + clusters < total) scale = scale_of(next);
+      for (int sb = 0; sb < a.sbs && ok; ++sb, ++gw, unit += split ? 2 : 1) {
+        if ((gw & 1) != me) continue;
+        if (!(ok = mbar_wait_warp(&bars->w_full[ws], round & 1, abort_flag, status,
                                   kSiteWFull)))
           break;
-        Half<kFmt> half;
-        half.load(wring + ws * kWTile<kFmt>, row, h, inv);
-        // The slot's last unit is at most kUnits back, so its barrier has not
-        // gone further.
-        if (last >= 0 && !(ok = mbar_wait_warp(&bars->done[last % kUnits], (last / kUnits) & 1,
-                                               abort_flag, status, kSiteDone)))
-          break;
-        last2 = last1, last1 = mine;
-        tc_fence_after();
-        const uint32_t dst = tmem + lanes + (uint32_t)(kACol0 + as * kACols);
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t v[16];
-          if constexpr (kTwo) {
-            uint32_t rest[16];
-            half.expand_pair(cc, v, rest);
-            tmem_st16(dst + kACols + 16 * cc, rest);
-          } else if constexpr (__is_same(T, __half)) {
-            half.expand_once(cc, v);
-          } else {
-            half.expand(cc, v);
+        for (int h = 0; h < 2; ++h) {
+          Half<kFmt> half;
+          half.load(wring + ws * kWTile<kFmt>, row, h, inv);
+          const int mine = split ? unit + h : unit;
+          // in pairs, the same half of each super-block has the same two slots
+          const int as = kTwo ? 2 * h : 2 * me + h, last = kTwo ? mine - 2 : last2;
+          // The slot's last unit is at most kUnits back, so its barrier has not
+          // gone further.
+          if (last >= 0 && !(ok = mbar_wait_warp(&bars->done[last % kUnits], (last / kUnits) & 1,
+                                                 abort_flag, status, kSiteDone)))
+            break;
+          last2 = last1, last1 = mine;
+          tc_fence_after();
+          const uint32_t dst = tmem + lanes + (uint32_t)(kACol0 + as * kACols);
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t v[16];
+            if constexpr (kTwo) {
+              uint32_t rest[16];
+              half.expand_pair(cc, v, rest);
+              tmem_st16(dst + kACols + 16 * cc, rest);
+            } else if constexpr (__is_same(T, __half)) {
+              half.expand_once(cc, v);
+            } else {
+              half.expand(cc, v);
+            }
+            tmem_st16(dst + 16 * cc, v);
           }
-          tmem_st16(dst + 16 * cc, v);
+          if (h == 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->w_empty[ws]);
+            if ((ws += 2) >= kWStages<kFmt>) ws -= kWStages<kFmt>, ++round;
+          }
+          if (h == 1 || split) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_leader_tmem(&bars->ready[mine % kUnits]);
+          }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->w_empty[ws]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_leader_tmem(&bars->ready[mine % kUnits], split ? 2 : 1);
       }
     }
   } else if (warp >= 12) {
@@ -711,26 +747,28 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
     // r of its 32 and items 8 j + 2 c, + 1: pairs of items go to shared memory
     // transposed, [item][row], and from there to Y in 16-byte pieces.
     const int q = warp % 4, me = (warp - 12) / 4;   // me: the accumulator half
+    griddep_wait();
     T* Y = static_cast<T*>(a.Y);
     constexpr int kCols = kGlu ? 16 : 32;          // output features of a warp
     constexpr int kPieces = kCols / 8;              // 16-byte units of an item
     constexpr bool kScaled = !__is_same(T, __half);
+    constexpr float kUp = kScaled ? 32768.0f : 1.0f;
     uint8_t* stage = out_stage + (warp - 12) * kOutWarp;
     // items of no expert: zeros
     for (long long i = a.offsets[a.E] + (long long)blockIdx.x; i < a.offsets[a.E + 1];
          i += gridDim.x)
       for (int m = 128 * me + 32 * q + lane; m < a.out; m += 256)
         Y[i * a.ldy + m] = from_f32<T>(0.0f);
-    int next = 0, uses = 0;
+    int turn = 0, uses = 0;
     for (int t = cluster; t < total && ok; t += clusters) {
-      const Tile w = tile_at(a, start, t);
-      const bool both = w.n > 128, here = both || next == me;
-      next = both ? 0 : next ^ 1;
+      const Tile w = take(t);
+      const bool both = w.n > 128, here = both || turn == me;
+      turn = both ? 0 : turn ^ 1;
       if (!here) continue;
       const int band = band_of(a, w.pair, rank);
       const bool mine = 2 * w.pair + rank < a.bands;
       const float* sc = a.scale + ((size_t)w.expert * a.bands + band) * kBand + 32 * q + (lane >> 2);
-      const float scale[4] = {sc[0], sc[8], sc[16], sc[24]};
+      const float scale[4] = {sc[0] * kUp, sc[8] * kUp, sc[16] * kUp, sc[24] * kUp};
       const int m0 = (band * 4 + q) * kCols;       // this warp's first output feature
       const int item0 = both ? 128 * me : 0;
       const int cols = min(128, w.n - item0), count = mine ? w.count - item0 : 0;
@@ -839,7 +877,8 @@ Kernel pick(int type, int fmt, int swiglu) {
 int smem_bytes(int fmt) {
   return fmt == Q6_FMT_Q4K ? kSmemBytes<Q6_FMT_Q4K> : kSmemBytes<Q6_FMT_Q6K>;
 }
-static_assert(kSmemBytes<Q6_FMT_Q6K> <= 227 * 1024, "shared memory");
+static_assert(kSmemBytes<Q6_FMT_Q4K> <= 227 * 1024 && kSmemBytes<Q6_FMT_Q6K> <= 227 * 1024,
+              "shared memory");
 
 // Fills a launch of `pairs` CTA pairs; attr holds two attributes.
 void pair_launch(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int fmt, unsigned pairs,
@@ -889,7 +928,7 @@ cudaError_t experts_tc_prepare() {
 }
 
 cudaError_t launch_experts_tc(const ExpertCall& c, const RowMaps& x, const float* scale,
-                              unsigned int* status, cudaStream_t s) {
+                              bool x_made, unsigned int* status, cudaStream_t s) {
   Args a;
   a.plane = c.plane;
   a.scale = reinterpret_cast<const float*>(c.plane + c.g.scale_off);
@@ -898,6 +937,7 @@ cudaError_t launch_experts_tc(const ExpertCall& c, const RowMaps& x, const float
   a.Y = c.Y, a.ldy = c.ldy;
   a.E = c.E, a.bands = c.g.bands, a.sbs = c.g.sbs, a.out = c.g.out;
   a.vec = (reinterpret_cast<uintptr_t>(c.Y) | (uintptr_t)(c.ldy * 2)) % 16 == 0;
+  a.early = x_made;
   // at most this many tiles
   const long long tiles =
       (c.items / kTileN + (c.items < c.E ? c.items : c.E) + 1) * (long long)((c.g.bands + 1) / 2);

@@ -57,12 +57,12 @@ int check_experts(int fmt, int E, int M, int K, int swiglu) {
   return Q6_OK;
 }
 
-// Items an expert, on average, up to which the few-token kernel runs. Measured,
-// few-token kernel / tensor cores, q4_K, 64 experts of 1536 x 2048: 30.8 / 32.9 us
-// at 2, 47.0 / 35.2 us at 4, 148 / 42.5 us at 16; 8 experts of 4096 x 4096: 24.6 /
-// 31.7, 33.6 / 32.4 and 79.9 / 32.4 us; q6_K crosses at the same place.
-constexpr int kFewItems = 3;
-bool on_tensor_cores(int64_t items, int E) { return items > kFewItems * (int64_t)E; }
+// The few-token kernel runs up to one item an expert on average. Measured, few-token
+// kernel / tensor cores in us, with 0.5, 1, 2 and 4 items an expert: q4_K, 64 experts
+// of 1536 x 2048 13.7 / 17.2, 24.3 / 23.2, 30.5 / 27.0, 46.3 / 29.3; 8 of 4096 x 4096
+// 13.6 / 15.8, 22.5 / 22.7, 24.6 / 25.9, 33.4 / 25.9; q6_K, 32 of 2056 x 1536
+// 14.8 / 14.2, 18.8 / 18.8, 26.1 / 22.4, 34.2 / 25.7.
+bool on_tensor_cores(int64_t items, int E) { return items > E; }
 // Bytes of the binary16 rows in item order that the tensor-core path makes (0:
 // it reads X itself), and where their scales follow.
 size_t rows_bytes(int64_t items, int K) { return q6::round_up((size_t)items * (size_t)K * 2, 256); }
@@ -193,8 +193,9 @@ int q6_experts_mmq(int fmt, const void* plane, int E, int M, int K, int swiglu, 
                                "expert rows")))
       return rc;
     if (path_out) *path_out = Q6_PATH_EXPERTS_TC;
-    return launched(q6::launch_experts_tc(c, maps, scale, status, (cudaStream_t)s),
-                    "grouped product");
+    return launched(
+        q6::launch_experts_tc(c, maps, scale, need > 0, status, (cudaStream_t)s),
+        "grouped product");
   }
   if (path_out) *path_out = Q6_PATH_EXPERTS_FEW;
   return launched(q6::launch_experts_few(c, (cudaStream_t)s), "grouped product");

@@ -186,9 +186,10 @@ struct RowMaps {
 };
 int encode_row_maps(RowMaps* maps, const void* X, long long n, int K, long long ld);
 // x: the items' rows as binary16 in order, scale (nullable): f32 [items], what
-// each is multiplied with. c.X, c.gather and c.rows are not used.
+// each is multiplied with; x_made: launch_expert_rows has just made them on s.
+// c.X, c.gather and c.rows are not used.
 cudaError_t launch_experts_tc(const ExpertCall& c, const RowMaps& x, const float* scale,
-                              unsigned int* status, cudaStream_t s);
+                              bool x_made, unsigned int* status, cudaStream_t s);
 // The items' rows of X as binary16 in item order: xh [items][K], and for bf16
 // (scaled by a power of two of the row) scale [items], that power.
 cudaError_t launch_expert_rows(const ExpertCall& c, int K, __half* xh, float* scale,

@@ -143,6 +143,34 @@ def test_experts_group_sizes(rng, fmt, counts):
     run_experts(rng, fmt, "bf16", rng.permutation(ids)[:, None], len(counts), 144, 512, False, True)
 
 
+@pytest.mark.parametrize("fmt", ["q4_K", "q6_K"])
+@pytest.mark.parametrize("type", ["bf16", "f16"])
+@pytest.mark.parametrize("M,K,swiglu,gather", [(130, 512, True, True), (129, 768, False, False)])
+def test_experts_few_but_crowded(rng, fmt, type, M, K, swiglu, gather):
+    """No more items than experts, but in a few of them: 1, 7, 8, 9, 17 and none."""
+    E = 45
+    counts = np.zeros(E, int)
+    counts[[0, 3, 4, 20, 44]] = 1, 9, 7, 17, 8
+    ids = np.concatenate([np.repeat(np.arange(E), counts), np.full(3, -1)])
+    path = run_experts(rng, fmt, type, rng.permutation(ids)[:, None], E, M, K, swiglu, gather)
+    assert path == "experts_few"
+
+
+@pytest.mark.parametrize("fmt", ["q4_K", "q6_K"])
+def test_experts_few_nonfinite_token_stays_alone(rng, fmt):
+    raw = raw_experts(4, fmt, 16, 40, 512)
+    w = q6.pack_experts(cuda(raw), fmt, 16, 40, 512)
+    g = q6.group_rows(cuda(np.full((12, 1), 9, np.int32)), 16)
+    X = cuda(rng.standard_normal((12, 512)), "bf16")
+    good = q6.experts_mmq(w, X, g)[0].clone()
+    X[1, 7], X[10, 300] = float("inf"), float("nan")
+    Y, path = q6.experts_mmq(w, X, g)
+    assert path == "experts_few"
+    assert not torch.isfinite(Y[1]).any() and torch.isnan(Y[10]).all()
+    rest = [n for n in range(12) if n not in (1, 10)]
+    assert torch.equal(Y[rest], good[rest])
+
+
 @pytest.mark.parametrize("fmt,K", [("q4_K", 18944), ("q6_K", 11008)])
 def test_experts_long_k(rng, fmt, K):
     run_experts(rng, fmt, "bf16", rng.integers(0, 2, (21, 1)), 2, 48, K, False, True)

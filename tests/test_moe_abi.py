@@ -55,10 +55,10 @@ def test_workspaces(lib):
     assert q6.group_workspace_bytes(100000, 8, 7) == 128 * 8 * 4
     bf16, f16 = 1, 2
     # few items: X is read as it is; many: binary16 rows, and bf16's scales
-    assert moe.experts_workspace_bytes(8, 512, bf16, 24, True) == 0
-    assert moe.experts_workspace_bytes(8, 512, bf16, 25, False) == -(-25 * 1024 // 256) * 256 + 25 * 4
-    assert moe.experts_workspace_bytes(8, 512, f16, 25, False) == 0
-    assert moe.experts_workspace_bytes(8, 512, f16, 25, True) == -(-25 * 1024 // 256) * 256
+    assert moe.experts_workspace_bytes(8, 512, bf16, 8, True) == 0
+    assert moe.experts_workspace_bytes(8, 512, bf16, 9, False) == -(-9 * 1024 // 256) * 256 + 9 * 4
+    assert moe.experts_workspace_bytes(8, 512, f16, 9, False) == 0
+    assert moe.experts_workspace_bytes(8, 512, f16, 9, True) == -(-9 * 1024 // 256) * 256
     assert q6.lora_workspace_bytes(80, 10, 16, 4096) == 0
     assert q6.lora_workspace_bytes(81, 10, 16, 4096) % (81 * 16 * 4) == 0
     assert q6.lora_workspace_bytes(81, 10, 16, 4096) > 0
