@@ -698,7 +698,8 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
         if (!(ok = mbar_wait_warp(&bars->w_full[ws], round & 1, abort_flag, status,
                                   kSiteWFull)))
           break;
-#pragma unroll
+// (binary16's longer code: 47.3 us rolled up, 48.0 us unrolled, 37.7 GFLOP)
+#pragma unroll (__is_same(T, __half) ? 1 : 2)
         for (int h = 0; h < 2; ++h) {
           Half<kFmt> half;
           half.load(wring + ws * kWTile<kFmt>, row, h, inv);

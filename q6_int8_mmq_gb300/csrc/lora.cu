@@ -763,9 +763,15 @@ template <typename TW, int JV>
 cudaError_t expand_v(const LoraCall& c, bool vec, cudaStream_t s) {
   const long long tiles = most_tiles(c.items, c.L, kExpandRows);
   const int warps = expand_warps<TW>(c.r), width = kColsWarp * warps;
-  // column parts: about two CTAs an SM (as run at a time), whole blocks each
+  // Column parts, whole blocks each: about two CTAs an SM, as run at a time, or twice
+  // that where T, which each CTA makes its factors of anew, is small. (Two against four
+  // an SM, us: 3314 tokens, 6 adapters, M 11008, bf16 of rank 64, 82.8 to 100.3 by how
+  // they fall against 87 to 88; 512 tokens, 4, M 4096, rank 16 10.7 / 8.8; f16 of rank
+  // 64, 1000, 8, M 4096 27.2 / 30.1; bf16 of rank 128, 2048, 1, M 4096 53.0 / 58.8.)
   const int blocks = (c.M + width - 1) / width;
-  long long parts = (2 * 152 + tiles - 1) / tiles;
+  const int t_bytes = (kThreeParts<TW> ? 3 : 2) * kExpandRows * t_pitch<TW>(c.r);
+  const int an_sm = t_bytes <= 16 * 1024 ? 4 : 2;
+  long long parts = (an_sm * 152 + tiles - 1) / tiles;
   if (parts > blocks) parts = blocks;
   const int part_cols = (int)((blocks + parts - 1) / parts) * width;
   const dim3 grid((unsigned)tiles, (unsigned)((c.M + part_cols - 1) / part_cols));
