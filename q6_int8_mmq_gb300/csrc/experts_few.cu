@@ -21,8 +21,12 @@
 // A CTA is 8 warps on R blocks of 16 rows times 8/R parts of K; the parts are
 // added through shared memory in a fixed order.
 //
-// Bound: weight bytes (0.5625 / 0.82 a weight); the instruction issue is
-// close behind (about 260 instructions per 16 x 256 weights at 8 tokens).
+// Bound: the latencies of a CTA's walk (its loads, then the sums of its parts) with
+// few tiles, instruction issue with many (about 260 instructions per 16 x 256
+// weights at 8 tokens; issue 46 % and DRAM 29 % busy at 8 experts of 4096 x 4096),
+// before the weight bytes (0.5625 / 0.82 a weight). One token, 8 of 64 q4_K experts
+// of 1536 x 2048 with swiglu, 14.2 MB: 8.2 us out of a graph. Persistent CTAs on
+// runs of rows, and three CTAs an SM, spilled and were not faster.
 #include "moe_internal.cuh"
 
 namespace q6 {

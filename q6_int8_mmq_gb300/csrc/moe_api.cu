@@ -173,7 +173,7 @@ int q6_experts_mmq(int fmt, const void* plane, int E, int M, int K, int swiglu, 
   if ((rc = q6::require_device(&status))) return rc;
   c.fmt = fmt, c.swiglu = swiglu, c.E = E;
   c.plane = static_cast<const uint8_t*>(plane);
-  c.X = X, c.type = type, c.ldx = ldx, c.nx = nx, c.gather = gather;
+  c.X = X, c.type = type, c.ldx = ldx, c.gather = gather;
   c.offsets = offsets, c.rows = rows, c.items = items;
   c.Y = Y, c.ldy = ldy;
   if (on_tensor_cores(items, E)) {

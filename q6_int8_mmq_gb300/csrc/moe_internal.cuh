@@ -167,7 +167,7 @@ struct ExpertCall {
   const uint8_t* plane;
   const void* X;
   int type;           // of X and Y
-  long long ldx, nx;  // X rows
+  long long ldx;      // of X rows
   int gather;         // X row of item i: rows[i], else i
   const int32_t* offsets;
   const int32_t* rows;

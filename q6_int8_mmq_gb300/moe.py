@@ -31,11 +31,11 @@ def _types():
 
 
 def _type(t, name, half=False):
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise Q6Error(Q6_EINVAL, f"{name} must be a torch tensor")
-    code = _types().get(t.dtype)
+    code = _types().get(getattr(t, "dtype", None))
     if code is None or (half and code == 0):
+        import torch
+        if not isinstance(t, torch.Tensor):
+            raise Q6Error(Q6_EINVAL, f"{name} must be a torch tensor")
         raise Q6Error(Q6_EINVAL, f"{name} must be {'' if half else 'float32, '}bfloat16 or "
                                  f"float16, not {t.dtype}")
     return code
@@ -52,38 +52,71 @@ def _rows2d(t, name, width=None):
 def _stream(stream, device):
     """The raw handle of the stream a call runs on: `stream`, or the current
     one of the tensors' device, which has to be the current device."""
-    import torch
-    if torch.cuda.current_device() != device.index:
+    current_device, current_stream = _current()
+    index = device.index
+    if current_device() != index:
         raise Q6Error(Q6_EINVAL, f"the tensors are on {device}, the current device is "
-                                 f"cuda:{torch.cuda.current_device()}")
-    if stream is not None:
-        return stream.cuda_stream
-    return _current_stream()(device.index)
+                                 f"cuda:{current_device()}")
+    return current_stream(index) if stream is None else stream.cuda_stream
 
 
 @functools.lru_cache(maxsize=None)
-def _current_stream():
-    """device index -> the current stream's raw handle (without a stream
-    object, where this PyTorch can)."""
+def _current():
+    """() -> the current device's index, and device index -> the current
+    stream's raw handle (the direct calls, where this PyTorch has them; a call
+    has a CUDA tensor, so CUDA is initialised)."""
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return (getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device,
+            getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            or (lambda index: torch.cuda.current_stream(index).cuda_stream))
 
 
-def _plain(t, dtype, shape, device):
-    """Whether t is a contiguous tensor of this dtype and shape on this device:
-    what _tensor() accepts, decided quickly. Anything else goes to _tensor()."""
+def _rows(t, name, dtype, shape, device):
+    """Checks a 2-D view of rows as _tensor() does and returns its row stride.
+    A contiguous tensor of this dtype and shape on this device, what callers
+    mostly have, is recognised quickly."""
     try:
-        return (t.dtype is dtype and t.shape == shape and t.is_contiguous()
-                and t.device == device)
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device
+                and device.type == "cuda"):
+            return max(shape[1], 1)
     except AttributeError:
-        return False
+        pass
+    return _row_stride(_tensor(t, name, dtype, shape, device, rows=True))
+
+
+def _whole(t, name, dtype, shape, device):
+    """The same for a tensor that has to be contiguous."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+            return
+    except AttributeError:
+        pass
+    _tensor(t, name, dtype, shape, device)
 
 
 def _on(stream):
     """Scratch and outputs are allocated on the stream the call runs on."""
     import torch
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(nbytes, device, stream):
+    import torch
+    return _empty(nbytes, torch.uint8, device, stream)
+
+
+@functools.lru_cache(maxsize=None)
+def _f32_i32():
+    import torch
+    return torch.float32, torch.int32
 
 
 # ---------------------------------------------------------------- grouping ---
@@ -151,7 +184,8 @@ def group_rows(ids, n_groups: int, out: Groups | None = None, stream=None) -> Gr
         raise Q6Error(Q6_EINVAL, "out holds another grouping than ids and n_groups ask for")
     ws = out.workspace
     _check(load().q6_group_rows(ids.data_ptr(), N, per_row, n_groups, out.offsets.data_ptr(),
-                                out.rows.data_ptr(), out.pos.data_ptr(), _ptr(ws),
+                                out.rows.data_ptr(), out.pos.data_ptr(),
+                                None if ws is None else ws.data_ptr(),
                                 0 if ws is None else ws.numel(), _stream(stream, ids.device)))
     return out
 
@@ -191,20 +225,21 @@ def moe_route(logits, topk: int, renormalize: bool = True, out: Route | None = N
     code = _type(logits, "logits")
     N = _rows2d(logits, "logits")
     E = logits.shape[1]
-    _tensor(logits, "logits", logits.dtype, (N, E), rows=True)
+    dev = logits.device
+    ldl = _rows(logits, "logits", logits.dtype, (N, E), dev)
     if out is None:
         with _on(stream):
-            out = alloc_route(N, E, topk, logits.device)
+            out = alloc_route(N, E, topk, dev)
     g = out.groups
-    if (g.N, g.per_row, g.n_groups, g.device) != (N, topk, E, logits.device):
+    if g.N != N or g.per_row != topk or g.n_groups != E or g.device != dev:
         raise Q6Error(Q6_EINVAL, f"out holds {g.N} x {g.per_row} of {g.n_groups} experts on "
-                                 f"{g.device}, not {N} x {topk} of {E} on {logits.device}")
+                                 f"{g.device}, not {N} x {topk} of {E} on {dev}")
     ws = g.workspace
-    _check(load().q6_moe_route(logits.data_ptr(), code, N, E, _row_stride(logits), topk,
-                               int(bool(renormalize)), out.ids.data_ptr(), out.weights.data_ptr(),
-                               g.offsets.data_ptr(), g.rows.data_ptr(), g.pos.data_ptr(),
-                               _ptr(ws), 0 if ws is None else ws.numel(),
-                               _stream(stream, logits.device)))
+    _check(load().q6_moe_route(logits.data_ptr(), code, N, E, ldl, topk,
+                               1 if renormalize else 0, out.ids.data_ptr(),
+                               out.weights.data_ptr(), g.offsets.data_ptr(), g.rows.data_ptr(),
+                               g.pos.data_ptr(), None if ws is None else ws.data_ptr(),
+                               0 if ws is None else ws.numel(), _stream(stream, dev)))
     return out
 
 
@@ -289,12 +324,11 @@ def experts_mmq(w: ExpertWeights, X, groups: Groups, gather: bool = True, out=No
     weights. X is bf16 or f16 (rows 16-byte aligned), the result the same.
     Items of no expert get zeros. Returns (Y [items, out_features], path
     name)."""
-    import torch
     code = _type(X, "X", half=True)
-    nx = _rows2d(X, "X", w.K)
-    dev, items = w.device, groups.items
-    if not _plain(X, X.dtype, (nx, w.K), dev):
-        _tensor(X, "X", X.dtype, (nx, w.K), dev, rows=True)
+    K = w.K
+    nx = _rows2d(X, "X", K)
+    dev, items, dtype = w.plane.device, groups.items, X.dtype
+    ldx = _rows(X, "X", dtype, (nx, K), dev)
     if groups.n_groups != w.E or groups.device != dev:
         raise Q6Error(Q6_EINVAL, f"a grouping of {groups.n_groups} groups on {groups.device} for "
                                  f"{w.E} experts on {dev}")
@@ -303,19 +337,16 @@ def experts_mmq(w: ExpertWeights, X, groups: Groups, gather: bool = True, out=No
                                  "items")
     shape = (items, w.out_features)
     if out is None:
-        with _on(stream):
-            out = torch.empty(shape, dtype=X.dtype, device=dev)
-    elif not _plain(out, X.dtype, shape, dev):
-        _tensor(out, "out", X.dtype, shape, dev, rows=True)
-    need, ws = experts_workspace_bytes(w.E, w.K, code, items, bool(gather)), None
+        out = _empty(shape, dtype, dev, stream)
+    ldy = _rows(out, "out", dtype, shape, dev)
+    need, ws = experts_workspace_bytes(w.E, K, code, items, bool(gather)), None
     if need:
-        with _on(stream):
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = _scratch(need, dev, stream)
     path = ctypes.c_int(-1)
-    _check(load().q6_experts_mmq(FORMATS[w.fmt], w.plane.data_ptr(), w.E, w.M, w.K, int(w.swiglu),
-                                 X.data_ptr(), code, nx, _row_stride(X), int(bool(gather)),
+    _check(load().q6_experts_mmq(FORMATS[w.fmt], w.plane.data_ptr(), w.E, w.M, K,
+                                 1 if w.swiglu else 0, X.data_ptr(), code, nx, ldx, 1 if gather else 0,
                                  groups.offsets.data_ptr(), groups.rows.data_ptr(), items,
-                                 out.data_ptr(), _row_stride(out), _ptr(ws), need,
+                                 out.data_ptr(), ldy, None if ws is None else ws.data_ptr(), need,
                                  ctypes.byref(path), _stream(stream, dev)))
     return out, PATH_NAMES.get(path.value, str(path.value))
 
@@ -324,29 +355,23 @@ def moe_combine(Y, pos, weights, shared=None, out=None, stream=None):
     """out [N, M] = shared + the weighted sum of each token's rows of Y
     [items, M] (bf16 or f16): pos [N, topk] int32 are their places (-1 adds
     nothing), weights [N, topk] f32, shared f32 [N, M] or None."""
-    import torch
+    f32, i32 = _f32_i32()
     code = _type(Y, "Y", half=True)
     items = _rows2d(Y, "Y")
-    dev, M = Y.device, Y.shape[1]
-    _tensor(Y, "Y", Y.dtype, (items, M), rows=True)
-    if not isinstance(pos, torch.Tensor) or pos.dim() != 2:
-        raise Q6Error(Q6_EINVAL, "pos must be a 2-D torch tensor [N, topk]")
-    N, topk = pos.shape
-    if not _plain(pos, torch.int32, (N, topk), dev):
-        _tensor(pos, "pos", torch.int32, (N, topk), dev)
-    if not _plain(weights, torch.float32, (N, topk), dev):
-        _tensor(weights, "weights", torch.float32, (N, topk), dev)
-    if shared is not None and not _plain(shared, torch.float32, (N, M), dev):
-        _tensor(shared, "shared", torch.float32, (N, M), dev, rows=True)
+    dev, dtype, M = Y.device, Y.dtype, Y.shape[1]
+    ldy = _rows(Y, "Y", dtype, (items, M), dev)
+    if getattr(pos, "dtype", None) is not i32 or pos.dim() != 2:
+        raise Q6Error(Q6_EINVAL, "pos must be a 2-D int32 torch tensor [N, topk]")
+    slots = N, topk = pos.shape
+    _whole(pos, "pos", i32, slots, dev)
+    _whole(weights, "weights", f32, slots, dev)
+    lds = 0 if shared is None else _rows(shared, "shared", f32, (N, M), dev)
     if out is None:
-        with _on(stream):
-            out = torch.empty((N, M), dtype=Y.dtype, device=dev)
-    elif not _plain(out, Y.dtype, (N, M), dev):
-        _tensor(out, "out", Y.dtype, (N, M), dev, rows=True)
-    _check(load().q6_moe_combine(Y.data_ptr(), code, _row_stride(Y), pos.data_ptr(),
-                                 weights.data_ptr(), N, topk, M, _ptr(shared),
-                                 0 if shared is None else _row_stride(shared), out.data_ptr(),
-                                 _row_stride(out), _stream(stream, dev)))
+        out = _empty((N, M), dtype, dev, stream)
+    ldo = _rows(out, "out", dtype, (N, M), dev)
+    _check(load().q6_moe_combine(Y.data_ptr(), code, ldy, pos.data_ptr(), weights.data_ptr(), N,
+                                 topk, M, None if shared is None else shared.data_ptr(), lds,
+                                 out.data_ptr(), ldo, _stream(stream, dev)))
     return out
 
 
@@ -389,28 +414,24 @@ def lora_add(adapters: LoraAdapters, X, groups: Groups, Y, out=None, stream=None
     (groups: the tokens grouped by adapter, one id a token); tokens of no
     adapter keep Y. X [N, K] is f32, bf16 or f16 (rows 16-byte aligned), Y and
     out are f32; without out the result goes into Y. Returns out."""
-    import torch
-    A = adapters.A
+    A, B, f32 = adapters.A, adapters.B, _f32_i32()[0]
     L, r, K = A.shape
-    M, dev, N = adapters.B.shape[1], A.device, groups.items
+    M, dev, N = B.shape[1], A.device, groups.items
     code = _type(X, "X")
-    if not _plain(X, X.dtype, (N, K), dev):
-        _tensor(X, "X", X.dtype, (N, K), dev, rows=True)
+    ldx = _rows(X, "X", X.dtype, (N, K), dev)
     if groups.n_groups != L or groups.per_row != 1 or groups.device != dev:
         raise Q6Error(Q6_EINVAL, f"adapters need one id a token in {L} groups on {dev}")
-    if not _plain(Y, torch.float32, (N, M), dev):
-        _tensor(Y, "Y", torch.float32, (N, M), dev, rows=True)
+    ldy = ldo = _rows(Y, "Y", f32, (N, M), dev)
     if out is None:
         out = Y
-    elif not _plain(out, torch.float32, (N, M), dev):
-        _tensor(out, "out", torch.float32, (N, M), dev, rows=True)
+    else:
+        ldo = _rows(out, "out", f32, (N, M), dev)
     need, ws = lora_workspace_bytes(N, L, r, K), None
     if need:
-        with _on(stream):
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(load().q6_lora_add(A.data_ptr(), adapters.B.data_ptr(), adapters.scale.data_ptr(),
-                              _types()[A.dtype], L, r, M, K, X.data_ptr(), code, _row_stride(X),
+        ws = _scratch(need, dev, stream)
+    _check(load().q6_lora_add(A.data_ptr(), B.data_ptr(), adapters.scale.data_ptr(),
+                              _types()[A.dtype], L, r, M, K, X.data_ptr(), code, ldx,
                               groups.offsets.data_ptr(), groups.rows.data_ptr(), N, Y.data_ptr(),
-                              _row_stride(Y), out.data_ptr(), _row_stride(out), _ptr(ws),
+                              ldy, out.data_ptr(), ldo, None if ws is None else ws.data_ptr(),
                               need, _stream(stream, dev)))
     return out
