@@ -18,8 +18,9 @@ int readable_raw(const uint8_t* raw, const uint8_t** src);
 // ------------------------------------------------------- routing, grouping ---
 constexpr int kMaxGroups = Q6_MAX_GROUPS;
 // Blocks that share one grouping: each owns a contiguous range of rows. One
-// block up to kGroupSingle items.
-constexpr int kGroupBlocks = 128;
+// block up to kGroupSingle items, else up to one an SM (8191 tokens to 8 of 256
+// experts 16.1 us, with 128 blocks 17.2).
+constexpr int kGroupBlocks = 152;
 constexpr int kGroupSingle = 512;
 inline int group_blocks(long long items, int N) {
   if (items <= kGroupSingle || N <= 1) return 1;
