@@ -83,14 +83,17 @@ expert_pack_kernel(const uint8_t* raw, int M, int swiglu, int bands, int sbs, ui
   }
 }
 
-// 2^e of each plane row, from an upper bound of its weights' size.
+// 2^e of each plane row, from an upper bound of its weights' size; negative for 32
+// rows of which one has a super-block whose bound is below kWideRange of the row's
+// (and not 0).
+constexpr float kWideRange = 1.0f / 128.0f;
 template <int kRaw>
 __global__ void __launch_bounds__(kBand)
 expert_scale_kernel(const uint8_t* plane, int sbs, float* scale) {
   constexpr int kTile = kRaw == kQ4Raw ? kQ4Tile : kQ6Tile;
   const size_t band = blockIdx.x;
   const int row = threadIdx.x;
-  float most = 0.0f;
+  float most = 0.0f, least = INFINITY;
   for (int sb = 0; sb < sbs; ++sb) {
     const uint8_t* t = plane + (band * sbs + sb) * kTile;
     float v;
@@ -101,9 +104,13 @@ expert_scale_kernel(const uint8_t* plane, int sbs, float* scale) {
       v = 128.0f * 32.0f *
           fabsf(__half2float(reinterpret_cast<const __half*>(t + 13 * 2048)[row]));
     }
-    if (v > most && v < 1e30f) most = v;  // an infinite or NaN scale shows whatever e is
+    if (!(v < 1e30f)) continue;  // an infinite or NaN scale shows whatever e is
+    most = fmaxf(most, v);
+    if (v > 0.0f) least = fminf(least, v);
   }
-  scale[band * kBand + row] = most > 0.0f ? ldexpf(1.0f, ilogbf(most) + 1 - 10) : 1.0f;
+  const float s = most > 0.0f ? ldexpf(1.0f, ilogbf(most) + 1 - 10) : 1.0f;
+  const bool wide = __any_sync(0xffffffffu, least < most * kWideRange);
+  scale[band * kBand + row] = wide ? -s : s;
 }
 
 template <int kRaw>

@@ -17,10 +17,12 @@
 // fused multiply-add of it with sc * d and -dmin * m, all times a power of two of
 // the row (the largest possible weight of a row just below 2^-5): what is rounded
 // to 11 bits is sc * d, dmin * m and the weight, each an eighth of the rounding of
-// a bf16 Y. (Rates, cycles a warp instruction of one scheduler: binary16 pairs 2,
-// integer logic and shifts 2, on two pipes; f32 1. With sc * q exact and d
-// multiplied in after that, 2.7 instead of 2 instructions a pair, 8 experts of
-// 4096 x 4096 took 28.8 instead of 27.0 us.) For a binary16 Y that would
+// a bf16 Y. That leaves binary16 2^9 of range above its smallest normal number, so
+// 32 rows of which one has super-blocks whose weights are less than 2^-7 of its
+// largest (marked when packed) go another way: sc * q exact, times d in the fused
+// multiply-add, 2^15 times larger. (Rates, cycles a warp instruction of one scheduler: binary16 pairs 2,
+// integer logic and shifts 2, on two pipes; f32 1. That way is 3.7 instead of 2.8
+// instructions a pair, and 8 experts of 4096 x 4096 took 28.8 instead of 27.0 us.) For a binary16 Y that would
 // show, so there the weight is rounded once (q4_K in f32, 2.6 instructions a
 // weight; q6_K with sc * d in two terms, 3.4).
 // In a binary16 silu(gate) * up the roundings of both products would still
@@ -237,7 +239,8 @@ __device__ __forceinline__ void store_tiles_t(uint32_t addr, uint32_t a, uint32_
 }
 
 // ------------------------------------------------------------ dequantising ---
-constexpr uint32_t kH2_2m15 = 0x02000200u, kH2_m2p19 = 0x80208020u,
+constexpr uint32_t kH2_2m15 = 0x02000200u, kH2_512 = 0x60006000u, kH2_256 = 0x5C005C00u,
+                   kH2_m2p19 = 0x80208020u,
                    kH2_1_16 = 0x2C002C00u, kH2_1056 = 0x64206420u;
 
 // A byte of a word as a binary16 pair, plus 1024.
@@ -282,29 +285,35 @@ struct Half<Q6_FMT_Q4K> {
   uint4 q[4];
   uint32_t sc, mn, d, dm;
   float df, dmf;
-  __device__ __forceinline__ void load(const uint8_t* tile, int row, int h, float inv) {
+  __device__ __forceinline__ void load(const uint8_t* tile, int row, int h, float inv, bool wide) {
     const uint4* p = reinterpret_cast<const uint4*>(tile) + row;
     const uint4 head = p[0];
 #pragma unroll
     for (int t = 0; t < 4; ++t) q[t] = p[(1 + 2 * t + h) * kBand];
     const float2 dd = unpack2<__half>(head.x);
     df = dd.x * inv, dmf = -dd.y * inv;
-    d = splat_h2(df * 512.0f), dm = splat_h2(dmf);
+    d = splat_h2(df * (wide ? 32768.0f : 512.0f)), dm = splat_h2(dmf);
     sc = h ? (head.w & 0x0F0F0F0Fu) | ((head.y >> 2) & 0x30303030u) : head.y & 0x3F3F3F3Fu;
     mn = h ? ((head.w >> 4) & 0x0F0F0F0Fu) | ((head.z >> 2) & 0x30303030u) : head.z & 0x3F3F3F3Fu;
   }
   // Chunk cc of the half (32 of K) as 16 words.
+  template <bool kWide>
   __device__ __forceinline__ void expand(int cc, uint32_t (&out)[16]) const {
-    const uint32_t s = hmul2u(hsub2u(byte_h2(sc, cc), kH2_1024), d);  // sc * d * 2^9
+    // sc * d * 2^9, or sc * 2^9
+    const uint32_t s = hmul2u(hsub2u(byte_h2(sc, cc), kH2_1024), kWide ? kH2_512 : d);
     const uint32_t s16 = hmul2u(s, kH2_1_16);  // for codes four bits up
-    const uint32_t m = hmul2u(hmul2u(hsub2u(byte_h2(mn, cc), kH2_1024), dm), kH2_2m15);
+    uint32_t m = hmul2u(hsub2u(byte_h2(mn, cc), kH2_1024), dm);  // -dmin * m
+    if (!kWide) m = hmul2u(m, kH2_2m15);
+    auto weight = [&](uint32_t code, uint32_t by) {
+      return kWide ? hfma2u(hmul2u(code, by), d, m) : hfma2u(code, by, m);
+    };
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const uint32_t w = word4(q[t], cc), w8 = w >> 8;
-      out[4 * t] = hfma2u(w & 0x000F000Fu, s, m);
-      out[4 * t + 1] = hfma2u(w & 0x00F000F0u, s16, m);
-      out[4 * t + 2] = hfma2u(w8 & 0x000F000Fu, s, m);
-      out[4 * t + 3] = hfma2u(w8 & 0x00F000F0u, s16, m);
+      out[4 * t] = weight(w & 0x000F000Fu, s);
+      out[4 * t + 1] = weight(w & 0x00F000F0u, s16);
+      out[4 * t + 2] = weight(w8 & 0x000F000Fu, s);
+      out[4 * t + 3] = weight(w8 & 0x00F000F0u, s16);
     }
   }
   // In f32, rounded once. The offsets of the codes go with the min (rounded to
@@ -352,7 +361,7 @@ struct Half<Q6_FMT_Q6K> {
   uint2 high[4];
   uint32_t sc[2], d;
   float df;
-  __device__ __forceinline__ void load(const uint8_t* tile, int row, int h, float inv) {
+  __device__ __forceinline__ void load(const uint8_t* tile, int row, int h, float inv, bool wide) {
     const uint4* p = reinterpret_cast<const uint4*>(tile) + row;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -362,19 +371,24 @@ struct Half<Q6_FMT_Q6K> {
     const uint32_t* s = reinterpret_cast<const uint32_t*>(p + 12 * kBand);
     sc[0] = s[h], sc[1] = s[2 + h];
     df = __half2float(reinterpret_cast<const __half*>(tile + 13 * 2048)[row]) * inv;
-    d = splat_h2(df * 512.0f);
+    d = splat_h2(df * (wide ? 65536.0f : 512.0f));
   }
+  template <bool kWide>
   __device__ __forceinline__ void expand(int cc, uint32_t (&out)[16]) const {
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {  // runs 0, 1 and 2, 3 of the chunk
-      const uint32_t s = hmul2u(hsub2u(byte_h2(sc[sub], cc), kH2_1152), d);  // sc * d * 2^9
-      const uint32_t o = hmul2u(s, kH2_m2p19);                                     // -32 * 2^-24 * s
+      // sc * d * 2^9, or sc * 2^8
+      const uint32_t s = hmul2u(hsub2u(byte_h2(sc[sub], cc), kH2_1152), kWide ? kH2_256 : d);
+      const uint32_t o = hmul2u(s, kH2_m2p19);  // -32 * 2^-24 * s
 #pragma unroll
       for (int t = 2 * sub; t < 2 * sub + 2; ++t) {
         uint32_t v[4];
         q6_pairs(word4(q[t], cc), cc < 2 ? high[t].x : high[t].y, cc % 2, v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) out[4 * t + i] = hfma2u(v[i], s, o);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = hfma2u(v[i], s, o);
+          out[4 * t + i] = kWide ? hmul2u(w, d) : w;
+        }
       }
     }
   }
@@ -664,7 +678,7 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
       if (!ok) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem + (first ? 0u : 128u);
-      ok = both || kTwo
+      ok = unit_shift<kTwo>(n) == 1
                ? tile_mmas<1, kTwo>(st, bars, xring, tmem, d_tmem, n, a.sbs, abort_flag, status)
                : tile_mmas<2, false>(st, bars, xring, tmem, d_tmem, n, a.sbs, abort_flag, status);
       if (!ok) break;
@@ -696,7 +710,8 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
     for (int t = cluster; t < total && ok; t += clusters) {
       const Tile w = take(t);
       const bool split = unit_shift<kTwo>(w.n) == 1;  // a unit for each half
-      const float inv = 1.0f / scale;
+      const float inv = 1.0f / fabsf(scale);
+      const bool wide = __any_sync(0xffffffffu, scale < 0.0f);
       if (t + clusters < total) scale = scale_of(next);
       for (int sb = 0; sb < a.sbs && ok; ++sb, ++gw, unit += split ? 2 : 1) {
         if ((gw & 1) != me) continue;
@@ -707,7 +722,7 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
 #pragma unroll (__is_same(T, __half) ? 1 : 2)
         for (int h = 0; h < 2; ++h) {
           Half<kFmt> half;
-          half.load(wring + ws * kWTile<kFmt>, row, h, inv);
+          half.load(wring + ws * kWTile<kFmt>, row, h, inv, wide);
           const int mine = split ? unit + h : unit;
           // in pairs, the same half of each super-block has the same two slots
           const int as = kTwo ? 2 * h : 2 * me + h, last = kTwo ? mine - 2 : last2;
@@ -719,19 +734,26 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
           last2 = last1, last1 = mine;
           tc_fence_after();
           const uint32_t dst = tmem + lanes + (uint32_t)(kACol0 + as * kACols);
+          auto all = [&](auto expand) {
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            uint32_t v[16];
-            if constexpr (kTwo) {
+            for (int cc = 0; cc < 4; ++cc) {
+              uint32_t v[16];
+              expand(cc, v);
+              tmem_st16(dst + 16 * cc, v);
+            }
+          };
+          if constexpr (kTwo) {
+            all([&](int cc, uint32_t(&v)[16]) {
               uint32_t rest[16];
               half.expand_pair(cc, v, rest);
               tmem_st16(dst + kACols + 16 * cc, rest);
-            } else if constexpr (__is_same(T, __half)) {
-              half.expand_once(cc, v);
-            } else {
-              half.expand(cc, v);
-            }
-            tmem_st16(dst + 16 * cc, v);
+            });
+          } else if constexpr (__is_same(T, __half)) {
+            all([&](int cc, uint32_t(&v)[16]) { half.expand_once(cc, v); });
+          } else if (!wide) {
+            all([&](int cc, uint32_t(&v)[16]) { half.template expand<false>(cc, v); });
+          } else {
+            all([&](int cc, uint32_t(&v)[16]) { half.template expand<true>(cc, v); });
           }
           if (h == 1) {
             __syncwarp();
@@ -774,7 +796,9 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
       const int band = band_of(a, w.pair, rank);
       const bool mine = 2 * w.pair + rank < a.bands;
       const float* sc = a.scale + ((size_t)w.expert * a.bands + band) * kBand + 32 * q + (lane >> 2);
-      const float scale[4] = {sc[0] * kUp, sc[8] * kUp, sc[16] * kUp, sc[24] * kUp};
+      // (in wide groups of rows the weights are not scaled down further)
+      auto up = [&](float s) { return s < 0.0f ? -s : s * kUp; };
+      const float scale[4] = {up(sc[0]), up(sc[8]), up(sc[16]), up(sc[24])};
       const int m0 = (band * 4 + q) * kCols;       // this warp's first output feature
       const int item0 = both ? 128 * me : 0;
       const int cols = min(128, w.n - item0), count = mine ? w.count - item0 : 0;

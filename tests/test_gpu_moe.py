@@ -211,6 +211,43 @@ def test_experts_wide_range(rng, N, fmt, type):
     check(torch.where(cuda(keep), Y.double(), 0.0), np.where(keep, want, 0), bound)
 
 
+@pytest.mark.parametrize("fmt", ["q4_K", "q6_K"])
+@pytest.mark.parametrize("type,first,step", [("bf16", 0, 3), ("bf16", 0, 1), ("f16", -8, 1)])
+@pytest.mark.parametrize("N,E", [(96, 2), (16, 24)])
+def test_experts_super_blocks_far_apart(rng, fmt, type, first, step, N, E):
+    """A row's super-blocks may differ by 2^21 in size, and a token may look at the small ones
+    alone. Bound, beside a result's rounding: a weight's two terms and their sum are each rounded to
+    11 bits, and the weight is off by 2^-12 of its super-block's largest possible weight."""
+    M, K = 72, 2048
+    raw = raw_experts(11, fmt, E, M, K)
+    blocks = raw.reshape(E, M, K // 256, ref.BLOCK[fmt])
+    d = np.array([2.0 ** (first - step * s) for s in range(K // 256)], np.float16)
+    at = 0 if fmt == "q4_K" else 208
+    blocks[..., at:at + 2] = d.view(np.uint8).reshape(-1, 2)
+    if fmt == "q4_K":
+        blocks[..., 2:4] = (-d).view(np.uint8).reshape(-1, 2)
+    largest = np.abs(d.astype(np.float64)) * (945 + 63 if fmt == "q4_K" else 4096)
+    x = np.zeros((N, K))
+    mine = np.arange(N) % (K // 256)                    # the super-block a token looks at
+    for n in range(N):
+        x[n, 256 * mine[n]:256 * mine[n] + 256] = rng.standard_normal(256)
+    ids = rng.integers(0, E, (N, 1))
+    X = cuda(x, type)
+    w = q6.pack_experts(cuda(raw), fmt, E, M, K)
+    g = q6.group_rows(cuda(ids.astype(np.int32)), E)
+    Y, path = q6.experts_mmq(w, X, g)
+    assert path == ("experts_tc" if N > E else "experts_few")
+    want, _ = ref.experts(raw, fmt, f64(X), ids, E, False, True, type)
+    rows = g.rows.cpu().numpy()
+    size = np.abs(f64(X)).sum(1) * largest[mine]
+    bound = ref.ROUND[type] * np.abs(want) + ((3 * 2.0 ** -11 + 2.0 ** -12) * size)[rows][:, None]
+    check(Y, want, bound)
+    for s in range(K // 256):                           # and as a whole, as in run_experts
+        of = mine[rows] == s
+        off = np.linalg.norm((f64(Y) - want)[of])
+        assert off <= 4 * ref.ROUND[type] * np.linalg.norm(want[of])
+
+
 def test_experts_nonfinite_token_stays_alone(rng):
     """A token with an infinity or a NaN leaves the others as they are."""
     raw = raw_experts(4, "q4_K", 2, 40, 512)
