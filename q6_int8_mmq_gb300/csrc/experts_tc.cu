@@ -60,7 +60,7 @@
 // Bound: the MMAs at 256 items a tile (8192 bf16 items of q4_K experts of 11008 x
 // 4096, 739 GFLOP: 500 us, 1.48 PFLOP/s; its tensor pipe 76 % busy at 100 us), the
 // dequantising warps at few (132 items over 32 q6_K experts of 2056 x 1536, 83 MB:
-// 27.7 us), where issue is 51 % and DRAM 41 % busy: about 1050 cycles a super-block
+// 28.9 us), where issue is 51 % and DRAM 41 % busy: about 1050 cycles a super-block
 // against 512 of MMA at 64 items.
 // Every wait is bounded (see q6_internal.cuh), and the pair meets once more
 // before either CTA leaves.
