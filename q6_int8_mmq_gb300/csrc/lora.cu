@@ -31,7 +31,8 @@
 // Bound: memory at the least (X, Y and out once; the adapters in use once from HBM
 // and once a tile from L2); expand by the latencies of 16 warps an SM (its factors
 // from shared memory, MMAs, DRAM 40 % busy). 3314 tokens of 6 adapters of rank 64 at
-// 4096 x 11008, 330 MB: 87 us, 3.8 TB/s, of it shrink 13.
+// 4096 x 11008, 330 MB: 85 us, 3.9 TB/s (87 without reading B and Y before T is
+// there; 1000 f16 tokens of 8 of rank 64 at 4096 x 4096 24.7 and 27.2).
 #include <cuda_bf16.h>
 
 #include "moe_internal.cuh"
@@ -583,11 +584,14 @@ expand_kernel(const LoraCall c, int part_cols) {
   uint8_t* bs = ts + kParts * kExpandRows * ld + warp * 2 * kColsWarp * pitch;
   const int m_end = min(c.M, ((int)blockIdx.y + 1) * part_cols);
   const int m_first = (int)blockIdx.y * part_cols + warp * kColsWarp;
-  griddep_wait();
+  // The kernel before is shrink, all of whose CTAs have passed their own wait once
+  // this one runs: everything but T is in memory, and T is waited for below.
   const Tile tile = find_tile(c.offsets, c.L, kExpandRows, blockIdx.x);
-  if (tile.group < 0) return;
   const bool none = tile.group == c.L;  // tokens without an adapter: Y alone
-  if (none && c.out == c.Y) return;
+  if (tile.group < 0 || (none && c.out == c.Y)) {
+    griddep_wait();
+    return;
+  }
   const TW* B = static_cast<const TW*>(c.B) + (size_t)tile.group * c.M * (size_t)c.r;
   const int units = c.r / 8;  // 16-byte units of a column
   auto load_b = [&](int m0, int buf) {
@@ -619,6 +623,7 @@ expand_kernel(const LoraCall c, int part_cols) {
   for (int h = 0; h < 4; ++h)
 #pragma unroll
     for (int q = 0; q < 2; ++q) y[h][q] = load_y(h, m_first + 4 * t + 16 * q);
+  griddep_wait();
   // T, four ranks at a time, the parts' loads in flight together
   for (int i = threadIdx.x; i < kExpandRows * (c.r / 4) && !none; i += width) {
     const int n = i / (c.r / 4), j = i % (c.r / 4) * 4;
@@ -767,9 +772,9 @@ cudaError_t expand_v(const LoraCall& c, bool vec, cudaStream_t s) {
   const int warps = expand_warps<TW>(c.r), width = kColsWarp * warps;
   // Column parts, whole blocks each: about two CTAs an SM, as run at a time, or twice
   // that where T, which each CTA makes its factors of anew, is small. (Two against four
-  // an SM, us: 3314 tokens, 6 adapters, M 11008, bf16 of rank 64, 82.8 to 100.3 by how
-  // they fall against 87 to 88; 512 tokens, 4, M 4096, rank 16 10.7 / 8.8; f16 of rank
-  // 64, 1000, 8, M 4096 27.2 / 30.1; bf16 of rank 128, 2048, 1, M 4096 53.0 / 58.8.)
+  // an SM, us: 3314 tokens, 6 adapters, M 11008, bf16 of rank 64, 80.4 to 97.9 by how
+  // they fall against 84.8 to 85.7; 512 tokens, 4, M 4096, rank 16 9.8 / 8.5; f16 of
+  // rank 64, 1000, 8, M 4096 24.7 / 27.1; bf16 of rank 128, 2048, 1, M 4096 52.0 / 57.9.)
   const int blocks = (c.M + width - 1) / width;
   const int t_bytes = (kThreeParts<TW> ? 3 : 2) * kExpandRows * t_pitch<TW>(c.r);
   const int an_sm = t_bytes <= 16 * 1024 ? 4 : 2;
