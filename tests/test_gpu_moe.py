@@ -504,3 +504,55 @@ def test_lora_past_2_31_values(rng):
     want, bound = ref.lora(np.zeros((3, M)), f64(last), f64(A), f64(B), f64(scale), ids[:3])
     check(out[-3:], want, bound)
     assert not out[:-3].any()
+
+
+# --------------------------------------------------- calls one behind another ---
+
+@pytest.mark.parametrize("type", ["bf16", "f16"])
+def test_calls_follow_each_other(rng, type):
+    """Calls in a row, whose kernels overlap (weights may be read while the rows of x are still
+    made, B and Y while T is), give what they give with the device idle between them: every step
+    has new weights in the memory of the last, new tokens and new groups."""
+    E, M, K, L, r, N = 6, 520, 1024, 3, 16, 300
+    raws = [cuda(raw_experts(20 + i, "q4_K", E, M, K)) for i in range(4)]
+    Xs = [cuda(rng.standard_normal((N, K)), type) for _ in range(4)]
+    lists = [cuda(rng.integers(-1, E, (N, 2)).astype(np.int32)) for _ in range(4)]
+    own = [cuda(rng.integers(-1, L, (N,)).astype(np.int32)) for _ in range(4)]
+    ABs = [(cuda(rng.standard_normal((L, r, K)), type), cuda(rng.standard_normal((L, M, r)), type))
+           for _ in range(4)]
+    scale = torch.ones(L, device="cuda")
+
+    def steps(idle):
+        wait = torch.cuda.synchronize if idle else (lambda: None)
+        raw, X = torch.empty_like(raws[0]), torch.empty_like(Xs[0])
+        A, B = torch.empty_like(ABs[0][0]), torch.empty_like(ABs[0][1])
+        plane = None
+        got = []
+        for i in range(24):
+            k = i * 5 % 4
+            raw.copy_(raws[k]), X.copy_(Xs[(k + i) % 4])
+            A.copy_(ABs[k][0]), B.copy_(ABs[k][1])
+            wait()
+            w = q6.pack_experts(raw, "q4_K", E, M, K)
+            if plane is not None:
+                plane.plane.copy_(w.plane)
+                w = plane
+            plane = w
+            wait()
+            g = q6.group_rows(lists[(i // 2) % 4], E)
+            wait()
+            Y, path = q6.experts_mmq(w, X, g)
+            assert path == "experts_tc"
+            wait()
+            t = q6.moe_combine(Y, g.pos, torch.full((N, 2), 0.5, device="cuda")).float()
+            wait()
+            mine = q6.group_rows(own[i % 4], L)
+            wait()
+            out = q6.lora_add(q6.LoraAdapters(A, B, scale), X, mine, t)
+            wait()
+            got += [Y.clone(), out.clone()]
+        q6.sync_status()
+        return got
+
+    for a, b in zip(steps(True), steps(False)):
+        assert torch.equal(a, b)
