@@ -60,7 +60,7 @@
 // Bound: the MMAs at 256 items a tile (8192 bf16 items of q4_K experts of 11008 x
 // 4096, 739 GFLOP: 500 us, 1.48 PFLOP/s; its tensor pipe 76 % busy at 100 us), the
 // dequantising warps at few (132 items over 32 q6_K experts of 2056 x 1536, 83 MB:
-// 28.9 us), where issue is 51 % and DRAM 41 % busy: about 1050 cycles a super-block
+// 29.5 us), where issue is 51 % and DRAM 41 % busy: about 1050 cycles a super-block
 // against 512 of MMA at 64 items.
 // Every wait is bounded (see q6_internal.cuh), and the pair meets once more
 // before either CTA leaves.
@@ -111,10 +111,11 @@ struct Args {
 
 template <int kFmt>
 constexpr int kWTile = kFmt == Q6_FMT_Q4K ? kQ4Tile : kQ6Tile;
+constexpr int kMaxSorted = 256;  // experts whose tiles are put in order of size
 constexpr int kOutWarp = 2048;  // epilogue staging of a warp: 32 items of 64 bytes
 template <int kFmt>
 constexpr int kSmemBytes = 1024 + kXStages * kXStage + kWStages<kFmt> * kWTile<kFmt> + 8 * kOutWarp +
-                           2 * (kMaxGroups + 1) * 4 + (int)sizeof(Bars);
+                           2 * (kMaxGroups + 1) * 4 + kMaxSorted + (int)sizeof(Bars);
 
 // True in one lane of the converged warp. TMA and MMA instructions take their
 // operands from uniform registers: one elected lane on values that all lanes
@@ -446,10 +447,17 @@ struct Tile {
 };
 __device__ __forceinline__ int tiles_of(int count) { return (count + kTileN - 1) / kTileN; }
 
-// Tile t of the list ordered by (expert, item tile, band pair); start[e] is
-// the number of (expert, item tile)s before expert e. Nothing past the last tile.
-__device__ __forceinline__ Tile tile_at(const Args& a, const int* start, const int* offs, int t,
-                                        int total) {
+// Items of an expert's tiles: equal parts, in steps of 32 (their last may hold
+// less, but never nothing).
+__device__ __forceinline__ int tile_items(int count) {
+  const int parts = tiles_of(count);
+  return parts ? ((count + parts - 1) / parts + 31) / 32 * 32 : 0;
+}
+// Tile t of the list ordered by (expert, item tile, band pair); start[i] is the
+// number of (expert, item tile)s before the i-th expert, which is i or, if sorted,
+// order[i]. Nothing (n = 0) past the last tile.
+__device__ __forceinline__ Tile tile_at(const Args& a, const int* start, const int* offs,
+                                        const uint8_t* order, bool sorted, int t, int total) {
   Tile r = {};
   if (t >= total) return r;
   const int pairs = (a.bands + 1) / 2;
@@ -460,11 +468,9 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* start, const i
     if (start[mid] <= item_tile) lo = mid;
     else hi = mid;
   }
-  r.expert = lo, r.pair = t % pairs;
-  const int begin = offs[lo], count = offs[lo + 1] - begin;
-  const int parts = tiles_of(count), j = item_tile - start[lo];
-  // equal parts, in steps of 32 (their last may hold less, but never nothing)
-  r.n = ((count + parts - 1) / parts + 31) / 32 * 32;
+  r.expert = sorted ? order[lo] : lo, r.pair = t % pairs;
+  const int begin = offs[r.expert], count = offs[r.expert + 1] - begin, j = item_tile - start[lo];
+  r.n = tile_items(count);
   r.first = (long long)begin + (long long)j * r.n;
   r.count = min(r.n, count - j * r.n);
   return r;
@@ -534,7 +540,8 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
   uint8_t* out_stage = wring + kWStages<kFmt> * kWTile<kFmt>;
   int* start = reinterpret_cast<int*>(out_stage + 8 * kOutWarp);
   int* offs = start + kMaxGroups + 1;  // a copy of the offsets
-  Bars* bars = reinterpret_cast<Bars*>(offs + kMaxGroups + 1);
+  uint8_t* order = reinterpret_cast<uint8_t*>(offs + kMaxGroups + 1);
+  Bars* bars = reinterpret_cast<Bars*>(order + kMaxSorted);
   static_assert(2 * (kMaxGroups + 1) * 4 % 8 == 0, "barriers are 8-byte aligned");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
@@ -565,13 +572,36 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
   // is in memory: where it made nothing but the rows of x, only their readers wait.
   if (!a.early) griddep_wait();
   griddep_launch_dependents();
-  for (int e = threadIdx.x; e <= a.E; e += kThreads) offs[e] = a.offsets[e];
-  __syncthreads();
+  // Tiles of more than 128 items (there are such with more than 128 items an expert)
+  // take longer the more they have, others all the same, by their weights: with any
+  // of them the largest come first. (8184 items unevenly over 64 experts of 2816 x
+  // 2048: 112 us, in the experts' order 114 to 120; 2048 over 8 of 4096 x 4096 61 and
+  // 67.) Not with more than 256 experts: their ranks, found by comparing each with
+  // all, would take microseconds, and shared memory has no room for a longer order.
+  bool large = false;
+  for (int e = threadIdx.x; e <= a.E; e += kThreads) {
+    const int begin = a.offsets[e];
+    offs[e] = begin;
+    large |= e < a.E && a.offsets[e + 1] - begin > 128;
+  }
+  const bool sorted = __syncthreads_or(large) && a.E <= kMaxSorted;
+  if (sorted) {
+    const int e = threadIdx.x, n = e < a.E ? tile_items(offs[e + 1] - offs[e]) : 0;
+    if (e < a.E) start[e] = n;
+    __syncthreads();
+    if (e < a.E) {
+      int before = 0;
+      for (int i = 0; i < a.E; ++i) before += start[i] > n || (start[i] == n && i < e);
+      order[before] = (uint8_t)e;
+    }
+    __syncthreads();
+  }
   if (warp == 3) {  // start[]: the running number of (expert, item tile) pairs
     int run = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
-      const int v = e < a.E ? tiles_of(offs[e + 1] - offs[e]) : 0;
+      const int at = sorted && e < a.E ? order[e] : e;
+      const int v = e < a.E ? tiles_of(offs[at + 1] - offs[at]) : 0;
       int x = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -590,11 +620,21 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
   const uint32_t tmem = bars->tmem_base;
   const int total = start[a.E] * ((a.bands + 1) / 2);
   // Each role works out its next tile while it has one: between two tiles that
-  // would stand still for 1300 cycles.
-  Tile next = tile_at(a, start, offs, cluster, total);
-  auto take = [&](int t) {
+  // would stand still for 1300 cycles. The pairs take the list in turn, with the
+  // largest tiles first every second time in reverse, so that their sums come out
+  // alike; the last time is not, for the pairs that started first have the rest (the
+  // last of a launch start about a microsecond later).
+  int pass = 0;
+  const int odd = sorted ? (total + clusters - 1) / clusters % 2 : 0;  // passes in all
+  auto number = [&] {
+    const bool reverse = sorted && pass % 2 == odd;
+    return pass * clusters + (reverse ? clusters - 1 - cluster : cluster);
+  };
+  Tile next = tile_at(a, start, offs, order, sorted, number(), total);
+  auto take = [&] {
     const Tile w = next;
-    next = tile_at(a, start, offs, t + clusters, total);
+    ++pass;
+    next = tile_at(a, start, offs, order, sorted, number(), total);
     return w;
   };
   bool ok = true;
@@ -604,8 +644,8 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
     // --------------------------------------------------------------- load x --
     griddep_wait();
     int g = 0;  // units opened
-    for (int t = cluster; t < total && ok; t += clusters) {
-      const Tile w = take(t);
+    while (next.n && ok) {
+      const Tile w = take();
       const int rows = w.n / 2;  // this CTA's
       const int box = box_of(w.n);
       const int shift = unit_shift<kTwo>(w.n);
@@ -639,8 +679,8 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
   } else if (warp == 3) {
     // ------------------------------------------------------- packed weights --
     int slot = 0, round = 0, g = 0;  // g: stages filled
-    for (int t = cluster; t < total && ok; t += clusters) {
-      const Tile w = take(t);
+    while (next.n && ok) {
+      const Tile w = take();
       const size_t band = (size_t)w.expert * a.bands + band_of(a, w.pair, rank);
       const uint8_t* src = a.plane + __shfl_sync(0xffffffffu, band, 0) * (size_t)a.sbs * kWTile<kFmt>;
       for (int sb = 0; sb < a.sbs; ++sb) {
@@ -668,8 +708,8 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
     // (Issued from one lane's own branch, 64 of K took 700 cycles.)
     MmaState st = {0, 0};
     int turn = 0, uses0 = 0, uses1 = 0;
-    for (int t = cluster; t < total && ok; t += clusters) {
-      const int n = (int)__reduce_max_sync(0xffffffffu, (unsigned)take(t).n);
+    while (next.n && ok) {
+      const int n = (int)__reduce_max_sync(0xffffffffu, (unsigned)take().n);
       const bool both = n > 128, first = both || turn == 0, second = both || turn == 1;
       if (first)
         ok = mbar_wait_warp(&bars->d_empty[0], (uses0 & 1) ^ 1, abort_flag, status, kSiteDEmpty);
@@ -706,13 +746,13 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
     auto scale_of = [&](const Tile& w) {
       return a.scale[((size_t)w.expert * a.bands + band_of(a, w.pair, rank)) * kBand + row];
     };
-    float scale = total > cluster ? scale_of(next) : 1.0f;
-    for (int t = cluster; t < total && ok; t += clusters) {
-      const Tile w = take(t);
+    float scale = next.n ? scale_of(next) : 1.0f;
+    while (next.n && ok) {
+      const Tile w = take();
       const bool split = unit_shift<kTwo>(w.n) == 1;  // a unit for each half
       const float inv = 1.0f / fabsf(scale);
       const bool wide = __any_sync(0xffffffffu, scale < 0.0f);
-      if (t + clusters < total) scale = scale_of(next);
+      if (next.n) scale = scale_of(next);
       for (int sb = 0; sb < a.sbs && ok; ++sb, ++gw, unit += split ? 2 : 1) {
         if ((gw & 1) != me) continue;
         if (!(ok = mbar_wait_warp(&bars->w_full[ws], round & 1, abort_flag, status,
@@ -788,8 +828,8 @@ experts_tc_kernel(const __grid_constant__ RowMaps maps, const Args a, unsigned i
       for (int m = 128 * me + 32 * q + lane; m < a.out; m += 256)
         Y[i * a.ldy + m] = from_f32<T>(0.0f);
     int turn = 0, uses = 0;
-    for (int t = cluster; t < total && ok; t += clusters) {
-      const Tile w = take(t);
+    while (next.n && ok) {
+      const Tile w = take();
       const bool both = w.n > 128, here = both || turn == me;
       turn = both ? 0 : turn ^ 1;
       if (!here) continue;

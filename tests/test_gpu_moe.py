@@ -171,6 +171,17 @@ def test_experts_few_nonfinite_token_stays_alone(rng, fmt):
     assert torch.equal(Y[rest], good[rest])
 
 
+@pytest.mark.parametrize("E", [256, 257, 1024])
+@pytest.mark.parametrize("type", ["bf16", "f16"])
+def test_experts_many_uneven(rng, E, type):
+    """Tiles of every size over as many experts as there may be."""
+    counts = np.ones(E, int)
+    counts[[3, 4, E // 2, E - 1]] = 140, 300, 0, 190
+    ids = rng.permutation(np.repeat(np.arange(E), counts))
+    path = run_experts(rng, "q4_K", type, ids[:, None], E, 40, 256, False, True)
+    assert path == "experts_tc"
+
+
 @pytest.mark.parametrize("fmt,K", [("q4_K", 18944), ("q6_K", 11008)])
 def test_experts_long_k(rng, fmt, K):
     run_experts(rng, fmt, "bf16", rng.integers(0, 2, (21, 1)), 2, 48, K, False, True)
