@@ -119,6 +119,13 @@ def _f32_i32():
     return torch.float32, torch.int32
 
 
+def _made(cls, **fields):
+    """An object of a frozen class from buffers allocated here, which need no checks."""
+    made = object.__new__(cls)
+    made.__dict__.update(fields)
+    return made
+
+
 # ---------------------------------------------------------------- grouping ---
 
 @functools.lru_cache(maxsize=256)
@@ -165,8 +172,11 @@ def alloc_groups(N: int, per_row: int, n_groups: int, device=None) -> Groups:
     def i32(*shape):
         return torch.empty(shape, dtype=torch.int32, device=dev)
 
-    return Groups(N, per_row, n_groups, i32(n_groups + 2), i32(N * per_row), i32(N, per_row),
-                  torch.empty(need, dtype=torch.uint8, device=dev) if need else None)
+    offsets = i32(n_groups + 2)
+    return _made(Groups, N=N, per_row=per_row, n_groups=n_groups, offsets=offsets,
+                 rows=i32(N * per_row), pos=i32(N, per_row), items=N * per_row,
+                 device=offsets.device,
+                 workspace=torch.empty(need, dtype=torch.uint8, device=dev) if need else None)
 
 
 def group_rows(ids, n_groups: int, out: Groups | None = None, stream=None) -> Groups:
@@ -210,9 +220,9 @@ def alloc_route(N: int, E: int, topk: int, device=None) -> Route:
     """Buffers for the routing of N tokens to topk of E experts."""
     import torch
     dev = device or torch.device("cuda")
-    return Route(torch.empty((N, topk), dtype=torch.int32, device=dev),
-                 torch.empty((N, topk), dtype=torch.float32, device=dev),
-                 alloc_groups(N, topk, E, dev))
+    return _made(Route, groups=alloc_groups(N, topk, E, dev),
+                 ids=torch.empty((N, topk), dtype=torch.int32, device=dev),
+                 weights=torch.empty((N, topk), dtype=torch.float32, device=dev))
 
 
 def moe_route(logits, topk: int, renormalize: bool = True, out: Route | None = None,
