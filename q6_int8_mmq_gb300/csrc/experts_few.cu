@@ -38,6 +38,7 @@ constexpr int kSmem = 104 * 1024;  // two CTAs an SM
 
 // Shared bytes of one super-block of 8 * NT staged tokens: x, the chunk-sum
 // pairs, the scales.
+constexpr int kAhead = 4;  // see prefetch_rows()
 template <int NT>
 constexpr int kSbBytes = 8 * NT * (512 + 32 + 4);
 // Super-blocks staged at a time (the partial sums reuse the space).
@@ -102,6 +103,16 @@ struct Block<Q6_FMT_Q6K> {
     }
   }
 };
+
+// Asks for the lines of 16 rows (the first of them row) of a q6_K tile, a line a
+// lane: its loads are more and smaller than q4_K's. (Five super-blocks ahead, 16
+// experts of 4096 x 11008 in use: q6_K 85.1 us, without 98.8; q4_K 71.2 and 69.4.)
+__device__ __forceinline__ void prefetch_rows(const uint8_t* tile, int row, int lane) {
+  constexpr int kUnits = 13;  // of 16 bytes a row; then d
+  const uint8_t* p = lane < 2 * kUnits ? tile + lane / 2 * 2048 + row * 16 + lane % 2 * 128
+                                       : tile + kUnits * 2048 + row * 2;
+  if (lane <= 2 * kUnits) asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 
 // acc += one super-block. xs: this super-block's staged x, [chunk][token][run]
 // 16-byte units; sums: [token][16] halves (8 hi, 8 lo); scale: [token].
@@ -295,6 +306,9 @@ __device__ __forceinline__ void run(const Args& a, int expert, long long first, 
     Block<kFmt> cur;
     if (active && part < count)
       cur.load(tiles + (size_t)(sb0 + part) * kTile, in_band, lane & 3);
+    if (kFmt == Q6_FMT_Q6K && active)
+      for (int k = 1; k <= kAhead && part + k * parts < count; ++k)
+        prefetch_rows(tiles + (size_t)(sb0 + part + k * parts) * kTile, row0 % kBand, lane);
     if (sb0) __syncthreads();  // the last stage has been read
     stage_x<T, NT>(a, first, valid, sb0, count, xs, sums, scale);
     __syncthreads();
@@ -303,6 +317,9 @@ __device__ __forceinline__ void run(const Args& a, int expert, long long first, 
         Block<kFmt> next;
         if (sb + parts < count)
           next.load(tiles + (size_t)(sb0 + sb + parts) * kTile, in_band, lane & 3);
+        if (kFmt == Q6_FMT_Q6K && sb + (kAhead + 1) * parts < count)
+          prefetch_rows(tiles + (size_t)(sb0 + sb + (kAhead + 1) * parts) * kTile, row0 % kBand,
+                        lane);
         multiply<NT>(cur, xs + sb * kTok * 32, sums + sb * kTok * 8, scale + sb * kTok, lane, acc);
         cur = next;
       }
