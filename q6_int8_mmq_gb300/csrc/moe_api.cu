@@ -59,9 +59,9 @@ int check_experts(int fmt, int E, int M, int K, int swiglu) {
 
 // The few-token kernel runs up to one item an expert on average. Measured, few-token
 // kernel / tensor cores in us, with 0.5, 1, 2 and 4 items an expert: q4_K, 64 experts
-// of 1536 x 2048 13.7 / 17.2, 24.3 / 23.2, 30.5 / 27.0, 46.3 / 29.3; 8 of 4096 x 4096
-// 13.6 / 15.8, 22.5 / 22.7, 24.6 / 25.9, 33.4 / 25.9; q6_K, 32 of 2056 x 1536
-// 14.8 / 14.2, 18.8 / 18.8, 26.1 / 22.4, 34.2 / 25.7.
+// of 1536 x 2048 13.6 / 17.8, 24.2 / 24.2, 30.6 / 28.1, 46.6 / 30.4; 8 of 4096 x 4096
+// 13.5 / 16.2, 22.7 / 23.5, 24.5 / 26.9, 33.6 / 27.0; q6_K, 32 of 2056 x 1536
+// 13.4 / 15.0, 16.9 / 20.0, 24.3 / 23.8, 35.1 / 27.4.
 bool on_tensor_cores(int64_t items, int E) { return items > E; }
 // Bytes of the binary16 rows in item order that the tensor-core path makes (0:
 // it reads X itself), and where their scales follow.
