@@ -555,7 +555,11 @@ int q6_pack_experts(int fmt, const uint8_t *raw, int E, int M, int K, int swiglu
 /* The grouped product over a grouping by expert:
  *   Y[i] = W[e(i)] x,  x = X[rows[i]] (gather != 0) or X[i],
  * for every sorted item i; with swiglu weights Y[i] = silu(gate) * up. Items
- * of no group get zeros.
+ * of no group get zeros. A weight enters the f32 sums with 11 significant bits
+ * of each of its terms (sc * d, dmin * m and their sum), 2^-12 of its
+ * super-block's largest possible weight at the least; with binary16 results on
+ * the tensor cores it is rounded once, with swiglu to 22 bits. Which kernel
+ * runs depends on items and E alone; the two round differently.
  *   X : device [nx][ldx] of `type` (bf16 or f16), 16-byte aligned, ldx % 8 ==
  *       0, ldx >= K; nx rows (every rows[i] < nx; without gather nx >= items).
  *   Y : device [items][ldy] of the same type, ldy >= M (M / 2 with swiglu);

@@ -100,17 +100,22 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _empty(shape, dtype, device, stream):
+@functools.lru_cache(maxsize=None)
+def _alloc():
     import torch
+    return torch.empty, torch.uint8, torch.cuda.stream
+
+
+def _empty(shape, dtype, device, stream):
+    empty, _, on = _alloc()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return empty(shape, dtype=dtype, device=device)
+    with on(stream):
+        return empty(shape, dtype=dtype, device=device)
 
 
 def _scratch(nbytes, device, stream):
-    import torch
-    return _empty(nbytes, torch.uint8, device, stream)
+    return _empty(nbytes, _alloc()[1], device, stream)
 
 
 @functools.lru_cache(maxsize=None)
