@@ -51,6 +51,8 @@ int check_experts(int fmt, int E, int M, int K, int swiglu) {
   if (E < 1 || E > Q6_MAX_GROUPS || M < 1 || K < 1 || K % 256 || (swiglu && M % 2))
     return fail(Q6_EINVAL, "1 <= E <= %d, M >= 1 (even with swiglu), K a multiple of 256",
                 Q6_MAX_GROUPS);
+  if (q6::expert_rows(M, swiglu) > q6::kMaxPlaneRows)
+    return fail(Q6_ESIZE, "an expert has more than %lld rows", q6::kMaxPlaneRows);
   const q6::ExpertGeom g = q6::expert_geom(fmt, E, M, K, swiglu);
   if ((long long)E * g.bands * (long long)g.sbs >= 1ll << 31)
     return fail(Q6_ESIZE, "the experts have too many tiles");

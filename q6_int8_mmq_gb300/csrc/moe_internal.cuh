@@ -147,10 +147,16 @@ struct ExpertGeom {
   int out;         // output features: M, or M / 2 with swiglu
   size_t scale_off, total;
 };
+// Plane rows of an expert (up to 2^31 + 8), and the most that leave the kernels'
+// row numbers, which run up to 128 + 32 past the last row, within 31 bits.
+constexpr long long kMaxPlaneRows = (1ll << 31) - 256;
+inline long long expert_rows(int M, int swiglu) {
+  return swiglu ? (M / 2 + 7ll) / 8 * 16 : M;
+}
 inline ExpertGeom expert_geom(int fmt, int E, int M, int K, int swiglu) {
   ExpertGeom g;
   g.out = swiglu ? M / 2 : M;
-  g.rows = swiglu ? (g.out + 7) / 8 * 16 : M;
+  g.rows = (int)expert_rows(M, swiglu);
   g.bands = (g.rows + kBand - 1) / kBand;
   g.sbs = K / 256;
   g.tile = fmt == Q6_FMT_Q4K ? kQ4Tile : kQ6Tile;

@@ -1,0 +1,38 @@
+"""Sizes of experts and adapters near the limits of the kernels' index arithmetic (CPU only: every
+call here returns before it touches a device)."""
+import ctypes
+
+import pytest
+
+import q6_int8_mmq_gb300 as q6
+from q6_int8_mmq_gb300 import build as q6build, moe
+
+FAKE = ctypes.c_void_p(0x10000)      # never dereferenced: the call is refused before
+BIG = 1 << 40
+MAX_ROWS = 2 ** 31 - 256             # plane rows of an expert
+
+
+@pytest.fixture(scope="module")
+def lib():
+    q6build.build()
+    return q6.load()
+
+
+@pytest.mark.parametrize("M,glu", [(2 ** 31 - 1, 0), (MAX_ROWS + 1, 0), (2 ** 31 - 2, 1),
+                                   (MAX_ROWS + 2, 1)])
+def test_experts_of_too_many_rows_are_refused(lib, M, glu):
+    """In 31 bits their bands would come out negative, and their plane small."""
+    nbytes = ctypes.c_size_t()
+    for fmt in (4, 6):
+        assert lib.q6_expert_plane_bytes(fmt, 1, M, 256, glu, ctypes.byref(nbytes)) == q6.Q6_ESIZE
+        assert lib.q6_pack_experts(fmt, FAKE, 1, M, 256, glu, FAKE, None) == q6.Q6_ESIZE
+        assert lib.q6_experts_mmq(fmt, FAKE, 1, M, 256, glu, FAKE, 1, 4, 256, 1, FAKE, FAKE, 4, FAKE,
+                                  1 << 31, FAKE, BIG, None, None) == q6.Q6_ESIZE
+    with pytest.raises(q6.Q6Error):
+        moe.expert_plane_bytes.__wrapped__("q4_K", 1, M, 256, bool(glu))
+
+
+def test_the_most_rows_have_the_plane_they_need(lib):
+    bands = MAX_ROWS // 128
+    assert moe.expert_plane_bytes("q4_K", 1, MAX_ROWS, 256) == bands * (128 * 144 + 128 * 4)
+    assert moe.expert_plane_bytes("q6_K", 1, MAX_ROWS, 256, True) == bands * (128 * 210 + 128 * 4)
