@@ -146,8 +146,9 @@ int q6_pack_experts(int fmt, const uint8_t* raw, int E, int M, int K, int swiglu
 }
 
 int q6_experts_workspace_bytes(int E, int K, int type, int64_t items, int gather, size_t* bytes) {
-  if (E < 1 || K < 1 || K % 256 || !half_type(type) || items < 0 || !bytes)
-    return fail(Q6_EINVAL, "E >= 1, K a multiple of 256, type bf16 or f16, items >= 0, bytes not NULL");
+  if (E < 1 || K < 1 || K % 256 || !half_type(type) || items < 0 || items >= 1ll << 31 || !bytes)
+    return fail(Q6_EINVAL,
+                "E >= 1, K a multiple of 256, type bf16 or f16, 0 <= items < 2^31, bytes not NULL");
   *bytes = experts_bytes(items, E, K, type, gather);
   return Q6_OK;
 }

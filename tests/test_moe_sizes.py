@@ -36,3 +36,14 @@ def test_the_most_rows_have_the_plane_they_need(lib):
     bands = MAX_ROWS // 128
     assert moe.expert_plane_bytes("q4_K", 1, MAX_ROWS, 256) == bands * (128 * 144 + 128 * 4)
     assert moe.expert_plane_bytes("q6_K", 1, MAX_ROWS, 256, True) == bands * (128 * 210 + 128 * 4)
+
+
+@pytest.mark.parametrize("items", [1 << 31, 1 << 62, -1])
+@pytest.mark.parametrize("K", [256, 1 << 20])
+def test_workspace_of_too_many_items_is_refused(lib, items, K):
+    """As in the product itself; 2^62 items' bytes would not fit 64 bits."""
+    nbytes = ctypes.c_size_t()
+    for type in (1, 2):
+        assert lib.q6_experts_workspace_bytes(4, K, type, items, 1, ctypes.byref(nbytes)) == q6.Q6_EINVAL
+    assert lib.q6_experts_workspace_bytes(4, K, 1, (1 << 31) - 1, 1, ctypes.byref(nbytes)) == q6.Q6_OK
+    assert nbytes.value >= ((1 << 31) - 1) * (2 * K + 4)
