@@ -587,7 +587,8 @@ int q6_moe_combine(const void *Y, int type, int64_t ldy, const int32_t *pos, con
  *   out[n] = Y[n] + scale[a] * B[a] (A[a] x[n]),  a the adapter of token n;
  * a token of no adapter keeps Y[n].
  *   A [L][r][K], B [L][M][r] of `type` (bf16 or f16), 16-byte aligned; scale
- *       f32 [L]. K % 32 == 0, r % 8 == 0, r <= Q6_LORA_MAX_RANK.
+ *       f32 [L]. K % 32 == 0, r % 8 == 0, r <= Q6_LORA_MAX_RANK. K and M up to
+ *       2^30, items up to 2^31 - 256.
  *   X : device [.][ldx] of `xtype` (f32, bf16, f16), 16-byte aligned rows,
  *       ldx >= K.
  *   offsets, rows : the grouping of the tokens by adapter (per_row 1, groups

@@ -223,9 +223,16 @@ int q6_moe_combine(const void* Y, int type, int64_t ldy, const int32_t* pos, con
                   "combination");
 }
 
+// Widths and items up to which the adapters' kernels' indices, which run up to a
+// step past the end, stay within 31 bits.
+static constexpr int kLoraMaxWidth = 1 << 30;
+static constexpr int64_t kLoraMaxItems = (1ll << 31) - 256;
+
 static int check_lora(int64_t items, int L, int r, int K) {
   if (items < 0 || items >= 1ll << 31 || L < 1 || L > Q6_MAX_GROUPS)
     return fail(Q6_EINVAL, "0 <= items < 2^31, 1 <= L <= %d", Q6_MAX_GROUPS);
+  if (items > kLoraMaxItems || K > kLoraMaxWidth)
+    return fail(Q6_ESIZE, "more than 2^31 - 256 items, or K above 2^30");
   if (r < 8 || r % 8 || r > Q6_LORA_MAX_RANK || K < 32 || K % 32)
     return fail(Q6_EINVAL, "the rank must be a multiple of 8 up to %d (pad with zeros), K one of 32",
                 Q6_LORA_MAX_RANK);
@@ -250,6 +257,7 @@ int q6_lora_add(const void* A, const void* B, const float* scale, int type, int 
     return fail(Q6_EINVAL, "adapters must be bf16 or f16, X f32, bf16 or f16");
   if (M < 1 || ldx < K || ldy < M || ldo < M)
     return fail(Q6_EINVAL, "M >= 1, ldx >= K, ldy >= M, ldo >= M");
+  if (M > kLoraMaxWidth) return fail(Q6_ESIZE, "M above 2^30");
   if (items == 0) return Q6_OK;
   if (!A || !B || !scale || !X || !offsets || !rows || !Y || !out)
     return fail(Q6_EINVAL, "null pointer");

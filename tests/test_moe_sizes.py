@@ -47,3 +47,24 @@ def test_workspace_of_too_many_items_is_refused(lib, items, K):
         assert lib.q6_experts_workspace_bytes(4, K, type, items, 1, ctypes.byref(nbytes)) == q6.Q6_EINVAL
     assert lib.q6_experts_workspace_bytes(4, K, 1, (1 << 31) - 1, 1, ctypes.byref(nbytes)) == q6.Q6_OK
     assert nbytes.value >= ((1 << 31) - 1) * (2 * K + 4)
+
+
+def test_adapters_of_too_many_columns_or_items_are_refused(lib):
+    """Column and tile numbers run up to a step past the last, and would leave 31 bits there."""
+    nbytes = ctypes.c_size_t()
+
+    def size(items, K):
+        return lib.q6_lora_workspace_bytes(items, 2, 8, K, ctypes.byref(nbytes))
+
+    def add(items=100, M=64, K=512):
+        ld = max(M, K)
+        return lib.q6_lora_add(FAKE, FAKE, FAKE, 1, 2, 8, M, K, FAKE, 1, ld, FAKE, FAKE, items, FAKE,
+                               ld, FAKE, ld, FAKE, BIG, None)
+
+    assert size(2 ** 31 - 256, 2 ** 30) == q6.Q6_OK
+    assert size(100, 2 ** 31 - 32) == q6.Q6_ESIZE
+    assert size(2 ** 31 - 255, 64) == q6.Q6_ESIZE
+    assert add(M=2 ** 31 - 1) == q6.Q6_ESIZE
+    assert add(M=2 ** 30 + 1) == q6.Q6_ESIZE
+    assert add(K=2 ** 31 - 32) == q6.Q6_ESIZE
+    assert add(items=2 ** 31 - 1) == q6.Q6_ESIZE
