@@ -78,11 +78,18 @@ cudaError_t combine_t(const void* Y, long long ldy, const int32_t* pos, const fl
                       long long ldo, cudaStream_t s) {
   const bool vec = M % 8 == 0 && aligned16(Y, ldy * 2) && aligned16(out, ldo * 2) &&
                    (!shared || aligned16(shared, lds * 4));
-  const int per = kThreads * (vec ? 8 : 1);
-  const dim3 grid((unsigned)N, (unsigned)((M + per - 1) / per));
-  return launch_pdl(vec ? combine_kernel<T, true> : combine_kernel<T, false>, grid, dim3(kThreads),
-                    0, s, static_cast<const T*>(Y), ldy, pos, weights, topk, M, shared, lds,
-                    static_cast<T*>(out), ldo);
+  // a launch takes as many columns as a grid has blocks for (65535 of 128 or 1024)
+  const int per = kThreads * (vec ? 8 : 1), most = 65535 * per;
+  for (int m = 0;;) {
+    const int cols = M - m < most ? M - m : most;
+    const dim3 grid((unsigned)N, (unsigned)((cols + per - 1) / per));
+    const cudaError_t e = launch_pdl(
+        vec ? combine_kernel<T, true> : combine_kernel<T, false>, grid, dim3(kThreads), 0, s,
+        static_cast<const T*>(Y) + m, ldy, pos, weights, topk, cols, shared ? shared + m : nullptr,
+        lds, static_cast<T*>(out) + m, ldo);
+    if (e != cudaSuccess || cols == M - m) return e;
+    m += cols;
+  }
 }
 
 }  // namespace
