@@ -32,6 +32,7 @@ struct DevState {
   bool init = false;
   int arch_ok = 0;
   unsigned int* status = nullptr;  // 256-byte block; word 0 is the status word
+  bool ready[q6::kKernelSets] = {};  // prepared (see q6::require_device)
 };
 
 std::mutex g_mu;
@@ -74,8 +75,7 @@ int device_state(DevState** out) {
     if ((e = cudaMemset(st.status, 0, 256))) return cuda_fail(e, "cudaMemset(status)");
     if ((e = q6::mmq_tc_prepare()) || (e = q6::mmq_skinny_prepare()) ||
         (e = q6::mmq_sync_prepare()) || (e = q6::q4k_skinny_mma_prepare()) ||
-        (e = q6::q4k_skinny_prepare()) || (e = q6::experts_few_prepare()) ||
-        (e = q6::experts_tc_prepare()) || (e = q6::lora_prepare()))
+        (e = q6::q4k_skinny_prepare()))
       return cuda_fail(e, "cudaFuncSetAttribute");
     if (!encoder()) return fail(Q6_ECUDA, "cuTensorMapEncodeTiled entry point not found");
     st.arch_ok = 1;
@@ -189,11 +189,23 @@ int encode_tc_maps_q4k(TcMaps* maps, const uint8_t* q4plane, const void* wq, con
 }  // namespace q6
 
 namespace q6 {
-int require_device(unsigned int** status) {
+int require_device(unsigned int** status, KernelSet set) {
   DevState* st;
   const int rc = device_state(&st);
-  if (!rc && status) *status = st->status;
-  return rc;
+  if (rc) return rc;
+  if (status) *status = st->status;
+  if (set == kPlainKernels) return Q6_OK;
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (st->ready[set]) return Q6_OK;
+  cudaError_t e = cudaSuccess;
+  if (set == kAdapterKernels) {
+    e = lora_prepare();
+  } else if (!(e = experts_few_prepare())) {
+    e = experts_tc_prepare();
+  }
+  if (e) return cuda_fail(e, "cudaFuncSetAttribute");
+  st->ready[set] = true;
+  return Q6_OK;
 }
 int readable_raw(const uint8_t* raw, const uint8_t** src) { return device_readable(raw, src); }
 int encode_row_maps(RowMaps* maps, const void* X, long long n, int K, long long ld) {

@@ -173,7 +173,7 @@ int q6_experts_mmq(int fmt, const void* plane, int E, int M, int K, int swiglu, 
       !aligned(rows, 4))
     return fail(Q6_EALIGN, "plane must be 256-byte, X and its rows 16-byte aligned");
   unsigned int* status;
-  if ((rc = q6::require_device(&status))) return rc;
+  if ((rc = q6::require_device(&status, q6::kExpertKernels))) return rc;
   c.fmt = fmt, c.swiglu = swiglu, c.E = E;
   c.plane = static_cast<const uint8_t*>(plane);
   c.X = X, c.type = type, c.ldx = ldx, c.gather = gather;
@@ -272,7 +272,7 @@ int q6_lora_add(const void* A, const void* B, const float* scale, int type, int 
   const size_t need = (size_t)c.splits * (size_t)items * (size_t)r * 4;
   if (need && (!workspace || workspace_bytes < need))
     return fail(Q6_ESIZE, "the adapters need a workspace of %zu bytes", need);
-  if ((rc = q6::require_device(nullptr))) return rc;
+  if ((rc = q6::require_device(nullptr, q6::kAdapterKernels))) return rc;
   c.A = A, c.B = B, c.scale = scale, c.type = type;
   c.L = L, c.r = r, c.K = K, c.M = M;
   c.X = X, c.xtype = xtype, c.ldx = ldx;
