@@ -559,7 +559,9 @@ int q6_pack_experts(int fmt, const uint8_t *raw, int E, int M, int K, int swiglu
  * of each of its terms (sc * d, dmin * m and their sum), 2^-12 of its
  * super-block's largest possible weight at the least; with binary16 results on
  * the tensor cores it is rounded once, with swiglu to 22 bits. Which kernel
- * runs depends on items and E alone; the two round differently.
+ * runs depends on items and E alone; the two round differently. An infinity in
+ * X makes infinities of the sign of its products, and NaN where a weight (as
+ * rounded) is 0; infinities of both signs, and any NaN, make NaN.
  *   X : device [nx][ldx] of `type` (bf16 or f16), 16-byte aligned, ldx % 8 ==
  *       0, ldx >= K; nx rows (every rows[i] < nx; without gather nx >= items).
  *   Y : device [items][ldy] of the same type, ldy >= M (M / 2 with swiglu);

@@ -15,8 +15,8 @@
 //
 // x is staged once per CTA as binary16 in B-fragment order, each token's 256
 // elements scaled by a power of two (largest value in [2^9, 2^10)), so that
-// bf16's range is kept and bf16 and f16 inputs are exact down to 2^-27 of the
-// largest.
+// bf16's range is kept and bf16 and f16 inputs are exact down to 2^-26 and 2^-23 of
+// the largest. Infinities and NaN stay what they are.
 //
 // A CTA is 8 warps on R blocks of 16 rows times 8/R parts of K; the parts are
 // added through shared memory in a fixed order.
@@ -218,14 +218,17 @@ __device__ __forceinline__ void multiply(const Block<Q6_FMT_Q6K>& b, const uint4
 
 // Stages super-blocks sb0..sb0+count-1 of the `valid` tokens: one warp per
 // (token, super-block), 8 elements a lane, kBatch of them in flight. What is
-// past `valid` stays unwritten: it only meets columns that are not stored.
-template <typename T, int NT>
+// past `valid` stays unwritten: it only meets columns that are not stored. odd:
+// for q4_K set where a token has infinities (see odd_tokens()).
+template <typename T, int kFmt, int NT>
 __device__ __forceinline__ void stage_x(const Args& a, long long first, int valid, int sb0,
-                                        int count, uint4* xs, uint32_t* sums, float* scale) {
+                                        int count, uint4* xs, uint32_t* sums, float* scale,
+                                        int* odd) {
   constexpr int kTok = 8 * NT, kBatch = 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T* X = static_cast<const T*>(a.X) + lane * 8;
   const int total = valid * count;
+  bool mine = false;
   for (int w0 = warp; w0 < total; w0 += kWarps * kBatch) {
     uint4 v[kBatch];
 #pragma unroll
@@ -249,12 +252,10 @@ __device__ __forceinline__ void stage_x(const Args& a, long long first, int vali
         f[2 * i] = p.x, f[2 * i + 1] = p.y;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float m = fabsf(f[i]);
-        if (m < __int_as_float(0x7f800000)) most = fmaxf(most, m);
-      }
+      for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(f[i]));
       // non-negative floats order as their bits
       most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+      if (kFmt == Q6_FMT_Q4K && most == __int_as_float(0x7f800000)) mine = true;
       // 2^e with most * 2^-e in [2^9, 2^10), e within [-116, 118] so that both
       // 2^e and 2^-e are normal
       const int e = min(max((int)(__float_as_uint(most) >> 23) - 127 - 9, -116), 118);
@@ -280,12 +281,68 @@ __device__ __forceinline__ void stage_x(const Args& a, long long first, int vali
       if (lane == 0) scale[sb * kTok + n] = __uint_as_float((uint32_t)(127 + e) << 23);
     }
   }
+  if (kFmt == Q6_FMT_Q4K && mine) *odd = 1;
+}
+
+// The product of one row of q4_K tiles with a row of x that has infinities: what
+// they, and infinite or NaN scales, make of it. The finite rest does not count.
+template <typename T>
+__device__ __forceinline__ float odd_product(const uint8_t* tiles, int row, int sbs, const T* x) {
+  const float inf = __int_as_float(0x7f800000);
+  float sum = 0.0f;
+  for (int u = 0; u < 32 * sbs; ++u) {  // 8 values each
+    const uint8_t* p = tiles + (size_t)(u / 32) * kQ4Tile + row * 16;
+    const float2 d = unpack2<__half>(*reinterpret_cast<const uint32_t*>(p));
+    const uint4 v = *reinterpret_cast<const uint4*>(x + 8 * u);
+    const bool all = !(fabsf(d.x) < inf && fabsf(d.y) < inf);
+    const int c = u / 4 % 8, t = u % 4, j = c % 4;
+    for (int i = 0; i < 8; ++i) {
+      const float2 pair = unpack2<T>(word4(v, i / 2));
+      const float f = i % 2 ? pair.y : pair.x;
+      if (!all && fabsf(f) < inf) continue;
+      const uint32_t w =
+          *reinterpret_cast<const uint32_t*>(p + (1 + 2 * t + c / 4) * 2048 + j * 4);
+      const uint32_t s = p[4 + j], m = p[8 + j], l = p[12 + j];
+      const uint32_t sc = c < 4 ? s & 63 : (l & 15) | (s >> 6) << 4;
+      const uint32_t mn = c < 4 ? m & 63 : l >> 4 | (m >> 6) << 4;
+      const uint32_t q = (w >> (4 * (i % 2 * 4 + i / 2))) & 15;
+      // both terms are exact, so their difference is 0 only where the weight is
+      sum += (d.x * (float)(sc * q) - d.y * (float)mn) * f;
+    }
+  }
+  return sum;
+}
+// The results of q4_K tokens with infinities once more, weight by weight: the MMAs
+// sum a code's terms and the min's apart, and where both come out infinite, or a
+// code is 0, they make NaN of a weight's infinite product. (A NaN makes NaN of all
+// its token's results there as here.) Of items first..last-1 of an expert, this
+// CTA's rows.
+template <typename T, bool kGlu>
+__device__ __forceinline__ void odd_tokens(const Args& a, int expert, long long first,
+                                           long long last) {
+  const int cols = (kGlu ? 8 : 16) * a.row_groups;
+  for (; first < last; ++first) {
+    const T* x = static_cast<const T*>(a.X) + (a.gather ? a.rows[first] : first) * a.ldx;
+    bool here = false;
+    for (int k = threadIdx.x; k < 256 * a.sbs; k += kThreads) here |= isinf(to_f32(x[k]));
+    if (!__syncthreads_or(here)) continue;
+    for (int c = threadIdx.x; c < cols; c += kThreads) {
+      const int m = (int)blockIdx.x * cols + c;
+      if (m >= a.out) continue;
+      const int row = (int)blockIdx.x * a.row_groups * 16 + (kGlu ? c / 8 * 16 + c % 8 : c);
+      const uint8_t* tiles =
+          a.plane + ((size_t)expert * a.bands + row / kBand) * (size_t)a.sbs * kQ4Tile;
+      float y = odd_product(tiles, row % kBand, a.sbs, x);
+      if (kGlu) y = y / (1.0f + __expf(-y)) * odd_product(tiles, row % kBand + 8, a.sbs, x);
+      static_cast<T*>(a.Y)[first * a.ldy + m] = from_f32<T>(y);
+    }
+  }
 }
 
 // The products of up to 8 * NT tokens of one expert with this CTA's rows.
 template <typename T, int kFmt, bool kGlu, int NT>
 __device__ __forceinline__ void run(const Args& a, int expert, long long first, int valid,
-                                    uint4* smem) {
+                                    uint4* smem, int* odd) {
   constexpr int kTile = kFmt == Q6_FMT_Q4K ? kQ4Tile : kQ6Tile;
   constexpr int kTok = 8 * NT;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -310,7 +367,7 @@ __device__ __forceinline__ void run(const Args& a, int expert, long long first, 
       for (int k = 1; k <= kAhead && part + k * parts < count; ++k)
         prefetch_rows(tiles + (size_t)(sb0 + part + k * parts) * kTile, row0 % kBand, lane);
     if (sb0) __syncthreads();  // the last stage has been read
-    stage_x<T, NT>(a, first, valid, sb0, count, xs, sums, scale);
+    stage_x<T, kFmt, NT>(a, first, valid, sb0, count, xs, sums, scale, odd);
     __syncthreads();
     if (active) {
       for (int sb = part; sb < count; sb += parts) {
@@ -356,8 +413,13 @@ __device__ __forceinline__ void run(const Args& a, int expert, long long first, 
 }
 
 template <typename T, int kFmt, bool kGlu>
-__global__ void __launch_bounds__(kThreads, 2) experts_few_kernel(const Args a) {
+__device__ __forceinline__ void experts_few(const Args& a) {
   extern __shared__ uint4 smem[];
+  __shared__ int odd;
+  if (kFmt == Q6_FMT_Q4K) {
+    if (threadIdx.x == 0) odd = 0;
+    __syncthreads();
+  }
   griddep_wait();
   griddep_launch_dependents();
   // the blockIdx.y-th expert that has items
@@ -386,23 +448,36 @@ __global__ void __launch_bounds__(kThreads, 2) experts_few_kernel(const Args a) 
   int left_items = (int)(a.offsets[expert + 1] - i0);
   for (long long first = i0; left_items > 0;) {
     if (left_items <= 8) {
-      run<T, kFmt, kGlu, 1>(a, expert, first, left_items, smem);
+      run<T, kFmt, kGlu, 1>(a, expert, first, left_items, smem, &odd);
       break;
     }
     const int n = min(left_items, 16);
-    run<T, kFmt, kGlu, 2>(a, expert, first, n, smem);
+    run<T, kFmt, kGlu, 2>(a, expert, first, n, smem, &odd);
     first += n;
     left_items -= n;
   }
+  if (kFmt == Q6_FMT_Q4K && odd) odd_tokens<T, kGlu>(a, expert, i0, a.offsets[expert + 1]);
+}
+
+// Two kernels, for the arguments: as a grid constant they cost q6_K 15.9 instead of
+// 13.7 us (16 items over 32 experts of 2056 x 1536), as plain ones q4_K, which has
+// odd_tokens() behind it, 25.1 instead of 22.0 us (8 over 8 of 4096 x 4096).
+template <typename T, bool kGlu>
+__global__ void __launch_bounds__(kThreads, 2)
+experts_few_q4_kernel(const __grid_constant__ Args a) {
+  experts_few<T, Q6_FMT_Q4K, kGlu>(a);
+}
+template <typename T, bool kGlu>
+__global__ void __launch_bounds__(kThreads, 2) experts_few_q6_kernel(const Args a) {
+  experts_few<T, Q6_FMT_Q6K, kGlu>(a);
 }
 
 typedef void (*Kernel)(const Args);
 template <typename T>
 Kernel pick_t(int fmt, int swiglu) {
   if (fmt == Q6_FMT_Q4K)
-    return swiglu ? experts_few_kernel<T, Q6_FMT_Q4K, true>
-                  : experts_few_kernel<T, Q6_FMT_Q4K, false>;
-  return swiglu ? experts_few_kernel<T, Q6_FMT_Q6K, true> : experts_few_kernel<T, Q6_FMT_Q6K, false>;
+    return swiglu ? experts_few_q4_kernel<T, true> : experts_few_q4_kernel<T, false>;
+  return swiglu ? experts_few_q6_kernel<T, true> : experts_few_q6_kernel<T, false>;
 }
 Kernel pick(int type, int fmt, int swiglu) {
   return type == Q6_TYPE_BF16 ? pick_t<__nv_bfloat16>(fmt, swiglu) : pick_t<__half>(fmt, swiglu);
