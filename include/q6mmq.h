@@ -592,7 +592,8 @@ int q6_moe_combine(const void *Y, int type, int64_t ldy, const int32_t *pos, con
  *       f32 [L]. K % 32 == 0, r % 8 == 0, r <= Q6_LORA_MAX_RANK. K and M up to
  *       2^30, items up to 2^31 - 256.
  *   X : device [.][ldx] of `xtype` (f32, bf16, f16), 16-byte aligned rows,
- *       ldx >= K.
+ *       ldx >= K. Infinities and NaN give what their products give; one in A
+ *       or B may give NaN instead of an infinity.
  *   offsets, rows : the grouping of the tokens by adapter (per_row 1, groups
  *       L, N = items).
  *   Y, out : device f32, ldy, ldo >= M; out may be Y (in place).
