@@ -20,7 +20,7 @@ template <int kRaw>
 __global__ void __launch_bounds__(kBand)
 expert_pack_kernel(const uint8_t* raw, int M, int swiglu, int bands, int sbs, uint8_t* plane) {
   constexpr int kTile = kRaw == kQ4Raw ? kQ4Tile : kQ6Tile;
-  constexpr int kPitch = (kRaw + 3) / 4 * 4 + 4;  // odd multiple of 4 bytes
+  constexpr int kPitch = ((kRaw + 3) / 4 | 1) * 4;  // odd multiple of 4 bytes
   __shared__ uint8_t blk[kBand * kPitch];
   const size_t tile = blockIdx.x;  // [expert][band][super-block]
   const int sb = (int)(tile % sbs);
