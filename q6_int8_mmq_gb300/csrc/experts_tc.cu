@@ -240,7 +240,7 @@ __device__ __forceinline__ void store_tiles_t(uint32_t addr, uint32_t a, uint32_
 }
 
 // ------------------------------------------------------------ dequantising ---
-constexpr uint32_t kH2_2m15 = 0x02000200u, kH2_512 = 0x60006000u, kH2_256 = 0x5C005C00u,
+constexpr uint32_t kH2_2m11 = 0x10001000u, kH2_2m15 = 0x02000200u, kH2_512 = 0x60006000u, kH2_256 = 0x5C005C00u,
                    kH2_m2p19 = 0x80208020u,
                    kH2_1_16 = 0x2C002C00u, kH2_1056 = 0x64206420u;
 
@@ -293,7 +293,7 @@ struct Half<Q6_FMT_Q4K> {
     for (int t = 0; t < 4; ++t) q[t] = p[(1 + 2 * t + h) * kBand];
     const float2 dd = unpack2<__half>(head.x);
     df = dd.x * inv, dmf = -dd.y * inv;
-    d = splat_h2(df * (wide ? 32768.0f : 512.0f)), dm = splat_h2(dmf);
+    d = splat_h2(df * (wide ? 32768.0f : 512.0f)), dm = splat_h2(dmf * (wide ? 2048.0f : 1.0f));
     sc = h ? (head.w & 0x0F0F0F0Fu) | ((head.y >> 2) & 0x30303030u) : head.y & 0x3F3F3F3Fu;
     mn = h ? ((head.w >> 4) & 0x0F0F0F0Fu) | ((head.z >> 2) & 0x30303030u) : head.z & 0x3F3F3F3Fu;
   }
@@ -303,8 +303,9 @@ struct Half<Q6_FMT_Q4K> {
     // sc * d * 2^9, or sc * 2^9
     const uint32_t s = hmul2u(hsub2u(byte_h2(sc, cc), kH2_1024), kWide ? kH2_512 : d);
     const uint32_t s16 = hmul2u(s, kH2_1_16);  // for codes four bits up
-    uint32_t m = hmul2u(hsub2u(byte_h2(mn, cc), kH2_1024), dm);  // -dmin * m
-    if (!kWide) m = hmul2u(m, kH2_2m15);
+    // -dmin * m (dm, which kWide makes 2^11 larger, is no subnormal either way)
+    uint32_t m = hsub2u(byte_h2(mn, cc), kH2_1024);
+    m = kWide ? hmul2u(hmul2u(m, kH2_2m11), dm) : hmul2u(hmul2u(m, dm), kH2_2m15);
     auto weight = [&](uint32_t code, uint32_t by) {
       return kWide ? hfma2u(hmul2u(code, by), d, m) : hfma2u(code, by, m);
     };

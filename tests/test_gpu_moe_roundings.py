@@ -25,7 +25,7 @@ def blocks(gen, fmt, E, M, K, spread):
     return raw.flatten(2)
 
 
-def rounding_squares(raw, fmt, kernel, type, glu):
+def rounding_squares(raw, fmt, kernel, type, glu, wide=False):
     """For each weight of raw [rows, bytes] an upper bound of the expected square of the error it
     enters the sums with. A rounding to 11 bits is uniform within half a step, at most 2^-11 of the
     value: a third of that, squared. What is rounded:
@@ -34,35 +34,36 @@ def rounding_squares(raw, fmt, kernel, type, glu):
                           and the weight
       tensor cores, f16   the weight; for q4_K its min's offset too, at most 2^-12 of sc * d. With
                           gate and up rows nothing (22 bits).
-    And half of the smallest binary16 step, at most 2^-19 of a row's largest possible weight, for
-    the min and the weight."""
+    And on the tensor cores half of the smallest binary16 step, at most 2^-34 of a row's largest
+    possible weight, or 2^-19 in bf16 products of rows not marked to keep a wide range, for the min
+    and the weight."""
     w = ref.dequantise(raw, fmt)
     b = raw.reshape(raw.shape[0], -1, ref.BLOCK[fmt])
-    at = 0 if fmt == "q4_K" else 208
-    d = np.abs(np.ascontiguousarray(b[..., at:at + 2]).view(np.float16).astype(np.float64))[..., 0]
+
+    def half(at):
+        return np.abs(np.ascontiguousarray(b[..., at:at + 2]).view(np.float16).astype(np.float64))[..., 0]
+
     one = (2.0 ** -11) ** 2 / 3
+    d = half(0 if fmt == "q4_K" else 208)
     if kernel == "experts_few":
         if fmt == "q4_K":
             return np.zeros_like(w)
         return np.where(np.abs(w) > 2048 * np.repeat(d, 256, 1), one * w ** 2, 0.0)
+    largest = (945 * d + 63 * half(2) if fmt == "q4_K" else 4096 * d).max(1)
+    floor = 2.0 ** -34 if wide or type == "f16" else 2.0 ** -19
+    sq = 2 * (floor * largest[:, None]) ** 2 / 3 + np.zeros_like(w)
     if type == "f16" and glu:
-        return np.zeros_like(w)
-    if fmt == "q4_K":
-        no_min, full = b.copy(), b.copy()
-        no_min[..., 2:4] = 0
-        full[..., 2:4], full[..., 16:] = 0, 255
-        code = ref.dequantise(no_min.reshape(raw.shape), fmt)
-        step = ref.dequantise(full.reshape(raw.shape), fmt) / 15          # sc * d
-        dmin = np.abs(np.ascontiguousarray(b[..., 2:4]).view(np.float16).astype(np.float64))[..., 0]
-        largest = (945 * d + 63 * dmin).max(1)
-        if type == "f16":
-            sq = one * w ** 2 + (2.0 ** -12 * step) ** 2 / 3
-        else:
-            sq = one * (code ** 2 + (code - w) ** 2 + w ** 2)
-    else:
-        largest = (4096 * d).max(1)
-        sq = (1 if type == "f16" else 2) * one * w ** 2
-    return sq + 2 * (2.0 ** -19 * largest[:, None]) ** 2 / 3
+        return sq
+    if fmt == "q6_K":
+        return sq + (1 if type == "f16" else 2) * one * w ** 2
+    no_min, full = b.copy(), b.copy()
+    no_min[..., 2:4] = 0
+    full[..., 2:4], full[..., 16:] = 0, 255
+    code = ref.dequantise(no_min.reshape(raw.shape), fmt)
+    step = ref.dequantise(full.reshape(raw.shape), fmt) / 15          # sc * d
+    if type == "f16":
+        return sq + one * w ** 2 + (2.0 ** -12 * step) ** 2 / 3
+    return sq + one * (code ** 2 + (code - w) ** 2 + w ** 2)
 
 
 def hold(rng, fmt, type, counts, M, K, swiglu, gather, spread, columns=None):
@@ -148,3 +149,54 @@ def test_many_tiles_of_many_experts(rng, fmt, type, swiglu):
 @pytest.mark.parametrize("xtype", ["bf16", "f16"])
 def test_lora_f16_adapters_of_16_bit_x(rng, N, L, r, K, M, xtype):
     run_lora(rng, N, L, r, K, M, xtype, "f16")
+
+
+@pytest.mark.parametrize("fmt", ["q4_K"])
+@pytest.mark.parametrize("type", ["bf16", "f16"])
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("N,E", [(240, 2), (40, 48)])
+@pytest.mark.parametrize("step", [2, 3])
+def test_super_blocks_far_apart_keep_their_bits(rng, fmt, type, swiglu, N, E, step):
+    """Rows whose super-blocks differ by up to 2^21, with scales of any mantissa, and tokens that look
+    at one super-block each: each super-block's results as a whole within 1.1 times the error of one
+    rounding and the stated roundings of the weights (over thousands of values), whose smallest is
+    half of a binary16 step or 2^-34 of the row's largest possible weight."""
+    M, K = 256, 2048
+    raw = blocks(torch.Generator().manual_seed(int(rng.integers(1 << 30))), fmt, E, M, K, 0.0).numpy()
+    b = raw.reshape(E, M, K // 256, ref.BLOCK[fmt])
+    level = 2.0 ** (6 - step * np.arange(K // 256))         # down to 2^-15
+
+    def scales():
+        return (level * rng.uniform(1, 2, b.shape[:3])).astype(np.float16)[..., None].view(np.uint8)
+
+    at = 0 if fmt == "q4_K" else 208
+    b[..., at:at + 2] = scales()
+    if fmt == "q4_K":
+        b[..., 2:4] = scales()
+    x, mine = np.zeros((N, K)), np.arange(N) % (K // 256)
+    for n in range(N):      # results of about 16, so that binary16 ones have all their bits
+        x[n, 256 * mine[n]:256 * mine[n] + 256] = rng.standard_normal(256) / level[mine[n]] / 256
+    X = cuda(x, type)
+    x = f64(X)
+    ids = rng.integers(0, E, (N, 1))
+    w = q6.pack_experts(cuda(raw), fmt, E, M, K, swiglu=swiglu)
+    Y, path = q6.experts_mmq(w, X, q6.group_rows(cuda(ids.astype(np.int32)), E))
+    assert path == ("experts_tc" if N > E else "experts_few")
+    want, _ = ref.experts(raw, fmt, x, ids, E, swiglu, True, type)
+    rounded = torch.from_numpy(want).to(TYPE[type]).double().numpy()
+    expected, got = (rounded - want) ** 2, f64(Y)
+    fits = np.isfinite(rounded) & (np.abs(rounded) < (60000 if type == "f16" else np.inf))
+    assert fits.mean() > 0.9 and np.isfinite(got[fits]).all()
+    offsets, token, _ = ref.group(ids, E)
+    for e in range(E):
+        i = np.arange(offsets[e], offsets[e + 1])
+        var = x[token[i]] ** 2 @ rounding_squares(raw[e], fmt, path, type, swiglu, True).T
+        if swiglu:
+            g, u = np.split(x[token[i]] @ ref.dequantise(raw[e], fmt).T, 2, axis=1)
+            s = 0.5 + 0.5 * np.tanh(g / 2)
+            slope = s * (1 + g * (1 - s))
+            var = (slope * u) ** 2 * var[:, :M // 2] + (g * s) ** 2 * var[:, M // 2:]
+        expected[i] += var
+    for s in range(K // 256):
+        of = (mine[token] == s)[:, None] & fits
+        assert np.linalg.norm((got - want)[of]) <= 1.1 * np.sqrt(expected[of].sum()), s
