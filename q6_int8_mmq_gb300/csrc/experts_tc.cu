@@ -242,7 +242,8 @@ __device__ __forceinline__ void store_tiles_t(uint32_t addr, uint32_t a, uint32_
 // ------------------------------------------------------------ dequantising ---
 constexpr uint32_t kH2_2m11 = 0x10001000u, kH2_2m15 = 0x02000200u, kH2_512 = 0x60006000u, kH2_256 = 0x5C005C00u,
                    kH2_m2p19 = 0x80208020u,
-                   kH2_1_16 = 0x2C002C00u, kH2_1056 = 0x64206420u;
+                   kH2_1_16 = 0x2C002C00u, kH2_4 = 0x44004400u,
+                   kH2_4_32nd = 0x44204420u;  // 4 + 32 / 256
 
 // A byte of a word as a binary16 pair, plus 1024.
 __device__ __forceinline__ uint32_t byte_h2(uint32_t w, int i) {
@@ -395,11 +396,12 @@ struct Half<Q6_FMT_Q6K> {
     }
   }
   // The scale sc * d as two binary16 terms: their sum and so the weight is
-  // rounded once.
+  // rounded once. (256 times larger, and the code as much smaller, so that the
+  // second term of a small super-block keeps its bits.)
   __device__ __forceinline__ void expand_once(int cc, uint32_t (&out)[16]) const {
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
-      const float s = df * (byte_f32(sc[sub], cc) - 128.0f);
+      const float s = 256.0f * df * (byte_f32(sc[sub], cc) - 128.0f);
       const uint32_t hi = splat_h2(s), lo = splat_h2(s - unpack2<__half>(hi).x);
 #pragma unroll
       for (int t = 2 * sub; t < 2 * sub + 2; ++t) {
@@ -407,7 +409,7 @@ struct Half<Q6_FMT_Q6K> {
         q6_pairs(word4(q[t], cc), cc < 2 ? high[t].x : high[t].y, cc % 2, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t c = hsub2u(v[i] | kH2_1024, kH2_1056);  // q - 32
+          const uint32_t c = hsub2u(v[i] | kH2_4, kH2_4_32nd);  // (q - 32) / 256
           out[4 * t + i] = hfma2u(c, hi, hmul2u(c, lo));
         }
       }
@@ -418,7 +420,7 @@ struct Half<Q6_FMT_Q6K> {
                                               uint32_t (&rest)[16]) const {
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
-      const float s = df * (byte_f32(sc[sub], cc) - 128.0f);
+      const float s = 256.0f * df * (byte_f32(sc[sub], cc) - 128.0f);
       const uint32_t hi = splat_h2(s), lo = splat_h2(s - unpack2<__half>(hi).x);
 #pragma unroll
       for (int t = 2 * sub; t < 2 * sub + 2; ++t) {
@@ -426,7 +428,7 @@ struct Half<Q6_FMT_Q6K> {
         q6_pairs(word4(q[t], cc), cc < 2 ? high[t].x : high[t].y, cc % 2, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t c = hsub2u(v[i] | kH2_1024, kH2_1056);  // q - 32
+          const uint32_t c = hsub2u(v[i] | kH2_4, kH2_4_32nd);  // (q - 32) / 256
           const uint32_t w = hfma2u(c, hi, hmul2u(c, lo));
           out[4 * t + i] = w;
           // c * hi - w is exact (17 bits less the upper 11)

@@ -151,7 +151,7 @@ def test_lora_f16_adapters_of_16_bit_x(rng, N, L, r, K, M, xtype):
     run_lora(rng, N, L, r, K, M, xtype, "f16")
 
 
-@pytest.mark.parametrize("fmt", ["q4_K"])
+@pytest.mark.parametrize("fmt", ["q4_K", "q6_K"])
 @pytest.mark.parametrize("type", ["bf16", "f16"])
 @pytest.mark.parametrize("swiglu", [False, True])
 @pytest.mark.parametrize("N,E", [(240, 2), (40, 48)])
