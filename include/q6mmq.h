@@ -556,9 +556,14 @@ int q6_pack_experts(int fmt, const uint8_t *raw, int E, int M, int K, int swiglu
  *   Y[i] = W[e(i)] x,  x = X[rows[i]] (gather != 0) or X[i],
  * for every sorted item i; with swiglu weights Y[i] = silu(gate) * up. Items
  * of no group get zeros. A weight enters the f32 sums with 11 significant bits
- * of each of its terms (sc * d, dmin * m and their sum), 2^-12 of its
- * super-block's largest possible weight at the least; with binary16 results on
- * the tensor cores it is rounded once, with swiglu to 22 bits. Which kernel
+ * of each of its terms (sc * d, dmin * m and their sum); with binary16 results
+ * on the tensor cores it is rounded once, with swiglu to 22 bits. On the tensor
+ * cores each of these roundings may also be off by 2^-12 of its super-block's
+ * largest possible weight (945 |d| + 63 |dmin|, 4096 |d|), or by 2^-34 of its
+ * row's where that is more, which it is in super-blocks 2^22 below the row's
+ * largest; and bf16 values of X below 2^-31 of their row's largest one lose
+ * bits, as those below 2^-26 (f16: 2^-23) of the largest of their 256 do with
+ * few items. Which kernel
  * runs depends on items and E alone; the two round differently. An infinity in
  * X makes infinities of the sign of its products, and NaN where a weight (as
  * rounded) is 0; infinities of both signs, and any NaN, make NaN.
@@ -578,7 +583,8 @@ int q6_experts_mmq(int fmt, const void *plane, int E, int M, int K, int swiglu, 
                    size_t workspace_bytes, int *path_out, q6_stream_t s);
 
 /* out[n] = shared[n] + sum over j of weights[n][j] * Y[pos[n][j]], in f32,
- * rounded once to Y's type (bf16 or f16); a slot with pos < 0 adds nothing.
+ * rounded once to Y's type (bf16 or f16); a slot with pos < 0 adds nothing,
+ * every other pos is the number of a row of Y (not checked).
  *   Y [items][ldy], out [N][ldo] of `type`; shared f32 [N][lds] or NULL; all
  *   leading dimensions >= M. out must not overlap Y or shared. */
 int q6_moe_combine(const void *Y, int type, int64_t ldy, const int32_t *pos, const float *weights,
@@ -596,7 +602,8 @@ int q6_moe_combine(const void *Y, int type, int64_t ldy, const int32_t *pos, con
  *       or B may give NaN instead of an infinity.
  *   offsets, rows : the grouping of the tokens by adapter (per_row 1, groups
  *       L, N = items).
- *   Y, out : device f32, ldy, ldo >= M; out may be Y (in place).
+ *   Y, out : device f32, ldy, ldo >= M; out may be Y (in place), and overlaps
+ *       nothing else.
  *   workspace : device, 16-byte aligned, at least q6_lora_workspace_bytes()
  *       (NULL when that is 0: up to 8 tokens an adapter on average). */
 int q6_lora_workspace_bytes(int64_t items, int L, int r, int K, size_t *bytes);

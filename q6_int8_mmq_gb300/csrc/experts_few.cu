@@ -25,7 +25,7 @@
 // few tiles, instruction issue with many (about 260 instructions per 16 x 256
 // weights at 8 tokens; issue 46 % and DRAM 29 % busy at 8 experts of 4096 x 4096),
 // before the weight bytes (0.5625 / 0.82 a weight). One token, 8 of 64 q4_K experts
-// of 1536 x 2048 with swiglu, 14.2 MB: 8.2 us out of a graph. Persistent CTAs on
+// of 1536 x 2048 with swiglu, 14.2 MB: 8.6 us out of a graph. Persistent CTAs on
 // runs of rows, and three CTAs an SM, spilled and were not faster.
 #include "moe_internal.cuh"
 
@@ -36,9 +36,10 @@ constexpr int kThreads = 256;
 constexpr int kWarps = 8;
 constexpr int kSmem = 104 * 1024;  // two CTAs an SM
 
+constexpr int kAhead = 4;  // see prefetch_rows()
+
 // Shared bytes of one super-block of 8 * NT staged tokens: x, the chunk-sum
 // pairs, the scales.
-constexpr int kAhead = 4;  // see prefetch_rows()
 template <int NT>
 constexpr int kSbBytes = 8 * NT * (512 + 32 + 4);
 // Super-blocks staged at a time (the partial sums reuse the space).

@@ -20,17 +20,19 @@
 // a bf16 Y. That leaves binary16 2^9 of range above its smallest normal number, so
 // 32 rows of which one has super-blocks whose weights are less than 2^-7 of its
 // largest (marked when packed) go another way: sc * q exact, times d in the fused
-// multiply-add, 2^15 times larger. (Rates, cycles a warp instruction of one scheduler: binary16 pairs 2,
-// integer logic and shifts 2, on two pipes; f32 1. That way is 3.7 instead of 2.8
-// instructions a pair, and 8 experts of 4096 x 4096 took 28.8 instead of 27.0 us.) For a binary16 Y that would
-// show, so there the weight is rounded once (q4_K in f32, 2.6 instructions a
-// weight; q6_K with sc * d in two terms, 3.4).
+// multiply-add, 2^15 times larger. (Rates, cycles a warp instruction of one
+// scheduler: binary16 pairs 2, integer logic and shifts 2, on two pipes; f32 1. That
+// way is 3.7 instead of 2.8 instructions a pair, and 8 experts of 4096 x 4096 took
+// 28.8 instead of 27.0 us.) The smallest step there is 2^-33 of a row's largest
+// possible weight: half of it is 2^-12 of a super-block's down to 2^-22 of the row's.
+// For a binary16 Y that would show, so there the weight is rounded once (q4_K in f32,
+// 2.6 instructions a weight; q6_K with sc * d in two terms, 3.4).
 // In a binary16 silu(gate) * up the roundings of both products would still
 // add up to 1.7 times that of Y; there a weight is a pair of binary16 values
 // in two A slots, and every x tile meets both.
 //
 // x comes as binary16 in item order: bf16 rows scaled by a power of two (exact
-// down to 2^-32 of the row's largest value), gathered ones copied, by a kernel
+// down to 2^-31 of the row's largest value), gathered ones copied, by a kernel
 // before this one; binary16 rows that are in order are read where they are.
 // TMA loads them as 128-byte-swizzled K-major tiles. (Gathering with TMA's own
 // row gather, 4 rows a request, was measured at about 60 cycles a request,
@@ -162,9 +164,10 @@ __device__ __forceinline__ void commit_own(uint64_t* bar) {
           smem_u32(bar))
       : "memory");
 }
-// Arrives on `bar` of CTA 0 of the pair after this warp's tcgen05 loads or stores, which the tcgen05 waits and fences around the barrier order;
-// nothing else is published, so the arrival needs no release (one of cluster
-// scope was measured at 1300 cycles behind the packed-weight reads).
+// Arrives on `bar` of CTA 0 of the pair after this warp's tcgen05 loads or stores,
+// which the tcgen05 waits and fences around the barrier order; nothing else is
+// published, so the arrival needs no release (one of cluster scope was measured at
+// 1300 cycles behind the packed-weight reads).
 __device__ __forceinline__ void arrive_leader_tmem(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .b32 ra;\n\t"
@@ -240,23 +243,22 @@ __device__ __forceinline__ void store_tiles_t(uint32_t addr, uint32_t a, uint32_
 }
 
 // ------------------------------------------------------------ dequantising ---
-constexpr uint32_t kH2_2m11 = 0x10001000u, kH2_2m15 = 0x02000200u, kH2_512 = 0x60006000u, kH2_256 = 0x5C005C00u,
-                   kH2_m2p19 = 0x80208020u,
-                   kH2_1_16 = 0x2C002C00u, kH2_4 = 0x44004400u,
-                   kH2_4_32nd = 0x44204420u;  // 4 + 32 / 256
+constexpr uint32_t kH2_2m11 = 0x10001000u, kH2_2m15 = 0x02000200u, kH2_512 = 0x60006000u,
+                   kH2_256 = 0x5C005C00u, kH2_m2p19 = 0x80208020u, kH2_1_16 = 0x2C002C00u,
+                   kH2_4 = 0x44004400u, kH2_4_8th = 0x44204420u;  // 4 + 32 / 256
 
 // A byte of a word as a binary16 pair, plus 1024.
 __device__ __forceinline__ uint32_t byte_h2(uint32_t w, int i) {
   return __byte_perm(w, 0x64u, 0x4040u | i << 8 | i);
 }
-// v * 2^k as a binary16 pair (both halves).
+// v as a binary16 pair (both halves).
 __device__ __forceinline__ uint32_t splat_h2(float v) {
   const __half2 h = __float2half2_rn(v);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The same in f32: a code in bits p.. of x, with the exponent of 2^(23 - p)
-// above it, is the float 2^(23 - p) + code.
+// A code as f32: in bits p.. of x, with the exponent of 2^(23 - p) above it, it is
+// the float 2^(23 - p) + code.
 __device__ __forceinline__ float code_f32(uint32_t x, uint32_t mask, uint32_t magic) {
   return __uint_as_float((x & mask) | magic);
 }
@@ -409,7 +411,7 @@ struct Half<Q6_FMT_Q6K> {
         q6_pairs(word4(q[t], cc), cc < 2 ? high[t].x : high[t].y, cc % 2, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t c = hsub2u(v[i] | kH2_4, kH2_4_32nd);  // (q - 32) / 256
+          const uint32_t c = hsub2u(v[i] | kH2_4, kH2_4_8th);  // (q - 32) / 256
           out[4 * t + i] = hfma2u(c, hi, hmul2u(c, lo));
         }
       }
@@ -428,7 +430,7 @@ struct Half<Q6_FMT_Q6K> {
         q6_pairs(word4(q[t], cc), cc < 2 ? high[t].x : high[t].y, cc % 2, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t c = hsub2u(v[i] | kH2_4, kH2_4_32nd);  // (q - 32) / 256
+          const uint32_t c = hsub2u(v[i] | kH2_4, kH2_4_8th);  // (q - 32) / 256
           const uint32_t w = hfma2u(c, hi, hmul2u(c, lo));
           out[4 * t + i] = w;
           // c * hi - w is exact (17 bits less the upper 11)
@@ -439,7 +441,8 @@ struct Half<Q6_FMT_Q6K> {
   }
 };
 
-// x / (1 + exp(-x)), within 2^-20 (0 below -87, where it is under 2^-118).
+// x / (1 + exp(-x)), within the exponential's 2 + 1.2 |x| and the division's 2 units of
+// 2^-23: 2^-20 where x is above -3, 2^-16 at -87 (0 below that, where it is under 2^-118).
 __device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
 
 // ---------------------------------------------------------------- schedule ---

@@ -1,7 +1,7 @@
 // Low-rank adapters of many requests beside a shared projection:
 //   out[n] = Y[n] + scale[a] * B[a] (A[a] x[n]),  a the adapter of token n.
-// Tokens come grouped by adapter, so a tile of up to 16 or 32 tokens shares
-// one A and one B.
+// Tokens come grouped by adapter, so a tile of tokens (up to 4 where there are few, else
+// 64 for A and 32 for B) shares one A and one B.
 //
 // Shrink: T[i] = scale[a] A[a] x (K long, r wide). Expand: out = Y + B[a] T (r
 // long, M wide).

@@ -121,9 +121,10 @@ __device__ __forceinline__ uint32_t word4(const uint4& v, int i) {
 //     12: the 16 scales plus 128, those of even sub-blocks first; then d (f16)
 //     of the 128 rows.
 // After the tiles, f32 [E][bands * 128]: 2^e of each row, with e such that
-// every weight of the row times 2^-e is below 2^10 (as binary16 the large ones
-// keep 11 bits, and nothing above 2^-34 of them is lost); -2^e for 32 rows of
-// which one has super-blocks far smaller than its largest (experts_tc.cu).
+// every weight of the row times 2^-e is below 2^10; -2^e for 32 rows of which one
+// has super-blocks far smaller than its largest. As binary16 at that size a weight is
+// rounded to 11 bits, or by at most 2^-34 of the row's largest possible one; bf16
+// products of other rows take it 2^15 smaller, by at most 2^-19 (experts_tc.cu).
 //
 // Plane rows: the weight's rows, or for gate/up weights (M = 2H raw rows, the
 // H gate rows first) blocks of 16: 8 gate rows, then their 8 up rows.

@@ -369,7 +369,8 @@ def experts_mmq(w: ExpertWeights, X, groups: Groups, gather: bool = True, out=No
 def moe_combine(Y, pos, weights, shared=None, out=None, stream=None):
     """out [N, M] = shared + the weighted sum of each token's rows of Y
     [items, M] (bf16 or f16): pos [N, topk] int32 are their places (-1 adds
-    nothing), weights [N, topk] f32, shared f32 [N, M] or None."""
+    nothing; others are below items, which is not checked), weights [N, topk]
+    f32, shared f32 [N, M] or None."""
     f32, i32 = _f32_i32()
     code = _type(Y, "Y", half=True)
     items = _rows2d(Y, "Y")
