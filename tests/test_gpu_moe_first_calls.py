@@ -32,8 +32,10 @@ def timed(call):
 
 
 def run(code):
-    r = subprocess.run([sys.executable, "-c", SETUP + code], cwd=ROOT, capture_output=True, text=True,
-                       timeout=300)
+    # kernels are loaded when they are first named, as by default
+    env = dict(os.environ, CUDA_MODULE_LOADING="LAZY")
+    r = subprocess.run([sys.executable, "-c", SETUP + code], cwd=ROOT, env=env, capture_output=True,
+                       text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
     return r.stdout
 
