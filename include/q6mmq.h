@@ -612,6 +612,85 @@ int q6_lora_add(const void *A, const void *B, const float *scale, int type, int 
                 const int32_t *rows, int64_t items, const float *Y, int64_t ldy, float *out,
                 int64_t ldo, void *workspace, size_t workspace_bytes, q6_stream_t s);
 
+/* ------------------------------------------------------------------------
+ * The 8-bit steps around the projections: the norm and the gated activation
+ * that end in quantised activations, and products of e4m3 blocks. No
+ * counterpart in the pages. The conventions at the top of this file hold;
+ * nothing is allocated and no call needs a workspace.
+ *
+ * Quantised rows come in two forms. Neither form's codes depend on the order
+ * of a sum.
+ *   int8: Xq, da, Xh, us exactly as q8_quantize_act_sums() lays them out, K a
+ *       multiple of 256 (Xq or Xh may be NULL, and us). Per 32 values t of a
+ *       row d = max|t| / 127, code = round(t / d), halves away from zero.
+ *   e4m3: xq [N][K] (sign, 4 exponent bits of bias 7, 3 mantissa bits; largest
+ *       448, no infinities), sx f32 [ceil(K / 128)][ldsx], ldsx = N rounded up
+ *       to 4 (q6_f8_act_bytes), K a multiple of 16. Per 128 values (the last
+ *       block of a row may have fewer) d = max|t| / 448, code = t * (448 /
+ *       max|t|) rounded to the nearest e4m3 value, ties to even.
+ *   The scale is d, times the row's 1 / rms for the norm. A block that holds
+ *   an infinity or a NaN gets codes 0 and a NaN scale; an e4m3 block whose
+ *   max|t| is below 2^-100 codes and scale 0. Scales past column N are not
+ *   written.
+ * Rows of X, W, residual and h: device, of a Q6_TYPE_*, every row 16-byte
+ * aligned (leading dimensions are in elements). Xq, xq, da, sx, Xh, us:
+ * 16-byte aligned. Outputs overlap nothing else, but for h. */
+#define Q6_NORM_MAX_K 131072
+
+#define Q6_PATH_F8_FEW 15 /* product of e4m3 blocks, weight rows on the tensor cores' lanes */
+#define Q6_PATH_F8_TC 16  /* product of e4m3 blocks, tokens on the tensor cores' lanes */
+
+/* Bytes of e4m3 activations (N >= 0, K % 16 == 0) and their scale row length. */
+int q6_f8_act_bytes(int N, int K, size_t *xq_bytes, size_t *sx_bytes, int *ldsx);
+/* Bytes of an e4m3 weight (M >= 1, K % 16 == 0): wq [M][K] as above, sw f32
+ * [ceil(M / 128)][ceil(K / 128)], a scale for each block of 128 x 128. */
+int q6_f8_weight_bytes(int M, int K, size_t *wq_bytes, size_t *sw_bytes);
+
+/* X [N][ldx] of `type` -> e4m3 rows. */
+int q6_f8_quantize_act(const void *X, int type, int N, int K, int64_t ldx, uint8_t *xq, float *sx,
+                       q6_stream_t s);
+/* W [M][ldw] of `type` -> e4m3 blocks, max|t| over the 128 x 128 values of each. */
+int q6_f8_quantize_weights(const void *W, int type, int M, int K, int64_t ldw, uint8_t *wq,
+                           float *sw, q6_stream_t s);
+
+/* The root-mean-square norm of a residual stream:
+ *   h = X + residual (h = X where residual is NULL), in f32
+ *   y = h / sqrt(mean(h^2) + eps) * weight, quantised: t = h * weight.
+ * The h that is stored is rounded to rtype; the norm is of the h before that.
+ *   residual [N][ldr] of rtype, or NULL (rtype, ldr, ldh are then not looked
+ *       at and h is NULL).
+ *   h : [N][ldh] of rtype, receives h; may be residual (in place).
+ *   weight [K] of wtype, 16-byte aligned.
+ *   eps: positive, a normal f32. K <= Q6_NORM_MAX_K.
+ * The squares of a row are summed in f32: a row whose sum is above f32's range
+ * is that of an infinite norm (scales 0, NaN where h is infinite). */
+int q6_rms_norm_q8(const void *X, int type, int64_t ldx, const void *residual, int rtype,
+                   int64_t ldr, const void *weight, int wtype, float eps, int N, int K, void *h,
+                   int64_t ldh, int8_t *Xq, float *da, uint16_t *Xh, float *us, q6_stream_t s);
+int q6_rms_norm_f8(const void *X, int type, int64_t ldx, const void *residual, int rtype,
+                   int64_t ldr, const void *weight, int wtype, float eps, int N, int K, void *h,
+                   int64_t ldh, uint8_t *xq, float *sx, q6_stream_t s);
+
+/* t = silu(gate) * up, quantised: X [N][ldx] holds K gate values, then K up
+ * values of each row (ldx >= 2 K), silu(g) = g / (1 + exp(-g)) within 2^-20 of
+ * its value where g > -3, 2^-16 at g = -87. */
+int q6_silu_mul_q8(const void *X, int type, int N, int K, int64_t ldx, int8_t *Xq, float *da,
+                   uint16_t *Xh, float *us, q6_stream_t s);
+int q6_silu_mul_f8(const void *X, int type, int N, int K, int64_t ldx, uint8_t *xq, float *sx,
+                   q6_stream_t s);
+
+/* The product of e4m3 activations and an e4m3 weight:
+ *   Y[n][m] = sum over blocks b of sx[b][n] * sw[m / 128][b] * P,
+ *   P = sum over the block's k of xq[n][k] * wq[m][k],
+ * in f32 and rounded once to `type`. The products are exact and the tensor
+ * cores' f32 sums of a block truncate: P is within 2^-17 of the sum of its
+ * products' sizes (measured: 2^-20.7 with products of one sign). A NaN code, or
+ * a scale that is not finite, makes NaN.
+ *   Y [N][ldy] of `type`, ldy >= M, aligned to its element.
+ *   path_out : NULL or receives the Q6_PATH_F8_* that ran. */
+int q6_f8_mmq(const uint8_t *wq, const float *sw, int M, int K, const uint8_t *xq, const float *sx,
+              int N, void *Y, int type, int64_t ldy, int *path_out, q6_stream_t s);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,14 +21,14 @@ Q6_OK, Q6_EINVAL, Q6_EALIGN, Q6_ESIZE, Q6_EARCH, Q6_ECUDA, Q6_ETIMEOUT = range(7
 (PATH_NONE, PATH_TC_RAW, PATH_TC_WEXP, PATH_SKINNY, PATH_TC_WH, PATH_SYNC_WEXP,
  PATH_SKINNY_FUSED, PATH_Q4K_TC_RAW, PATH_Q4K_TC_WQ, PATH_TC_FUSED_RAW,
  PATH_TC_FUSED_WH, PATH_Q4K_SKINNY, PATH_Q4K_SKINNY_FUSED, PATH_EXPERTS_FEW,
- PATH_EXPERTS_TC) = range(15)
+ PATH_EXPERTS_TC, PATH_F8_FEW, PATH_F8_TC) = range(17)
 PATH_NAMES = {PATH_NONE: "none", PATH_TC_RAW: "tc_raw", PATH_TC_WEXP: "tc_wexp",
               PATH_SKINNY: "skinny", PATH_TC_WH: "tc_wh", PATH_SYNC_WEXP: "sync_wexp",
               PATH_SKINNY_FUSED: "skinny_fused", PATH_Q4K_TC_RAW: "q4k_tc_raw",
               PATH_Q4K_TC_WQ: "q4k_tc_wq", PATH_TC_FUSED_RAW: "tc_fused_raw",
               PATH_TC_FUSED_WH: "tc_fused_wh", PATH_Q4K_SKINNY: "q4k_skinny",
               PATH_Q4K_SKINNY_FUSED: "q4k_skinny_fused", PATH_EXPERTS_FEW: "experts_few",
-              PATH_EXPERTS_TC: "experts_tc"}
+              PATH_EXPERTS_TC: "experts_tc", PATH_F8_FEW: "f8_few", PATH_F8_TC: "f8_tc"}
 SKINNY_MAX_N = 16
 SKINNY_GROUPS_MAX_N = 96
 SKINNY_GROUP_N = 32
@@ -42,6 +42,7 @@ FUSED_MAX_N = 2
 _P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)
 _IP = ctypes.POINTER(ctypes.c_int)
 _L = ctypes.c_int64
+_F = ctypes.c_float
 SIGNATURES = [
     ("q6_last_error", ctypes.c_char_p, []),
     ("q6_device_check", _I, []),
@@ -82,6 +83,16 @@ SIGNATURES = [
     ("q6_lora_workspace_bytes", _I, [_L, _I, _I, _I, _SZ]),
     ("q6_lora_add", _I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _L, _P, _P, _L, _P, _L, _P, _L,
                          _P, ctypes.c_size_t, _P]),
+    ("q6_f8_act_bytes", _I, [_I, _I, _SZ, _SZ, _IP]),
+    ("q6_f8_weight_bytes", _I, [_I, _I, _SZ, _SZ]),
+    ("q6_f8_quantize_act", _I, [_P, _I, _I, _I, _L, _P, _P, _P]),
+    ("q6_f8_quantize_weights", _I, [_P, _I, _I, _I, _L, _P, _P, _P]),
+    ("q6_rms_norm_q8", _I, [_P, _I, _L, _P, _I, _L, _P, _I, _F, _I, _I, _P, _L, _P, _P, _P, _P,
+                            _P]),
+    ("q6_rms_norm_f8", _I, [_P, _I, _L, _P, _I, _L, _P, _I, _F, _I, _I, _P, _L, _P, _P, _P]),
+    ("q6_silu_mul_q8", _I, [_P, _I, _I, _I, _L, _P, _P, _P, _P, _P]),
+    ("q6_silu_mul_f8", _I, [_P, _I, _I, _I, _L, _P, _P, _P]),
+    ("q6_f8_mmq", _I, [_P, _P, _I, _I, _P, _P, _I, _P, _I, _L, _IP, _P]),
 ]
 
 
@@ -664,3 +675,6 @@ from .moe import (ExpertWeights, Groups, LoraAdapters, Route, alloc_groups,  # n
                   alloc_route, expert_plane_bytes, experts_mmq, group_rows,
                   group_workspace_bytes, lora_add, lora_workspace_bytes, moe_combine, moe_route,
                   pack_experts)
+from .f8 import (F8Activations, F8Weights, alloc_f8_activations, alloc_f8_weights,  # noqa: E402,F401
+                 f8_act_bytes, f8_mmq, f8_quantize_act, f8_quantize_weights, f8_weight_bytes,
+                 rms_norm_f8, rms_norm_q8, silu_mul_f8, silu_mul_q8)

@@ -7,6 +7,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "f8_internal.cuh"
 #include "moe_internal.cuh"
 #include "q6_internal.cuh"
 
@@ -200,6 +201,8 @@ int require_device(unsigned int** status, KernelSet set) {
   cudaError_t e = cudaSuccess;
   if (set == kAdapterKernels) {
     e = lora_prepare();
+  } else if (set == kBlockKernels) {
+    e = f8_mmq_prepare();
   } else if (!(e = experts_few_prepare())) {
     e = experts_tc_prepare();
   }
@@ -216,6 +219,10 @@ int encode_row_maps(RowMaps* maps, const void* X, long long n, int K, long long 
     if (rc) return rc;
   }
   return Q6_OK;
+}
+int encode_f8_map(CUtensorMap* map, const void* base, int rows, int K, int box, const char* what) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, (uint64_t)K, (uint64_t)rows,
+                   (uint64_t)K, 128, (uint32_t)box, CU_TENSOR_MAP_SWIZZLE_128B, what);
 }
 // Records `code` and its text as the calling thread's last error (for the
 // entry points defined in other translation units).

@@ -1,0 +1,70 @@
+// Internal declarations of the 8-bit steps around the projections: activations
+// quantised by the norm or the gated activation that makes them, and the
+// products of e4m3 blocks.
+#pragma once
+
+#include "moe_internal.cuh"
+
+namespace q6 {
+
+// Elements of one scale: of a row of int8 codes, and of a row (or a side of a
+// weight block) of e4m3 codes.
+constexpr int kQ8Block = 32, kF8Block = 128;
+inline int f8_blocks(int n) { return (int)(((long long)n + kF8Block - 1) / kF8Block); }
+// Distance of the scale rows: N rounded up to 4.
+inline int scale_ld(int N) { return (int)(((long long)N + 3) / 4 * 4); }
+
+// Where quantised rows go: int8 (q, xh, us as q8_quantize_act_sums; any of them
+// NULL) or e4m3 (q), with their scales [blocks][lds].
+struct RowSink {
+  bool f8;
+  uint8_t* q;
+  __half* xh;
+  float* us;
+  float* scale;
+  int lds;
+};
+// Rows of X [N][ldx] as codes.
+cudaError_t launch_quantize_rows(const void* X, int type, int N, int K, long long ldx,
+                                 const RowSink& out, cudaStream_t s);
+// silu(gate) * up of rows [N][ldx] of K gate, then K up values.
+cudaError_t launch_silu_mul(const void* X, int type, int N, int K, long long ldx,
+                            const RowSink& out, cudaStream_t s);
+struct NormCall {
+  const void* X;
+  int type;
+  long long ldx;
+  const void* residual;  // or NULL
+  int rtype;
+  long long ldr;
+  const void* weight;
+  int wtype;
+  float eps;
+  int N, K;
+  void* h;  // of rtype; NULL without residual
+  long long ldh;
+};
+cudaError_t launch_rms_norm(const NormCall& c, const RowSink& out, cudaStream_t s);
+cudaError_t launch_f8_quantize_weights(const void* W, int type, int M, int K, long long ldw,
+                                       uint8_t* wq, float* sw, cudaStream_t s);
+
+struct F8Call {
+  const uint8_t* wq;
+  const float* sw;
+  int M, K;
+  const uint8_t* xq;
+  const float* sx;
+  int N, ldsx;
+  void* Y;
+  int type;
+  long long ldy;
+};
+// A tensor map of bytes [rows][K] in boxes of 128 of K x `box` rows with the
+// 128-byte swizzle (api.cu).
+int encode_f8_map(CUtensorMap* map, const void* base, int rows, int K, int box, const char* what);
+cudaError_t f8_mmq_prepare();
+// *path receives the Q6_PATH_F8_* that ran; Q6_OK, or the error recorded.
+int launch_f8_mmq(const F8Call& c, int* path, cudaError_t* e, unsigned int* status,
+                  cudaStream_t s);
+
+}  // namespace q6

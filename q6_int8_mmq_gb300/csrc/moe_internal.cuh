@@ -12,7 +12,7 @@ namespace q6 {
 // Kernels that have attributes to raise before their first launch. That loads them
 // (1.7 ms for the two sets together, 2.1 ms for the kernels of the shared projections),
 // so each set is prepared by the first call that runs it.
-enum KernelSet { kPlainKernels, kExpertKernels, kAdapterKernels, kKernelSets };
+enum KernelSet { kPlainKernels, kExpertKernels, kAdapterKernels, kBlockKernels, kKernelSets };
 // The calling thread's current device, checked and prepared, and `set` on it
 // (api.cu); *status (nullable) receives its status word.
 int require_device(unsigned int** status, KernelSet set = kPlainKernels);

@@ -96,5 +96,20 @@ __device__ __forceinline__ float recip_or_zero(float d) {
   return d >= 0x1p-126f ? __frcp_rn(d) : 0.0f;
 }
 
+// Block c of token n: us = da * S as its hi/lo pair (and the padding of an
+// odd super-block count, written by the last super-block's blocks).
+__device__ __forceinline__ void store_us(float* __restrict__ us, int n, int K, int c, float v) {
+  float hi, lo;
+  tf32_split(v, hi, lo);
+  const int b = c >> 3, i = c & 7, nsb = K >> 8;
+  float* row = us + (size_t)n * q4_min_ld(K) + 16 * b;
+  row[i] = hi;
+  row[8 + i] = lo;
+  if ((nsb & 1) && b == nsb - 1) {
+    row[16 + i] = 0.0f;
+    row[24 + i] = 0.0f;
+  }
+}
+
 }  // namespace
 }  // namespace q6

@@ -23,21 +23,6 @@
 namespace q6 {
 namespace {
 
-// Block c of token n: us = da * S as its hi/lo pair (and the padding of an
-// odd super-block count, written by the last super-block's blocks).
-__device__ __forceinline__ void store_us(float* __restrict__ us, int n, int K, int c, float v) {
-  float hi, lo;
-  tf32_split(v, hi, lo);
-  const int b = c >> 3, i = c & 7, nsb = K >> 8;
-  float* row = us + (size_t)n * q4_min_ld(K) + 16 * b;
-  row[i] = hi;
-  row[8 + i] = lo;
-  if ((nsb & 1) && b == nsb - 1) {
-    row[16 + i] = 0.0f;
-    row[24 + i] = 0.0f;
-  }
-}
-
 // Small inputs (a few tokens): each thread owns eight consecutive elements
 // (two float4 loads issued together); four threads form one 32-element block
 // and reduce amax with two xor-shuffles. K % 256 == 0 makes the group count a

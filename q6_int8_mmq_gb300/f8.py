@@ -1,0 +1,249 @@
+"""The 8-bit steps around the projections: the norm with the residual's addition
+and the gated activation that end in quantised activations, and products of
+e4m3 blocks (8-bit floating point, a scale for each 128).
+
+Argument marshalling over the C ABI, as in the package's other calls. Sums are
+f32; nothing is kept between calls.
+"""
+from __future__ import annotations
+
+import ctypes
+import dataclasses
+import functools
+
+from . import (PATH_NAMES, Q6_EINVAL, Activations, Q6Error, _check, _same_device, act_plane_bytes,
+               alloc_activations, load)
+from .moe import _empty, _made, _on, _rows, _rows2d, _stream, _type, _types, _whole
+
+
+@functools.lru_cache(maxsize=None)
+def _f8():
+    import torch
+    return torch.float8_e4m3fn
+
+
+@functools.lru_cache(maxsize=256)
+def f8_act_bytes(N: int, K: int):
+    """(xq_bytes, sx_bytes, ldsx) of N x K e4m3 activations."""
+    a, b, ld = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_int()
+    _check(load().q6_f8_act_bytes(N, K, ctypes.byref(a), ctypes.byref(b), ctypes.byref(ld)))
+    return a.value, b.value, ld.value
+
+
+@functools.lru_cache(maxsize=256)
+def f8_weight_bytes(M: int, K: int):
+    """(wq_bytes, sw_bytes) of an M x K e4m3 weight."""
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load().q6_f8_weight_bytes(M, K, ctypes.byref(a), ctypes.byref(b)))
+    return a.value, b.value
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+@dataclasses.dataclass(frozen=True)
+class F8Activations:
+    """e4m3 activations on the device: xq [N, K] float8_e4m3fn, sx [ceil(K / 128), ldsx] f32, the
+    scale of each token's 128 values (ldsx: N rounded up to 4; the columns past N are not
+    looked at). Checked once, when made; read-only."""
+    N: int
+    K: int
+    xq: object
+    sx: object
+
+    def __post_init__(self):
+        import torch
+        _same_device((self.xq, "xq", _f8(), (self.N, self.K)),
+                     (self.sx, "sx", torch.float32,
+                      (_blocks(self.K), f8_act_bytes(self.N, self.K)[2])))
+
+    @property
+    def device(self):
+        return self.sx.device
+
+
+@dataclasses.dataclass(frozen=True)
+class F8Weights:
+    """An e4m3 weight on the device, as checkpoints hold it: wq [M, K] float8_e4m3fn, sw
+    [ceil(M / 128), ceil(K / 128)] f32, the scale of each block of 128 x 128. Checked once, when
+    made; read-only."""
+    M: int
+    K: int
+    wq: object
+    sw: object
+
+    def __post_init__(self):
+        import torch
+        f8_weight_bytes(self.M, self.K)      # the sizes the kernels take
+        _same_device((self.wq, "wq", _f8(), (self.M, self.K)),
+                     (self.sw, "sw", torch.float32, (_blocks(self.M), _blocks(self.K))))
+
+    @property
+    def device(self):
+        return self.wq.device
+
+
+def alloc_f8_activations(N: int, K: int, device=None) -> F8Activations:
+    """Buffers for N x K e4m3 activations (K a multiple of 16)."""
+    import torch
+    dev, ldsx = device or torch.device("cuda"), f8_act_bytes(N, K)[2]
+    return _made(F8Activations, N=N, K=K, xq=torch.empty((N, K), dtype=_f8(), device=dev),
+                 sx=torch.empty((_blocks(K), ldsx), dtype=torch.float32, device=dev))
+
+
+def alloc_f8_weights(M: int, K: int, device=None) -> F8Weights:
+    """Buffers for an M x K e4m3 weight (K a multiple of 16)."""
+    import torch
+    dev = device or torch.device("cuda")
+    f8_weight_bytes(M, K)
+    return _made(F8Weights, M=M, K=K, wq=torch.empty((M, K), dtype=_f8(), device=dev),
+                 sw=torch.empty((_blocks(M), _blocks(K)), dtype=torch.float32, device=dev))
+
+
+def _input(X, name):
+    """(type code, rows, columns, row stride) of a 2-D view of rows."""
+    code = _type(X, name)
+    n = _rows2d(X, name)
+    return code, n, X.shape[1], _rows(X, name, X.dtype, tuple(X.shape), X.device)
+
+
+def _sink(out, cls, N, K, dev, alloc, stream):
+    """The quantised rows a call writes: `out`, which has to fit, or new ones."""
+    if out is None:
+        with _on(stream):
+            return alloc(N, K, dev)
+    if not isinstance(out, cls):
+        raise Q6Error(Q6_EINVAL, f"out must be {cls.__name__}, not {type(out).__name__}")
+    if out.N != N or out.K != K or out.device != dev:
+        raise Q6Error(Q6_EINVAL, f"out holds {out.N} x {out.K} activations on {out.device}, not "
+                                 f"{N} x {K} on {dev}")
+    return out
+
+
+def _q8_sink(out, N, K, dev, want_xh, want_xq, want_us, stream):
+    act_plane_bytes(N, K)
+    if out is None and not (want_xh or want_xq):
+        raise Q6Error(Q6_EINVAL, "one of want_xh and want_xq is needed")
+    out = _sink(out, Activations, N, K, dev,
+                lambda n, k, d: alloc_activations(n, k, d, want_xh, want_xq, want_us), stream)
+    return out, [None if t is None else t.data_ptr() for t in (out.xq, out.da, out.xh, out.us)]
+
+
+def _f8_sink(out, N, K, dev, stream):
+    out = _sink(out, F8Activations, N, K, dev, alloc_f8_activations, stream)
+    return out, [out.xq.data_ptr(), out.sx.data_ptr()]
+
+
+def f8_quantize_act(X, out: F8Activations | None = None, stream=None) -> F8Activations:
+    """Quantises activations X [N, K] (f32, bf16 or f16 rows, 16-byte aligned; K a multiple of
+    16) to e4m3 with a scale for each 128 of a row: largest magnitude / 448."""
+    code, N, K, ldx = _input(X, "X")
+    out, (xq, sx) = _f8_sink(out, N, K, X.device, stream)
+    _check(load().q6_f8_quantize_act(X.data_ptr(), code, N, K, ldx, xq, sx,
+                                     _stream(stream, X.device)))
+    return out
+
+
+def f8_quantize_weights(W, out: F8Weights | None = None, stream=None) -> F8Weights:
+    """Quantises a weight W [M, K] (f32, bf16 or f16 rows, 16-byte aligned; K a multiple of 16)
+    to e4m3 with a scale for each block of 128 x 128: largest magnitude / 448."""
+    code, M, K, ldw = _input(W, "W")
+    if out is None:
+        with _on(stream):
+            out = alloc_f8_weights(M, K, W.device)
+    elif not isinstance(out, F8Weights) or (out.M, out.K, out.device) != (M, K, W.device):
+        raise Q6Error(Q6_EINVAL, f"out must be F8Weights of {M} x {K} on {W.device}")
+    _check(load().q6_f8_quantize_weights(W.data_ptr(), code, M, K, ldw, out.wq.data_ptr(),
+                                         out.sw.data_ptr(), _stream(stream, W.device)))
+    return out
+
+
+def _norm(entry, sink, X, weight, eps, residual, h, stream):
+    code, N, K, ldx = _input(X, "X")
+    dev = X.device
+    wtype = _type(weight, "weight")
+    _whole(weight, "weight", weight.dtype, (K,), dev)
+    rtype = ldr = ldh = 0
+    if residual is not None:
+        rtype = _type(residual, "residual")
+        ldr = ldh = _rows(residual, "residual", residual.dtype, (N, K), dev)
+        if h is None:
+            h = residual
+        else:
+            ldh = _rows(h, "h", residual.dtype, (N, K), dev)
+    elif h is not None:
+        raise Q6Error(Q6_EINVAL, "h without a residual")
+    out, buffers = sink(N, K, dev)
+    _check(entry(X.data_ptr(), code, ldx, None if residual is None else residual.data_ptr(), rtype,
+                 ldr, weight.data_ptr(), wtype, eps, N, K, None if h is None else h.data_ptr(), ldh,
+                 *buffers, _stream(stream, dev)))
+    return out, X if residual is None else h
+
+
+def rms_norm_q8(X, weight, eps: float, residual=None, h=None, out: Activations | None = None,
+                want_xh: bool = True, want_xq: bool = True, want_us: bool = False, stream=None):
+    """h = X + residual, and the root-mean-square norm h / sqrt(mean(h^2) + eps) * weight as int8
+    activations for mmq() and q4k_mmq() (want_us): X, residual [N, K] of f32, bf16 or f16 each
+    (rows 16-byte aligned, K a multiple of 256), weight [K]. h gets the sum, rounded to
+    residual's type; without h it goes into residual. Without a residual it is the norm of X.
+    Codes are those of h * weight, the norm is in the scales. Returns (Activations, h)."""
+    return _norm(load().q6_rms_norm_q8,
+                 lambda n, k, d: _q8_sink(out, n, k, d, want_xh, want_xq, want_us, stream),
+                 X, weight, eps, residual, h, stream)
+
+
+def rms_norm_f8(X, weight, eps: float, residual=None, h=None, out: F8Activations | None = None,
+                stream=None):
+    """The same norm as e4m3 activations for f8_mmq() (K a multiple of 16). Returns
+    (F8Activations, h)."""
+    return _norm(load().q6_rms_norm_f8, lambda n, k, d: _f8_sink(out, n, k, d, stream),
+                 X, weight, eps, residual, h, stream)
+
+
+def _silu(entry, sink, X, stream):
+    code, N, width, ldx = _input(X, "X")
+    if width % 2:
+        raise Q6Error(Q6_EINVAL, f"X has {width} columns, not gate and up halves")
+    out, buffers = sink(N, width // 2, X.device)
+    _check(entry(X.data_ptr(), code, N, width // 2, ldx, *buffers, _stream(stream, X.device)))
+    return out
+
+
+def silu_mul_q8(X, out: Activations | None = None, want_xh: bool = True, want_xq: bool = True,
+                want_us: bool = False, stream=None) -> Activations:
+    """silu(gate) * up of X [N, 2 K] (f32, bf16 or f16 rows, 16-byte aligned: K gate, then K up
+    values) as int8 activations for mmq() and q4k_mmq() (want_us); K a multiple of 256."""
+    return _silu(load().q6_silu_mul_q8,
+                 lambda n, k, d: _q8_sink(out, n, k, d, want_xh, want_xq, want_us, stream), X, stream)
+
+
+def silu_mul_f8(X, out: F8Activations | None = None, stream=None) -> F8Activations:
+    """The same as e4m3 activations for f8_mmq(); K a multiple of 16."""
+    return _silu(load().q6_silu_mul_f8, lambda n, k, d: _f8_sink(out, n, k, d, stream), X, stream)
+
+
+def f8_mmq(w: F8Weights, act: F8Activations, out=None, dtype=None, stream=None):
+    """Y [N, M] = the product of e4m3 activations and an e4m3 weight, each block of 128 of K times
+    its two scales, summed in f32 and rounded once to dtype (f32, bf16 or f16; bf16 without dtype
+    or out). Returns (Y, path name)."""
+    M, K, N, dev = w.M, w.K, act.N, w.wq.device
+    if act.K != K or act.device != dev:
+        raise Q6Error(Q6_EINVAL, f"activations of K = {act.K} on {act.device} for weights of "
+                                 f"K = {K} on {dev}")
+    if out is None:
+        if dtype is None:
+            import torch
+            dtype = torch.bfloat16
+        if dtype not in _types():
+            raise Q6Error(Q6_EINVAL, f"dtype must be float32, bfloat16 or float16, not {dtype}")
+        out = _empty((N, M), dtype, dev, stream)
+    elif dtype is not None and getattr(out, "dtype", None) is not dtype:
+        raise Q6Error(Q6_EINVAL, f"out is not of dtype {dtype}")
+    code = _type(out, "out")
+    ldy = _rows(out, "out", out.dtype, (N, M), dev)
+    path = ctypes.c_int(-1)
+    _check(load().q6_f8_mmq(w.wq.data_ptr(), w.sw.data_ptr(), M, K, act.xq.data_ptr(),
+                            act.sx.data_ptr(), N, out.data_ptr(), code, ldy, ctypes.byref(path),
+                            _stream(stream, dev)))
+    return out, PATH_NAMES.get(path.value, str(path.value))
