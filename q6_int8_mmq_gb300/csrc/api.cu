@@ -202,7 +202,7 @@ int require_device(unsigned int** status, KernelSet set) {
   if (set == kAdapterKernels) {
     e = lora_prepare();
   } else if (set == kBlockKernels) {
-    e = f8_mmq_prepare();
+    if (!(e = f8_few_prepare())) e = f8_tc_prepare();
   } else if (!(e = experts_few_prepare())) {
     e = experts_tc_prepare();
   }
@@ -223,6 +223,10 @@ int encode_row_maps(RowMaps* maps, const void* X, long long n, int K, long long 
 int encode_f8_map(CUtensorMap* map, const void* base, int rows, int K, int box, const char* what) {
   return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, (uint64_t)K, (uint64_t)rows,
                    (uint64_t)K, 128, (uint32_t)box, CU_TENSOR_MAP_SWIZZLE_128B, what);
+}
+int encode_f8_scales(CUtensorMap* map, const float* sx, int ld, int rows, int n) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, sx, (uint64_t)ld, (uint64_t)rows,
+                   (uint64_t)ld * 4, (uint32_t)n, 1, CU_TENSOR_MAP_SWIZZLE_NONE, "sx");
 }
 // Records `code` and its text as the calling thread's last error (for the
 // entry points defined in other translation units).

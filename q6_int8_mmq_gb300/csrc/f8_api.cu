@@ -37,6 +37,9 @@ bool rows_aligned(const void* p, int type, int64_t ld) {
 constexpr int kMost = INT32_MAX - 512;
 constexpr int64_t kMostElements = 1ll << 40;
 
+// Tokens up to which the weight's rows are the tensor cores' lanes.
+constexpr int kFewTokens = 128;
+
 int check_f8(int rows, int K) {
   if (rows < 0 || K < 1 || K % 16) return fail(Q6_EINVAL, "rows >= 0, K a positive multiple of 16");
   if (rows > kMost || K > kMost || (int64_t)rows * K > kMostElements)
@@ -201,10 +204,12 @@ int q6_f8_mmq(const uint8_t* wq, const float* sw, int M, int K, const uint8_t* x
   unsigned int* status;
   if ((rc = q6::require_device(&status, q6::kBlockKernels))) return rc;
   const q6::F8Call c = {wq, sw, M, K, xq, sx, N, q6::scale_ld(N), Y, type, ldy};
-  int path = Q6_PATH_NONE;
+  const bool few = N <= kFewTokens;
   cudaError_t e = cudaSuccess;
-  if ((rc = q6::launch_f8_mmq(c, &path, &e, status, (cudaStream_t)s))) return rc;
-  if (path_out) *path_out = path;
+  if ((rc = few ? q6::launch_f8_few(c, &e, status, (cudaStream_t)s)
+                : q6::launch_f8_tc(c, &e, status, (cudaStream_t)s)))
+    return rc;
+  if (path_out) *path_out = few ? Q6_PATH_F8_FEW : Q6_PATH_F8_TC;
   return launched(e, "block product");
 }
 

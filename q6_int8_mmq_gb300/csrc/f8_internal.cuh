@@ -62,9 +62,12 @@ struct F8Call {
 // A tensor map of bytes [rows][K] in boxes of 128 of K x `box` rows with the
 // 128-byte swizzle (api.cu).
 int encode_f8_map(CUtensorMap* map, const void* base, int rows, int K, int box, const char* what);
-cudaError_t f8_mmq_prepare();
-// *path receives the Q6_PATH_F8_* that ran; Q6_OK, or the error recorded.
-int launch_f8_mmq(const F8Call& c, int* path, cudaError_t* e, unsigned int* status,
-                  cudaStream_t s);
+// Token scales [rows][ld] in boxes of n x 1.
+int encode_f8_scales(CUtensorMap* map, const float* sx, int ld, int rows, int n);
+// *e receives the launch's error; returns Q6_OK, or a code whose text is recorded.
+cudaError_t f8_few_prepare();
+int launch_f8_few(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStream_t s);
+cudaError_t f8_tc_prepare();
+int launch_f8_tc(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStream_t s);
 
 }  // namespace q6

@@ -9,6 +9,7 @@
 // token and the tile lies in one block row of weights, so the product of the
 // scales is one number a thread and block.
 #include "f8_internal.cuh"
+#include "f8_tc.cuh"
 
 namespace q6 {
 namespace {
@@ -31,30 +32,6 @@ constexpr int kSmemBytes = 1024 + kStages * kStage + (int)sizeof(Bars);
 struct Maps {
   CUtensorMap x, w;
 };
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(p));
-  return p != 0;
-}
-// D[tmem] (+)= A[smem] * B[smem]^T, e4m3, f32 sums.
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
-                                        uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 ad, {%1, %5};\n\t"
-      "mov.b64 bd, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kSw128DescHi)
-      : "memory");
-}
-// Instruction descriptor, kind::f8f6f4: e4m3 x e4m3 -> f32, both K-major.
-__host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -190,7 +167,7 @@ cudaError_t launch_t(const Maps& maps, const F8Call& c, unsigned int* status, cu
 
 }  // namespace
 
-cudaError_t f8_mmq_prepare() {
+cudaError_t f8_tc_prepare() {
   cudaError_t e = cudaSuccess;
   auto raise = [&](auto kernel) {
     if (!e) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
@@ -201,14 +178,12 @@ cudaError_t f8_mmq_prepare() {
   return e;
 }
 
-int launch_f8_mmq(const F8Call& c, int* path, cudaError_t* e, unsigned int* status,
-                  cudaStream_t s) {
+int launch_f8_tc(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStream_t s) {
   Maps maps;
   int rc;
   if ((rc = encode_f8_map(&maps.x, c.xq, c.N, c.K, 128, "xq")) ||
       (rc = encode_f8_map(&maps.w, c.wq, c.M, c.K, 128, "wq")))
     return rc;
-  *path = Q6_PATH_F8_TC;
   *e = c.type == Q6_TYPE_F32    ? launch_t<float>(maps, c, status, s)
        : c.type == Q6_TYPE_BF16 ? launch_t<__nv_bfloat16>(maps, c, status, s)
                                 : launch_t<__half>(maps, c, status, s);
