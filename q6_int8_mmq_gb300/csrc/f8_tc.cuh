@@ -1,18 +1,10 @@
 // Device helpers of the e4m3 tensor-core products.
 #pragma once
 
-#include "q6_internal.cuh"
+#include "tc_pair.cuh"
 
 namespace q6 {
 
-// True in one lane of the converged warp (see experts_tc.cu on what it saves).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(p));
-  return p != 0;
-}
 // D[tmem] (+)= A[smem] * B[smem]^T, e4m3, f32 sums (K = 32 an instruction, 32
 // bytes of a row), issued by one thread.
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
@@ -32,10 +24,6 @@ __host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
          | (0u << 7) | (0u << 10)       // A, B format: e4m3
          | ((uint32_t)(N >> 3) << 17)   // N >> 3
          | ((uint32_t)(M >> 4) << 24);  // M >> 4
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 // A box on its way into L2.
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
