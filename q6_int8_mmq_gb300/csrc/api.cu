@@ -224,9 +224,17 @@ int encode_f8_map(CUtensorMap* map, const void* base, int rows, int K, int box, 
   return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, (uint64_t)K, (uint64_t)rows,
                    (uint64_t)K, 128, (uint32_t)box, CU_TENSOR_MAP_SWIZZLE_128B, what);
 }
-int encode_f8_scales(CUtensorMap* map, const float* sx, int ld, int rows, int n) {
+int encode_f8_scales(CUtensorMap* map, const float* sx, int ld, int rows, int n, int box) {
   return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, sx, (uint64_t)ld, (uint64_t)rows,
-                   (uint64_t)ld * 4, (uint32_t)n, 1, CU_TENSOR_MAP_SWIZZLE_NONE, "sx");
+                   (uint64_t)ld * 4, (uint32_t)n, (uint32_t)box, CU_TENSOR_MAP_SWIZZLE_NONE, "sx");
+}
+int encode_f8_results(CUtensorMap* map, const F8Call& c, int cols, int rows) {
+  const CUtensorMapDataType dt = c.type == Q6_TYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : c.type == Q6_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return encode_2d(map, dt, c.Y, (uint64_t)c.M, (uint64_t)c.N,
+                   (uint64_t)c.ldy * (c.type == Q6_TYPE_F32 ? 4 : 2), (uint32_t)cols, (uint32_t)rows,
+                   CU_TENSOR_MAP_SWIZZLE_64B, "Y");
 }
 // Records `code` and its text as the calling thread's last error (for the
 // entry points defined in other translation units).

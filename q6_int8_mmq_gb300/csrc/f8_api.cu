@@ -192,7 +192,8 @@ int q6_f8_mmq(const uint8_t* wq, const float* sw, int M, int K, const uint8_t* x
   int rc = check_f8(N, K);
   if (rc || (rc = check_f8(M, K))) return rc;
   if (M < 1) return fail(Q6_EINVAL, "M >= 1");
-  if ((int64_t)q6::f8_blocks(M) * q6::f8_blocks(N) > INT32_MAX)
+  // blocks of all tiles, which a CTA may have to count
+  if ((double)q6::f8_blocks(M) * q6::f8_blocks(N) * q6::f8_blocks(K) > INT32_MAX)
     return fail(Q6_ESIZE, "the product has too many tiles");
   if (!any_type(type)) return fail(Q6_EINVAL, "unknown type %d", type);
   if (ldy < M) return fail(Q6_EINVAL, "ldy (%lld) < M (%d)", (long long)ldy, M);

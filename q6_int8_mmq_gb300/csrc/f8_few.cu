@@ -278,7 +278,7 @@ int launch_f8_few(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStr
   int rc;
   if ((rc = encode_f8_map(&maps.x, c.xq, c.N, c.K, n, "xq")) ||
       (rc = encode_f8_map(&maps.w, c.wq, c.M, c.K, 128, "wq")) ||
-      (rc = encode_f8_scales(&maps.sx, c.sx, c.ldsx, f8_blocks(c.K), n)))
+      (rc = encode_f8_scales(&maps.sx, c.sx, c.ldsx, f8_blocks(c.K), n, 1)))
     return rc;
   const int split = split_of(c);
   *e = c.type == Q6_TYPE_F32    ? launch_t<float>(maps, c, n, split, status, s)

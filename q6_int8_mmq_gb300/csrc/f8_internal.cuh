@@ -62,8 +62,10 @@ struct F8Call {
 // A tensor map of bytes [rows][K] in boxes of 128 of K x `box` rows with the
 // 128-byte swizzle (api.cu).
 int encode_f8_map(CUtensorMap* map, const void* base, int rows, int K, int box, const char* what);
-// Token scales [rows][ld] in boxes of n x 1.
-int encode_f8_scales(CUtensorMap* map, const float* sx, int ld, int rows, int n);
+// Token scales [rows][ld] in boxes of n tokens x `box` rows.
+int encode_f8_scales(CUtensorMap* map, const float* sx, int ld, int rows, int n, int box);
+// Y in boxes of `cols` x `rows` with the 64-byte swizzle.
+int encode_f8_results(CUtensorMap* map, const F8Call& c, int cols, int rows);
 // *e receives the launch's error; returns Q6_OK, or a code whose text is recorded.
 cudaError_t f8_few_prepare();
 int launch_f8_few(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStream_t s);

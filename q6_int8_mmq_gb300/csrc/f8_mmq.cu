@@ -3,18 +3,25 @@
 //   Y[n][m] = sum_b sx[b][n] * sw[m / 128][b] * (sum_{k in b} xq[n][k] * wq[m][k])
 //
 // A pair of CTAs (cluster of two, cta_group::2) computes a tile of 256 tokens
-// (MMA M; 128 tokens, one TMEM lane each, a CTA) by kBN weight rows. Each block
-// of 128 of K is four tcgen05 MMAs (kind::f8f6f4, K = 32) into accumulators of
-// its own, which eight warps of each CTA add, times the block's two scales, to
+// (MMA M; 128 tokens, one TMEM lane each, a CTA) by kBN weight rows (MMA N). Each
+// block of 128 of K is four tcgen05 MMAs (kind::f8f6f4, K = 32) into an accumulator
+// of its own, which eight warps of each CTA add, times the block's two scales, to
 // f32 sums in registers while the next blocks' MMAs run: a thread has one token
 // and columns of one block row of weights, so the product of the scales is one
 // number a thread and block, and a value costs half a packed multiply-add.
 //
-// Warp roles (12 warps, persistent CTAs, one an SM): 0 loads tiles by TMA (128-
-// byte swizzle), 1 of CTA 0 issues the pair's MMAs, 2 allocates TMEM, 4-11 sum:
-// each warpgroup half of the tile's columns.
-// TMEM: slots of kMmaN columns, 512 in all. A slot's MMAs are given out as soon
-// as both CTAs have read what was in it.
+// Warp roles (12 warps, persistent CTAs, one an SM):
+//   0      loads tiles by TMA (128-byte swizzle)
+//   1, 3   of CTA 0 issue the pair's MMAs, every other block each
+//   2      allocates TMEM, multiplies the scales
+//   4-11   sum: each warpgroup half of the tile's columns
+// TMEM: slots of kBN columns, 512 in all.
+// A stage of the ring has two barriers. `full` of CTA 0 says that both CTAs' copies
+// are there and that the slot its MMAs write has been read by all; `done` of each
+// CTA that the MMAs are through and the products of its scales written, for those
+// who sum and for the next copies.
+// What the sums wait for is what bounds the kernel, so all that they need besides
+// (the scales' way from memory, their products) is the work of another warp.
 // Every wait is bounded (see q6_internal.cuh), and the pair meets once more
 // before either CTA leaves.
 #include "f8_internal.cuh"
@@ -27,33 +34,45 @@ constexpr int kThreads = 384;
 constexpr int kTileN = 256;            // tokens of a pair
 constexpr int kXTile = 128 * 128;      // bytes of a CTA's tokens of a stage
 constexpr int kGroup = 8;              // token tiles walked together
+constexpr int kChunk = 8;              // blocks of K whose token scales come together
+constexpr int kChunkBytes = kChunk * 128 * 4;
+constexpr int kPart = 64;              // bytes of a row that are stored at a time
+constexpr int kOutBytes = 32 * kPart;  // of a warp
 // Registers of a thread: 128 + 256 threads share the 384 * 168 of the launch.
-constexpr int kRegsFew = 72, kRegsMany = 216;
+#ifndef RF
+#define RF 40
+#define RM 232
+#endif
+constexpr int kRegsFew = RF, kRegsMany = RM;
 
-enum : uint32_t { kSiteEmpty = 48, kSiteFull, kSiteSlot, kSiteDone, kSiteDrain };
+enum : uint32_t { kSiteDone = 48, kSiteFull, kSiteScale, kSiteDrain };
 
-template <int kBN, int kMmaN>
+template <int kBN>
 struct Cfg {
-  static constexpr int kUnits = kBN / kMmaN;      // accumulators of a block of K
-  static constexpr int kSlots = 512 / kMmaN;
+  static constexpr int kSlots = 512 / kBN;
   static constexpr int kWRows = kBN / 2;          // of a CTA
   static constexpr int kStage = kXTile + kWRows * 128;
-  static constexpr int kStages = kBN == 256 ? 6 : 8;
+  static constexpr int kStages = kBN == 256 ? 5 : 7;
   static constexpr int kCols = kBN / 2;           // of a warpgroup
-  // warps of the pair that read a slot
-  static constexpr int kReaders = kUnits == 2 ? 8 : 16;
+  // Products of scales kept: a stage's MMAs are through only after all who sum have
+  // read the slot kSlots blocks before, so those of kStages + kSlots blocks back
+  // are not needed any more when the stage's next ones are written.
+  static constexpr int kProducts = kBN == 256 ? 8 : 16;
+  static_assert(kProducts >= kStages + kSlots);
   struct Bars {
-    uint64_t full[kStages], empty[kStages];
-    uint64_t done[kSlots], taken[kSlots];
+    uint64_t full[kStages], done[kStages];
+    uint64_t s_full[2];
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
   };
-  static constexpr int kSmem = 1024 + kStages * kStage + (int)sizeof(Bars);
+  static constexpr int kSmem =
+      1024 + kStages * kStage + 8 * 2 * kOutBytes + 2 * kChunkBytes + kProducts * 1024 + (int)sizeof(Bars);
 };
+constexpr int kReaders = 16;  // warps of the pair that read a slot
 
 struct Maps {
-  CUtensorMap x, w;
+  CUtensorMap x, w, sx, y;
 };
 
 // D[tmem] (+)= A[smem] * B[smem]^T over the CTA pair, e4m3, f32 sums.
@@ -78,6 +97,34 @@ __device__ __forceinline__ void fma2(float2& acc, uint32_t a, uint32_t b, uint64
       : "r"(a), "r"(b), "l"(s));
 }
 
+// The address of CTA 0's `bar` from any CTA of the pair, and an arrival there as
+// arrive_leader_tmem()'s.
+__device__ __forceinline__ uint32_t leader_address(uint64_t* bar) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+  return a;
+}
+__device__ __forceinline__ void arrive_at_leader(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A box from shared memory to its place in global memory; what was begun since the
+// last call as a group; and the wait until all but kLeft groups have been read.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(src)), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void tma_stores_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void tma_stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
+
 // Tile t: token tiles in groups of kGroup, a group's weight tiles one after
 // another with its token tiles next to each other, so that what the pairs work on
 // at a time shares both its tokens and its weights in L2.
@@ -90,29 +137,44 @@ __device__ __forceinline__ Tile tile_at(int t, int n_tiles, int m_tiles) {
   return {first + at % here, at / here};
 }
 
-template <typename T, int kBN, int kMmaN>
+// Sixteen bytes of results: kPer of them from a thread's pairs of sums.
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float2* a) {
+  if constexpr (sizeof(T) == 4)
+    return make_uint4(__float_as_uint(a[0].x), __float_as_uint(a[0].y), __float_as_uint(a[1].x),
+                      __float_as_uint(a[1].y));
+  else
+    return make_uint4(pack2<T>(a[0].x, a[0].y), pack2<T>(a[1].x, a[1].y), pack2<T>(a[2].x, a[2].y),
+                      pack2<T>(a[3].x, a[3].y));
+}
+
+template <typename T, int kBN>
 __global__ void __launch_bounds__(kThreads, 1)
-f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, unsigned int* status) {
-  using S = Cfg<kBN, kMmaN>;
-  constexpr int kStages = S::kStages, kSlots = S::kSlots, kUnits = S::kUnits;
+f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsigned int* status) {
+  using S = Cfg<kBN>;
+  constexpr int kStages = S::kStages, kSlots = S::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  typename S::Bars* bars = reinterpret_cast<typename S::Bars*>(ring + kStages * S::kStage);
+  uint8_t* out_stage = ring + kStages * S::kStage;
+  float* scales = reinterpret_cast<float*>(out_stage + 8 * 2 * kOutBytes);
+  float* products = scales + 2 * kChunk * 128;  // [block % kProducts][half][token]
+  typename S::Bars* bars = reinterpret_cast<typename S::Bars*>(products + S::kProducts * 256);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
   volatile int* abort_flag = &bars->abort;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&bars->full[i], 1), mbar_init(&bars->empty[i], 1);
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&bars->done[i], 1);
-      mbar_init(&bars->taken[i], S::kReaders);  // used in CTA 0
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bars->full[i], 1 + kReaders);  // used in CTA 0
+      mbar_init(&bars->done[i], 2);
     }
-    mbar_init(&bars->drain, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars->s_full[i], 1);
+    mbar_init(&bars->drain, 2);
     bars->abort = 0;
     mbar_fence_init();
     tma_prefetch_desc(&maps.x);
     tma_prefetch_desc(&maps.w);
+    tma_prefetch_desc(&maps.sx);
   }
   if (warp == 2) tmem_alloc_pair(&bars->tmem_base, 512);
   griddep_wait();
@@ -129,64 +191,108 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, unsigned int* s
   if (warp < 4) {
     regs_dealloc<kRegsFew>();
     if (warp == 0) {
-      int g = 0;
+      // ---------------------------------------------------------------- tiles --
+      long long g = 0;
       for (int t = cluster; t < tiles && ok; t += clusters) {
         const Tile w = tile_at(t, n_tiles, m_tiles);
         const int n0 = __shfl_sync(0xffffffffu, w.n * kTileN + 128 * rank, 0);
-        const int m0 = __shfl_sync(0xffffffffu, w.m * kBN + kMmaN / 2 * rank, 0);
+        const int m0 = __shfl_sync(0xffffffffu, w.m * kBN + S::kWRows * rank, 0);
         for (int b = 0; b < blocks; ++b, ++g) {
-          const int slot = g % kStages;
-          if (!(ok = mbar_wait_warp(&bars->empty[slot], (g / kStages & 1) ^ 1, abort_flag, status,
-                                    kSiteEmpty)))
+          const int slot = (int)(g % kStages);
+          if (!(ok = mbar_wait_warp(&bars->done[slot], (uint32_t)(g / kStages & 1) ^ 1, abort_flag,
+                                    status, kSiteDone)))
             break;
           if (elect_one()) {
             uint8_t* at = ring + slot * S::kStage;
             if (rank == 0) mbar_arrive_expect_tx(&bars->full[slot], 2 * S::kStage);
             tma_load_2d_pair(at, &maps.x, &bars->full[slot], b * 128, n0);
-#pragma unroll
-            for (int u = 0; u < kUnits; ++u)
-              tma_load_2d_pair(at + kXTile + u * kMmaN / 2 * 128, &maps.w, &bars->full[slot], b * 128,
-                               m0 + u * kMmaN);
+            tma_load_2d_pair(at + kXTile, &maps.w, &bars->full[slot], b * 128, m0);
           }
           __syncwarp();
         }
       }
       // the last stages' MMAs are through, and this CTA has been told, before it leaves
-      for (int k = g > kStages ? g - kStages : 0; k < g && ok; ++k)
-        ok = mbar_wait_warp(&bars->empty[k % kStages], k / kStages & 1, abort_flag, status, kSiteEmpty);
+      for (long long k = g > kStages ? g - kStages : 0; k < g && ok; ++k)
+        ok = mbar_wait_warp(&bars->done[k % kStages], (uint32_t)(k / kStages & 1), abort_flag, status,
+                            kSiteDone);
       if (!ok && lane == 0) {
         // Copies in flight land before the CTA exits. They count on a barrier of the
         // pair, so they are given 1 ms.
         for (const long long t0 = clock64(); clock64() - t0 < 2100000;) {
         }
       }
-    } else if (warp == 1 && rank == 0) {
-      const uint32_t base = sw128_desc_lo(smem_u32(ring));
-      int g = 0, u = 0;
+    } else if (warp == 2) {
+      // --------------------------------------------------------------- scales --
+      // Chunks of kChunk blocks of the tokens' scales come by TMA, one ahead; of the
+      // weights' lane 8 h + i has block i's of half h, one chunk ahead too.
+      int asked = 0, tile_a = cluster, b_a = 0;
+      float sw_next = 0.0f;
+      auto ask = [&] {
+        if (tile_a >= tiles) return;
+        const Tile w = tile_at(tile_a, n_tiles, m_tiles);
+        const int n0 = __shfl_sync(0xffffffffu, w.n * kTileN + 128 * rank, 0);
+        const int half = lane / kChunk % 2;
+        // past the last band of weights the last one again, whose result is not stored
+        const int band = min((w.m * kBN + S::kCols * half) / 128, (c.M - 1) / 128);
+        sw_next = c.sw[(size_t)band * blocks + min(b_a + lane % kChunk, blocks - 1)];
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&bars->s_full[asked & 1], kChunkBytes);
+          tma_load_2d(scales + (asked & 1) * kChunk * 128, &maps.sx, &bars->s_full[asked & 1], n0, b_a);
+        }
+        __syncwarp();
+        ++asked;
+        if ((b_a += kChunk) >= blocks) b_a = 0, tile_a += clusters;
+      };
+      ask();
+      int stage = 0, phase = 1, chunk = 0, put = 0;
       for (int t = cluster; t < tiles && ok; t += clusters) {
-        for (int b = 0; b < blocks && ok; ++b, ++g) {
-          const int slot = g % kStages;
-          if (!(ok = mbar_wait_warp(&bars->full[slot], g / kStages & 1, abort_flag, status, kSiteFull)))
+        for (int b = 0; b < blocks && ok; b += kChunk, ++chunk) {
+          const float sw = sw_next;
+          ask();
+          if (!(ok = mbar_wait_warp(&bars->s_full[chunk & 1], chunk >> 1 & 1, abort_flag, status, kSiteScale)))
             break;
+          const float* from = scales + (chunk & 1) * kChunk * 128 + lane;
+          for (int i = 0; i < kChunk && b + i < blocks; ++i) {
+            const float w0 = __shfl_sync(0xffffffffu, sw, i), w1 = __shfl_sync(0xffffffffu, sw, kChunk + i);
+            if (!(ok = mbar_wait_warp(&bars->done[stage], phase, abort_flag, status, kSiteDone))) break;
+            float* to = products + put * 256 + lane;
 #pragma unroll
-          for (int h = 0; h < kUnits; ++h, ++u) {
-            const int d = u % kSlots;
-            if (!(ok = mbar_wait_warp(&bars->taken[d], (u / kSlots & 1) ^ 1, abort_flag, status,
-                                      kSiteSlot)))
-              break;
-            tc_fence_after();
-            if (elect_one()) {
-              const uint32_t x = base + slot * (S::kStage >> 4);
-              const uint32_t w = x + ((kXTile + h * kMmaN / 2 * 128) >> 4);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_f8_pair(tmem + kMmaN * d, x + 2 * k, w + 2 * k, idesc_f8(256, kMmaN), k > 0);
-              commit_pair(&bars->done[d]);
-              if (h == kUnits - 1) commit_pair(&bars->empty[slot]);
+            for (int j = 0; j < 128; j += 32) {
+              const float x = from[i * 128 + j];
+              to[j] = x * w0;
+              to[128 + j] = x * w1;
             }
             __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->done[stage]);
+            if (++stage == kStages) stage = 0, phase ^= 1;
+            put = (put + 1) % S::kProducts;
           }
         }
+      }
+      if (!ok && lane == 0) {  // copies in flight land before the CTA exits
+        volatile int no_abort = 0;
+        for (int i = asked > 2 ? asked - 2 : 0; i < asked; ++i)
+          mbar_wait_bounded(&bars->s_full[i & 1], i >> 1 & 1, &no_abort, status, kSiteScale);
+      }
+    } else if (rank == 0) {
+      // ----------------------------------------------------------------- MMAs --
+      const uint32_t base = sw128_desc_lo(smem_u32(ring));
+      const long long total = (long long)((tiles - cluster + clusters - 1) / clusters) * blocks;
+      for (long long g = warp >> 1; g < total; g += 2) {
+        const int slot = (int)(g % kStages);
+        if (!(ok = mbar_wait_warp(&bars->full[slot], (uint32_t)(g / kStages & 1), abort_flag, status,
+                                  kSiteFull)))
+          break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t x = base + slot * (S::kStage >> 4), w = x + (kXTile >> 4);
+          const uint32_t d = tmem + kBN * (uint32_t)(g % kSlots);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_f8_pair(d, x + 2 * k, w + 2 * k, idesc_f8(256, kBN), k > 0);
+          commit_pair(&bars->done[slot]);
+        }
+        __syncwarp();
       }
       if (elect_one()) {  // MMAs in flight end before TMEM is freed
         volatile int no_abort = 0;
@@ -196,80 +302,114 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, unsigned int* s
       __syncwarp();
     }
   } else {
+    // ------------------------------------------------------------------- sums --
     regs_alloc<kRegsMany>();
-    constexpr int kCols = S::kCols, kParts = kCols / 32;
+    constexpr int kCols = S::kCols;
     const int q = warp % 4, me = (warp - 4) / 4;
     // this warp's lanes and first column of a slot
-    const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + (kUnits == 2 ? 0 : kCols * me);
-    int u = kUnits == 2 ? me : 0;  // accumulators so far
+    const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + kCols * me;
+    const float* mine = products + 128 * me + 32 * q + lane;
+    const uint32_t leader = leader_address(&bars->full[0]);
+    int left = (tiles - cluster + clusters - 1) / clusters * blocks;  // blocks not begun
+    int stage = 0, phase = 0, slot = 0, get = 0, free_stage = kSlots % kStages;
+    uint32_t at = 0;
+    uint64_t s = 0;
+    // The next block's sums and products of scales are there: the sums at column
+    // `at`, the product in both halves of s.
+    auto begin = [&] {
+      ok = mbar_wait_warp(&bars->done[stage], phase, abort_flag, status, kSiteDone);
+      tc_fence_after();
+      at = src + kBN * slot;
+      if (++stage == kStages) stage = 0, phase ^= 1;
+      slot = (slot + 1) % kSlots;
+      --left;
+    };
+    auto product = [&] {
+      const float f = mine[get * 256];
+      asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "f"(f));
+      get = (get + 1) % S::kProducts;
+    };
+    // the first blocks' slots are free
+    if (lane == 0)
+      for (int i = 0; i < kSlots; ++i) arrive_at_leader(leader + 8 * i);
+    uint32_t va[32], vb[32];
+    begin();
+    tmem_ld(at, va);
+    tmem_ld(at + 32, vb);
+    float2 acc[kCols / 2];
+    auto add = [&](float2* to, const uint32_t(&v)[32]) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) fma2(to[i], v[2 * i], v[2 * i + 1], s);
+    };
     for (int t = cluster; t < tiles && ok; t += clusters) {
-      const Tile w = tile_at(t, n_tiles, m_tiles);
-      const int n = w.n * kTileN + 128 * rank + 32 * q + lane;
-      const int m0 = w.m * kBN + kCols * me;
-      const bool live = n < c.N;
-      // past the last band of weights the last one again, whose result is not stored
-      const float* sw = c.sw + (size_t)min(m0 / 128, (c.M - 1) / 128) * blocks;
-      const float* sx = c.sx + n;
-      float2 acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      // scales two blocks ahead
-      float x0 = live ? sx[0] : 0.0f, w0 = sw[0], x1 = 0.0f, w1 = 0.0f;
-      if (blocks > 1) x1 = live ? sx[c.ldsx] : 0.0f, w1 = sw[1];
-      for (int b = 0; b < blocks; ++b, u += kUnits) {
-        const float sf = x0 * w0;
-        uint64_t s;
-        asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "f"(sf));
-        x0 = x1, w0 = w1;
-        if (b + 2 < blocks) x1 = live ? sx[(size_t)(b + 2) * c.ldsx] : 0.0f, w1 = sw[b + 2];
-        const int d = u % kSlots;
-        if (!(ok = mbar_wait_warp(&bars->done[d], u / kSlots & 1, abort_flag, status, kSiteDone)))
-          break;
-        tc_fence_after();
-        uint32_t v[2][32];
-        tmem_ld32(src + kMmaN * d, v[0]);
-        tmem_wait(v[0]);
-#pragma unroll
-        for (int p = 0; p < kParts; ++p) {
-          if (p + 1 < kParts) {
-            tmem_ld32_before(src + kMmaN * d + 32 * (p + 1), v[(p + 1) & 1], v[p & 1]);
-          } else {  // all is in registers
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_leader_tmem(&bars->taken[d]);
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            fma2(acc[16 * p + i], v[p & 1][2 * i], v[p & 1][2 * i + 1], s);
-          if (p + 1 < kParts) tmem_wait_ld_after(v[(p + 1) & 1], acc + 16 * p);
+#pragma unroll 1
+      for (int i = 0; i < blocks && ok; ++i) {
+        product();
+        tmem_wait_ld2(va, vb);
+        if constexpr (kCols == 128) {
+          add(acc, va);
+          tmem_ld_after(at + 64, va, acc);
+          add(acc + 16, vb);
+          tmem_ld_after(at + 96, vb, acc + 16);
+          tmem_wait_ld2(va, vb);
         }
+        float2* rest = acc + kCols / 2 - 32;
+        // all is in registers: the MMAs of the block kSlots further may write
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at_leader(leader + 8 * free_stage);
+        if (++free_stage == kStages) free_stage = 0;
+        add(rest, va);
+        // while the last values are added, the next block's begin to come
+        const bool more = left > 0;
+        if (more) {
+          begin();
+          tmem_ld_after(at, va, rest);
+        }
+        add(rest + 16, vb);
+        if (more) tmem_ld_after(at + 32, vb, rest + 16);
       }
-      if (ok && live) {
-        T* y = static_cast<T*>(c.Y) + (size_t)n * c.ldy + m0;
-        const int cols = c.M - m0;
-        constexpr int kPer = 16 / sizeof(T);
-        if (cols >= kCols && (reinterpret_cast<uintptr_t>(y) & 15) == 0) {
+      if (!ok) break;
+      const Tile w = tile_at(t, n_tiles, m_tiles);
+      const int n0 = w.n * kTileN + 128 * rank + 32 * q, m0 = w.m * kBN + kCols * me;
+      constexpr int kPer = kPart / (int)sizeof(T);  // results of a row stored at a time
+      if (n0 >= c.N || m0 >= c.M) continue;
+      if (store) {
+        // 64 bytes of 32 rows at a time, the 16-byte units of a row as the 64-byte
+        // swizzle has them, so that a lane's row goes to banks of its own
+        uint8_t* buf = out_stage + (warp - 4) * 2 * kOutBytes;
 #pragma unroll
-          for (int i = 0; i < kCols; i += kPer) {
-            uint4 o;
-            if constexpr (sizeof(T) == 4) {
-              o.x = __float_as_uint(acc[i / 2].x), o.y = __float_as_uint(acc[i / 2].y);
-              o.z = __float_as_uint(acc[i / 2 + 1].x), o.w = __float_as_uint(acc[i / 2 + 1].y);
-            } else {
-              o.x = pack2<T>(acc[i / 2].x, acc[i / 2].y);
-              o.y = pack2<T>(acc[i / 2 + 1].x, acc[i / 2 + 1].y);
-              o.z = pack2<T>(acc[i / 2 + 2].x, acc[i / 2 + 2].y);
-              o.w = pack2<T>(acc[i / 2 + 3].x, acc[i / 2 + 3].y);
-            }
-            *reinterpret_cast<uint4*>(y + i) = o;
+        for (int p = 0; p < kCols / kPer; ++p) {
+          uint8_t* to = buf + (p & 1) * kOutBytes;
+          if (p >= 2) {
+            if (lane == 0) tma_stores_read<1>();
+            __syncwarp();
           }
-        } else {
 #pragma unroll
-          for (int i = 0; i < kCols; ++i)
-            if (i < cols) y[i] = from_f32<T>(i % 2 ? acc[i / 2].y : acc[i / 2].x);
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(to + lane * kPart + ((j ^ (lane >> 1 & 3)) * 16)) =
+                pack16<T>(acc + p * kPer / 2 + j * (8 / (int)sizeof(T)));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (m0 + p * kPer < c.M) tma_store_2d(&maps.y, to, m0 + p * kPer, n0);
+            tma_stores_commit();  // a group a part, with nothing in it past the last column
+          }
         }
+        if (lane == 0) tma_stores_read<0>();
+        __syncwarp();
+      } else if (n0 + lane < c.N) {
+        T* y = static_cast<T*>(c.Y) + (size_t)(n0 + lane) * c.ldy + m0;
+        const int cols = c.M - m0;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i)
+          if (i < cols) y[i] = from_f32<T>(i % 2 ? acc[i / 2].y : acc[i / 2].x);
       }
     }
+    // loads begun for a block that was given up have ended
+    tmem_wait_ld2(va, vb);
   }
   tc_fence_before();
   __syncthreads();
@@ -280,14 +420,15 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, unsigned int* s
   }
 }
 
-template <typename T, int kBN, int kMmaN>
-cudaError_t launch_n(const Maps& maps, const F8Call& c, unsigned int* status, cudaStream_t s) {
+template <typename T, int kBN>
+cudaError_t launch_n(const Maps& maps, const F8Call& c, int store, unsigned int* status,
+                     cudaStream_t s) {
   const long long tiles = (((long long)c.M + kBN - 1) / kBN) * (((long long)c.N + kTileN - 1) / kTileN);
   const unsigned pairs = (unsigned)(tiles < 76 ? tiles : 76);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<kBN, kMmaN>::kSmem;
+  cfg.dynamicSmemBytes = Cfg<kBN>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -297,22 +438,19 @@ cudaError_t launch_n(const Maps& maps, const F8Call& c, unsigned int* status, cu
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, f8_mmq_kernel<T, kBN, kMmaN>, maps, c, status);
+  return cudaLaunchKernelEx(&cfg, f8_mmq_kernel<T, kBN>, maps, c, store, status);
 }
-// Whether 128 weight rows a tile leave fewer rounds of half the work.
+// Whether 128 weight rows a tile are faster: they take 5/8 of the time of 256.
 bool narrow(const F8Call& c) {
   const long long n = ((long long)c.N + kTileN - 1) / kTileN;
   const long long wide = n * (((long long)c.M + 255) / 256), thin = n * (((long long)c.M + 127) / 128);
-  return (thin + 75) / 76 < 2 * ((wide + 75) / 76);
+  return 5 * ((thin + 75) / 76) < 8 * ((wide + 75) / 76);
 }
-#ifndef F8_MMAN
-#define F8_MMAN 128
-#endif
 template <typename T>
-cudaError_t launch_t(const Maps& maps, const F8Call& c, bool thin, unsigned int* status,
+cudaError_t launch_t(const Maps& maps, const F8Call& c, bool thin, int store, unsigned int* status,
                      cudaStream_t s) {
-  return thin ? launch_n<T, 128, 128>(maps, c, status, s)
-              : launch_n<T, 256, F8_MMAN>(maps, c, status, s);
+  return thin ? launch_n<T, 128>(maps, c, store, status, s)
+              : launch_n<T, 256>(maps, c, store, status, s);
 }
 
 }  // namespace
@@ -324,8 +462,8 @@ cudaError_t f8_tc_prepare() {
   };
   auto all = [&](auto t) {
     using T = decltype(t);
-    raise(f8_mmq_kernel<T, 128, 128>, Cfg<128, 128>::kSmem);
-    raise(f8_mmq_kernel<T, 256, F8_MMAN>, Cfg<256, F8_MMAN>::kSmem);
+    raise(f8_mmq_kernel<T, 128>, Cfg<128>::kSmem);
+    raise(f8_mmq_kernel<T, 256>, Cfg<256>::kSmem);
   };
   all(float());
   all(__nv_bfloat16());
@@ -335,14 +473,19 @@ cudaError_t f8_tc_prepare() {
 
 int launch_f8_tc(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStream_t s) {
   const bool thin = narrow(c);
+  // results by TMA where their rows start on 16 bytes
+  const int size = c.type == Q6_TYPE_F32 ? 4 : 2;
+  const int store = reinterpret_cast<uintptr_t>(c.Y) % 16 == 0 && c.ldy * size % 16 == 0;
   Maps maps;
   int rc;
   if ((rc = encode_f8_map(&maps.x, c.xq, c.N, c.K, 128, "xq")) ||
-      (rc = encode_f8_map(&maps.w, c.wq, c.M, c.K, thin || F8_MMAN == 128 ? 64 : 128, "wq")))
+      (rc = encode_f8_map(&maps.w, c.wq, c.M, c.K, thin ? 64 : 128, "wq")) ||
+      (rc = encode_f8_scales(&maps.sx, c.sx, c.ldsx, f8_blocks(c.K), 128, kChunk)) ||
+      (store && (rc = encode_f8_results(&maps.y, c, kPart / size, 32))))
     return rc;
-  *e = c.type == Q6_TYPE_F32    ? launch_t<float>(maps, c, thin, status, s)
-       : c.type == Q6_TYPE_BF16 ? launch_t<__nv_bfloat16>(maps, c, thin, status, s)
-                                : launch_t<__half>(maps, c, thin, status, s);
+  *e = c.type == Q6_TYPE_F32    ? launch_t<float>(maps, c, thin, store, status, s)
+       : c.type == Q6_TYPE_BF16 ? launch_t<__nv_bfloat16>(maps, c, thin, store, status, s)
+                                : launch_t<__half>(maps, c, thin, store, status, s);
   return Q6_OK;
 }
 

@@ -64,4 +64,15 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
                : "memory");
 }
 
+// The same after the math on the 16 sums s, which took its values from registers
+// that this load may then use.
+__device__ __forceinline__ void tmem_ld_after(uint32_t addr, uint32_t (&r)[32], float2* s) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "+f"(s[0].x), "+f"(s[0].y), "+f"(s[1].x), "+f"(s[1].y), "+f"(s[2].x), "+f"(s[2].y), "+f"(s[3].x), "+f"(s[3].y), "+f"(s[4].x), "+f"(s[4].y), "+f"(s[5].x), "+f"(s[5].y), "+f"(s[6].x), "+f"(s[6].y), "+f"(s[7].x), "+f"(s[7].y), "+f"(s[8].x), "+f"(s[8].y), "+f"(s[9].x), "+f"(s[9].y), "+f"(s[10].x), "+f"(s[10].y), "+f"(s[11].x), "+f"(s[11].y), "+f"(s[12].x), "+f"(s[12].y), "+f"(s[13].x), "+f"(s[13].y), "+f"(s[14].x), "+f"(s[14].y), "+f"(s[15].x), "+f"(s[15].y)
+      : "r"(addr)
+      : "memory");
+}
+
 }  // namespace q6
