@@ -6,22 +6,26 @@
 // (MMA M; 128 tokens, one TMEM lane each, a CTA) by kBN weight rows (MMA N). Each
 // block of 128 of K is four tcgen05 MMAs (kind::f8f6f4, K = 32) into an accumulator
 // of its own, which eight warps of each CTA add, times the block's two scales, to
-// f32 sums in registers while the next blocks' MMAs run: a thread has one token
-// and columns of one block row of weights, so the product of the scales is one
-// number a thread and block, and a value costs half a packed multiply-add.
+// f32 sums in registers while the next blocks' MMAs run: a thread has one token and
+// columns of one block row of weights, so the product of the scales is one number a
+// thread and block, and a value costs half a packed multiply-add.
 //
 // Warp roles (12 warps, persistent CTAs, one an SM):
 //   0      loads tiles by TMA (128-byte swizzle)
 //   1, 3   of CTA 0 issue the pair's MMAs, every other block each
 //   2      allocates TMEM, multiplies the scales
 //   4-11   sum: each warpgroup half of the tile's columns
-// TMEM: slots of kBN columns, 512 in all.
-// A stage of the ring has two barriers. `full` of CTA 0 says that both CTAs' copies
-// are there and that the slot its MMAs write has been read by all; `done` of each
-// CTA that the MMAs are through and the products of its scales written, for those
-// who sum and for the next copies.
-// What the sums wait for is what bounds the kernel, so all that they need besides
-// (the scales' way from memory, their products) is the work of another warp.
+// TMEM: slots of kBN columns, 512 in all. A block's MMAs wait for its stage of the
+// ring to be full and for its slot to be taken by those who sum; `done` says that they
+// are through and that the products of its scales are written.
+// What bounds it is how fast sums are taken: a warp's block is a chain of a look at a
+// barrier, loads from TMEM and a hand-back, about 450 cycles besides its multiply-
+// adds, and from there to the next sums in the slot are 300 cycles of signals and 700
+// of MMAs. So all else (the scales' way from memory, their products) is the work of
+// another warp. (Measured on 8192 x 22016 x 4096, us: scales loaded by those who sum
+// 716, fetched for them but multiplied there 682, this 514. Sixteen warps that sum:
+// 605. Slots of 128 columns for each warpgroup: 506, but 402 against 385 for
+// 8192 x 8192 x 8192.)
 // Every wait is bounded (see q6_internal.cuh), and the pair meets once more
 // before either CTA leaves.
 #include "f8_internal.cuh"
@@ -33,41 +37,37 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kTileN = 256;            // tokens of a pair
 constexpr int kXTile = 128 * 128;      // bytes of a CTA's tokens of a stage
+
 constexpr int kGroup = 8;              // token tiles walked together
 constexpr int kChunk = 8;              // blocks of K whose token scales come together
 constexpr int kChunkBytes = kChunk * 128 * 4;
 constexpr int kPart = 64;              // bytes of a row that are stored at a time
 constexpr int kOutBytes = 32 * kPart;  // of a warp
 // Registers of a thread: 128 + 256 threads share the 384 * 168 of the launch.
-#ifndef RF
-#define RF 40
-#define RM 232
-#endif
-constexpr int kRegsFew = RF, kRegsMany = RM;
+constexpr int kRegsFew = 40, kRegsMany = 232;
 
-enum : uint32_t { kSiteDone = 48, kSiteFull, kSiteScale, kSiteDrain };
+enum : uint32_t { kSiteDone = 48, kSiteFull, kSiteSlot, kSiteScale, kSiteDrain };
 
 template <int kBN>
 struct Cfg {
   static constexpr int kSlots = 512 / kBN;
-  static constexpr int kWRows = kBN / 2;          // of a CTA
-  static constexpr int kStage = kXTile + kWRows * 128;
+  static constexpr int kStage = kXTile + kBN / 2 * 128;  // bytes of a CTA
   static constexpr int kStages = kBN == 256 ? 5 : 7;
   static constexpr int kCols = kBN / 2;           // of a warpgroup
-  // Products of scales kept: a stage's MMAs are through only after all who sum have
-  // read the slot kSlots blocks before, so those of kStages + kSlots blocks back
-  // are not needed any more when the stage's next ones are written.
-  static constexpr int kProducts = kBN == 256 ? 8 : 16;
-  static_assert(kProducts >= kStages + kSlots);
   struct Bars {
-    uint64_t full[kStages], done[kStages];
+    uint64_t full[kStages], done[kStages], taken[kSlots];
     uint64_t s_full[2];
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
   };
-  static constexpr int kSmem =
-      1024 + kStages * kStage + 8 * 2 * kOutBytes + 2 * kChunkBytes + kProducts * 1024 + (int)sizeof(Bars);
+  // Products of scales kept, [block][half][token]: a stage's MMAs are through only
+  // after all who sum have read the slot kSlots blocks before, so those of kStages +
+  // kSlots blocks back are not needed any more when the stage's next ones are written.
+  static constexpr int kProducts = kBN == 256 ? 8 : 16;
+  static_assert(kProducts >= kStages + kSlots);
+  static constexpr int kSmem = 1024 + kStages * kStage + 8 * 2 * kOutBytes + 2 * kChunkBytes +
+                               kProducts * 1024 + (int)sizeof(Bars);
 };
 constexpr int kReaders = 16;  // warps of the pair that read a slot
 
@@ -158,16 +158,17 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* out_stage = ring + kStages * S::kStage;
   float* scales = reinterpret_cast<float*>(out_stage + 8 * 2 * kOutBytes);
-  float* products = scales + 2 * kChunk * 128;  // [block % kProducts][half][token]
+  float* products = scales + 2 * kChunk * 128;
   typename S::Bars* bars = reinterpret_cast<typename S::Bars*>(products + S::kProducts * 256);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
   volatile int* abort_flag = &bars->abort;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&bars->full[i], 1 + kReaders);  // used in CTA 0
+      mbar_init(&bars->full[i], 1);  // used in CTA 0
       mbar_init(&bars->done[i], 2);
     }
+    for (int i = 0; i < kSlots; ++i) mbar_init(&bars->taken[i], kReaders);  // used in CTA 0
     for (int i = 0; i < 2; ++i) mbar_init(&bars->s_full[i], 1);
     mbar_init(&bars->drain, 2);
     bars->abort = 0;
@@ -196,7 +197,7 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
       for (int t = cluster; t < tiles && ok; t += clusters) {
         const Tile w = tile_at(t, n_tiles, m_tiles);
         const int n0 = __shfl_sync(0xffffffffu, w.n * kTileN + 128 * rank, 0);
-        const int m0 = __shfl_sync(0xffffffffu, w.m * kBN + S::kWRows * rank, 0);
+        const int m0 = __shfl_sync(0xffffffffu, w.m * kBN + kBN / 2 * rank, 0);
         for (int b = 0; b < blocks; ++b, ++g) {
           const int slot = (int)(g % kStages);
           if (!(ok = mbar_wait_warp(&bars->done[slot], (uint32_t)(g / kStages & 1) ^ 1, abort_flag,
@@ -234,7 +235,8 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
         const int half = lane / kChunk % 2;
         // past the last band of weights the last one again, whose result is not stored
         const int band = min((w.m * kBN + S::kCols * half) / 128, (c.M - 1) / 128);
-        sw_next = c.sw[(size_t)band * blocks + min(b_a + lane % kChunk, blocks - 1)];
+        const int b = b_a + lane % kChunk;
+        sw_next = b < blocks ? c.sw[(size_t)band * blocks + b] : 0.0f;
         if (elect_one()) {
           mbar_arrive_expect_tx(&bars->s_full[asked & 1], kChunkBytes);
           tma_load_2d(scales + (asked & 1) * kChunk * 128, &maps.sx, &bars->s_full[asked & 1], n0, b_a);
@@ -277,22 +279,26 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
     } else if (rank == 0) {
       // ----------------------------------------------------------------- MMAs --
       const uint32_t base = sw128_desc_lo(smem_u32(ring));
-      const long long total = (long long)((tiles - cluster + clusters - 1) / clusters) * blocks;
-      for (long long g = warp >> 1; g < total; g += 2) {
-        const int slot = (int)(g % kStages);
-        if (!(ok = mbar_wait_warp(&bars->full[slot], (uint32_t)(g / kStages & 1), abort_flag, status,
-                                  kSiteFull)))
+      // Everything is worked out before the waits: from a slot's last hand-back to its
+      // MMAs is part of what bounds the kernel.
+      const int all = (tiles - cluster + clusters - 1) / clusters * blocks;
+      int g = warp >> 1, stage = g, full_phase = 0, slot = g, taken_phase = 1;
+      for (; g < all; g += 2) {
+        const uint32_t x = base + stage * (S::kStage >> 4), w = x + (kXTile >> 4);
+        const uint32_t d = tmem + kBN * slot;
+        if (!(ok = mbar_wait_warp(&bars->full[stage], full_phase, abort_flag, status, kSiteFull)) ||
+            !(ok = mbar_wait_warp(&bars->taken[slot], taken_phase, abort_flag, status, kSiteSlot)))
           break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t x = base + slot * (S::kStage >> 4), w = x + (kXTile >> 4);
-          const uint32_t d = tmem + kBN * (uint32_t)(g % kSlots);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             umma_f8_pair(d, x + 2 * k, w + 2 * k, idesc_f8(256, kBN), k > 0);
-          commit_pair(&bars->done[slot]);
+          commit_pair(&bars->done[stage]);
         }
         __syncwarp();
+        if ((stage += 2) >= kStages) stage -= kStages, full_phase ^= 1;
+        if ((slot += 2) >= kSlots) slot -= kSlots, taken_phase ^= 1;
       }
       if (elect_one()) {  // MMAs in flight end before TMEM is freed
         volatile int no_abort = 0;
@@ -309,44 +315,34 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
     // this warp's lanes and first column of a slot
     const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + kCols * me;
     const float* mine = products + 128 * me + 32 * q + lane;
-    const uint32_t leader = leader_address(&bars->full[0]);
-    int left = (tiles - cluster + clusters - 1) / clusters * blocks;  // blocks not begun
-    int stage = 0, phase = 0, slot = 0, get = 0, free_stage = kSlots % kStages;
-    uint32_t at = 0;
-    uint64_t s = 0;
-    // The next block's sums and products of scales are there: the sums at column
-    // `at`, the product in both halves of s.
-    auto begin = [&] {
-      ok = mbar_wait_warp(&bars->done[stage], phase, abort_flag, status, kSiteDone);
-      tc_fence_after();
-      at = src + kBN * slot;
-      if (++stage == kStages) stage = 0, phase ^= 1;
-      slot = (slot + 1) % kSlots;
-      --left;
-    };
-    auto product = [&] {
-      const float f = mine[get * 256];
-      asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "f"(f));
-      get = (get + 1) % S::kProducts;
-    };
-    // the first blocks' slots are free
-    if (lane == 0)
-      for (int i = 0; i < kSlots; ++i) arrive_at_leader(leader + 8 * i);
-    uint32_t va[32], vb[32];
-    begin();
-    tmem_ld(at, va);
-    tmem_ld(at + 32, vb);
-    float2 acc[kCols / 2];
-    auto add = [&](float2* to, const uint32_t(&v)[32]) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) fma2(to[i], v[2 * i], v[2 * i + 1], s);
-    };
-    for (int t = cluster; t < tiles && ok; t += clusters) {
+    const uint32_t leader = leader_address(&bars->taken[0]);
+    int stage = 0, phase = 0, get = 0, turn = 0;
+    bool seen = false;  // this lane has seen the next block done
+    for (int t = cluster; t < tiles; t += clusters) {
+      float2 acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
 #pragma unroll 1
-      for (int i = 0; i < blocks && ok; ++i) {
-        product();
+      for (int i = 0; i < blocks; ++i) {
+        ok = __all_sync(0xffffffffu, seen) ||
+             mbar_wait_warp(&bars->done[stage], phase, abort_flag, status, kSiteDone);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = src + kBN * turn;
+        const float f = mine[get * 256];
+        uint64_t s;  // the product of the scales, in both halves
+        asm volatile("mov.b64 %0, {%1, %1};" : "=l"(s) : "f"(f));
+        get = (get + 1) % S::kProducts;
+        if (++stage == kStages) stage = 0, phase ^= 1;
+        auto add = [&](float2* to, const uint32_t(&v)[32]) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) fma2(to[j], v[2 * j], v[2 * j + 1], s);
+        };
+        // No load is in flight from one iteration to the next: the compiler does not
+        // know that its registers are not to be moved before the wait.
+        uint32_t va[32], vb[32];
+        tmem_ld(at, va);
+        tmem_ld(at + 32, vb);
         tmem_wait_ld2(va, vb);
         if constexpr (kCols == 128) {
           add(acc, va);
@@ -355,21 +351,15 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
           tmem_ld_after(at + 96, vb, acc + 16);
           tmem_wait_ld2(va, vb);
         }
-        float2* rest = acc + kCols / 2 - 32;
-        // all is in registers: the MMAs of the block kSlots further may write
+        // all is in registers: the MMAs of a later block may write
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_at_leader(leader + 8 * free_stage);
-        if (++free_stage == kStages) free_stage = 0;
-        add(rest, va);
-        // while the last values are added, the next block's begin to come
-        const bool more = left > 0;
-        if (more) {
-          begin();
-          tmem_ld_after(at, va, rest);
-        }
-        add(rest + 16, vb);
-        if (more) tmem_ld_after(at + 32, vb, rest + 16);
+        if (lane == 0) arrive_at_leader(leader + 8 * turn);
+        turn = (turn + 1) % kSlots;
+        // (a look at a barrier takes 200 cycles, so it comes before the last adds)
+        seen = mbar_test_wait(&bars->done[stage], phase);
+        add(acc + kCols / 2 - 32, va);
+        add(acc + kCols / 2 - 16, vb);
       }
       if (!ok) break;
       const Tile w = tile_at(t, n_tiles, m_tiles);
@@ -408,8 +398,6 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
           if (i < cols) y[i] = from_f32<T>(i % 2 ? acc[i / 2].y : acc[i / 2].x);
       }
     }
-    // loads begun for a block that was given up have ended
-    tmem_wait_ld2(va, vb);
   }
   tc_fence_before();
   __syncthreads();
