@@ -4,7 +4,7 @@
 // it lies in memory (128 rows, a TMEM lane each, by 128 of K: one TMA box with
 // the 128-byte swizzle), so no instruction is spent on a weight: the tokens are
 // B, 16 to 128 of them (MMA N). Each block's accumulator is added to f32 sums in
-// registers by four warps, thread = weight row, times sw[b] * sx[b][n] of each
+// registers by four warps (eight for 128 tokens), thread = weight row, times sw[b] * sx[b][n] of each
 // token n.
 //
 // K is split over the CTAs of a cluster so that about two CTAs an SM stream
@@ -16,7 +16,6 @@
 namespace q6 {
 namespace {
 
-constexpr int kThreads = 192;
 constexpr int kWTile = 128 * 128;
 constexpr int kMaxSplit = 8;
 
@@ -26,6 +25,9 @@ template <int kN>
 struct Few {
   static constexpr int kStages = kN == 16 ? 6 : kN == 32 ? 5 : kN == 64 ? 4 : 3;
   static constexpr int kSlots = kN == 128 ? 2 : 4;
+  // warps that sum, and a warp's tokens: so many that two CTAs' registers fit an SM
+  static constexpr int kWarps = kN == 128 ? 8 : 4, kCols = kN * 4 / kWarps;
+  static constexpr int kThreads = 64 + 32 * kWarps;
   static constexpr int kXTile = kN * 128, kStage = kWTile + kXTile;
   static constexpr int kSx = kN * 4 < 128 ? 128 : kN * 4;  // a stage's token scales
   struct Bars {
@@ -56,10 +58,10 @@ __device__ __forceinline__ float load_from(const float* p, int rank) {
 }
 
 template <typename T, int kN>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(Few<kN>::kThreads, 2)
 f8_few_kernel(const __grid_constant__ Maps maps, const F8Call c, int split, unsigned int* status) {
   using S = Few<kN>;
-  constexpr int kStages = S::kStages, kSlots = S::kSlots;
+  constexpr int kStages = S::kStages, kSlots = S::kSlots, kThreads = S::kThreads, kCols = S::kCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -72,8 +74,8 @@ f8_few_kernel(const __grid_constant__ Maps maps, const F8Call c, int split, unsi
   const int first = (int)((long long)blocks * rank / split);
   const int last = (int)((long long)blocks * (rank + 1) / split);
   if (warp == 0 && elect_one()) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&bars->full[i], 1), mbar_init(&bars->empty[i], 4);
-    for (int i = 0; i < kSlots; ++i) mbar_init(&bars->done[i], 1), mbar_init(&bars->taken[i], 4);
+    for (int i = 0; i < kStages; ++i) mbar_init(&bars->full[i], 1), mbar_init(&bars->empty[i], S::kWarps);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&bars->done[i], 1), mbar_init(&bars->taken[i], S::kWarps);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     mbar_fence_init();
@@ -95,10 +97,11 @@ f8_few_kernel(const __grid_constant__ Maps maps, const F8Call c, int split, unsi
   const uint32_t tmem = bars->tmem_base;
   const int n_blocks = last - first;
   bool ok = true;
-  float acc[kN];
+  float acc[kCols];
 #pragma unroll
-  for (int i = 0; i < kN; ++i) acc[i] = 0.0f;
-  const int row = 32 * (warp & 3) + lane;  // of this thread's weight row, in warps 2 .. 5
+  for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
+  // this thread's weight row and first token, in the warps that sum
+  const int row = 32 * (warp & 3) + lane, n0 = (warp - 2) / 4 * kCols;
   if (warp == 0) {
     int g = 0;
     for (; g < n_blocks; ++g) {
@@ -145,8 +148,8 @@ f8_few_kernel(const __grid_constant__ Maps maps, const F8Call c, int split, unsi
     }
     __syncwarp();
   } else {
-    constexpr int kPart = kN < 32 ? kN : 32;  // columns read at a time
-    const uint32_t src = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    constexpr int kPart = kCols < 32 ? kCols : 32;  // columns read at a time
+    const uint32_t src = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + n0;
     const float* sw = c.sw + (size_t)mb * blocks + first;
     float next = n_blocks > 0 ? sw[0] : 0.0f;
     for (int g = 0; g < n_blocks; ++g) {
@@ -158,9 +161,9 @@ f8_few_kernel(const __grid_constant__ Maps maps, const F8Call c, int split, unsi
           !(ok = mbar_wait_warp(&bars->done[d], g / kSlots & 1, abort_flag, status, kSiteDone)))
         break;
       tc_fence_after();
-      const float4* sx = reinterpret_cast<const float4*>(scales + slot * S::kSx);
+      const float4* sx = reinterpret_cast<const float4*>(scales + slot * S::kSx) + n0 / 4;
 #pragma unroll
-      for (int h = 0; h < kN / kPart; ++h) {
+      for (int h = 0; h < kCols / kPart; ++h) {
         uint32_t v[kPart];
         tmem_ld(src + kN * d + kPart * h, v);
         tmem_wait(v);
@@ -181,10 +184,10 @@ f8_few_kernel(const __grid_constant__ Maps maps, const F8Call c, int split, unsi
     const int m = mb * 128 + row;
     if (split == 1) {
       if (m < c.M) {
-        T* y = static_cast<T*>(c.Y) + m;
+        T* y = static_cast<T*>(c.Y) + (size_t)n0 * c.ldy + m;
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
-          if (i < c.N) y[(size_t)i * c.ldy] = from_f32<T>(acc[i]);
+        for (int i = 0; i < kCols; ++i)
+          if (n0 + i < c.N) y[(size_t)i * c.ldy] = from_f32<T>(acc[i]);
       }
     }
   }
@@ -200,8 +203,8 @@ f8_few_kernel(const __grid_constant__ Maps maps, const F8Call c, int split, unsi
     float* sums = reinterpret_cast<float*>(ring);
     if (warp >= 2) {
 #pragma unroll
-      for (int i = 0; i < kN; ++i)
-        if (i < c.N) sums[i * 128 + row] = acc[i];
+      for (int i = 0; i < kCols; ++i)
+        if (n0 + i < c.N) sums[(n0 + i) * 128 + row] = acc[i];
     }
     cluster_sync();
     const int total = c.N * 128;
@@ -220,7 +223,7 @@ cudaError_t launch_n(const Maps& maps, const F8Call& c, int split, unsigned int*
                      cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((c.M + 127) / 128) * (unsigned)split);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Few<kN>::kThreads);
   cfg.dynamicSmemBytes = Few<kN>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

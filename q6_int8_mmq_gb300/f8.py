@@ -102,83 +102,102 @@ def alloc_f8_weights(M: int, K: int, device=None) -> F8Weights:
 
 
 def _input(X, name):
-    """(type code, rows, columns, row stride) of a 2-D view of rows."""
+    """(type code, shape, device, row stride) of a 2-D view of rows."""
+    try:
+        code, shape, dev = _types().get(X.dtype), X.shape, X.device
+        if code is not None and len(shape) == 2 and X.is_contiguous() and dev.type == "cuda":
+            return code, shape, dev, shape[1] or 1
+    except AttributeError:
+        pass
     code = _type(X, name)
-    n = _rows2d(X, name)
-    return code, n, X.shape[1], _rows(X, name, X.dtype, tuple(X.shape), X.device)
+    _rows2d(X, name)
+    return code, X.shape, X.device, _rows(X, name, X.dtype, X.shape, X.device)
 
 
-def _sink(out, cls, N, K, dev, alloc, stream):
-    """The quantised rows a call writes: `out`, which has to fit, or new ones."""
-    if out is None:
-        with _on(stream):
-            return alloc(N, K, dev)
+def _fits(out, cls, N, K, dev):
+    """Whether the rows a call writes go to `out`; raises if they do not fit."""
+    if out.__class__ is cls and out.N == N and out.K == K and out.device == dev:
+        return
     if not isinstance(out, cls):
         raise Q6Error(Q6_EINVAL, f"out must be {cls.__name__}, not {type(out).__name__}")
     if out.N != N or out.K != K or out.device != dev:
         raise Q6Error(Q6_EINVAL, f"out holds {out.N} x {out.K} activations on {out.device}, not "
                                  f"{N} x {K} on {dev}")
-    return out
 
 
-def _q8_sink(out, N, K, dev, want_xh, want_xq, want_us, stream):
+def _q8_out(out, N, K, dev, want_xh, want_xq, want_us, stream):
+    """int8 activations of N x K: `out`, which has to fit, or new ones."""
+    if out is not None:
+        _fits(out, Activations, N, K, dev)
+        return out
     act_plane_bytes(N, K)
-    if out is None and not (want_xh or want_xq):
+    if not (want_xh or want_xq):
         raise Q6Error(Q6_EINVAL, "one of want_xh and want_xq is needed")
-    out = _sink(out, Activations, N, K, dev,
-                lambda n, k, d: alloc_activations(n, k, d, want_xh, want_xq, want_us), stream)
-    return out, [None if t is None else t.data_ptr() for t in (out.xq, out.da, out.xh, out.us)]
+    with _on(stream):
+        return alloc_activations(N, K, dev, want_xh, want_xq, want_us)
 
 
-def _f8_sink(out, N, K, dev, stream):
-    out = _sink(out, F8Activations, N, K, dev, alloc_f8_activations, stream)
-    return out, [out.xq.data_ptr(), out.sx.data_ptr()]
+def _q8_pointers(act):
+    xq, xh, us = act.xq, act.xh, act.us
+    return (None if xq is None else xq.data_ptr(), act.da.data_ptr(),
+            None if xh is None else xh.data_ptr(), None if us is None else us.data_ptr())
+
+
+def _f8_out(out, N, K, dev, stream):
+    if out is not None:
+        _fits(out, F8Activations, N, K, dev)
+        return out
+    with _on(stream):
+        return alloc_f8_activations(N, K, dev)
 
 
 def f8_quantize_act(X, out: F8Activations | None = None, stream=None) -> F8Activations:
     """Quantises activations X [N, K] (f32, bf16 or f16 rows, 16-byte aligned; K a multiple of
     16) to e4m3 with a scale for each 128 of a row: largest magnitude / 448."""
-    code, N, K, ldx = _input(X, "X")
-    out, (xq, sx) = _f8_sink(out, N, K, X.device, stream)
-    _check(load().q6_f8_quantize_act(X.data_ptr(), code, N, K, ldx, xq, sx,
-                                     _stream(stream, X.device)))
+    code, (N, K), dev, ldx = _input(X, "X")
+    out = _f8_out(out, N, K, dev, stream)
+    _check(load().q6_f8_quantize_act(X.data_ptr(), code, N, K, ldx, out.xq.data_ptr(),
+                                     out.sx.data_ptr(), _stream(stream, dev)))
     return out
 
 
 def f8_quantize_weights(W, out: F8Weights | None = None, stream=None) -> F8Weights:
     """Quantises a weight W [M, K] (f32, bf16 or f16 rows, 16-byte aligned; K a multiple of 16)
     to e4m3 with a scale for each block of 128 x 128: largest magnitude / 448."""
-    code, M, K, ldw = _input(W, "W")
+    code, (M, K), dev, ldw = _input(W, "W")
     if out is None:
         with _on(stream):
-            out = alloc_f8_weights(M, K, W.device)
-    elif not isinstance(out, F8Weights) or (out.M, out.K, out.device) != (M, K, W.device):
-        raise Q6Error(Q6_EINVAL, f"out must be F8Weights of {M} x {K} on {W.device}")
+            out = alloc_f8_weights(M, K, dev)
+    elif not isinstance(out, F8Weights) or (out.M, out.K, out.device) != (M, K, dev):
+        raise Q6Error(Q6_EINVAL, f"out must be F8Weights of {M} x {K} on {dev}")
     _check(load().q6_f8_quantize_weights(W.data_ptr(), code, M, K, ldw, out.wq.data_ptr(),
-                                         out.sw.data_ptr(), _stream(stream, W.device)))
+                                         out.sw.data_ptr(), _stream(stream, dev)))
     return out
 
 
-def _norm(entry, sink, X, weight, eps, residual, h, stream):
-    code, N, K, ldx = _input(X, "X")
-    dev = X.device
-    wtype = _type(weight, "weight")
-    _whole(weight, "weight", weight.dtype, (K,), dev)
-    rtype = ldr = ldh = 0
-    if residual is not None:
-        rtype = _type(residual, "residual")
-        ldr = ldh = _rows(residual, "residual", residual.dtype, (N, K), dev)
-        if h is None:
-            h = residual
-        else:
-            ldh = _rows(h, "h", residual.dtype, (N, K), dev)
-    elif h is not None:
-        raise Q6Error(Q6_EINVAL, "h without a residual")
-    out, buffers = sink(N, K, dev)
-    _check(entry(X.data_ptr(), code, ldx, None if residual is None else residual.data_ptr(), rtype,
-                 ldr, weight.data_ptr(), wtype, eps, N, K, None if h is None else h.data_ptr(), ldh,
-                 *buffers, _stream(stream, dev)))
-    return out, X if residual is None else h
+def _norm_args(X, weight, residual, h):
+    """What both norms pass on of their inputs: (shape, device, h, arguments up to the weight's
+    type, h's pointer and row stride)."""
+    code, shape, dev, ldx = _input(X, "X")
+    types = _types()
+    wtype = types.get(getattr(weight, "dtype", None))
+    if (wtype is None or weight.device != dev or weight.dim() != 1 or weight.shape[0] != shape[1]
+            or not weight.is_contiguous()):
+        wtype = _type(weight, "weight")
+        _whole(weight, "weight", weight.dtype, (shape[1],), dev)
+    if residual is None:
+        if h is not None:
+            raise Q6Error(Q6_EINVAL, "h without a residual")
+        return shape, dev, X, (X.data_ptr(), code, ldx, None, 0, 0, weight.data_ptr(), wtype), None, 0
+    rtype = _type(residual, "residual")
+    dtype = residual.dtype
+    ldr = ldh = _rows(residual, "residual", dtype, shape, dev)
+    r = p = residual.data_ptr()
+    if h is None:
+        h = residual
+    else:
+        ldh, p = _rows(h, "h", dtype, shape, dev), h.data_ptr()
+    return shape, dev, h, (X.data_ptr(), code, ldx, r, rtype, ldr, weight.data_ptr(), wtype), p, ldh
 
 
 def rms_norm_q8(X, weight, eps: float, residual=None, h=None, out: Activations | None = None,
@@ -188,39 +207,48 @@ def rms_norm_q8(X, weight, eps: float, residual=None, h=None, out: Activations |
     (rows 16-byte aligned, K a multiple of 256), weight [K]. h gets the sum, rounded to
     residual's type; without h it goes into residual. Without a residual it is the norm of X.
     Codes are those of h * weight, the norm is in the scales. Returns (Activations, h)."""
-    return _norm(load().q6_rms_norm_q8,
-                 lambda n, k, d: _q8_sink(out, n, k, d, want_xh, want_xq, want_us, stream),
-                 X, weight, eps, residual, h, stream)
+    (N, K), dev, h, args, p, ldh = _norm_args(X, weight, residual, h)
+    out = _q8_out(out, N, K, dev, want_xh, want_xq, want_us, stream)
+    _check(load().q6_rms_norm_q8(*args, eps, N, K, p, ldh, *_q8_pointers(out), _stream(stream, dev)))
+    return out, h
 
 
 def rms_norm_f8(X, weight, eps: float, residual=None, h=None, out: F8Activations | None = None,
                 stream=None):
     """The same norm as e4m3 activations for f8_mmq() (K a multiple of 16). Returns
     (F8Activations, h)."""
-    return _norm(load().q6_rms_norm_f8, lambda n, k, d: _f8_sink(out, n, k, d, stream),
-                 X, weight, eps, residual, h, stream)
+    (N, K), dev, h, args, p, ldh = _norm_args(X, weight, residual, h)
+    out = _f8_out(out, N, K, dev, stream)
+    _check(load().q6_rms_norm_f8(*args, eps, N, K, p, ldh, out.xq.data_ptr(), out.sx.data_ptr(),
+                                 _stream(stream, dev)))
+    return out, h
 
 
-def _silu(entry, sink, X, stream):
-    code, N, width, ldx = _input(X, "X")
+def _gate_up(X):
+    code, (N, width), dev, ldx = _input(X, "X")
     if width % 2:
         raise Q6Error(Q6_EINVAL, f"X has {width} columns, not gate and up halves")
-    out, buffers = sink(N, width // 2, X.device)
-    _check(entry(X.data_ptr(), code, N, width // 2, ldx, *buffers, _stream(stream, X.device)))
-    return out
+    return code, N, width // 2, dev, ldx
 
 
 def silu_mul_q8(X, out: Activations | None = None, want_xh: bool = True, want_xq: bool = True,
                 want_us: bool = False, stream=None) -> Activations:
     """silu(gate) * up of X [N, 2 K] (f32, bf16 or f16 rows, 16-byte aligned: K gate, then K up
     values) as int8 activations for mmq() and q4k_mmq() (want_us); K a multiple of 256."""
-    return _silu(load().q6_silu_mul_q8,
-                 lambda n, k, d: _q8_sink(out, n, k, d, want_xh, want_xq, want_us, stream), X, stream)
+    code, N, K, dev, ldx = _gate_up(X)
+    out = _q8_out(out, N, K, dev, want_xh, want_xq, want_us, stream)
+    _check(load().q6_silu_mul_q8(X.data_ptr(), code, N, K, ldx, *_q8_pointers(out),
+                                 _stream(stream, dev)))
+    return out
 
 
 def silu_mul_f8(X, out: F8Activations | None = None, stream=None) -> F8Activations:
     """The same as e4m3 activations for f8_mmq(); K a multiple of 16."""
-    return _silu(load().q6_silu_mul_f8, lambda n, k, d: _f8_sink(out, n, k, d, stream), X, stream)
+    code, N, K, dev, ldx = _gate_up(X)
+    out = _f8_out(out, N, K, dev, stream)
+    _check(load().q6_silu_mul_f8(X.data_ptr(), code, N, K, ldx, out.xq.data_ptr(),
+                                 out.sx.data_ptr(), _stream(stream, dev)))
+    return out
 
 
 def f8_mmq(w: F8Weights, act: F8Activations, out=None, dtype=None, stream=None):
