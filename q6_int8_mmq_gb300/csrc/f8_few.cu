@@ -3,19 +3,20 @@
 // What bounds it is the weight, read once. It is the tensor cores' A operand as
 // it lies in memory (128 rows, a TMEM lane each, by 128 of K: one TMA box with
 // the 128-byte swizzle), so no instruction is spent on a weight: the tokens are
-// B, 16 to 128 of them (MMA N). Each block's accumulator is added to f32 sums in
-// registers by four warps (eight for 128 tokens), thread = weight row, times sw[b] * sx[b][n] of each
+// B, 16 to 64 of them (MMA N). Each block's accumulator is added to f32 sums in
+// registers by four warps, thread = weight row, times sw[b] * sx[b][n] of each
 // token n.
 //
 // K is split over the CTAs of a cluster so that about two CTAs an SM stream
-// weights; they exchange their sums through distributed shared memory, and each
-// adds up a part of the results, in the order of K.
+// weights. Each sends its sums to the CTAs of the cluster that add up a part of them
+// each, in the order of K, through distributed shared memory.
 #include "f8_internal.cuh"
 #include "f8_tc.cuh"
 
 namespace q6 {
 namespace {
 
+constexpr int kThreads = 192;
 constexpr int kWTile = 128 * 128;
 constexpr int kMaxSplit = 8;
 
@@ -23,13 +24,12 @@ enum : uint32_t { kSiteEmpty = 56, kSiteFull, kSiteSlot, kSiteDone, kSiteDrain }
 
 template <int kN>
 struct Few {
-  static constexpr int kStages = kN == 16 ? 6 : kN == 32 ? 5 : kN == 64 ? 4 : 3;
-  static constexpr int kSlots = kN == 128 ? 2 : 4;
-  // warps that sum, and a warp's tokens: so many that two CTAs' registers fit an SM
-  static constexpr int kWarps = kN == 128 ? 8 : 4, kCols = kN * 4 / kWarps;
-  static constexpr int kThreads = 64 + 32 * kWarps;
+  static constexpr int kStages = kN == 16 ? 5 : kN == 32 ? 4 : 3;
+  static constexpr int kSlots = 4;
   static constexpr int kXTile = kN * 128, kStage = kWTile + kXTile;
   static constexpr int kSx = kN * 4 < 128 ? 128 : kN * 4;  // a stage's token scales
+  // the cluster's sums that this CTA adds up: [CTA][a part of the tokens' rows]
+  static constexpr int kSums = (32 * kN + kMaxSplit * kMaxSplit) * 16;
   struct Bars {
     uint64_t full[kStages], empty[kStages];
     uint64_t done[kSlots], taken[kSlots];
@@ -37,36 +37,54 @@ struct Few {
     uint32_t tmem_base;
     int abort;
   };
-  static constexpr int kSmem = 1024 + kStages * (kStage + kSx) + (int)sizeof(Bars);
+  static constexpr int kSmem = 1024 + kStages * (kStage + kSx) + kSums + (int)sizeof(Bars);
 };
 
 struct Maps {
   CUtensorMap x, w, sx;
 };
 
-// A value of the same place in the shared memory of CTA `rank` of the cluster.
-__device__ __forceinline__ float load_from(const float* p, int rank) {
-  float v;
+// Stores to the same place in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ void store_at(float4* p, int rank, const float4& v) {
   asm volatile(
       "{\n\t.reg .b32 ra;\n\t"
-      "mapa.shared::cluster.u32 ra, %1, %2;\n\t"
-      "ld.shared::cluster.f32 %0, [ra];\n\t}\n"
-      : "=f"(v)
-      : "r"(smem_u32(p)), "r"(rank)
+      "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
+      "st.shared::cluster.v4.f32 [ra], {%2, %3, %4, %5};\n\t}\n" ::"r"(smem_u32(p)),
+      "r"(rank), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
       : "memory");
-  return v;
+}
+// Four results next to each other, `left` of them inside Y; `vec`: they may be stored
+// at once.
+template <typename T>
+__device__ __forceinline__ void store4(T* y, const float4& v, int left, bool vec) {
+  if (vec && left >= 4) {
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(y) = v;
+    else *reinterpret_cast<uint2*>(y) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+  } else {
+    if (left > 0) y[0] = from_f32<T>(v.x);
+    if (left > 1) y[1] = from_f32<T>(v.y);
+    if (left > 2) y[2] = from_f32<T>(v.z);
+    if (left > 3) y[3] = from_f32<T>(v.w);
+  }
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 template <typename T, int kN>
-__global__ void __launch_bounds__(Few<kN>::kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 2)
 f8_few_kernel(const __grid_constant__ Maps maps, const F8Call c, int split, unsigned int* status) {
   using S = Few<kN>;
-  constexpr int kStages = S::kStages, kSlots = S::kSlots, kThreads = S::kThreads, kCols = S::kCols;
+  constexpr int kStages = S::kStages, kSlots = S::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* scales = ring + kStages * S::kStage;
-  typename S::Bars* bars = reinterpret_cast<typename S::Bars*>(scales + kStages * S::kSx);
+  float* sums = reinterpret_cast<float*>(scales + kStages * S::kSx);
+  typename S::Bars* bars = reinterpret_cast<typename S::Bars*>(sums + S::kSums / 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &bars->abort;
   const int rank = blockIdx.x % split, mb = blockIdx.x / split;
@@ -74,8 +92,8 @@ f8_few_kernel(const __grid_constant__ Maps maps, const F8Call c, int split, unsi
   const int first = (int)((long long)blocks * rank / split);
   const int last = (int)((long long)blocks * (rank + 1) / split);
   if (warp == 0 && elect_one()) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&bars->full[i], 1), mbar_init(&bars->empty[i], S::kWarps);
-    for (int i = 0; i < kSlots; ++i) mbar_init(&bars->done[i], 1), mbar_init(&bars->taken[i], S::kWarps);
+    for (int i = 0; i < kStages; ++i) mbar_init(&bars->full[i], 1), mbar_init(&bars->empty[i], 4);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&bars->done[i], 1), mbar_init(&bars->taken[i], 4);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     mbar_fence_init();
@@ -89,6 +107,7 @@ f8_few_kernel(const __grid_constant__ Maps maps, const F8Call c, int split, unsi
     tmem_alloc(&bars->tmem_base, kSlots * kN);
     tmem_relinquish();
   }
+  if (split > 1) cluster_arrive();  // this CTA's shared memory may be written to
   griddep_wait();
   griddep_launch_dependents();
   tc_fence_before();
@@ -97,11 +116,10 @@ f8_few_kernel(const __grid_constant__ Maps maps, const F8Call c, int split, unsi
   const uint32_t tmem = bars->tmem_base;
   const int n_blocks = last - first;
   bool ok = true;
-  float acc[kCols];
+  float acc[kN];
 #pragma unroll
-  for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
-  // this thread's weight row and first token, in the warps that sum
-  const int row = 32 * (warp & 3) + lane, n0 = (warp - 2) / 4 * kCols;
+  for (int i = 0; i < kN; ++i) acc[i] = 0.0f;
+  const int quarter = warp & 3;  // of the 128 rows, in the warps that sum
   if (warp == 0) {
     int g = 0;
     for (; g < n_blocks; ++g) {
@@ -148,22 +166,25 @@ f8_few_kernel(const __grid_constant__ Maps maps, const F8Call c, int split, unsi
     }
     __syncwarp();
   } else {
-    constexpr int kPart = kCols < 32 ? kCols : 32;  // columns read at a time
-    const uint32_t src = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + n0;
+    constexpr int kPart = kN < 32 ? kN : 32;  // columns read at a time
+    const uint32_t src = tmem + ((uint32_t)(32 * quarter) << 16);
     const float* sw = c.sw + (size_t)mb * blocks + first;
-    float next = n_blocks > 0 ? sw[0] : 0.0f;
+    // lane l has the scales of the weights' blocks l, 32 + l, ..., 32 blocks ahead (a load
+    // takes longer than a block)
+    auto fetch = [&](int g) { return g + lane < n_blocks ? sw[g + lane] : 0.0f; };
+    float sw_now = 0.0f, sw_next = fetch(0);
     for (int g = 0; g < n_blocks; ++g) {
       const int slot = g % kStages, d = g % kSlots;
-      const float s = next;
-      if (g + 1 < n_blocks) next = sw[g + 1];
+      if (g % 32 == 0) sw_now = sw_next, sw_next = fetch(g + 32);
+      const float s = __shfl_sync(0xffffffffu, sw_now, g % 32);
       // the copies' barrier makes the scales visible, the MMAs' the sums
       if (!(ok = mbar_wait_warp(&bars->full[slot], g / kStages & 1, abort_flag, status, kSiteFull)) ||
           !(ok = mbar_wait_warp(&bars->done[d], g / kSlots & 1, abort_flag, status, kSiteDone)))
         break;
       tc_fence_after();
-      const float4* sx = reinterpret_cast<const float4*>(scales + slot * S::kSx) + n0 / 4;
+      const float4* sx = reinterpret_cast<const float4*>(scales + slot * S::kSx);
 #pragma unroll
-      for (int h = 0; h < kCols / kPart; ++h) {
+      for (int h = 0; h < kN / kPart; ++h) {
         uint32_t v[kPart];
         tmem_ld(src + kN * d + kPart * h, v);
         tmem_wait(v);
@@ -181,14 +202,18 @@ f8_few_kernel(const __grid_constant__ Maps maps, const F8Call c, int split, unsi
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->taken[d]), mbar_arrive(&bars->empty[slot]);
     }
-    const int m = mb * 128 + row;
-    if (split == 1) {
-      if (m < c.M) {
-        T* y = static_cast<T*>(c.Y) + (size_t)n0 * c.ldy + m;
+    const int row = 32 * quarter + lane;
+    if (split > 1) {
+      // [token][row], over the ring: every stage was waited for, so nothing is under way
+      float* own = reinterpret_cast<float*>(ring) + row;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i)
-          if (n0 + i < c.N) y[(size_t)i * c.ldy] = from_f32<T>(acc[i]);
-      }
+      for (int i = 0; i < kN; ++i)
+        if (i < c.N) own[128 * i] = acc[i];
+    } else if (mb * 128 + row < c.M) {
+      T* y = static_cast<T*>(c.Y) + mb * 128 + row;
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (i < c.N) y[(size_t)i * c.ldy] = from_f32<T>(acc[i]);
     }
   }
   tc_fence_before();
@@ -198,23 +223,30 @@ f8_few_kernel(const __grid_constant__ Maps maps, const F8Call c, int split, unsi
     tmem_dealloc(tmem, kSlots * kN);
   }
   if (split > 1) {
-    // Sums [n][row] over the ring, which nothing reads or writes any more (every
-    // stage was waited for). The cluster's CTAs add up tokens and rows in turn.
-    float* sums = reinterpret_cast<float*>(ring);
-    if (warp >= 2) {
+    // Fours of rows of a token: CTA r adds up those from r * part on.
+    const int fours = 32 * c.N, part = (fours + split - 1) / split;
+    float4* in = reinterpret_cast<float4*>(sums);
+    cluster_wait();
+    for (int e = threadIdx.x; e < fours; e += kThreads) {
+      const int to = e / part;
+      store_at(in + rank * part + e - to * part, to, reinterpret_cast<const float4*>(ring)[e]);
+    }
+    cluster_arrive();
+    cluster_wait();
+    const bool vec = (reinterpret_cast<uintptr_t>(c.Y) | (uintptr_t)(c.ldy * (long long)sizeof(T))) %
+                         (4 * sizeof(T)) == 0;
+    for (int i = threadIdx.x; i < part && rank * part + i < fours; i += kThreads) {
+      float4 v = in[i];
 #pragma unroll
-      for (int i = 0; i < kCols; ++i)
-        if (n0 + i < c.N) sums[(n0 + i) * 128 + row] = acc[i];
+      for (int r = 1; r < kMaxSplit; ++r) {
+        if (r < split) {
+          const float4 p = in[r * part + i];
+          v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+        }
+      }
+      const int e = rank * part + i, m = mb * 128 + e % 32 * 4;
+      store4(static_cast<T*>(c.Y) + (size_t)(e / 32) * c.ldy + m, v, c.M - m, vec);
     }
-    cluster_sync();
-    const int total = c.N * 128;
-    for (int e = rank * kThreads + threadIdx.x; e < total; e += split * kThreads) {
-      float v = load_from(sums + e, 0);
-      for (int r = 1; r < split; ++r) v += load_from(sums + e, r);
-      const int m = mb * 128 + e % 128;
-      if (m < c.M) static_cast<T*>(c.Y)[(size_t)(e / 128) * c.ldy + m] = from_f32<T>(v);
-    }
-    cluster_sync();
   }
 }
 
@@ -223,7 +255,7 @@ cudaError_t launch_n(const Maps& maps, const F8Call& c, int split, unsigned int*
                      cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((c.M + 127) / 128) * (unsigned)split);
-  cfg.blockDim = dim3(Few<kN>::kThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Few<kN>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -241,8 +273,7 @@ cudaError_t launch_t(const Maps& maps, const F8Call& c, int n, int split, unsign
                      cudaStream_t s) {
   return n == 16   ? launch_n<T, 16>(maps, c, split, status, s)
          : n == 32 ? launch_n<T, 32>(maps, c, split, status, s)
-         : n == 64 ? launch_n<T, 64>(maps, c, split, status, s)
-                   : launch_n<T, 128>(maps, c, split, status, s);
+                   : launch_n<T, 64>(maps, c, split, status, s);
 }
 
 // Parts of K: as many as leave all CTAs resident, two an SM.
@@ -261,13 +292,16 @@ cudaError_t f8_few_prepare() {
   cudaError_t e = cudaSuccess;
   auto raise = [&](auto kernel, int smem) {
     if (!e) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // two CTAs an SM want all of its shared memory
+    if (!e)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
   };
   auto all = [&](auto t) {
     using T = decltype(t);
     raise(f8_few_kernel<T, 16>, Few<16>::kSmem);
     raise(f8_few_kernel<T, 32>, Few<32>::kSmem);
     raise(f8_few_kernel<T, 64>, Few<64>::kSmem);
-    raise(f8_few_kernel<T, 128>, Few<128>::kSmem);
   };
   all(float());
   all(__nv_bfloat16());
@@ -276,7 +310,7 @@ cudaError_t f8_few_prepare() {
 }
 
 int launch_f8_few(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStream_t s) {
-  const int n = c.N <= 16 ? 16 : c.N <= 32 ? 32 : c.N <= 64 ? 64 : 128;
+  const int n = c.N <= 16 ? 16 : c.N <= 32 ? 32 : 64;
   Maps maps;
   int rc;
   if ((rc = encode_f8_map(&maps.x, c.xq, c.N, c.K, n, "xq")) ||
