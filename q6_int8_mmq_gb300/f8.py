@@ -84,10 +84,18 @@ class F8Weights:
         return self.wq.device
 
 
+def _cuda(device):
+    import torch
+    dev = torch.device("cuda" if device is None else device)
+    if dev.type != "cuda":
+        raise Q6Error(Q6_EINVAL, f"buffers have to be on a CUDA device, not {dev}")
+    return dev
+
+
 def alloc_f8_activations(N: int, K: int, device=None) -> F8Activations:
     """Buffers for N x K e4m3 activations (K a multiple of 16)."""
     import torch
-    dev, ldsx = device or torch.device("cuda"), f8_act_bytes(N, K)[2]
+    dev, ldsx = _cuda(device), f8_act_bytes(N, K)[2]
     return _made(F8Activations, N=N, K=K, xq=torch.empty((N, K), dtype=_f8(), device=dev),
                  sx=torch.empty((_blocks(K), ldsx), dtype=torch.float32, device=dev))
 
@@ -95,7 +103,7 @@ def alloc_f8_activations(N: int, K: int, device=None) -> F8Activations:
 def alloc_f8_weights(M: int, K: int, device=None) -> F8Weights:
     """Buffers for an M x K e4m3 weight (K a multiple of 16)."""
     import torch
-    dev = device or torch.device("cuda")
+    dev = _cuda(device)
     f8_weight_bytes(M, K)
     return _made(F8Weights, M=M, K=K, wq=torch.empty((M, K), dtype=_f8(), device=dev),
                  sw=torch.empty((_blocks(M), _blocks(K)), dtype=torch.float32, device=dev))
@@ -189,14 +197,21 @@ def _norm_args(X, weight, residual, h):
         if h is not None:
             raise Q6Error(Q6_EINVAL, "h without a residual")
         return shape, dev, X, (X.data_ptr(), code, ldx, None, 0, 0, weight.data_ptr(), wtype), None, 0
-    rtype = _type(residual, "residual")
-    dtype = residual.dtype
-    ldr = ldh = _rows(residual, "residual", dtype, shape, dev)
+    rtype = types.get(getattr(residual, "dtype", None))
+    if rtype is None:
+        rtype = _type(residual, "residual")
+    dtype, width = residual.dtype, shape[1] or 1
+    ldr = ldh = (width if residual.shape == shape and residual.device == dev and residual.is_contiguous()
+                 else _rows(residual, "residual", dtype, shape, dev))
     r = p = residual.data_ptr()
     if h is None:
         h = residual
     else:
-        ldh, p = _rows(h, "h", dtype, shape, dev), h.data_ptr()
+        try:
+            plain = h.dtype is dtype and h.shape == shape and h.device == dev and h.is_contiguous()
+        except AttributeError:
+            plain = False
+        ldh, p = width if plain else _rows(h, "h", dtype, shape, dev), h.data_ptr()
     return shape, dev, h, (X.data_ptr(), code, ldx, r, rtype, ldr, weight.data_ptr(), wtype), p, ldh
 
 
@@ -268,8 +283,10 @@ def f8_mmq(w: F8Weights, act: F8Activations, out=None, dtype=None, stream=None):
         out = _empty((N, M), dtype, dev, stream)
     elif dtype is not None and getattr(out, "dtype", None) is not dtype:
         raise Q6Error(Q6_EINVAL, f"out is not of dtype {dtype}")
-    code = _type(out, "out")
-    ldy = _rows(out, "out", out.dtype, (N, M), dev)
+    code, ldy = _types().get(getattr(out, "dtype", None)), M
+    if code is None or out.shape != (N, M) or out.device != dev or not out.is_contiguous():
+        code = _type(out, "out")
+        ldy = _rows(out, "out", out.dtype, (N, M), dev)
     path = ctypes.c_int(-1)
     _check(load().q6_f8_mmq(w.wq.data_ptr(), w.sw.data_ptr(), M, K, act.xq.data_ptr(),
                             act.sx.data_ptr(), N, out.data_ptr(), code, ldy, ctypes.byref(path),
