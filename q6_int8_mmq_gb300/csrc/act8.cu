@@ -258,9 +258,10 @@ __global__ void __launch_bounds__(256, kRowCtas<T, kF8, kGlu, kU>) rows_kernel(c
 }
 
 // One row a CTA, kU parts a warp in flight together. The scales (and for us the sums)
-// of its blocks wait in shared memory for the row's factor.
+// of its blocks wait in shared memory for the row's factor. (At most 85 registers: with
+// 64 the norm of 8192 x 4096 bf16 takes 48.4 instead of 39.7 us, unbound 42.2.)
 template <typename T, typename R, bool kF8, bool kAdd, int kU>
-__global__ void __launch_bounds__(kU > 1 ? 256 : 1024) norm_kernel(const NormCall c, const RowSink o) {
+__global__ void __launch_bounds__(kU > 1 ? 256 : 1024, kU > 1 ? 3 : 1) norm_kernel(const NormCall c, const RowSink o) {
   using S = Shape<kF8, (int)(sizeof(T) > sizeof(R) ? sizeof(T) : sizeof(R))>;
   constexpr int kPer = S::kPer, kLanes = S::kLanes, kPartK = S::kPart;
   extern __shared__ float kept[];

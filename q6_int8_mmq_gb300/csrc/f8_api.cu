@@ -32,9 +32,9 @@ bool rows_aligned(const void* p, int type, int64_t ld) {
   return aligned(p, 16) && ld % (type == Q6_TYPE_F32 ? 4 : 8) == 0;
 }
 
-// Sizes up to which the kernels' indices, which run up to a tile past the end,
-// stay within 31 bits.
-constexpr int kMost = INT32_MAX - 512;
+// Sizes up to which the kernels' indices, which run up to four parts of 512 past the
+// end, stay within 31 bits.
+constexpr int kMost = INT32_MAX - 4096;
 constexpr int64_t kMostElements = 1ll << 40;
 
 // Tokens up to which the weight's rows are the tensor cores' lanes. (With 128 tokens that
