@@ -183,6 +183,13 @@ def f8_quantize_weights(W, out: F8Weights | None = None, stream=None) -> F8Weigh
     return out
 
 
+def _eps(eps):
+    try:
+        return float(eps)
+    except (TypeError, ValueError):
+        raise Q6Error(Q6_EINVAL, f"eps must be a number, not {eps!r}") from None
+
+
 def _norm_args(X, weight, residual, h):
     """What both norms pass on of their inputs: (shape, device, h, arguments up to the weight's
     type, h's pointer and row stride)."""
@@ -224,7 +231,7 @@ def rms_norm_q8(X, weight, eps: float, residual=None, h=None, out: Activations |
     Codes are those of h * weight, the norm is in the scales. Returns (Activations, h)."""
     (N, K), dev, h, args, p, ldh = _norm_args(X, weight, residual, h)
     out = _q8_out(out, N, K, dev, want_xh, want_xq, want_us, stream)
-    _check(load().q6_rms_norm_q8(*args, eps, N, K, p, ldh, *_q8_pointers(out), _stream(stream, dev)))
+    _check(load().q6_rms_norm_q8(*args, _eps(eps), N, K, p, ldh, *_q8_pointers(out), _stream(stream, dev)))
     return out, h
 
 
@@ -234,7 +241,7 @@ def rms_norm_f8(X, weight, eps: float, residual=None, h=None, out: F8Activations
     (F8Activations, h)."""
     (N, K), dev, h, args, p, ldh = _norm_args(X, weight, residual, h)
     out = _f8_out(out, N, K, dev, stream)
-    _check(load().q6_rms_norm_f8(*args, eps, N, K, p, ldh, out.xq.data_ptr(), out.sx.data_ptr(),
+    _check(load().q6_rms_norm_f8(*args, _eps(eps), N, K, p, ldh, out.xq.data_ptr(), out.sx.data_ptr(),
                                  _stream(stream, dev)))
     return out, h
 

@@ -207,6 +207,55 @@ def test_quantise_of_values_that_are_not_finite_and_of_the_smallest():
     assert (w.wq[1, 256:384].float() == 448).all() and not w.wq[0, 256:384].float().any()
 
 
+@pytest.mark.parametrize("f8", [False, True])
+def test_norm_of_many_wide_rows(f8):
+    """More rows than one a SM, each longer than its CTA reads at a time."""
+    g = gen(7)
+    N, K = 160, 66560
+    x, r = activations(g, N, K, BF16), activations(g, N, K, F32)
+    w = 1 + 0.3 * randn(g, K)
+    h, t, root, rel, root_rel = ref.norm(x, r, w, 1e-6)
+    if f8:
+        act, got = q6.rms_norm_f8(x, w, 1e-6, residual=r)
+        check_f8(act, N, t, rel, root, root_rel)
+    else:
+        act, got = q6.rms_norm_q8(x, w, 1e-6, residual=r, want_us=True)
+        check_q8(act, N, t, rel, root, root_rel)
+    assert ((got.double() - h).abs() <= 2 * ref.U * h.abs()).all()
+
+
+def test_of_no_rows():
+    w = torch.ones(512, device="cuda")
+    for dtype in TYPES:
+        x = torch.empty(0, 512, dtype=dtype, device="cuda")
+        assert q6.f8_quantize_act(x).xq.shape == (0, 512)
+        assert q6.rms_norm_f8(x, w, 1e-6, residual=x)[0].xq.shape == (0, 512)
+        assert q6.rms_norm_q8(x, w, 1e-6)[0].xq.shape == (0, 512)
+        assert q6.silu_mul_f8(x).xq.shape == (0, 256) and q6.silu_mul_q8(x).xh.shape == (0, 256)
+    q6.sync_status()
+
+
+def test_any_sizes():
+    """Forty random sizes through a chain of calls: the same checks as above."""
+    import random
+    rng = random.Random(11)
+    for i in range(40):
+        g = gen(1000 + i)
+        N = int(round(2 ** rng.uniform(0, 10.5)))
+        M, K = int(round(2 ** rng.uniform(0, 11.5))), 16 * int(round(2 ** rng.uniform(0, 7.5)))
+        dtype = TYPES[i % 3]
+        x, r = activations(g, N, K, dtype), activations(g, N, K, TYPES[i // 3 % 3])
+        weight = (1 + 0.3 * randn(g, K)).to(TYPES[i // 9 % 3])
+        h, t, root, rel, root_rel = ref.norm(x, r, weight, 1e-5)
+        act, _ = q6.rms_norm_f8(x, weight, 1e-5, residual=r)
+        check_f8(act, N, t, rel, root, root_rel)
+        w = q6.f8_quantize_weights((randn(g, 2 * M, K) * torch.exp(randn(g, 2 * M, 1))).to(dtype))
+        Y, _ = check_product(w, act, TYPES[(i + 1) % 3] if TYPES[(i + 1) % 3] is not F16 else BF16)
+        if M % 16 == 0:
+            t, rel = ref.silu_mul(Y)
+            check_f8(q6.silu_mul_f8(Y), N, t, rel)
+
+
 def test_scales_past_the_last_token_are_left():
     x = torch.ones(5, 256, device="cuda")
     f8, q8 = q6.alloc_f8_activations(5, 256), q6.alloc_activations(5, 256)
@@ -576,6 +625,8 @@ def test_calls_that_do_not_fit_are_refused():
                  lambda: q6.rms_norm_f8(x, weight[:256], 1e-6),
                  lambda: q6.rms_norm_f8(x, weight.double(), 1e-6),
                  lambda: q6.rms_norm_f8(x, weight, 0.0),
+                 lambda: q6.rms_norm_f8(x, weight, "small"),
+                 lambda: q6.rms_norm_q8(x, weight, None),
                  lambda: q6.rms_norm_f8(x, weight, 1e-6, h=x),
                  lambda: q6.rms_norm_f8(x, weight, 1e-6, residual=x.half(), h=x),
                  lambda: q6.rms_norm_f8(x, weight, 1e-6, residual=wide),
