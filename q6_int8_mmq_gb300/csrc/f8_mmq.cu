@@ -52,7 +52,12 @@ template <int kBN>
 struct Cfg {
   static constexpr int kSlots = 512 / kBN;
   static constexpr int kStage = kXTile + kBN / 2 * 128;  // bytes of a CTA
-  static constexpr int kStages = kBN == 256 ? 5 : 7;
+  // An even number: a barrier of a stage is then always waited for by the same of the two
+  // warps that issue MMAs, phase by phase. (With an odd one, a warp whose blocks' copies
+  // came early could be a whole ring ahead of the other and take the phase before the
+  // last for the one that it waits for, which has the same parity.)
+  static constexpr int kStages = kBN == 256 ? 4 : 6;
+  static_assert(kStages % 2 == 0 && kSlots % 2 == 0);
   static constexpr int kCols = kBN / 2;           // of a warpgroup
   struct Bars {
     uint64_t full[kStages], done[kStages], taken[kSlots];
@@ -218,29 +223,35 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
     regs_dealloc<kRegsFew>();
     if (warp == 0) {
       // ---------------------------------------------------------------- tiles --
-      long long g = 0;
+      // (A block's turn is to be shorter than its 256 or 512 cycles of MMAs: with 64-bit
+      // counts and their remainders it took 500.)
+      int stage = 0, phase = 1, blocks_in = 0;
       for (int t = cluster; t < tiles && ok; t += clusters) {
         const Tile w = tile_at(t, n_tiles, m_tiles);
         const int n0 = __shfl_sync(0xffffffffu, w.n * kTileN + 128 * rank, 0);
         const int m0 = __shfl_sync(0xffffffffu, w.m * kBN + kBN / 2 * rank, 0);
-        for (int b = 0; b < blocks; ++b, ++g) {
-          const int slot = (int)(g % kStages);
-          if (!(ok = mbar_wait_warp(&bars->done[slot], (uint32_t)(g / kStages & 1) ^ 1, abort_flag,
-                                    status, kSiteDone)))
+#pragma unroll 1
+        for (int k = 0; k < 128 * blocks; k += 128) {
+          uint8_t* at = ring + stage * S::kStage;
+          uint64_t* full = &bars->full[stage];
+          if (blocks_in >= kStages &&
+              !(ok = mbar_wait_warp(&bars->done[stage], phase, abort_flag, status, kSiteDone)))
             break;
           if (elect_one()) {
-            uint8_t* at = ring + slot * S::kStage;
-            if (rank == 0) mbar_arrive_expect_tx(&bars->full[slot], 2 * S::kStage);
-            tma_load_2d_pair(at, &maps.x, &bars->full[slot], b * 128, n0);
-            tma_load_2d_pair(at + kXTile, &maps.w, &bars->full[slot], b * 128, m0);
+            if (rank == 0) mbar_arrive_expect_tx(full, 2 * S::kStage);
+            tma_load_2d_pair(at, &maps.x, full, k, n0);
+            tma_load_2d_pair(at + kXTile, &maps.w, full, k, m0);
           }
           __syncwarp();
+          blocks_in = min(blocks_in + 1, kStages);
+          if (++stage == kStages) stage = 0, phase ^= 1;
         }
       }
       // the last stages' MMAs are through, and this CTA has been told, before it leaves
-      for (long long k = g > kStages ? g - kStages : 0; k < g && ok; ++k)
-        ok = mbar_wait_warp(&bars->done[k % kStages], (uint32_t)(k / kStages & 1), abort_flag, status,
-                            kSiteDone);
+      for (int i = 0; i < blocks_in && ok; ++i) {
+        if (--stage < 0) stage = kStages - 1, phase ^= 1;
+        ok = mbar_wait_warp(&bars->done[stage], phase ^ 1, abort_flag, status, kSiteDone);
+      }
       if (!ok && lane == 0) {
         // Copies in flight land before the CTA exits. They count on a barrier of the
         // pair, so they are given 1 ms.
@@ -397,7 +408,7 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
 #pragma unroll
       for (int p = 0; p < kCols / kPer; ++p) {
         uint8_t* to = buf + (p & 1) * kOutBytes;
-        if (p >= 2) {
+        if (p >= 2) {  // what was in the buffer has been read
           if (store == 16 && lane == 0) tma_stores_read<1>();
           __syncwarp();
         }
