@@ -13,19 +13,21 @@
 // Warp roles (12 warps, persistent CTAs, one an SM):
 //   0      loads tiles by TMA (128-byte swizzle)
 //   1, 3   of CTA 0 issue the pair's MMAs, every other block each
-//   2      allocates TMEM, multiplies the scales
+//   2      allocates TMEM, loads the tokens' scales
 //   4-11   sum: each warpgroup half of the tile's columns
 // TMEM: slots of kBN columns, 512 in all. A block's MMAs wait for its stage of the
 // ring to be full and for its slot to be taken by those who sum; `done` says that they
-// are through and that the products of its scales are written.
+// are through, and so that the tokens' scales, counted with the stage's tiles, are there.
 // What bounds it is how fast sums are taken: a warp's block is a chain of a look at a
 // barrier, loads from TMEM and a hand-back, about 450 cycles besides its multiply-
 // adds, and from there to the next sums in the slot are 300 cycles of signals and 700
-// of MMAs. So all else (the scales' way from memory, their products) is the work of
-// another warp. (Measured on 8192 x 22016 x 4096, us: scales loaded by those who sum
-// 716, fetched for them but multiplied there 682, this 514. Sixteen warps that sum:
-// 605. Slots of 128 columns for each warpgroup: 506, but 402 against 385 for
-// 8192 x 8192 x 8192.)
+// of MMAs. So the scales bring no wait of their own: the tokens' come by the stage's
+// barrier, the weights' in registers, 32 blocks at a time. (Measured on
+// 8192 x 22016 x 4096, us: scales loaded by those who sum 716, waited for on a barrier of
+// their own 682, multiplied by a warp of their own and this, both 531 to 567. That warp
+// took 480 cycles a block, too long for 128 weight rows: 256 x 4096 x 4096 13.9 us, this
+// 11.6. Sixteen warps that sum: 605 against 514. Slots of 128 columns for each warpgroup:
+// 506, but 402 against 385 for 8192 x 8192 x 8192.)
 // Every wait is bounded (see q6_internal.cuh), and the pair meets once more
 // before either CTA leaves.
 #include "f8_internal.cuh"
@@ -39,14 +41,13 @@ constexpr int kTileN = 256;            // tokens of a pair
 constexpr int kXTile = 128 * 128;      // bytes of a CTA's tokens of a stage
 
 constexpr int kGroup = 8;              // token tiles walked together
-constexpr int kChunk = 8;              // blocks of K whose token scales come together
-constexpr int kChunkBytes = kChunk * 128 * 4;
+constexpr int kScaleBytes = 128 * 4;   // a block's scales of a CTA's tokens
 constexpr int kPart = 64;              // bytes of a row that are stored at a time
 constexpr int kOutBytes = 32 * kPart;  // of a warp
 // Registers of a thread: 128 + 256 threads share the 384 * 168 of the launch.
 constexpr int kRegsFew = 40, kRegsMany = 232;
 
-enum : uint32_t { kSiteDone = 48, kSiteFull, kSiteSlot, kSiteScale, kSiteDrain };
+enum : uint32_t { kSiteDone = 48, kSiteFull, kSiteSlot, kSiteDrain };
 
 template <int kBN>
 struct Cfg {
@@ -61,18 +62,16 @@ struct Cfg {
   static constexpr int kCols = kBN / 2;           // of a warpgroup
   struct Bars {
     uint64_t full[kStages], done[kStages], taken[kSlots];
-    uint64_t s_full[2];
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
   };
-  // Products of scales kept, [block][half][token]: a stage's MMAs are through only
-  // after all who sum have read the slot kSlots blocks before, so those of kStages +
-  // kSlots blocks back are not needed any more when the stage's next ones are written.
-  static constexpr int kProducts = kBN == 256 ? 8 : 16;
-  static_assert(kProducts >= kStages + kSlots);
-  static constexpr int kSmem = 1024 + kStages * kStage + 8 * 2 * kOutBytes + 2 * kChunkBytes +
-                               kProducts * 1024 + (int)sizeof(Bars);
+  // Blocks whose tokens' scales are kept: a stage's MMAs are through only after all who
+  // sum have read the slot kSlots blocks before, and so have added what came before that.
+  static constexpr int kScales = kBN == 256 ? 8 : 16;
+  static_assert(kScales > kStages + kSlots + 1);
+  static constexpr int kSmem =
+      1024 + kStages * kStage + 8 * 2 * kOutBytes + kScales * kScaleBytes + (int)sizeof(Bars);
 };
 constexpr int kReaders = 16;  // warps of the pair that read a slot
 
@@ -188,18 +187,16 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* out_stage = ring + kStages * S::kStage;
   float* scales = reinterpret_cast<float*>(out_stage + 8 * 2 * kOutBytes);
-  float* products = scales + 2 * kChunk * 128;
-  typename S::Bars* bars = reinterpret_cast<typename S::Bars*>(products + S::kProducts * 256);
+  typename S::Bars* bars = reinterpret_cast<typename S::Bars*>(scales + S::kScales * 128);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
   volatile int* abort_flag = &bars->abort;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars->full[i], 1);  // used in CTA 0
-      mbar_init(&bars->done[i], 2);
+      mbar_init(&bars->done[i], 1);
     }
     for (int i = 0; i < kSlots; ++i) mbar_init(&bars->taken[i], kReaders);  // used in CTA 0
-    for (int i = 0; i < 2; ++i) mbar_init(&bars->s_full[i], 1);
     mbar_init(&bars->drain, 2);
     bars->abort = 0;
     mbar_fence_init();
@@ -208,12 +205,12 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
     tma_prefetch_desc(&maps.sx);
   }
   if (warp == 2) tmem_alloc_pair(&bars->tmem_base, 512);
-  griddep_wait();
-  griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the pair's barriers are initialised
   tc_fence_after();
+  griddep_wait();
+  griddep_launch_dependents();
   const uint32_t tmem = bars->tmem_base;
   const int blocks = (c.K + kF8Block - 1) / kF8Block;
   const int m_tiles = (c.M + kBN - 1) / kBN, n_tiles = (c.N + kTileN - 1) / kTileN;
@@ -238,7 +235,7 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
               !(ok = mbar_wait_warp(&bars->done[stage], phase, abort_flag, status, kSiteDone)))
             break;
           if (elect_one()) {
-            if (rank == 0) mbar_arrive_expect_tx(full, 2 * S::kStage);
+            if (rank == 0) mbar_arrive_expect_tx(full, 2 * (S::kStage + kScaleBytes));
             tma_load_2d_pair(at, &maps.x, full, k, n0);
             tma_load_2d_pair(at + kXTile, &maps.w, full, k, m0);
           }
@@ -260,57 +257,22 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
       }
     } else if (warp == 2) {
       // --------------------------------------------------------------- scales --
-      // Chunks of kChunk blocks of the tokens' scales come by TMA, one ahead; of the
-      // weights' lane 8 h + i has block i's of half h, one chunk ahead too.
-      int asked = 0, tile_a = cluster, b_a = 0;
-      float sw_next = 0.0f;
-      auto ask = [&] {
-        if (tile_a >= tiles) return;
-        const Tile w = tile_at(tile_a, n_tiles, m_tiles);
-        const int n0 = __shfl_sync(0xffffffffu, w.n * kTileN + 128 * rank, 0);
-        const int half = lane / kChunk % 2;
-        // past the last band of weights the last one again, whose result is not stored
-        const int band = min((w.m * kBN + S::kCols * half) / 128, (c.M - 1) / 128);
-        const int b = b_a + lane % kChunk;
-        sw_next = b < blocks ? c.sw[(size_t)band * blocks + b] : 0.0f;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(&bars->s_full[asked & 1], kChunkBytes);
-          tma_load_2d(scales + (asked & 1) * kChunk * 128, &maps.sx, &bars->s_full[asked & 1], n0, b_a);
-        }
-        __syncwarp();
-        ++asked;
-        if ((b_a += kChunk) >= blocks) b_a = 0, tile_a += clusters;
-      };
-      ask();
-      int stage = 0, phase = 1, chunk = 0, put = 0;
+      // (counted on the stage's barrier with its tiles)
+      int stage = 0, phase = 1, at = 0, blocks_in = 0;
       for (int t = cluster; t < tiles && ok; t += clusters) {
-        for (int b = 0; b < blocks && ok; b += kChunk, ++chunk) {
-          const float sw = sw_next;
-          ask();
-          if (!(ok = mbar_wait_warp(&bars->s_full[chunk & 1], chunk >> 1 & 1, abort_flag, status, kSiteScale)))
+        const int n0 =
+            __shfl_sync(0xffffffffu, tile_at(t, n_tiles, m_tiles).n * kTileN + 128 * rank, 0);
+#pragma unroll 1
+        for (int b = 0; b < blocks; ++b) {
+          if (blocks_in >= kStages &&
+              !(ok = mbar_wait_warp(&bars->done[stage], phase, abort_flag, status, kSiteDone)))
             break;
-          const float* from = scales + (chunk & 1) * kChunk * 128 + lane;
-          for (int i = 0; i < kChunk && b + i < blocks; ++i) {
-            const float w0 = __shfl_sync(0xffffffffu, sw, i), w1 = __shfl_sync(0xffffffffu, sw, kChunk + i);
-            if (!(ok = mbar_wait_warp(&bars->done[stage], phase, abort_flag, status, kSiteDone))) break;
-            float* to = products + put * 256 + lane;
-#pragma unroll
-            for (int j = 0; j < 128; j += 32) {
-              const float x = from[i * 128 + j];
-              to[j] = x * w0;
-              to[128 + j] = x * w1;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->done[stage]);
-            if (++stage == kStages) stage = 0, phase ^= 1;
-            put = (put + 1) % S::kProducts;
-          }
+          if (elect_one()) tma_load_2d_pair(scales + at * 128, &maps.sx, &bars->full[stage], n0, b);
+          __syncwarp();
+          blocks_in = min(blocks_in + 1, kStages);
+          at = (at + 1) % S::kScales;
+          if (++stage == kStages) stage = 0, phase ^= 1;
         }
-      }
-      if (!ok && lane == 0) {  // copies in flight land before the CTA exits
-        volatile int no_abort = 0;
-        for (int i = asked > 2 ? asked - 2 : 0; i < asked; ++i)
-          mbar_wait_bounded(&bars->s_full[i & 1], i >> 1 & 1, &no_abort, status, kSiteScale);
       }
     } else if (rank == 0) {
       // ----------------------------------------------------------------- MMAs --
@@ -350,25 +312,39 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
     const int q = warp % 4, me = (warp - 4) / 4;
     // this warp's lanes and first column of a slot
     const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + kCols * me;
-    const float* mine = products + 128 * me + 32 * q + lane;
+    const float* mine = scales + 32 * q + lane;
     const uint32_t leader = leader_address(&bars->taken[0]);
-    int stage = 0, phase = 0, get = 0, turn = 0;
+    int stage = 0, phase = 0, get = 0;
     bool seen = false;  // this lane has seen the next block done
+    // The weights' scales: lane i has block i's of 32, the next 32 are on their way. (Past
+    // the last band of weights the last one again, whose result is not stored.)
+    auto weight_scale = [&](int t, int b) {
+      if (t >= tiles) return 0.0f;
+      const int band = min((tile_at(t, n_tiles, m_tiles).m * kBN + kCols * me) / 128, (c.M - 1) / 128);
+      return b + lane < blocks ? c.sw[(size_t)band * blocks + b + lane] : 0.0f;
+    };
+    float sw = 0.0f, sw_next = weight_scale(cluster, 0);
     for (int t = cluster; t < tiles; t += clusters) {
       float2 acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
 #pragma unroll 1
       for (int i = 0; i < blocks; ++i) {
+        if (i % 32 == 0) {
+          sw = sw_next;
+          sw_next = i + 32 < blocks ? weight_scale(t, i + 32) : weight_scale(t + clusters, 0);
+        }
+        const float of_weights = __shfl_sync(0xffffffffu, sw, i % 32);
         ok = __all_sync(0xffffffffu, seen) ||
              mbar_wait_warp(&bars->done[stage], phase, abort_flag, status, kSiteDone);
         if (!ok) break;
         tc_fence_after();
+        const int turn = get % kSlots;
         const uint32_t at = src + kBN * turn;
-        const float f = mine[get * 256];
+        const float f = mine[get * 128] * of_weights;
         uint64_t s;  // the product of the scales, in both halves
-        asm volatile("mov.b64 %0, {%1, %1};" : "=l"(s) : "f"(f));
-        get = (get + 1) % S::kProducts;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "f"(f));
+        get = (get + 1) % S::kScales;
         if (++stage == kStages) stage = 0, phase ^= 1;
         auto add = [&](float2* to, const uint32_t(&v)[32]) {
 #pragma unroll
@@ -391,7 +367,6 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_at_leader(leader + 8 * turn);
-        turn = (turn + 1) % kSlots;
         // (a look at a barrier takes 200 cycles, so it comes before the last adds)
         seen = mbar_test_wait(&bars->done[stage], phase);
         add(acc + kCols / 2 - 32, va);
@@ -505,7 +480,7 @@ int launch_f8_tc(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStre
   int rc;
   if ((rc = encode_f8_map(&maps.x, c.xq, c.N, c.K, 128, "xq")) ||
       (rc = encode_f8_map(&maps.w, c.wq, c.M, c.K, thin ? 64 : 128, "wq")) ||
-      (rc = encode_f8_scales(&maps.sx, c.sx, c.ldsx, f8_blocks(c.K), 128, kChunk)) ||
+      (rc = encode_f8_scales(&maps.sx, c.sx, c.ldsx, f8_blocks(c.K), 128, 1)) ||
       (store == 16 && (rc = encode_f8_results(&maps.y, c, kPart / size, 32))))
     return rc;
   *e = c.type == Q6_TYPE_F32    ? launch_t<float>(maps, c, thin, store, status, s)
