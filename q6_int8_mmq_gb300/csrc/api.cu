@@ -27,7 +27,7 @@ int cuda_fail(cudaError_t e, const char* what) {
   return fail(Q6_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-constexpr int kMaxDevices = 64;
+using q6::kMaxDevices;
 
 struct DevState {
   bool init = false;

@@ -28,8 +28,9 @@
 // took 480 cycles a block, too long for 128 weight rows: 256 x 4096 x 4096 13.9 us, this
 // 11.6. Sixteen warps that sum: 605 against 514. Slots of 128 columns for each warpgroup:
 // 506, but 402 against 385 for 8192 x 8192 x 8192.)
-// Every wait is bounded (see q6_internal.cuh), and the pair meets once more
-// before either CTA leaves.
+// Where the tiles are few, clusters of two or four pairs split K (form_of()).
+// Every wait is bounded (see q6_internal.cuh), and the cluster meets once
+// more before any CTA leaves.
 #include "f8_internal.cuh"
 #include "f8_tc.cuh"
 
@@ -103,9 +104,9 @@ __device__ __forceinline__ void fma2(float2& acc, uint32_t a, uint32_t b, uint64
 
 // The address of CTA 0's `bar` from any CTA of the pair, and an arrival there as
 // arrive_leader_tmem()'s.
-__device__ __forceinline__ uint32_t leader_address(uint64_t* bar) {
+__device__ __forceinline__ uint32_t leader_address(uint64_t* bar, uint32_t lead) {
   uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(bar)), "r"(lead));
   return a;
 }
 __device__ __forceinline__ void arrive_at_leader(uint32_t bar) {
@@ -177,7 +178,7 @@ __device__ __forceinline__ void store_rows(T* y, long long ldy, const uint8_t* f
   }
 }
 
-template <typename T, int kBN>
+template <typename T, int kBN, int kParts>
 __global__ void __launch_bounds__(kThreads, 1)
 f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsigned int* status) {
   using S = Cfg<kBN>;
@@ -189,7 +190,17 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
   float* scales = reinterpret_cast<float*>(out_stage + 8 * 2 * kOutBytes);
   typename S::Bars* bars = reinterpret_cast<typename S::Bars*>(scales + S::kScales * 128);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)cluster_rank(), cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
+  const int cluster = blockIdx.x / (2 * kParts), clusters = gridDim.x / (2 * kParts);
+  // of the cluster's pairs, and of the pair's CTAs
+  const int pair = kParts > 1 ? (int)cluster_rank() / 2 : 0, rank = (int)cluster_rank() % 2;
+  const uint32_t lead = 2 * pair;
+  // this pair's blocks of K
+  const int all_blocks = (c.K + kF8Block - 1) / kF8Block;
+  const int first = all_blocks * pair / kParts, blocks = all_blocks * (pair + 1) / kParts - first;
+  const int m_tiles = (c.M + kBN - 1) / kBN, n_tiles = (c.N + kTileN - 1) / kTileN;
+  const int tiles = m_tiles * n_tiles;
+  const Tile tile_0 = tile_at(cluster, n_tiles, m_tiles);
+  auto tile_of = [&](int t) { return t == cluster ? tile_0 : tile_at(t, n_tiles, m_tiles); };
   volatile int* abort_flag = &bars->abort;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -212,9 +223,6 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t tmem = bars->tmem_base;
-  const int blocks = (c.K + kF8Block - 1) / kF8Block;
-  const int m_tiles = (c.M + kBN - 1) / kBN, n_tiles = (c.N + kTileN - 1) / kTileN;
-  const int tiles = m_tiles * n_tiles;
   bool ok = true;
   if (warp < 4) {
     regs_dealloc<kRegsFew>();
@@ -224,11 +232,11 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
       // counts and their remainders it took 500.)
       int stage = 0, phase = 1, blocks_in = 0;
       for (int t = cluster; t < tiles && ok; t += clusters) {
-        const Tile w = tile_at(t, n_tiles, m_tiles);
+        const Tile w = tile_of(t);
         const int n0 = __shfl_sync(0xffffffffu, w.n * kTileN + 128 * rank, 0);
         const int m0 = __shfl_sync(0xffffffffu, w.m * kBN + kBN / 2 * rank, 0);
 #pragma unroll 1
-        for (int k = 0; k < 128 * blocks; k += 128) {
+        for (int k = 128 * first; k < 128 * (first + blocks); k += 128) {
           uint8_t* at = ring + stage * S::kStage;
           uint64_t* full = &bars->full[stage];
           if (blocks_in >= kStages &&
@@ -236,8 +244,8 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
             break;
           if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(full, 2 * (S::kStage + kScaleBytes));
-            tma_load_2d_pair(at, &maps.x, full, k, n0);
-            tma_load_2d_pair(at + kXTile, &maps.w, full, k, m0);
+            tma_load_2d_pair(at, &maps.x, full, k, n0, lead);
+            tma_load_2d_pair(at + kXTile, &maps.w, full, k, m0, lead);
           }
           __syncwarp();
           blocks_in = min(blocks_in + 1, kStages);
@@ -261,13 +269,14 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
       int stage = 0, phase = 1, at = 0, blocks_in = 0;
       for (int t = cluster; t < tiles && ok; t += clusters) {
         const int n0 =
-            __shfl_sync(0xffffffffu, tile_at(t, n_tiles, m_tiles).n * kTileN + 128 * rank, 0);
+            __shfl_sync(0xffffffffu, tile_of(t).n * kTileN + 128 * rank, 0);
 #pragma unroll 1
         for (int b = 0; b < blocks; ++b) {
           if (blocks_in >= kStages &&
               !(ok = mbar_wait_warp(&bars->done[stage], phase, abort_flag, status, kSiteDone)))
             break;
-          if (elect_one()) tma_load_2d_pair(scales + at * 128, &maps.sx, &bars->full[stage], n0, b);
+          if (elect_one())
+            tma_load_2d_pair(scales + at * 128, &maps.sx, &bars->full[stage], n0, first + b, lead);
           __syncwarp();
           blocks_in = min(blocks_in + 1, kStages);
           at = (at + 1) % S::kScales;
@@ -292,7 +301,7 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             umma_f8_pair(d, x + 2 * k, w + 2 * k, idesc_f8(256, kBN), k > 0);
-          commit_pair(&bars->done[stage]);
+          commit_pair(&bars->done[stage], lead);
         }
         __syncwarp();
         if ((stage += 2) >= kStages) stage -= kStages, full_phase ^= 1;
@@ -308,20 +317,20 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
   } else {
     // ------------------------------------------------------------------- sums --
     regs_alloc<kRegsMany>();
-    constexpr int kCols = S::kCols;
+    constexpr int kCols = S::kCols, kMine = kParts > 1 ? kCols / 2 : kCols;  // columns summed, stored
     const int q = warp % 4, me = (warp - 4) / 4;
     // this warp's lanes and first column of a slot
     const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + kCols * me;
     const float* mine = scales + 32 * q + lane;
-    const uint32_t leader = leader_address(&bars->taken[0]);
+    const uint32_t leader = leader_address(&bars->taken[0], lead);
     int stage = 0, phase = 0, get = 0;
     bool seen = false;  // this lane has seen the next block done
     // The weights' scales: lane i has block i's of 32, the next 32 are on their way. (Past
     // the last band of weights the last one again, whose result is not stored.)
     auto weight_scale = [&](int t, int b) {
       if (t >= tiles) return 0.0f;
-      const int band = min((tile_at(t, n_tiles, m_tiles).m * kBN + kCols * me) / 128, (c.M - 1) / 128);
-      return b + lane < blocks ? c.sw[(size_t)band * blocks + b + lane] : 0.0f;
+      const int band = min((tile_of(t).m * kBN + kCols * me) / 128, (c.M - 1) / 128);
+      return b + lane < blocks ? c.sw[(size_t)band * all_blocks + first + b + lane] : 0.0f;
     };
     float sw = 0.0f, sw_next = weight_scale(cluster, 0);
     for (int t = cluster; t < tiles; t += clusters) {
@@ -372,16 +381,58 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
         add(acc + kCols / 2 - 32, va);
         add(acc + kCols / 2 - 16, vb);
       }
+      const Tile w = tile_of(t);
+      const int n0 = w.n * kTileN + 128 * rank + 32 * q;
+      int m0 = w.m * kBN + kCols * me;
+      if constexpr (kParts > 1) {
+        // Two pairs add up a half each of a warp's columns (of four pairs the first two those
+        // of warpgroup 0, the others those of 1). The others' sums of it come into their
+        // rings, which nothing uses any more: [pair that sent][warp][four columns][lane].
+        const int owner = kParts == 4 ? 2 * me : 0;
+        float4* in = reinterpret_cast<float4*>(ring) + (warp - 4) * (kMine / 4) * 32 + lane;
+        constexpr int kFrom = 8 * (kMine / 4) * 32;
+        static_assert((kParts - 1) * kFrom * 16 <= kStages * S::kStage);
+        cluster_sync();
+        if (n0 < c.N) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int p = owner + h;
+            if (p == pair) continue;
+#pragma unroll
+            for (int j = 0; j < kMine / 4; ++j) {
+              const float2* a = acc + h * kMine / 2 + 2 * j;
+              store_at(in + (pair - (pair > p)) * kFrom + 32 * j, 2 * p + rank,
+                       make_float4(a[0].x, a[0].y, a[1].x, a[1].y));
+            }
+          }
+          if (pair == owner + 1) {
+#pragma unroll
+            for (int j = 0; j < kMine / 2; ++j) acc[j] = acc[kMine / 2 + j];
+          }
+        }
+        cluster_sync();
+        if (pair < owner || pair > owner + 1) continue;
+        if (n0 < c.N) {
+#pragma unroll
+          for (int i = 0; i < kParts - 1; ++i) {
+#pragma unroll
+            for (int j = 0; j < kMine / 4; ++j) {
+              const float4 v = in[i * kFrom + 32 * j];
+              acc[2 * j].x += v.x, acc[2 * j].y += v.y;
+              acc[2 * j + 1].x += v.z, acc[2 * j + 1].y += v.w;
+            }
+          }
+        }
+        m0 += kMine * (pair - owner);
+      }
       if (!ok) break;
-      const Tile w = tile_at(t, n_tiles, m_tiles);
-      const int n0 = w.n * kTileN + 128 * rank + 32 * q, m0 = w.m * kBN + kCols * me;
       constexpr int kPer = kPart / (int)sizeof(T);  // results of a row stored at a time
       if (n0 >= c.N || m0 >= c.M) continue;
       // 64 bytes of 32 rows at a time, the 16-byte units of a row as the 64-byte swizzle has
       // them, so that a lane's row goes to banks of its own
       uint8_t* buf = out_stage + (warp - 4) * 2 * kOutBytes;
 #pragma unroll
-      for (int p = 0; p < kCols / kPer; ++p) {
+      for (int p = 0; p < kMine / kPer; ++p) {
         uint8_t* to = buf + (p & 1) * kOutBytes;
         if (p >= 2) {  // what was in the buffer has been read
           if (store == 16 && lane == 0) tma_stores_read<1>();
@@ -410,6 +461,7 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
       __syncwarp();
     }
   }
+  if (kParts > 1 && warp < 4) cluster_sync(), cluster_sync();  // those of the sums' way
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -419,37 +471,60 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
   }
 }
 
-template <typename T, int kBN>
-cudaError_t launch_n(const Maps& maps, const F8Call& c, int store, unsigned int* status,
-                     cudaStream_t s) {
-  const long long tiles = (((long long)c.M + kBN - 1) / kBN) * (((long long)c.N + kTileN - 1) / kTileN);
-  const unsigned pairs = (unsigned)(tiles < 76 ? tiles : 76);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * pairs);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<kBN>::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
+long long tiles_of(long long n, int size) { return (n + size - 1) / size; }
+template <int kBN, int kParts>
+void launch_of(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], unsigned clusters, cudaStream_t s) {
+  *cfg = {};
+  cfg->gridDim = dim3(2 * kParts * clusters);
+  cfg->blockDim = dim3(kThreads);
+  cfg->dynamicSmemBytes = Cfg<kBN>::kSmem;
+  cfg->stream = s;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = 2 * kParts;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, f8_mmq_kernel<T, kBN>, maps, c, store, status);
+  cfg->attrs = attr;
+  cfg->numAttrs = 2;
 }
-// Whether 128 weight rows a tile are faster: they take 5/8 of the time of 256.
-bool narrow(const F8Call& c) {
-  const long long n = ((long long)c.N + kTileN - 1) / kTileN;
-  const long long wide = n * (((long long)c.M + 255) / 256), thin = n * (((long long)c.M + 127) / 128);
-  return 5 * ((thin + 75) / 76) < 8 * ((wide + 75) / 76);
+template <typename T, int kBN, int kParts>
+cudaError_t launch_n(const Maps& maps, const F8Call& c, int store, unsigned int* status,
+                     cudaStream_t s) {
+  const long long tiles = tiles_of(c.M, kBN) * tiles_of(c.N, kTileN);
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  launch_of<kBN, kParts>(&cfg, attr, (unsigned)(kParts > 1 || tiles < 76 ? tiles : 76), s);
+  return cudaLaunchKernelEx(&cfg, f8_mmq_kernel<T, kBN, kParts>, maps, c, store, status);
+}
+// Clusters of two and of four pairs that a device holds at a time (each SM one CTA, the
+// SMs of a cluster near one another): 36 and 15 of 152 SMs.
+struct Room {
+  int of_two = 0, of_four = 0;
+};
+Room g_room[kMaxDevices];  // written once, under the lock that every call takes
+
+struct Form {
+  bool thin;  // 128 weight rows a tile, not 256
+  int parts;  // of K, a pair each
+};
+// 128 weight rows a tile take 5/8 of the time of 256. Where they leave most pairs without
+// a tile, K is split: a block of K takes a pair 0.2 to 0.26 us, the sums' way to the pairs
+// that add them up 1 us (two pairs) or 1.8 (four). (us, 256 tokens. 1024 weight rows, four
+// pairs against one: K = 2048 6.6, 6.4; 2560 6.9, 7.3; 8192 10.3, 17.9. 4096 rows, two
+// against one: K = 2560 9.0, 8.5; 3584 10.1, 10.3; 8192 15.3, 18.8.)
+Form form_of(const F8Call& c, const Room& room) {
+  const long long n = tiles_of(c.N, kTileN), wide = n * tiles_of(c.M, 256), thin = n * tiles_of(c.M, 128);
+  const int blocks = f8_blocks(c.K);
+  if (5 * ((thin + 75) / 76) >= 8 * ((wide + 75) / 76)) return {false, 1};
+  return {true, blocks >= 18 && thin <= room.of_four ? 4 : blocks >= 28 && thin <= room.of_two ? 2 : 1};
 }
 template <typename T>
-cudaError_t launch_t(const Maps& maps, const F8Call& c, bool thin, int store, unsigned int* status,
+cudaError_t launch_t(const Maps& maps, const F8Call& c, Form f, int store, unsigned int* status,
                      cudaStream_t s) {
-  return thin ? launch_n<T, 128>(maps, c, store, status, s)
-              : launch_n<T, 256>(maps, c, store, status, s);
+  return !f.thin        ? launch_n<T, 256, 1>(maps, c, store, status, s)
+         : f.parts == 1 ? launch_n<T, 128, 1>(maps, c, store, status, s)
+         : f.parts == 2 ? launch_n<T, 128, 2>(maps, c, store, status, s)
+                        : launch_n<T, 128, 4>(maps, c, store, status, s);
 }
 
 }  // namespace
@@ -461,17 +536,31 @@ cudaError_t f8_tc_prepare() {
   };
   auto all = [&](auto t) {
     using T = decltype(t);
-    raise(f8_mmq_kernel<T, 128>, Cfg<128>::kSmem);
-    raise(f8_mmq_kernel<T, 256>, Cfg<256>::kSmem);
+    raise(f8_mmq_kernel<T, 128, 1>, Cfg<128>::kSmem);
+    raise(f8_mmq_kernel<T, 128, 2>, Cfg<128>::kSmem);
+    raise(f8_mmq_kernel<T, 128, 4>, Cfg<128>::kSmem);
+    raise(f8_mmq_kernel<T, 256, 1>, Cfg<256>::kSmem);
   };
   all(float());
   all(__nv_bfloat16());
   all(__half());
+  int device = 0;
+  if (!e) e = cudaGetDevice(&device);
+  if (e) return e;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  launch_of<128, 2>(&cfg, attr, 1, nullptr);
+  e = cudaOccupancyMaxActiveClusters(&g_room[device].of_two, f8_mmq_kernel<float, 128, 2>, &cfg);
+  launch_of<128, 4>(&cfg, attr, 1, nullptr);
+  if (!e)
+    e = cudaOccupancyMaxActiveClusters(&g_room[device].of_four, f8_mmq_kernel<float, 128, 4>, &cfg);
   return e;
 }
 
 int launch_f8_tc(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStream_t s) {
-  const bool thin = narrow(c);
+  int device = 0;
+  if ((*e = cudaGetDevice(&device))) return Q6_OK;  // (the caller reports *e)
+  const Form form = form_of(c, g_room[device]);
   // results by TMA where their rows start on 16 bytes, else in words of 4 or 2 bytes
   const int size = c.type == Q6_TYPE_F32 ? 4 : 2;
   const uintptr_t where = reinterpret_cast<uintptr_t>(c.Y) | (uintptr_t)(c.ldy * size);
@@ -479,13 +568,13 @@ int launch_f8_tc(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStre
   Maps maps;
   int rc;
   if ((rc = encode_f8_map(&maps.x, c.xq, c.N, c.K, 128, "xq")) ||
-      (rc = encode_f8_map(&maps.w, c.wq, c.M, c.K, thin ? 64 : 128, "wq")) ||
+      (rc = encode_f8_map(&maps.w, c.wq, c.M, c.K, form.thin ? 64 : 128, "wq")) ||
       (rc = encode_f8_scales(&maps.sx, c.sx, c.ldsx, f8_blocks(c.K), 128, 1)) ||
       (store == 16 && (rc = encode_f8_results(&maps.y, c, kPart / size, 32))))
     return rc;
-  *e = c.type == Q6_TYPE_F32    ? launch_t<float>(maps, c, thin, store, status, s)
-       : c.type == Q6_TYPE_BF16 ? launch_t<__nv_bfloat16>(maps, c, thin, store, status, s)
-                                : launch_t<__half>(maps, c, thin, store, status, s);
+  *e = c.type == Q6_TYPE_F32    ? launch_t<float>(maps, c, form, store, status, s)
+       : c.type == Q6_TYPE_BF16 ? launch_t<__nv_bfloat16>(maps, c, form, store, status, s)
+                                : launch_t<__half>(maps, c, form, store, status, s);
   return Q6_OK;
 }
 

@@ -75,4 +75,14 @@ __device__ __forceinline__ void tmem_ld_after(uint32_t addr, uint32_t (&r)[32], 
       : "memory");
 }
 
+// Stores to the same place in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ void store_at(float4* p, int rank, const float4& v) {
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\t"
+      "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
+      "st.shared::cluster.v4.f32 [ra], {%2, %3, %4, %5};\n\t}\n" ::"r"(smem_u32(p)),
+      "r"(rank), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+      : "memory");
+}
+
 }  // namespace q6

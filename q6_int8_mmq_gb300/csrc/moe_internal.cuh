@@ -13,6 +13,7 @@ namespace q6 {
 // (1.7 ms for the two sets together, 2.1 ms for the kernels of the shared projections),
 // so each set is prepared by the first call that runs it.
 enum KernelSet { kPlainKernels, kExpertKernels, kAdapterKernels, kBlockKernels, kKernelSets };
+constexpr int kMaxDevices = 64;
 // The calling thread's current device, checked and prepared, and `set` on it
 // (api.cu); *status (nullable) receives its status word.
 int require_device(unsigned int** status, KernelSet set = kPlainKernels);

@@ -16,12 +16,12 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 // Arrives once on `bar` of both CTAs when every MMA issued so far by this
-// thread has completed.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+// thread has completed. (`lead`, here and below: the cluster's rank of the pair's CTA 0.)
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t lead = 0) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
       "[%0], %1;" ::"r"(smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"((uint16_t)(3u << lead))
       : "memory");
 }
 // The same on this CTA's `bar` alone.
@@ -45,13 +45,13 @@ __device__ __forceinline__ void arrive_leader_tmem(uint64_t* bar) {
 }
 // A TMA load into this CTA that counts on `bar` of CTA 0 of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                                 int c0, int c1) {
+                                                 int c0, int c1, uint32_t lead = 0) {
   asm volatile(
       "{\n\t.reg .b32 ra;\n\t"
-      "mapa.shared::cluster.u32 ra, %2, 0;\n\t"
+      "mapa.shared::cluster.u32 ra, %2, %5;\n\t"
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4}], [ra];\n\t}\n" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(lead)
       : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {

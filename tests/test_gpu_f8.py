@@ -326,6 +326,36 @@ def test_product_at_size(N, M, K):
     check_product(w, act, BF16)
 
 
+# Few tiles and a long K: pairs of CTAs that share a tile, each with a part of K.
+@pytest.mark.parametrize("K", [2176, 2304, 2448, 3568, 3600, 11008])
+@pytest.mark.parametrize("N,M", [(65, 1), (129, 129), (257, 1000), (300, 70), (200, 2056), (65, 4608), (130, 4700)])
+def test_product_of_few_tiles_and_a_long_k(N, M, K):
+    w, act = operands(gen(N + K), N, M, K)
+    check_product(w, act, TYPES[(N + K // 16) % 3])
+
+
+@pytest.mark.parametrize("N,M,K", [(70, 640, 2560), (300, 1000, 3600), (130, 2056, 3600)])
+def test_few_tiles_of_whole_numbers_are_exact(N, M, K):
+    test_product_of_whole_numbers_is_exact(N, M, K)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [200, 2056])
+def test_few_tiles_into_rows_of_a_larger_matrix(M, dtype):
+    """Every alignment of Y and its rows, nothing written beside it, the same bits each time."""
+    N = 140
+    w, act = operands(gen(M), N, M, 3600)
+    want, _ = check_product(w, act, dtype)
+    for ld, at in ((M, 0), (M + 1, 0), (M + 8, 8), (M + 16, 3), (M + 3, 1)):
+        big = torch.full(((N + 2) * ld + 8,), 7.0, dtype=dtype, device="cuda")
+        Y = torch.as_strided(big, (N, M), (ld, 1), ld + at)
+        for _ in range(4):
+            got, _ = q6.f8_mmq(w, act, out=Y)
+            assert torch.equal(got, want)
+            Y.fill_(7.0)
+        assert (big == 7).all()
+
+
 @pytest.mark.parametrize("N,M,K", [(1, 640, 1024), (6, 300, 2048), (24, 513, 1024), (130, 300, 768), (700, 1025, 528)])
 def test_product_of_whole_numbers_is_exact(N, M, K):
     """Codes -4 .. 4 and scales that are powers of two: every sum fits f32."""
