@@ -18,6 +18,8 @@
 // TMEM: slots of kBN columns, 512 in all. A block's MMAs wait for its stage of the
 // ring to be full and for its slot to be taken by those who sum; `done` says that they
 // are through, and so that the tokens' scales, counted with the stage's tiles, are there.
+// 256 columns are taken and written in two halves, 64 columns of each warpgroup, so that
+// MMAs go on while the second is read (3314 x 4096 x 11008: 109.6 -> 107.5 us).
 // What bounds it is how fast sums are taken: a warp's block is a chain of a look at a
 // barrier, loads from TMEM and a hand-back, about 450 cycles besides its multiply-
 // adds, and from there to the next sums in the slot are 300 cycles of signals and 700
@@ -61,8 +63,9 @@ struct Cfg {
   static constexpr int kStages = kBN == 256 ? 4 : 6;
   static_assert(kStages % 2 == 0 && kSlots % 2 == 0);
   static constexpr int kCols = kBN / 2;           // of a warpgroup
+  static constexpr int kHalves = kBN / 128;       // of a slot, taken one by one
   struct Bars {
-    uint64_t full[kStages], done[kStages], taken[kSlots];
+    uint64_t full[kStages], done[kStages], taken[kSlots * kHalves];
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
@@ -207,7 +210,7 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
       mbar_init(&bars->full[i], 1);  // used in CTA 0
       mbar_init(&bars->done[i], 1);
     }
-    for (int i = 0; i < kSlots; ++i) mbar_init(&bars->taken[i], kReaders);  // used in CTA 0
+    for (int i = 0; i < kSlots * S::kHalves; ++i) mbar_init(&bars->taken[i], kReaders);  // used in CTA 0
     mbar_init(&bars->drain, 2);
     bars->abort = 0;
     mbar_fence_init();
@@ -293,17 +296,23 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
       for (; g < all; g += 2) {
         const uint32_t x = base + stage * (S::kStage >> 4), w = x + (kXTile >> 4);
         const uint32_t d = tmem + kBN * slot;
-        if (!(ok = mbar_wait_warp(&bars->full[stage], full_phase, abort_flag, status, kSiteFull)) ||
-            !(ok = mbar_wait_warp(&bars->taken[slot], taken_phase, abort_flag, status, kSiteSlot)))
-          break;
-        tc_fence_after();
-        if (elect_one()) {
+        if (!(ok = mbar_wait_warp(&bars->full[stage], full_phase, abort_flag, status, kSiteFull))) break;
+        // half h: 64 rows of each CTA's weights, from the (64 h)th on
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_f8_pair(d, x + 2 * k, w + 2 * k, idesc_f8(256, kBN), k > 0);
-          commit_pair(&bars->done[stage], lead);
+        for (int h = 0; h < S::kHalves; ++h) {
+          if (!(ok = mbar_wait_warp(&bars->taken[slot * S::kHalves + h], taken_phase, abort_flag, status,
+                                    kSiteSlot)))
+            break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_f8_pair(d + 128 * h, x + 2 * k, w + 512 * h + 2 * k, idesc_f8(256, 128), k > 0);
+            if (h == S::kHalves - 1) commit_pair(&bars->done[stage], lead);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (!ok) break;
         if ((stage += 2) >= kStages) stage -= kStages, full_phase ^= 1;
         if ((slot += 2) >= kSlots) slot -= kSlots, taken_phase ^= 1;
       }
@@ -320,7 +329,7 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
     constexpr int kCols = S::kCols, kMine = kParts > 1 ? kCols / 2 : kCols;  // columns summed, stored
     const int q = warp % 4, me = (warp - 4) / 4;
     // this warp's lanes and first column of a slot
-    const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + kCols * me;
+    const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + 64 * me;
     const float* mine = scales + 32 * q + lane;
     const uint32_t leader = leader_address(&bars->taken[0], lead);
     int stage = 0, phase = 0, get = 0;
@@ -366,16 +375,19 @@ f8_mmq_kernel(const __grid_constant__ Maps maps, const F8Call c, int store, unsi
         tmem_ld(at + 32, vb);
         tmem_wait_ld2(va, vb);
         if constexpr (kCols == 128) {
+          tc_fence_before();  // the first half is in registers
+          __syncwarp();
+          if (lane == 0) arrive_at_leader(leader + 16 * turn);
           add(acc, va);
-          tmem_ld_after(at + 64, va, acc);
+          tmem_ld_after(at + 128, va, acc);
           add(acc + 16, vb);
-          tmem_ld_after(at + 96, vb, acc + 16);
+          tmem_ld_after(at + 160, vb, acc + 16);
           tmem_wait_ld2(va, vb);
         }
-        // all is in registers: the MMAs of a later block may write
+        // all is in registers
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_at_leader(leader + 8 * turn);
+        if (lane == 0) arrive_at_leader(leader + 8 * (S::kHalves * turn + S::kHalves - 1));
         // (a look at a barrier takes 200 cycles, so it comes before the last adds)
         seen = mbar_test_wait(&bars->done[stage], phase);
         add(acc + kCols / 2 - 32, va);
