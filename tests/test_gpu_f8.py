@@ -575,6 +575,41 @@ def test_back_to_back_products_of_changing_operands():
         assert torch.equal(got, q6.f8_mmq(wide, buf)[0])
 
 
+@pytest.mark.parametrize("N,M", [(140, 1000), (140, 2056), (600, 1100)])
+def test_shared_tiles_back_to_back_in_graphs_and_on_two_streams(N, M):
+    """Products whose tiles several pairs of CTAs share, right behind what writes their operands."""
+    K = 3600
+    g = gen(M)
+    xs = [activations(g, N, K, BF16) for _ in range(4)]
+    w = q6.f8_quantize_weights(randn(g, M, K))
+    want = [q6.f8_mmq(w, q6.f8_quantize_act(x))[0].clone() for x in xs]
+    buf, out = q6.alloc_f8_activations(N, K), torch.empty(N, M, dtype=BF16, device="cuda")
+    for k in range(24):
+        q6.f8_quantize_act(xs[k % 4], out=buf)
+        q6.f8_mmq(w, buf, out=out)
+        got = out.clone()
+        q6.f8_mmq(w, buf, out=out)
+        assert torch.equal(got, want[k % 4]) and torch.equal(out, got)
+    graphs = []
+    for _ in range(2):
+        x, torch_graph = xs[0].clone(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(torch_graph):
+            act = q6.f8_quantize_act(x)
+            ys = [q6.f8_mmq(w, act)[0] for _ in range(3)]
+        graphs.append((torch_graph, x, ys, torch.cuda.Stream()))
+    for k in range(6):
+        for i, (gr, x, ys, stream) in enumerate(graphs):     # both at a time
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                x.copy_(xs[(k + i) % 4])
+                gr.replay()
+        for i, (gr, x, ys, stream) in enumerate(graphs):
+            torch.cuda.current_stream().wait_stream(stream)
+            assert all(torch.equal(y, want[(k + i) % 4]) for y in ys)
+    q6.sync_status()
+
+
 def test_offsets_past_32_bits():
     K, M, N = 16384, 270000, 3
     wq = torch.zeros(M, K, dtype=torch.uint8, device="cuda")       # 4.4 GB of codes
