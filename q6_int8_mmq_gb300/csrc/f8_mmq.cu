@@ -4,8 +4,8 @@
 //
 // A pair of CTAs (cluster of two, cta_group::2) computes a tile of 256 tokens
 // (MMA M; 128 tokens, one TMEM lane each, a CTA) by kBN weight rows (MMA N). Each
-// block of 128 of K is four tcgen05 MMAs (kind::f8f6f4, K = 32) into an accumulator
-// of its own, which eight warps of each CTA add, times the block's two scales, to
+// block of 128 of K is four tcgen05 MMAs (kind::f8f6f4, 128 rows, K = 32), or eight,
+// into an accumulator of its own, which eight warps of each CTA add, times the block's two scales, to
 // f32 sums in registers while the next blocks' MMAs run: a thread has one token and
 // columns of one block row of weights, so the product of the scales is one number a
 // thread and block, and a value costs half a packed multiply-add.
@@ -559,13 +559,17 @@ cudaError_t f8_tc_prepare() {
   int device = 0;
   if (!e) e = cudaGetDevice(&device);
   if (e) return e;
+  auto room = [](auto kernel, const cudaLaunchConfig_t& cfg) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) cudaGetLastError(), n = 0;  // none
+    return n;
+  };
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   launch_of<128, 2>(&cfg, attr, 1, nullptr);
-  e = cudaOccupancyMaxActiveClusters(&g_room[device].of_two, f8_mmq_kernel<float, 128, 2>, &cfg);
+  g_room[device].of_two = room(f8_mmq_kernel<float, 128, 2>, cfg);
   launch_of<128, 4>(&cfg, attr, 1, nullptr);
-  if (!e)
-    e = cudaOccupancyMaxActiveClusters(&g_room[device].of_four, f8_mmq_kernel<float, 128, 4>, &cfg);
+  g_room[device].of_four = room(f8_mmq_kernel<float, 128, 4>, cfg);
   return e;
 }
 
