@@ -326,6 +326,13 @@ def test_product_at_size(N, M, K):
     check_product(w, act, BF16)
 
 
+@pytest.mark.parametrize("N", [1, 16, 17, 32, 33, 64])
+@pytest.mark.parametrize("M,K", [(19585, 1040), (40000, 2064)])
+def test_product_of_more_rows_than_all_sms_take_at_once(N, M, K):
+    w, act = operands(gen(N + K), N, M, K)
+    check_product(w, act, TYPES[N % 3])
+
+
 # Few tiles and a long K: pairs of CTAs that share a tile, each with a part of K.
 @pytest.mark.parametrize("K", [2176, 2304, 2448, 3568, 3600, 11008])
 @pytest.mark.parametrize("N,M", [(65, 1), (129, 129), (257, 1000), (300, 70), (200, 2056), (65, 4608), (130, 4700)])
