@@ -175,9 +175,18 @@ def _stream(stream=None):
 
 # ---------------------------------------------------------------- sizes ---
 
+def _c_ints(**sizes):
+    """The C ABI's sizes are 32-bit, and ctypes drops the bits above without a word: a size that
+    does not fit is refused here, where every buffer's size is asked for."""
+    for name, n in sizes.items():
+        if not -2 ** 31 <= n < 2 ** 31:
+            raise Q6Error(Q6_ESIZE, f"{name} = {n} does not fit 32 bits")
+
+
 @functools.lru_cache(maxsize=256)
 def act_plane_bytes(N: int, K: int):
     """(xq_bytes, da_bytes, xh_bytes, ldda) of an N x K activation."""
+    _c_ints(N=N, K=K)
     a, b, c, ld = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_int()
     _check(load().q8_act_plane_bytes(N, K, ctypes.byref(a), ctypes.byref(b), ctypes.byref(c),
                                      ctypes.byref(ld)))
@@ -187,6 +196,7 @@ def act_plane_bytes(N: int, K: int):
 @functools.lru_cache(maxsize=256)
 def act_sums_bytes(N: int, K: int):
     """(us_bytes, ldus) of the block-sum pairs of an N x K activation."""
+    _c_ints(N=N, K=K)
     a, ld = ctypes.c_size_t(), ctypes.c_int()
     _check(load().q8_act_sums_bytes(N, K, ctypes.byref(a), ctypes.byref(ld)))
     return a.value, ld.value
@@ -195,6 +205,7 @@ def act_sums_bytes(N: int, K: int):
 @functools.lru_cache(maxsize=256)
 def plane_bytes(M: int, K: int):
     """(packed plane bytes, W_exp bytes) of an M x K q6_K weight."""
+    _c_ints(M=M, K=K)
     a, b = ctypes.c_size_t(), ctypes.c_size_t()
     _check(load().q6k_plane_bytes(M, K, ctypes.byref(a), ctypes.byref(b)))
     return a.value, b.value
@@ -539,6 +550,7 @@ def sync_status(stream=None):
 @functools.lru_cache(maxsize=256)
 def q4k_plane_bytes(M: int, K: int):
     """(packed q4_K plane bytes, operand plane bytes) of an M x K weight."""
+    _c_ints(M=M, K=K)
     a, b = ctypes.c_size_t(), ctypes.c_size_t()
     _check(load().q4k_plane_bytes(M, K, ctypes.byref(a), ctypes.byref(b)))
     return a.value, b.value

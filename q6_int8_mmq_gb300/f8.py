@@ -11,8 +11,8 @@ import ctypes
 import dataclasses
 import functools
 
-from . import (PATH_NAMES, Q6_EINVAL, Activations, Q6Error, _check, _same_device, act_plane_bytes,
-               alloc_activations, load)
+from . import (PATH_NAMES, Q6_EINVAL, Activations, Q6Error, _c_ints, _check, _same_device,
+               act_plane_bytes, alloc_activations, load)
 from .moe import _empty, _made, _on, _rows, _rows2d, _stream, _type, _types, _whole
 
 
@@ -25,6 +25,7 @@ def _f8():
 @functools.lru_cache(maxsize=256)
 def f8_act_bytes(N: int, K: int):
     """(xq_bytes, sx_bytes, ldsx) of N x K e4m3 activations."""
+    _c_ints(N=N, K=K)
     a, b, ld = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_int()
     _check(load().q6_f8_act_bytes(N, K, ctypes.byref(a), ctypes.byref(b), ctypes.byref(ld)))
     return a.value, b.value, ld.value
@@ -33,6 +34,7 @@ def f8_act_bytes(N: int, K: int):
 @functools.lru_cache(maxsize=256)
 def f8_weight_bytes(M: int, K: int):
     """(wq_bytes, sw_bytes) of an M x K e4m3 weight."""
+    _c_ints(M=M, K=K)
     a, b = ctypes.c_size_t(), ctypes.c_size_t()
     _check(load().q6_f8_weight_bytes(M, K, ctypes.byref(a), ctypes.byref(b)))
     return a.value, b.value
