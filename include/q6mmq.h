@@ -692,6 +692,13 @@ int q6_silu_mul_f8(const void *X, int type, int N, int K, int64_t ldx, uint8_t *
 int q6_f8_mmq(const uint8_t *wq, const float *sw, int M, int K, const uint8_t *xq, const float *sx,
               int N, void *Y, int type, int64_t ldy, int *path_out, q6_stream_t s);
 
+/* How q6_f8_mmq() runs a product of these sizes on the calling thread's current
+ * device: the path, the tokens and weight rows of a tile, the parts of K that the
+ * CTAs (with Q6_PATH_F8_TC pairs of CTAs) of a cluster take, and how many such
+ * clusters the device runs at a time (0 where it could not say). All 0 for N == 0.
+ * Sizes are refused as by q6_f8_mmq(). */
+int q6_f8_mmq_form(int M, int K, int N, int *path, int *tokens, int *rows, int *parts, int *room);
+
 #ifdef __cplusplus
 }
 #endif

@@ -93,6 +93,7 @@ SIGNATURES = [
     ("q6_silu_mul_q8", _I, [_P, _I, _I, _I, _L, _P, _P, _P, _P, _P]),
     ("q6_silu_mul_f8", _I, [_P, _I, _I, _I, _L, _P, _P, _P]),
     ("q6_f8_mmq", _I, [_P, _P, _I, _I, _P, _P, _I, _P, _I, _L, _IP, _P]),
+    ("q6_f8_mmq_form", _I, [_I, _I, _I, _IP, _IP, _IP, _IP, _IP]),
 ]
 
 
@@ -687,6 +688,7 @@ from .moe import (ExpertWeights, Groups, LoraAdapters, Route, alloc_groups,  # n
                   alloc_route, expert_plane_bytes, experts_mmq, group_rows,
                   group_workspace_bytes, lora_add, lora_workspace_bytes, moe_combine, moe_route,
                   pack_experts)
-from .f8 import (F8Activations, F8Weights, alloc_f8_activations, alloc_f8_weights,  # noqa: E402,F401
-                 f8_act_bytes, f8_mmq, f8_quantize_act, f8_quantize_weights, f8_weight_bytes,
-                 rms_norm_f8, rms_norm_q8, silu_mul_f8, silu_mul_q8)
+from .f8 import (F8Activations, F8Form, F8Weights, alloc_f8_activations,  # noqa: E402,F401
+                 alloc_f8_weights, f8_act_bytes, f8_mmq, f8_mmq_form, f8_quantize_act,
+                 f8_quantize_weights, f8_weight_bytes, rms_norm_f8, rms_norm_q8, silu_mul_f8,
+                 silu_mul_q8)

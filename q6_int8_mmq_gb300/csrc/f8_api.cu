@@ -79,6 +79,16 @@ int check_rows(const void* X, int type, int64_t ldx, int64_t width) {
   return Q6_OK;
 }
 
+int check_product(int M, int K, int N) {
+  int rc = check_f8(N, K);
+  if (rc || (rc = check_f8(M, K))) return rc;
+  if (M < 1) return fail(Q6_EINVAL, "M >= 1");
+  // blocks of all tiles, which a CTA may have to count
+  if ((double)q6::f8_blocks(M) * q6::f8_blocks(N) * q6::f8_blocks(K) > INT32_MAX)
+    return fail(Q6_ESIZE, "the product has too many tiles");
+  return Q6_OK;
+}
+
 int norm_entry(const q6::NormCall& c, const q6::RowSink& out, q6_stream_t s) {
   if (!any_type(c.type) || !any_type(c.wtype) || (c.residual && !any_type(c.rtype)))
     return fail(Q6_EINVAL, "unknown type");
@@ -188,15 +198,26 @@ int q6_silu_mul_f8(const void* X, int type, int N, int K, int64_t ldx, uint8_t* 
                   "gated activation");
 }
 
+int q6_f8_mmq_form(int M, int K, int N, int* path, int* tokens, int* rows, int* parts, int* room) {
+  if (!path || !tokens || !rows || !parts || !room) return fail(Q6_EINVAL, "null pointer");
+  *path = Q6_PATH_NONE;
+  *tokens = *rows = *parts = *room = 0;
+  int rc = check_product(M, K, N);
+  if (rc || N == 0 || (rc = q6::require_device(nullptr, q6::kBlockKernels))) return rc;
+  const bool few = N <= kFewTokens;
+  q6::F8Form f = {};
+  const cudaError_t e = few ? q6::f8_few_form(M, K, N, &f) : q6::f8_tc_form(M, K, N, &f);
+  if (e) return fail(Q6_ECUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+  *path = few ? Q6_PATH_F8_FEW : Q6_PATH_F8_TC;
+  *tokens = f.tokens, *rows = f.rows, *parts = f.parts, *room = f.room;
+  return Q6_OK;
+}
+
 int q6_f8_mmq(const uint8_t* wq, const float* sw, int M, int K, const uint8_t* xq, const float* sx,
               int N, void* Y, int type, int64_t ldy, int* path_out, q6_stream_t s) {
   if (path_out) *path_out = Q6_PATH_NONE;
-  int rc = check_f8(N, K);
-  if (rc || (rc = check_f8(M, K))) return rc;
-  if (M < 1) return fail(Q6_EINVAL, "M >= 1");
-  // blocks of all tiles, which a CTA may have to count
-  if ((double)q6::f8_blocks(M) * q6::f8_blocks(N) * q6::f8_blocks(K) > INT32_MAX)
-    return fail(Q6_ESIZE, "the product has too many tiles");
+  int rc = check_product(M, K, N);
+  if (rc) return rc;
   if (!any_type(type)) return fail(Q6_EINVAL, "unknown type %d", type);
   if (ldy < M) return fail(Q6_EINVAL, "ldy (%lld) < M (%d)", (long long)ldy, M);
   if (N == 0) return Q6_OK;

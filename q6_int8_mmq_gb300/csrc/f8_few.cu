@@ -276,15 +276,26 @@ cudaError_t launch_t(const Maps& maps, const F8Call& c, int n, int split, unsign
                    : launch_n<T, 64>(maps, c, split, status, s);
 }
 
+// Clusters of 1 to kMaxSplit CTAs that a device runs at a time, two CTAs an SM (a cluster's
+// SMs are near one another): 304, 152, 97, 74, 58, 46, 38 and 36 of 152 SMs.
+struct Room {
+  int of[kMaxSplit + 1] = {};
+};
+Room g_room[kMaxDevices];  // written once, under the lock that every call takes
+// Asked about in place of f8_few_kernel, of which the query counts one CTA an SM, as of
+// every kernel that allocates TMEM; the same in threads and shared memory.
+__global__ void __launch_bounds__(kThreads, 2) room_kernel() {}
+
 // Parts of K: as many as leave all CTAs resident, two an SM.
-int split_of(const F8Call& c) {
-  const long long bands = ((long long)c.M + 127) / 128;
-  const int blocks = f8_blocks(c.K);
+int split_of(int M, int K) {
+  const long long bands = ((long long)M + 127) / 128;
+  const int blocks = f8_blocks(K);
   long long split = 304 / bands;
   if (split > kMaxSplit) split = kMaxSplit;
   if (split > blocks) split = blocks;
   return split < 1 ? 1 : (int)split;
 }
+int width_of(int N) { return N <= 16 ? 16 : N <= 32 ? 32 : 64; }
 
 }  // namespace
 
@@ -306,18 +317,44 @@ cudaError_t f8_few_prepare() {
   all(float());
   all(__nv_bfloat16());
   all(__half());
+  raise(room_kernel, Few<64>::kSmem);
+  int device = 0;
+  if (!e) e = cudaGetDevice(&device);
+  if (e) return e;
+  for (int i = 1; i <= kMaxSplit; ++i) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)i);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Few<64>::kSmem;  // the most of the three; two CTAs an SM with each
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)i;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int& n = g_room[device].of[i];
+    if (cudaOccupancyMaxActiveClusters(&n, room_kernel, &cfg)) cudaGetLastError(), n = 0;
+  }
+  return e;
+}
+
+cudaError_t f8_few_form(int M, int K, int N, F8Form* form) {
+  int device = 0;
+  const cudaError_t e = cudaGetDevice(&device);
+  const int split = split_of(M, K);
+  *form = {width_of(N), 128, split, g_room[device].of[split]};
   return e;
 }
 
 int launch_f8_few(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStream_t s) {
-  const int n = c.N <= 16 ? 16 : c.N <= 32 ? 32 : 64;
+  const int n = width_of(c.N);
   Maps maps;
   int rc;
   if ((rc = encode_f8_map(&maps.x, c.xq, c.N, c.K, n, "xq")) ||
       (rc = encode_f8_map(&maps.w, c.wq, c.M, c.K, 128, "wq")) ||
       (rc = encode_f8_scales(&maps.sx, c.sx, c.ldsx, f8_blocks(c.K), n, 1)))
     return rc;
-  const int split = split_of(c);
+  const int split = split_of(c.M, c.K);
   *e = c.type == Q6_TYPE_F32    ? launch_t<float>(maps, c, n, split, status, s)
        : c.type == Q6_TYPE_BF16 ? launch_t<__nv_bfloat16>(maps, c, n, split, status, s)
                                 : launch_t<__half>(maps, c, n, split, status, s);

@@ -66,6 +66,14 @@ int encode_f8_map(CUtensorMap* map, const void* base, int rows, int K, int box, 
 int encode_f8_scales(CUtensorMap* map, const float* sx, int ld, int rows, int n, int box);
 // Y in boxes of `cols` x `rows` with the 64-byte swizzle.
 int encode_f8_results(CUtensorMap* map, const F8Call& c, int cols, int rows);
+// How a product of these sizes runs on the current device (prepared): a tile's tokens and
+// weight rows, the parts of K that the CTAs (or pairs of CTAs) of a cluster take, and the
+// clusters of that many that run at a time (0 where the device could not say).
+struct F8Form {
+  int tokens, rows, parts, room;
+};
+cudaError_t f8_few_form(int M, int K, int N, F8Form* form);
+cudaError_t f8_tc_form(int M, int K, int N, F8Form* form);
 // *e receives the launch's error; returns Q6_OK, or a code whose text is recorded.
 cudaError_t f8_few_prepare();
 int launch_f8_few(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStream_t s);

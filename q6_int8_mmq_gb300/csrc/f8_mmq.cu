@@ -508,10 +508,10 @@ cudaError_t launch_n(const Maps& maps, const F8Call& c, int store, unsigned int*
   launch_of<kBN, kParts>(&cfg, attr, (unsigned)(kParts > 1 || tiles < 76 ? tiles : 76), s);
   return cudaLaunchKernelEx(&cfg, f8_mmq_kernel<T, kBN, kParts>, maps, c, store, status);
 }
-// Clusters of two and of four pairs that a device holds at a time (each SM one CTA, the
-// SMs of a cluster near one another): 36 and 15 of 152 SMs.
+// Clusters of one, two and four pairs that a device holds at a time (each SM one CTA, the
+// SMs of a cluster near one another): 76, 36 and 15 of 152 SMs.
 struct Room {
-  int of_two = 0, of_four = 0;
+  int of_one = 0, of_two = 0, of_four = 0;
 };
 Room g_room[kMaxDevices];  // written once, under the lock that every call takes
 
@@ -526,9 +526,9 @@ struct Form {
 // that add them up 1 us (two pairs) or 1.8 (four). (us, 256 tokens. 1024 weight rows, four
 // pairs against one: K = 2048 6.6, 6.4; 2560 6.9, 7.3; 8192 10.3, 17.9. 4096 rows, two
 // against one: K = 2560 9.0, 8.5; 3584 10.1, 10.3; 8192 15.3, 18.8.)
-Form form_of(const F8Call& c, const Room& room) {
-  const long long n = tiles_of(c.N, kTileN), wide = n * tiles_of(c.M, 256), thin = n * tiles_of(c.M, 128);
-  const int blocks = f8_blocks(c.K);
+Form form_of(int M, int K, int N, const Room& room) {
+  const long long n = tiles_of(N, kTileN), wide = n * tiles_of(M, 256), thin = n * tiles_of(M, 128);
+  const int blocks = f8_blocks(K);
   if (5 * ((thin + 75) / 76) >= 8 * ((wide + 75) / 76)) return {false, 1};
   return {true, blocks >= 18 && thin <= room.of_four ? 4 : blocks >= 28 && thin <= room.of_two ? 2 : 1};
 }
@@ -568,6 +568,8 @@ cudaError_t f8_tc_prepare() {
   };
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
+  launch_of<128, 1>(&cfg, attr, 1, nullptr);
+  g_room[device].of_one = room(f8_mmq_kernel<float, 128, 1>, cfg);
   launch_of<128, 2>(&cfg, attr, 1, nullptr);
   g_room[device].of_two = room(f8_mmq_kernel<float, 128, 2>, cfg);
   launch_of<128, 4>(&cfg, attr, 1, nullptr);
@@ -575,10 +577,20 @@ cudaError_t f8_tc_prepare() {
   return e;
 }
 
+cudaError_t f8_tc_form(int M, int K, int N, F8Form* form) {
+  int device = 0;
+  const cudaError_t e = cudaGetDevice(&device);
+  const Room& room = g_room[device];
+  const Form f = form_of(M, K, N, room);
+  *form = {kTileN, f.thin ? 128 : 256, f.parts,
+           f.parts == 1 ? room.of_one : f.parts == 2 ? room.of_two : room.of_four};
+  return e;
+}
+
 int launch_f8_tc(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStream_t s) {
   int device = 0;
   if ((*e = cudaGetDevice(&device))) return Q6_OK;  // (the caller reports *e)
-  const Form form = form_of(c, g_room[device]);
+  const Form form = form_of(c.M, c.K, c.N, g_room[device]);
   // results by TMA where their rows start on 16 bytes, else in words of 4 or 2 bytes
   const int size = c.type == Q6_TYPE_F32 ? 4 : 2;
   const uintptr_t where = reinterpret_cast<uintptr_t>(c.Y) | (uintptr_t)(c.ldy * size);

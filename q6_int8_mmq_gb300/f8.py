@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import functools
+from typing import NamedTuple
 
 from . import (PATH_NAMES, Q6_EINVAL, Activations, Q6Error, _c_ints, _check, _same_device,
                act_plane_bytes, alloc_activations, load)
@@ -301,3 +302,23 @@ def f8_mmq(w: F8Weights, act: F8Activations, out=None, dtype=None, stream=None):
                             act.sx.data_ptr(), N, out.data_ptr(), code, ldy, ctypes.byref(path),
                             _stream(stream, dev)))
     return out, PATH_NAMES.get(path.value, str(path.value))
+
+
+class F8Form(NamedTuple):
+    """How a product of e4m3 blocks runs: the path's name, the tokens and weight rows of a tile,
+    the parts of K that the CTAs (on the path "f8_tc" pairs of CTAs) of a cluster take, and how
+    many such clusters the device runs at a time (0 where it could not say)."""
+    path: str
+    tokens: int
+    rows: int
+    parts: int
+    room: int
+
+
+def f8_mmq_form(M: int, K: int, N: int) -> F8Form:
+    """How f8_mmq() runs N tokens on an M x K weight on the current device."""
+    _c_ints(M=M, K=K, N=N)
+    form = [ctypes.c_int() for _ in range(5)]
+    _check(load().q6_f8_mmq_form(M, K, N, *map(ctypes.byref, form)))
+    path, *rest = (v.value for v in form)
+    return F8Form(PATH_NAMES.get(path, str(path)), *rest)

@@ -1,0 +1,54 @@
+"""Which kernel takes a product of e4m3 blocks: each of them runs at the sizes meant for it, and is right
+there."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import q6_int8_mmq_gb300 as q6  # noqa: E402
+import f8_reference as ref  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def test_sizes_are_refused_as_by_the_product():
+    for M, K, N in ((0, 512, 3), (64, 40, 3), (64, 0, 3), (64, 512, -1), (2 ** 31 - 1, 16, 1),
+                    (2 ** 30, 16, 2 ** 30), (2 ** 32 + 64, 512, 3), (64, 512, 2 ** 32 + 3)):
+        with pytest.raises(q6.Q6Error):
+            q6.f8_mmq_form(M, K, N)
+    assert q6.f8_mmq_form(64, 512, 0) == ("none", 0, 0, 0, 0)
+    assert q6.load().q6_f8_mmq_form(64, 512, 0, None, None, None, None, None) == q6.Q6_EINVAL
+
+
+# (N, M, K) -> path, tokens and rows of a tile, parts of K
+FORMS = [((1, 128, 128), ("f8_few", 16, 128, 1)),        # a single block of K
+         ((16, 300, 400), ("f8_few", 16, 128, 4)),       # as many parts as blocks
+         ((17, 1000, 2064), ("f8_few", 32, 128, 8)),
+         ((32, 2056, 1040), ("f8_few", 32, 128, 8)),
+         ((33, 8000, 1040), ("f8_few", 64, 128, 4)),
+         ((64, 22016, 528), ("f8_few", 64, 128, 1)),     # more bands than the SMs take in two parts
+         ((65, 1024, 1152), ("f8_tc", 256, 128, 1)),     # few tiles, a short K
+         ((65, 1024, 3600), ("f8_tc", 256, 128, 4)),
+         ((300, 1000, 3600), ("f8_tc", 256, 128, 2)),
+         ((2048, 4096, 528), ("f8_tc", 256, 256, 1))]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sizes,form", FORMS)
+def test_every_form_runs_where_it_is_meant_to(sizes, form):
+    """Codes -4 .. 4 and scales that are powers of two: every sum fits f32, so the result is exact."""
+    N, M, K = sizes
+    chosen = q6.f8_mmq_form(M, K, N)
+    assert chosen[:4] == form and chosen.room > 0
+    g = torch.Generator(device="cuda").manual_seed(N)
+    small = lambda *s: torch.randint(-4, 5, s, generator=g, device="cuda").float()  # noqa: E731
+    power = lambda *s: torch.exp2(torch.randint(-2, 3, s, generator=g, device="cuda").float())  # noqa: E731
+    act = q6.F8Activations(N, K, small(N, K).to(torch.float8_e4m3fn), power(-(-K // 128), -(-N // 4) * 4))
+    w = q6.F8Weights(M, K, small(M, K).to(torch.float8_e4m3fn), power(-(-M // 128), -(-K // 128)))
+    Y, path = q6.f8_mmq(w, act, dtype=torch.float32)
+    q6.sync_status()
+    assert path == form[0]
+    assert torch.equal(Y.double(), ref.product(act.xq, act.sx, w.wq, w.sw, torch.float32)[0])
