@@ -286,14 +286,15 @@ Room g_room[kMaxDevices];  // written once, under the lock that every call takes
 // every kernel that allocates TMEM; the same in threads and shared memory.
 __global__ void __launch_bounds__(kThreads, 2) room_kernel() {}
 
-// Parts of K: as many as leave all CTAs resident, two an SM.
-int split_of(int M, int K) {
+// Parts of K: as many as leave the clusters of all bands of weights resident. (One token,
+// K = 4096, us: 36 bands in eight parts 6.4; 37 in eight 9.1, in seven 6.5; 39 in seven 9.5, in
+// six 6.6; 47 in six 11.5, in five 7.6; 59 in five 12.5, in four 8.6; 75 in four 13.6, in three
+// 10.1; 98 in three 16.0, in two 12.9.)
+int split_of(int M, int K, const Room& room) {
   const long long bands = ((long long)M + 127) / 128;
-  const int blocks = f8_blocks(K);
-  long long split = 304 / bands;
-  if (split > kMaxSplit) split = kMaxSplit;
-  if (split > blocks) split = blocks;
-  return split < 1 ? 1 : (int)split;
+  int split = f8_blocks(K) < kMaxSplit ? f8_blocks(K) : kMaxSplit;
+  while (split > 1 && bands > room.of[split]) --split;
+  return split;
 }
 int width_of(int N) { return N <= 16 ? 16 : N <= 32 ? 32 : 64; }
 
@@ -341,12 +342,15 @@ cudaError_t f8_few_prepare() {
 cudaError_t f8_few_form(int M, int K, int N, F8Form* form) {
   int device = 0;
   const cudaError_t e = cudaGetDevice(&device);
-  const int split = split_of(M, K);
+  if (e) return e;
+  const int split = split_of(M, K, g_room[device]);
   *form = {width_of(N), 128, split, g_room[device].of[split]};
   return e;
 }
 
 int launch_f8_few(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStream_t s) {
+  int device = 0;
+  if ((*e = cudaGetDevice(&device))) return Q6_OK;  // (the caller reports *e)
   const int n = width_of(c.N);
   Maps maps;
   int rc;
@@ -354,7 +358,7 @@ int launch_f8_few(const F8Call& c, cudaError_t* e, unsigned int* status, cudaStr
       (rc = encode_f8_map(&maps.w, c.wq, c.M, c.K, 128, "wq")) ||
       (rc = encode_f8_scales(&maps.sx, c.sx, c.ldsx, f8_blocks(c.K), n, 1)))
     return rc;
-  const int split = split_of(c.M, c.K);
+  const int split = split_of(c.M, c.K, g_room[device]);
   *e = c.type == Q6_TYPE_F32    ? launch_t<float>(maps, c, n, split, status, s)
        : c.type == Q6_TYPE_BF16 ? launch_t<__nv_bfloat16>(maps, c, n, split, status, s)
                                 : launch_t<__half>(maps, c, n, split, status, s);
