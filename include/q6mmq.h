@@ -684,9 +684,11 @@ int q6_silu_mul_f8(const void *X, int type, int N, int K, int64_t ldx, uint8_t *
  *   P = sum over the block's k of xq[n][k] * wq[m][k],
  * in f32 and rounded once to `type`. The products are exact and the tensor
  * cores' f32 sums of a block truncate: P is within 2^-17 of the sum of its
- * products' sizes (measured: 2^-20.7 with products of one sign). A NaN code, or
- * a scale that is not finite, makes NaN. The two scales are multiplied in f32
- * first: their product should be a normal number.
+ * products' sizes (measured: 2^-20.7 with products of one sign). The two scales
+ * are multiplied in f32 first: their product should be a normal number. Values
+ * that are not finite go through the formula as IEEE arithmetic has it: a NaN
+ * code or scale makes NaN, an infinite scale an infinity, or NaN where P or the
+ * other scale is 0 or infinities of both signs meet.
  *   Y [N][ldy] of `type`, ldy >= M, aligned to its element.
  *   path_out : NULL or receives the Q6_PATH_F8_* that ran. */
 int q6_f8_mmq(const uint8_t *wq, const float *sw, int M, int K, const uint8_t *xq, const float *sx,

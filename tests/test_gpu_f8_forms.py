@@ -80,3 +80,34 @@ def test_every_number_of_parts_is_exact(N, parts):
     for M in (128 * bands, 128 * bands - 127):
         assert q6.f8_mmq_form(M, K, N).parts == parts
         check_exact(N, M, K)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,M,K", [(5, 300, 1040), (40, 1000, 528), (70, 300, 528), (70, 1024, 3600),
+                                   (300, 1000, 3600), (2048, 4096, 400)])
+def test_infinite_and_nan_scales_go_through_the_formula(N, M, K):
+    """What 64-bit arithmetic makes of the blocks' sums, infinities and NaN of them in the same places."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    blocks, inf, nan = -(-K // 128), float("inf"), float("nan")
+    x = torch.randint(-2, 3, (N, K), generator=g, device="cuda").float()
+    w = torch.randint(-2, 3, (M, K), generator=g, device="cuda").float()
+    x[3, 128:256] = 0                                     # a block whose sum is 0
+    sx, sw = torch.ones(blocks, -(-N // 4) * 4, device="cuda"), torch.ones(-(-M // 128), blocks, device="cuda")
+    sx[0, 0] = inf                                        # meets sums of both signs, and zeros
+    sx[1, 1], sx[2, 1], sx[1, 3] = -inf, 0.0, inf
+    sx[0, 4] = nan
+    sw[0, 1] = inf                                        # the first 128 rows
+    if M > 128:
+        sw[-1, 2] = nan
+    act = q6.F8Activations(N, K, x.to(torch.float8_e4m3fn), sx)
+    weight = q6.F8Weights(M, K, w.to(torch.float8_e4m3fn), sw)
+    Y, _ = q6.f8_mmq(weight, act, dtype=torch.float32)
+    q6.sync_status()
+    want = torch.zeros(N, M, dtype=torch.float64, device="cuda")
+    for b in range(blocks):
+        at = slice(128 * b, min(128 * b + 128, K))
+        each = sx[b, :N].double()[:, None] * sw[:, b].double().repeat_interleave(128)[:M]
+        want += each * (x[:, at].double() @ w[:, at].double().t())
+    assert torch.equal(Y.isnan(), want.isnan())
+    assert torch.equal(Y.double().nan_to_num(nan=0.0), want.nan_to_num(nan=0.0))
+    assert want.isnan().any() and (want == inf).any() and (want == -inf).any() and want[2].isfinite().any()
