@@ -1,5 +1,6 @@
 // Activations quantised by the step that makes them: the root-mean-square norm
-// with the residual's addition, silu(gate) * up, or nothing but the reading.
+// with the residual's addition, silu(gate) * up, or (e4m3 alone; the int8 codes of f32
+// rows are quantize.cu's) nothing but the reading.
 //
 //   norm   h = x + residual,  t = h * weight,  r = 1 / sqrt(mean(h^2) + eps)
 //   silu   t = gate / (1 + exp(-gate)) * up,   r = 1
@@ -403,12 +404,6 @@ cudaError_t rows_as(const void* X, int type, int N, int K, long long ldx, const 
          : type == Q6_TYPE_BF16 ? rows_t<__nv_bfloat16, kF8, kGlu>(X, N, K, ldx, out, s)
                                 : rows_t<__half, kF8, kGlu>(X, N, K, ldx, out, s);
 }
-template <bool kGlu>
-cudaError_t rows_of(const void* X, int type, int N, int K, long long ldx, const RowSink& out,
-                    cudaStream_t s) {
-  return out.f8 ? rows_as<true, kGlu>(X, type, N, K, ldx, out, s)
-                : rows_as<false, kGlu>(X, type, N, K, ldx, out, s);
-}
 
 template <typename T, typename R, bool kF8, bool kAdd, int kU>
 cudaError_t norm_u(const NormCall& c, const RowSink& out, int most, cudaStream_t s) {
@@ -449,13 +444,14 @@ cudaError_t weights_t(const void* W, int M, int K, long long ldw, uint8_t* wq, f
 
 }  // namespace
 
-cudaError_t launch_quantize_rows(const void* X, int type, int N, int K, long long ldx,
-                                 const RowSink& out, cudaStream_t s) {
-  return rows_of<false>(X, type, N, K, ldx, out, s);
+cudaError_t launch_f8_quantize_rows(const void* X, int type, int N, int K, long long ldx,
+                                    const RowSink& out, cudaStream_t s) {
+  return rows_as<true, false>(X, type, N, K, ldx, out, s);
 }
 cudaError_t launch_silu_mul(const void* X, int type, int N, int K, long long ldx,
                             const RowSink& out, cudaStream_t s) {
-  return rows_of<true>(X, type, N, K, ldx, out, s);
+  return out.f8 ? rows_as<true, true>(X, type, N, K, ldx, out, s)
+                : rows_as<false, true>(X, type, N, K, ldx, out, s);
 }
 cudaError_t launch_rms_norm(const NormCall& c, const RowSink& out, cudaStream_t s) {
   return c.type == Q6_TYPE_F32    ? norm_of<float>(c, out, s)

@@ -139,7 +139,8 @@ int q6_f8_quantize_act(const void* X, int type, int N, int K, int64_t ldx, uint8
   if ((rc = check_rows(X, type, ldx, K)) || (rc = check_f8_sink(xq, sx)) ||
       (rc = q6::require_device(nullptr)))
     return rc;
-  return launched(q6::launch_quantize_rows(X, type, N, K, ldx, f8_sink(N, xq, sx), (cudaStream_t)s),
+  return launched(q6::launch_f8_quantize_rows(X, type, N, K, ldx, f8_sink(N, xq, sx),
+                                              (cudaStream_t)s),
                   "quantiser");
 }
 

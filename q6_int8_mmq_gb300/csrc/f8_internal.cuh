@@ -24,9 +24,9 @@ struct RowSink {
   float* scale;
   int lds;
 };
-// Rows of X [N][ldx] as codes.
-cudaError_t launch_quantize_rows(const void* X, int type, int N, int K, long long ldx,
-                                 const RowSink& out, cudaStream_t s);
+// Rows of X [N][ldx] as e4m3 codes.
+cudaError_t launch_f8_quantize_rows(const void* X, int type, int N, int K, long long ldx,
+                                    const RowSink& out, cudaStream_t s);
 // silu(gate) * up of rows [N][ldx] of K gate, then K up values.
 cudaError_t launch_silu_mul(const void* X, int type, int N, int K, long long ldx,
                             const RowSink& out, cudaStream_t s);
