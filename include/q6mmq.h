@@ -673,7 +673,8 @@ int q6_rms_norm_f8(const void *X, int type, int64_t ldx, const void *residual, i
 
 /* t = silu(gate) * up, quantised: X [N][ldx] holds K gate values, then K up
  * values of each row (ldx >= 2 K), silu(g) = g / (1 + exp(-g)) within 2^-20 of
- * its value where g > -3, 2^-16 at g = -87. */
+ * its value where g > -3, 2^-16 at g = -87, and 0 below g = -87.34 (where its
+ * value is above -1.03e-36). */
 int q6_silu_mul_q8(const void *X, int type, int N, int K, int64_t ldx, int8_t *Xq, float *da,
                    uint16_t *Xh, float *us, q6_stream_t s);
 int q6_silu_mul_f8(const void *X, int type, int N, int K, int64_t ldx, uint8_t *xq, float *sx,
