@@ -37,9 +37,10 @@ bool rows_aligned(const void* p, int type, int64_t ld) {
 constexpr int kMost = INT32_MAX - 4096;
 constexpr int64_t kMostElements = 1ll << 40;
 
-// Tokens up to which the weight's rows are the tensor cores' lanes. (With 128 tokens that
-// way, eight warps summing, 11008 x 4096 took 23.9 us, 4096 x 4096 15.8 and 4096 x 11008
-// 25.4; tokens on the lanes 18.9, 13.8 and 31.6.)
+// Tokens up to which the weight's rows are the tensor cores' lanes. (The next width, 128
+// tokens that way, eight warps summing: 11008 x 4096 23.9 us, 4096 x 4096 15.8 and 4096 x
+// 11008 25.4; tokens on the lanes 18.0, 10.5 and 18.1. 64 tokens this way 12.8, 8.2 and
+// 12.8, 65 the other way 17.6, 10.2 and 17.8.)
 constexpr int kFewTokens = 64;
 
 int check_f8(int rows, int K) {

@@ -47,7 +47,9 @@ constexpr int kGroup = 8;              // token tiles walked together
 constexpr int kScaleBytes = 128 * 4;   // a block's scales of a CTA's tokens
 constexpr int kPart = 64;              // bytes of a row that are stored at a time
 constexpr int kOutBytes = 32 * kPart;  // of a warp
-// Registers of a thread: 128 + 256 threads share the 384 * 168 of the launch.
+// Registers of a thread: 128 + 256 threads share the 384 * 168 of the launch. (With 256
+// weight rows the 16-bit forms spill 8 bytes, outside the loop over K's blocks: a product
+// of 4864 x 4096 reads them back 17480 times with K = 1024 and with 4096.)
 constexpr int kRegsFew = 40, kRegsMany = 232;
 
 enum : uint32_t { kSiteDone = 48, kSiteFull, kSiteSlot, kSiteDrain };
