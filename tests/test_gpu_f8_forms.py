@@ -32,7 +32,7 @@ FORMS = [((1, 128, 128), ("f8_few", 16, 128, 1)),        # a single block of K
          ((64, 22016, 528), ("f8_few", 64, 128, 1)),     # more bands than the SMs take in two parts
          ((65, 1024, 1152), ("f8_tc", 256, 128, 1)),     # few tiles, a short K
          ((65, 1024, 3600), ("f8_tc", 256, 128, 4)),
-         ((300, 1000, 3600), ("f8_tc", 256, 128, 2)),
+         ((300, 1300, 3600), ("f8_tc", 256, 128, 2)),
          ((2048, 4096, 528), ("f8_tc", 256, 256, 1))]
 
 
@@ -76,8 +76,10 @@ def test_all_clusters_of_a_few_tokens_run_at_a_time(N, K):
 def test_every_number_of_parts_is_exact(N, parts):
     """The largest weight that is split into this many parts, and a row less."""
     K = 1040
-    bands = max(b for b in range(1, 320) if q6.f8_mmq_form(128 * b, K, N).parts == parts)
-    for M in (128 * bands, 128 * bands - 127):
+    bands = [b for b in range(1, 320) if q6.f8_mmq_form(128 * b, K, N).parts == parts]
+    if not bands:
+        pytest.skip("this device has as much room for clusters of one more")
+    for M in (128 * bands[-1], 128 * bands[-1] - 127):
         assert q6.f8_mmq_form(M, K, N).parts == parts
         check_exact(N, M, K)
 
